@@ -337,6 +337,163 @@ dec_status decode_layer(dec_handle* h, const dec_layer_weights* Wt, dec_bf16* hi
  * [K3 P1§4]. ptr and bytes multiples of 16. */
 dec_status dec_prefetch_l2(dec_handle* h, const void* ptr, size_t bytes, cudaStream_t stream);
 
+/* ------------------------------------------------------------------ attention
+ *
+ * What stands between the input projection and the out-projection of a decode
+ * layer that serves requests: the positions and cache slots of a step's
+ * tokens, rotary positions with the write of k and v into a paged cache, and
+ * attention over that cache. The sources leave the attention core open; these
+ * are the plain operators of a softmax-attention layer.
+ *
+ * A batch is a list of requests. Request b has own_len[b] tokens of its own
+ * in the cache after this step, the last row_start[b + 1] - row_start[b] of
+ * which are this step's rows; before them come prefix_len tokens that all
+ * requests of the batch share. A request may have no rows (a finished one),
+ * and rows at and behind row_start[requests] belong to none (padding).
+ * Lengths, tables and slots are device memory, so a captured graph can be
+ * replayed with new ones. int32 arrays need 4-byte alignment only. */
+
+/* The paged key / value cache of one layer. Block i holds
+ * [kv_heads][block_size][head_dim] values at k + i * block_stride (and at
+ * v + i * block_stride); slot s is token s % block_size of block
+ * s / block_size. k and v may interleave in one pool (a larger stride). */
+typedef struct dec_kv_cache {
+  dec_bf16* k;
+  dec_bf16* v;
+  int64_t block_stride; /* elements; at least kv_heads * block_size * head_dim, a multiple of 8 */
+  int blocks;           /* blocks * block_size < 2^31 */
+  int block_size;       /* 16, 32, 64 or 128 */
+  int kv_heads;         /* 1..128 */
+  int head_dim;         /* 64 or 128 */
+} dec_kv_cache;
+
+/* The requests of one step, as attention reads them. */
+typedef struct dec_batch {
+  int requests;               /* 1..64 */
+  int max_new;                /* at least the rows of any one request, 1..64 */
+  const int32_t* row_start;   /* [requests + 1] first row of each request, not decreasing */
+  const int32_t* own_len;     /* [requests] own tokens in the cache, this step's included */
+  const int32_t* block_table; /* [requests][max_blocks] cache blocks of the own tokens, in order */
+  int max_blocks;             /* at least 1 */
+  const int32_t* prefix_table; /* [ceil(prefix_len / block_size)] blocks of the shared prefix; NULL if none */
+  int prefix_len;             /* 0: no shared prefix */
+} dec_batch;
+
+/* Outputs of dec_batch_tables (device memory). */
+typedef struct dec_step_tables {
+  int32_t* row_start; /* [requests + 1] */
+  int32_t* own_len;   /* [requests]; may be ctx_len itself */
+  int32_t* positions; /* [rows] */
+  int32_t* slots;     /* [rows] */
+  int32_t* left;      /* [2] */
+} dec_step_tables;
+
+/* Positions, slots and block-table entries of one step, built on the GPU from
+ * the requests' lengths. Request b holds ctx_len[b] own tokens in the cache
+ * and gets new_len[b] more (negative values count as 0):
+ *   row_start = exclusive running sum of new_len, held at `rows`
+ *   own_len   = ctx_len + the request's rows
+ *   position of row i of request b = position_offset + ctx_len[b] + i
+ * A request whose rows reach past its ceil(ctx_len / block_size) held blocks
+ * gets blocks from the free list free_blocks[0 .. *free_count), taken from its
+ * end, requests in order, and they are entered in its row of
+ * block_table [requests][max_blocks]; the entries it holds stay as they are.
+ *   slots[t] = block_table[b][j / block_size] * block_size + j % block_size
+ * for row t's own token j, and -1 where it has no block: the free list was
+ * used up (such entries become -1), j is past max_blocks blocks, or the held
+ * entry is negative. Rows behind the last request get slot -1 and position 0.
+ *   left[0] = free blocks that remain (pass it as the next step's free_count,
+ *             it may be the same memory), left[1] = rows of requests that got
+ *             no slot
+ * A request that ends gives its blocks back when the caller puts them behind
+ * the remaining ones in free_blocks and raises the count. Rows that new_len
+ * gives past `rows` are left out (row_start is held at rows). One launch, no
+ * workspace; the results depend on the inputs alone.
+ * 1 <= requests <= 1024, 1 <= rows <= 2^20, block_size 16, 32, 64 or 128,
+ * 1 <= max_blocks <= 2^24, position_offset >= 0. Apart from the pairs named
+ * above, no output may overlap an input. */
+dec_status dec_batch_tables(dec_handle* h, const int32_t* ctx_len, const int32_t* new_len, int requests,
+                            const int32_t* free_blocks, const int32_t* free_count, int32_t* block_table,
+                            int max_blocks, int block_size, int position_offset, int rows,
+                            const dec_step_tables* out, cudaStream_t stream);
+
+/* How rotary frequencies are stretched for contexts longer than the original
+ * length L, by a factor f >= 1, for pairs i of R = rotary_dim:
+ * f_i = base^(-2 i / R) radians a position, and then
+ *  NONE:   f_i
+ *  LINEAR: f_i / f
+ *  NTK:    f_i of base * f^(R / (R - 2))
+ *  BANDS:  k f_i + (1 - k) f_i / f, k = clamp((turns_i - low) / (high - low)),
+ *          turns_i = L f_i / 2 pi: pairs that turn fast are kept, slow ones
+ *          divided, a blend by turns between
+ *  YARN:   the same blend as a ramp over the pair's index i, from
+ *          floor(c(high)) to ceil(c(low)), c(t) = R ln(L / 2 pi t) / (2 ln base),
+ *          held in [0, R - 1] (Peng et al., "YaRN", 2023); its factor on the
+ *          logits, 0.1 ln f + 1 on q and k each, is dec_rope's magnitude */
+typedef enum dec_rope_scaling {
+  DEC_ROPE_NONE = 0,
+  DEC_ROPE_LINEAR = 1,
+  DEC_ROPE_NTK = 2,
+  DEC_ROPE_BANDS = 3,
+  DEC_ROPE_YARN = 4
+} dec_rope_scaling;
+
+/* Write the rotary_dim / 2 phase steps that dec_rope_append reads: step i is
+ * the fraction of a turn that pair i moves per position, f_i / 2 pi, in units
+ * of 2^-64 turns (computed in 64-bit floating point). Position times step,
+ * modulo 2^64, is then the angle modulo a turn at any int32 position, exact
+ * to 2^-53 of the step's own rounding, with no range reduction left.
+ * rotary_dim a multiple of 16 in [16, 128], base > 1, factor >= 1;
+ * original_len > 0 and 0 < low < high are read by BANDS and YARN only. */
+dec_status dec_rope_phases(dec_handle* h, uint64_t* phases, int rotary_dim, double base, int scaling, double factor,
+                           double original_len, double low, double high, cudaStream_t stream);
+
+typedef struct dec_rope {
+  int rotary_dim;         /* leading elements of each head that turn: a multiple of 16 up to head_dim; 0: none */
+  int interleaved;        /* 0: pairs (i, i + rotary_dim / 2); 1: pairs (2 i, 2 i + 1) */
+  float magnitude;        /* factor on cos and sin (1 unless the scaling asks for another), finite */
+  const uint64_t* phases; /* [rotary_dim / 2] from dec_rope_phases, 16-byte aligned; NULL if rotary_dim is 0 */
+} dec_rope;
+
+/* Turn q and k by their rows' positions and write k and v into the cache:
+ *   q_out[t] = R(positions[t]) q[t]          (all `rows` rows)
+ *   cache.k[slots[t]] = R(positions[t]) k[t], cache.v[slots[t]] = v[t]
+ * where R turns each pair (a, b) of the first rotary_dim elements of a head
+ * to (a c - b s, b c + a s), c and s being magnitude times cos and sin, and
+ * leaves the rest of the head. fp32 math, one bf16 rounding. Rows whose slot
+ * is negative or past the cache write no k and v. No two rows may have the
+ * same slot. q [rows][q_heads * head_dim] with row stride ldq, and k, v
+ * [rows][kv_heads * head_dim] with row strides ldk, ldv, may be columns of
+ * one projection's output; q_out (row stride ldqo) may be q itself with the
+ * same stride. q and q_out both NULL (q_heads 0): only the cache is written.
+ * 1 <= rows <= 2^20, q_heads <= 1024, strides multiples of 8. */
+dec_status dec_rope_append(dec_handle* h, const dec_rope* rope, const dec_bf16* q, int64_t ldq, const dec_bf16* k,
+                           int64_t ldk, const dec_bf16* v, int64_t ldv, dec_bf16* q_out, int64_t ldqo, int rows,
+                           int q_heads, const int32_t* positions, const int32_t* slots, const dec_kv_cache* cache,
+                           cudaStream_t stream);
+
+dec_status dec_attention_workspace_size(const dec_handle* h, int M, int q_heads, const dec_kv_cache* cache,
+                                        const dec_batch* batch, size_t* bytes);
+
+/* Attention of a step's rows over the cache: for row i of the n of request b
+ * and query head g (key / value head g / (q_heads / kv_heads)),
+ *   out = sum_j p_j v_j, p = softmax_j(scale q . k_j)
+ * over the prefix_len shared tokens and the own tokens
+ * j < own_len[b] - n + i + 1: each row sees the rows before it. The shared
+ * prefix is read once for all rows, not once a request. Tokens in a block
+ * whose table entry is outside [0, blocks), or past max_blocks blocks, are
+ * not there. A row that sees no token gets zeros; rows of no request are left
+ * as they were. What the cache holds outside the visible tokens (infinities
+ * and NaN too) does not matter.
+ * q [M][q_heads * head_dim] with row stride ldq, out the same with ldo; out
+ * must not overlap q. 1 <= M <= 64, q_heads a multiple of kv_heads, at most
+ * 128 query heads to a key head, scale > 0 and finite. Scores, softmax
+ * statistics and sums are fp32; the weights p are rounded to bf16 for the
+ * product with v. */
+dec_status dec_attention(dec_handle* h, const dec_bf16* q, int64_t ldq, const dec_kv_cache* cache,
+                         const dec_batch* batch, float scale, dec_bf16* out, int64_t ldo, int M, int q_heads,
+                         void* ws, size_t ws_bytes, cudaStream_t stream);
+
 /* ------------------------------------------------------------------ measurement */
 
 /* Per-kernel timing record returned by dec_profile_read. */

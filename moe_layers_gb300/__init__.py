@@ -48,6 +48,27 @@ class _MoeWeights(ctypes.Structure):
                [(n, ctypes.c_void_p) for n in ("gamma", "W_r", "Wg", "Wu", "Wd", "Wg_s", "Wu_s", "Wd_s")]
 
 
+class _KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("block_stride", ctypes.c_int64),
+                ("blocks", ctypes.c_int), ("block_size", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int)]
+
+
+class _Batch(ctypes.Structure):
+    _fields_ = [("requests", ctypes.c_int), ("max_new", ctypes.c_int), ("row_start", ctypes.c_void_p),
+                ("own_len", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("max_blocks", ctypes.c_int),
+                ("prefix_table", ctypes.c_void_p), ("prefix_len", ctypes.c_int)]
+
+
+class _StepTables(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("row_start", "own_len", "positions", "slots", "left")]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("magnitude", ctypes.c_float),
+                ("phases", ctypes.c_void_p)]
+
+
 class _KernelTime(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 32), ("launches", ctypes.c_int), ("total_ms", ctypes.c_double)]
 
@@ -65,6 +86,7 @@ def _load():
                            "(the CUDA path has no fallback)")
     lib = ctypes.CDLL(LIB_PATH)
     P, I, Z, U64, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint64, ctypes.c_float
+    I64 = ctypes.c_int64
     sig = {
         "dec_create": [ctypes.POINTER(P), I],
         "dec_destroy": [P],
@@ -91,6 +113,14 @@ def _load():
         "decode_layer_workspace_size": [P, ctypes.POINTER(_LayerWeights), I, ctypes.POINTER(Z)],
         "decode_layer": [P, ctypes.POINTER(_LayerWeights), P, I, ctypes.POINTER(_LayerTrace), P, Z, P],
         "dec_prefetch_l2": [P, P, Z, P],
+        "dec_batch_tables": [P, P, P, I, P, P, P, I, I, I, I, ctypes.POINTER(_StepTables), P],
+        "dec_rope_phases": [P, P, I, ctypes.c_double, I, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                            ctypes.c_double, P],
+        "dec_rope_append": [P, ctypes.POINTER(_Rope), P, I64, P, I64, P, I64, P, I64, I, I, P, P,
+                            ctypes.POINTER(_KvCache), P],
+        "dec_attention_workspace_size": [P, I, I, ctypes.POINTER(_KvCache), ctypes.POINTER(_Batch),
+                                         ctypes.POINTER(Z)],
+        "dec_attention": [P, P, I64, ctypes.POINTER(_KvCache), ctypes.POINTER(_Batch), F, P, I64, I, I, P, Z, P],
         "dec_test_wait_timeout": [P, P],
         "dec_test_routing_wait_timeout": [P, I, P],
         "dec_test_delayed_copy": [P, P, P, Z, U64, P],
@@ -159,6 +189,7 @@ class Handle:
         self._h = h
         self.device = int(device)
         self._ws = {}
+        self._stream_ws = {}
 
     @property
     def ptr(self):
@@ -169,6 +200,7 @@ class Handle:
             _load().dec_destroy(self._h)
             self._h = ctypes.c_void_p()
             self._ws.clear()
+            self._stream_ws.clear()
 
     def __enter__(self):
         return self
@@ -194,6 +226,17 @@ class Handle:
             t.zero_()
         self._ws[key] = (t, layout)
         return t
+
+    def stream_workspace(self, key, stream: int, nbytes: int):
+        """A workspace of at least nbytes per key and stream, for calls that need no
+        zeroed memory. One that is outgrown is kept until the handle closes: a
+        captured graph may still use it."""
+        import torch
+        held = self._stream_ws.setdefault((key, stream), [])
+        if not held or held[-1].numel() < nbytes:
+            size = max(int(nbytes), 256, 2 * held[-1].numel() if held else 0)
+            held.append(torch.empty(size, dtype=torch.uint8, device=f"cuda:{self.device}"))
+        return held[-1]
 
     def set_force_variant(self, v: int) -> None:
         _check(_load().dec_set_force_variant(self._h, int(v)), "dec_set_force_variant")
@@ -487,6 +530,220 @@ def decode_layer(h: Handle, weights: LayerWeights, hidden, trace=False, stream=N
         tr.h1, tr.idx, tr.w, tr.scores = (_ptr(out.get(n)) for n in ("h1", "idx", "w", "scores"))
     _check(lib.decode_layer(h.ptr, ctypes.byref(cw), _ptr(hidden), M, ctypes.byref(tr) if tr is not None else None,
                             _ptr(ws), ws.numel(), _stream(stream)), "decode_layer")
+    return out
+
+
+# ---------------------------------------------------------------------------- attention
+def _int32(t, name: str, ndim: int = 1):
+    import torch
+    _require(t, torch.int32, name, ndim)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _stream_of(h: Handle, stream) -> int:
+    """The given stream, else the current one of the handle's device."""
+    import torch
+    return (torch.cuda.current_stream(h.device) if stream is None else stream).cuda_stream
+
+
+class KvCache:
+    """Paged key / value cache of one layer (see dec_kv_cache): k and v bf16
+    [blocks, kv_heads, block_size, head_dim], each block contiguous (the two may
+    interleave in one pool). Make a new one to describe other tensors."""
+
+    def __init__(self, k, v):
+        import torch
+        for n, t in (("k", k), ("v", v)):
+            _require(t, torch.bfloat16, n, 4)
+            _, heads, size, dim = t.shape
+            if t.stride()[1:] != (size * dim, dim, 1):
+                raise ValueError(f"{n}: the heads, tokens and elements of a block must be contiguous")
+        if k.shape != v.shape or (k.shape[0] > 1 and k.stride(0) != v.stride(0)) or k.device != v.device:
+            raise ValueError("k and v must have the same shape, block stride and device")
+        self.k, self.v = k, v
+        blocks, heads, size, dim = k.shape
+        stride = k.stride(0) if blocks > 1 else heads * size * dim
+        self._c = _KvCache(k.data_ptr(), v.data_ptr(), stride, blocks, size, heads, dim)
+        self._ref = ctypes.byref(self._c)
+        self.head_dim, self.device_index = dim, k.device.index
+
+
+class StepTables:
+    """Outputs of dec_batch_tables: int32 device tensors row_start [requests + 1],
+    own_len [requests], positions [rows], slots [rows] and left [2]."""
+
+    def __init__(self, row_start, own_len, positions, slots, left):
+        for n, t in (("row_start", row_start), ("own_len", own_len), ("positions", positions), ("slots", slots),
+                     ("left", left)):
+            _int32(t, n)
+        if any(t.device != row_start.device for t in (own_len, positions, slots, left)):
+            raise ValueError("the tables must be on one device")
+        if row_start.numel() != own_len.numel() + 1 or positions.numel() != slots.numel() or left.numel() != 2:
+            raise ValueError("row_start needs one element more than own_len, positions as many as slots, left two")
+        self.row_start, self.own_len, self.positions, self.slots, self.left = row_start, own_len, positions, slots, left
+        self._c = _StepTables(*(t.data_ptr() for t in (row_start, own_len, positions, slots, left)))
+        self._ref = ctypes.byref(self._c)
+        self.requests, self.rows, self.device_index = own_len.numel(), positions.numel(), row_start.device.index
+
+    @classmethod
+    def empty(cls, requests: int, rows: int, device="cuda"):
+        import torch
+        return cls(*(torch.empty(n, dtype=torch.int32, device=device) for n in (requests + 1, requests, rows, rows, 2)))
+
+
+class Batch:
+    """The requests of one step as attention reads them (see dec_batch): int32
+    row_start [requests + 1], own_len [requests], block_table [requests,
+    max_blocks]; max_new bounds the rows of one request; prefix_table holds the
+    blocks of a prefix of prefix_len tokens that all requests share."""
+
+    def __init__(self, row_start, own_len, block_table, max_new: int = 1, prefix_table=None, prefix_len: int = 0):
+        _int32(row_start, "row_start")
+        _int32(own_len, "own_len")
+        _int32(block_table, "block_table", 2)
+        if row_start.numel() != own_len.numel() + 1 or block_table.shape[0] != own_len.numel():
+            raise ValueError("row_start needs one element more than own_len, block_table as many rows")
+        if prefix_len > 0:
+            _int32(prefix_table, "prefix_table")
+        if any(t.device != own_len.device for t in (row_start, block_table) + ((prefix_table,) if prefix_len > 0 else ())):
+            raise ValueError("the tables must be on one device")
+        self.row_start, self.own_len, self.block_table, self.prefix_table = row_start, own_len, block_table, prefix_table
+        self.max_new, self.prefix_len = int(max_new), int(prefix_len)
+        self._c = _Batch(own_len.numel(), self.max_new, row_start.data_ptr(), own_len.data_ptr(),
+                         block_table.data_ptr(), block_table.shape[1], prefix_table.data_ptr() if prefix_len > 0 else None,
+                         self.prefix_len)
+        self._ref = ctypes.byref(self._c)
+        self.device_index = own_len.device.index
+
+
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
+
+
+class Rope:
+    """Rotary positions of the first rotary_dim elements of each head (see
+    dec_rope and dec_rope_phases; rotary_dim 0: none). scaling: "none",
+    "linear", "ntk", "bands" or "yarn" by `factor`; low and high are the turns
+    within original_len between which "bands" (default 1 and 4) and "yarn"
+    (1 and 32) blend."""
+
+    def __init__(self, h: Handle, rotary_dim: int, base: float = 10000.0, interleaved: bool = False,
+                 scaling: str = "none", factor: float = 1.0, original_len: float = 8192.0, low: float = 1.0,
+                 high: Optional[float] = None, magnitude: float = 1.0, stream=None):
+        import torch
+        if scaling not in ROPE_SCALING:
+            raise ValueError(f"scaling must be one of {sorted(ROPE_SCALING)}")
+        high = (4.0 if scaling == "bands" else 32.0) if high is None else high
+        self.phases = None
+        if rotary_dim:
+            self.phases = torch.empty(max(rotary_dim // 2, 1), dtype=torch.int64, device=f"cuda:{h.device}")
+            _check(_load().dec_rope_phases(h.ptr, self.phases.data_ptr(), int(rotary_dim), float(base),
+                                           ROPE_SCALING[scaling], float(factor), float(original_len), float(low),
+                                           float(high), _stream_of(h, stream)), "dec_rope_phases")
+        self._c = _Rope(int(rotary_dim), 1 if interleaved else 0, float(magnitude), _ptr(self.phases))
+        self._ref = ctypes.byref(self._c)
+
+
+def dec_batch_tables(h: Handle, ctx_len, new_len, free_blocks, free_count, block_table, block_size: int,
+                     out: Optional[StepTables] = None, rows: Optional[int] = None, position_offset: int = 0,
+                     stream=None) -> StepTables:
+    """Positions, slots and block-table entries of one step from the requests'
+    lengths (int32 tensors); block_table [requests, max_blocks] is updated in
+    place. `out` gives the output tensors, else they are made for `rows` rows."""
+    for n, t in (("ctx_len", ctx_len), ("new_len", new_len), ("free_blocks", free_blocks), ("free_count", free_count)):
+        _int32(t, n)
+    _int32(block_table, "block_table", 2)
+    n = ctx_len.numel()
+    if out is None:
+        if rows is None:
+            raise ValueError("rows is required without out")
+        out = StepTables.empty(n, rows, ctx_len.device)
+    if new_len.numel() != n or block_table.shape[0] != n or out.requests != n or free_count.numel() < 1:
+        raise ValueError("ctx_len, new_len, block_table and out must be of as many requests, free_count of one value")
+    if rows is not None and rows != out.rows:
+        raise ValueError("rows differs from out's")
+    _same_device(h, ctx_len, new_len, free_blocks, free_count, block_table, out)
+    _check(_load().dec_batch_tables(h.ptr, ctx_len.data_ptr(), new_len.data_ptr(), n, free_blocks.data_ptr(),
+                                    free_count.data_ptr(), block_table.data_ptr(), block_table.shape[1],
+                                    int(block_size), int(position_offset), out.rows, out._ref, _stream_of(h, stream)),
+           "dec_batch_tables")
+    return out
+
+
+def _same_device(h: Handle, *things) -> None:
+    for t in things:
+        index = t.device_index if hasattr(t, "device_index") else t.device.index
+        if index != h.device:
+            raise ValueError(f"every tensor must be on the handle's device, cuda:{h.device}")
+
+
+def dec_rope_append(h: Handle, rope: Rope, q, k, v, positions, slots, cache: KvCache, q_out=None, stream=None):
+    """Turn q and k (bf16 [rows, heads * head_dim], rows may be strided) by their
+    positions, write k and v into the cache at their slots; returns the turned
+    q (q_out, which may be q; None with q None: only the cache is written)."""
+    import torch
+    for n, t in (("k", k), ("v", v)):
+        _require(t, torch.bfloat16, n, 2)
+    _int32(positions, "positions")
+    _int32(slots, "slots")
+    rows, d = k.shape[0], cache.head_dim
+    if k.shape != v.shape or k.shape[1] != cache.k.shape[1] * d:
+        raise ValueError("k and v must be [rows, kv_heads * head_dim]")
+    if positions.numel() != rows or slots.numel() != rows:
+        raise ValueError("positions and slots must have one element per row")
+    heads = 0
+    if q is not None:
+        _require(q, torch.bfloat16, "q", 2)
+        if q.shape[0] != rows or q.shape[1] % d != 0:
+            raise ValueError("q must be [rows, q_heads * head_dim]")
+        heads = q.shape[1] // d
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        _require(q_out, torch.bfloat16, "q_out", 2)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        _same_device(h, q, q_out)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _same_device(h, k, v, positions, slots, cache)
+    _check(_load().dec_rope_append(h.ptr, rope._ref, _ptr(q), 0 if q is None else _rows(q, "q"), k.data_ptr(),
+                                   _rows(k, "k"), v.data_ptr(), _rows(v, "v"), _ptr(q_out),
+                                   0 if q is None else _rows(q_out, "q_out"), rows, heads, positions.data_ptr(),
+                                   slots.data_ptr(), cache._ref, _stream_of(h, stream)), "dec_rope_append")
+    return q_out
+
+
+def dec_attention_workspace_size(h: Handle, M: int, q_heads: int, cache: KvCache, batch: Batch) -> int:
+    nb = ctypes.c_size_t()
+    _check(_load().dec_attention_workspace_size(h.ptr, int(M), int(q_heads), cache._ref, batch._ref,
+                                                ctypes.byref(nb)), "dec_attention_workspace_size")
+    return nb.value
+
+
+def dec_attention(h: Handle, q, cache: KvCache, batch: Batch, scale: float, out=None, stream=None, ws=None):
+    """Attention of a step's rows q (bf16 [M, q_heads * head_dim], rows may be
+    strided) over the batch's shared prefix and own tokens in the cache. Without
+    `out`, rows that belong to no request are zero."""
+    import torch
+    _require(q, torch.bfloat16, "q", 2)
+    M, width = q.shape
+    if width % cache.head_dim != 0:
+        raise ValueError("q must be [M, q_heads * head_dim]")
+    if out is None:
+        out = torch.zeros((M, width), dtype=torch.bfloat16, device=q.device)
+    _require(out, torch.bfloat16, "out", 2)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if batch.prefix_len > 0 and batch.prefix_table.numel() * cache.k.shape[2] < batch.prefix_len:
+        raise ValueError("prefix_table holds fewer blocks than prefix_len tokens need")
+    _same_device(h, q, out, cache, batch)
+    heads, sp = width // cache.head_dim, _stream_of(h, stream)
+    if ws is None:
+        ws = h.stream_workspace("attention", sp, dec_attention_workspace_size(h, M, heads, cache, batch))
+    _check(_load().dec_attention(h.ptr, q.data_ptr(), _rows(q, "q"), cache._ref, batch._ref, float(scale),
+                                 out.data_ptr(), _rows(out, "out"), M, heads, ws.data_ptr(), ws.numel(), sp),
+           "dec_attention")
     return out
 
 

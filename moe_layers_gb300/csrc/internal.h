@@ -175,6 +175,52 @@ cudaError_t launch_route_table(dec_handle* h, const int32_t* idx, int M, int k, 
                                int* table, uint16_t* xs, cudaStream_t s);
 cudaError_t launch_combine(dec_handle* h, const float* y, const int* table, const float* w, int M, int k, int E,
                            const float* ys, const uint16_t* res, uint16_t* out, int H, cudaStream_t s);
+// ---------------------------------------------------------------- attention
+cudaError_t launch_tables(dec_handle* h, const int32_t* ctx_len, const int32_t* new_len, int n,
+                          const int32_t* free_blocks, const int32_t* free_count, int32_t* table, int max_blocks,
+                          int block_size, int offset, int rows, const dec_step_tables& out, cudaStream_t s);
+cudaError_t launch_rope_phases(dec_handle* h, uint64_t* phases, int r, double base, int scaling, double factor,
+                               double length, double low, double high, cudaStream_t s);
+cudaError_t launch_rope_append(dec_handle* h, const dec_rope& rope, const uint16_t* q, long long ldq,
+                               const uint16_t* k, long long ldk, const uint16_t* v, long long ldv, uint16_t* qo,
+                               long long ldqo, int rows, int q_heads, const int32_t* positions, const int32_t* slots,
+                               const dec_kv_cache& cache, cudaStream_t s);
+
+struct AttentionParams {
+  const uint16_t* q;
+  long long ldq;
+  uint16_t* out;
+  long long ldo;
+  const uint16_t *k, *v;
+  long long block_stride;
+  int blocks, shift;  // block_size = 1 << shift
+  int kv_heads, q_heads, dim;
+  int requests, max_new, max_blocks, prefix_len, M;
+  const int32_t *row_start, *own_len, *block_table, *prefix_table;
+  float scale;
+};
+size_t attention_ws_bytes(const dec_handle* h, int M, int q_heads, const dec_kv_cache& cache, const dec_batch& batch);
+cudaError_t launch_attention(dec_handle* h, const AttentionParams& P, int M, cudaStream_t s);
+
+// Checked by the callers (api_attention.cu): shapes and pointers of an attention call.
+bool cache_ok(const dec_kv_cache* c);
+bool batch_ok(const dec_batch* b);
+bool rope_ok(const dec_rope* r, int head_dim);
+bool attention_shape_ok(int M, int q_heads, const dec_kv_cache* c, const dec_batch* b);
+
+// Makes the handle's device current for the lifetime of the object.
+struct DeviceGuard {
+  int prev = -1;
+  bool ok = true;
+  explicit DeviceGuard(int device) {
+    ok = cudaGetDevice(&prev) == cudaSuccess && (prev == device || cudaSetDevice(device) == cudaSuccess);
+    if (ok && prev == device) prev = -1;
+  }
+  ~DeviceGuard() {
+    if (ok && prev >= 0) cudaSetDevice(prev);
+  }
+};
+
 cudaError_t launch_prefetch(dec_handle* h, const void* p, size_t bytes, int ctas, cudaStream_t s);
 cudaError_t launch_wait_timeout_probe(dec_handle* h, cudaStream_t s);
 cudaError_t launch_occupy(dec_handle* h, int ctas, uint64_t hold_ns, cudaStream_t s);

@@ -274,3 +274,102 @@ def decode_layer(h, gamma1, W_in, W_o, gamma2, Wr, k: int, expert: ExpertFn, sha
     m = moe_layer(h1, gamma2, Wr, k, expert, shared, residual=h1, eps=eps, storage=storage)
     return dict(a=a, y_in=y_in, h1=h1, b=m["b"], logits=m["logits"], scores=m["scores"], idx=m["idx"], w=m["w"],
                 out=m["out"], unrounded=dict(a=a_x, y_in=y_x, h1=h1_x, b=m["b_unrounded"]))
+
+
+# ----------------------------------------------------------------------------- attention
+def batch_tables(ctx_len, new_len, free_blocks, free_count: int, table, block_size: int, offset: int, rows: int):
+    """A step's tables from the requests' lengths, one request and one row at a
+    time. Returns dict(row_start, own_len, positions, slots, left, table)."""
+    table = np.array(table, dtype=np.int64)
+    free = [int(x) for x in free_blocks[:max(int(free_count), 0)]]
+    row_start, own_len = [0], []
+    positions, slots = np.zeros(rows, np.int64), np.full(rows, -1, np.int64)
+    missing = 0
+    for b, (c, n) in enumerate(zip(ctx_len, new_len)):
+        c, n = max(int(c), 0), max(int(n), 0)
+        first = row_start[-1]
+        n = min(n, rows - first)
+        held = min(-(-c // block_size), table.shape[1])
+        for j in range(held, min(-(-(c + n) // block_size), table.shape[1])):
+            table[b, j] = free.pop() if free else -1
+        for i in range(n):
+            t, j = first + i, c + i
+            positions[t] = offset + j
+            block = table[b, j // block_size] if j // block_size < table.shape[1] else -1
+            if block >= 0:
+                slots[t] = block * block_size + j % block_size
+            else:
+                missing += 1
+        row_start.append(first + n)
+        own_len.append(c + n)
+    return dict(row_start=np.array(row_start), own_len=np.array(own_len), positions=positions, slots=slots,
+                left=np.array([len(free), missing]), table=table)
+
+
+def rope_frequencies(rot: int, base: float, scaling: str = "none", factor: float = 1.0, length: float = 8192.0,
+                     low: float = 1.0, high: float = 4.0) -> np.ndarray:
+    """Radians per position of each pair of the first ``rot`` elements of a head."""
+    i = np.arange(rot // 2)
+    f = base ** (-2.0 * i / rot)
+    if scaling == "linear":
+        return f / factor
+    if scaling == "ntk":
+        return (base * factor ** (rot / (rot - 2.0))) ** (-2.0 * i / rot)
+    if scaling == "bands":
+        keep = np.clip((length * f / (2 * np.pi) - low) / (high - low), 0.0, 1.0)
+        return keep * f + (1 - keep) * f / factor
+    if scaling == "yarn":
+        def index(turns):
+            return rot * np.log(length / (2 * np.pi * turns)) / (2 * np.log(base))
+        lo, hi = max(np.floor(index(high)), 0.0), min(np.ceil(index(low)), rot - 1.0)
+        drop = np.clip((i - lo) / max(hi - lo, 0.001), 0.0, 1.0)
+        return (1 - drop) * f + drop * f / factor
+    return f
+
+
+def rope(x, positions, freq, interleaved: bool = False, magnitude: float = 1.0) -> np.ndarray:
+    """x [rows, heads, dim]: pairs of the leading 2 len(freq) elements of each head
+    turned by position * freq; angles by fmod of the 64-bit product."""
+    x = as_f64(x).copy()
+    r = 2 * len(freq)
+    if r == 0:
+        return x
+    angle = np.asarray(positions, np.float64)[:, None] * freq[None, :]
+    c, s = magnitude * np.cos(angle)[:, None, :], magnitude * np.sin(angle)[:, None, :]
+    a_at, b_at = (slice(0, r, 2), slice(1, r, 2)) if interleaved else (slice(0, r // 2), slice(r // 2, r))
+    a, b = x[..., a_at].copy(), x[..., b_at].copy()
+    x[..., a_at], x[..., b_at] = a * c - b * s, b * c + a * s
+    return x
+
+
+def attention(q, k_cache, v_cache, row_start, own_len, table, scale: float, prefix_table=(), prefix_len: int = 0):
+    """q [rows, q_heads, dim] over caches [blocks, kv_heads, block_size, dim], one
+    row and head at a time. Returns (out, sum of p |v|, largest scale sum |q k|
+    over the visible keys), the last two for error bounds; rows of no request are
+    NaN in out."""
+    q = as_f64(q)
+    rows, heads, dim = q.shape
+    blocks, kv_heads, size, _ = k_cache.shape
+    out, spread = np.full(q.shape, np.nan), np.zeros(q.shape)
+    reach = np.zeros((rows, heads))
+    for b in range(len(own_len)):
+        first, n = int(row_start[b]), int(row_start[b + 1]) - int(row_start[b])
+        for i in range(n):
+            sees = int(own_len[b]) - n + i + 1
+            at = [(int(prefix_table[j // size]), j % size) for j in range(prefix_len)]
+            at += [(int(table[b][j // size]), j % size) for j in range(min(sees, len(table[b]) * size))]
+            at = [(blk, o) for blk, o in at if 0 <= blk < blocks]
+            out[first + i] = 0.0
+            if not at:
+                continue
+            blk, o = np.array(at).T
+            for g in range(heads):
+                k = as_f64(k_cache[blk, g // (heads // kv_heads), o])
+                v = as_f64(v_cache[blk, g // (heads // kv_heads), o])
+                s = scale * (k @ q[first + i, g])
+                p = np.exp(s - s.max())
+                p /= p.sum()
+                out[first + i, g] = p @ v
+                spread[first + i, g] = p @ np.abs(v)
+                reach[first + i, g] = scale * (np.abs(k) @ np.abs(q[first + i, g])).max()
+    return out, spread, reach
