@@ -483,11 +483,11 @@ dec_status dec_attention_workspace_size(const dec_handle* h, int M, int q_heads,
  * prefix is read once for all rows, not once a request. Tokens in a block
  * whose table entry is outside [0, blocks), or past max_blocks blocks, are
  * not there. A row that sees no token gets zeros; rows of no request are left
- * as they were. What the cache holds outside the visible tokens (infinities
- * and NaN too) does not matter.
+ * as they were. Places of the cache that hold none of these tokens do not
+ * matter (they may hold infinities and NaN).
  * q [M][q_heads * head_dim] with row stride ldq, out the same with ldo; out
  * must not overlap q. 1 <= M <= 64, q_heads a multiple of kv_heads, at most
- * 128 query heads to a key head, scale > 0 and finite. Scores, softmax
+ * 1024 in all and 128 to a key head, scale > 0 and finite. Scores, softmax
  * statistics and sums are fp32; the weights p are rounded to bf16 for the
  * product with v. */
 dec_status dec_attention(dec_handle* h, const dec_bf16* q, int64_t ldq, const dec_kv_cache* cache,

@@ -48,7 +48,7 @@ bool rope_ok(const dec_rope* r, int head_dim) {
 
 bool attention_shape_ok(int M, int q_heads, const dec_kv_cache* c, const dec_batch* b) {
   return M >= 1 && M <= kMaxAttentionRows && cache_ok(c) && batch_ok(b) && q_heads >= c->kv_heads &&
-         q_heads % c->kv_heads == 0 && q_heads / c->kv_heads <= 128 &&
+         q_heads % c->kv_heads == 0 && q_heads / c->kv_heads <= 128 && q_heads <= 1024 &&
          (long long)b->max_blocks * c->block_size <= 0x7fffffffLL;
 }
 
@@ -161,8 +161,7 @@ dec_status dec_attention(dec_handle* h, const dec_bf16* q, int64_t ldq, const de
   P.block_table = batch->block_table;
   P.prefix_table = batch->prefix_table;
   P.scale = scale;
-  LaunchScope scope(h, "attention", stream);
-  return status(launch_attention(h, P, M, stream));
+  return status(launch_attention(h, P, ws, stream));
 }
 
 }  // extern "C"

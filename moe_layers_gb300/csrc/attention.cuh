@@ -1,0 +1,169 @@
+// What the attention kernels share: how a step's work is cut into tiles and
+// divided among CTAs, and where the parts of a row that several CTAs computed
+// are kept until they are joined.
+//
+// A step has parts: part 0 is the shared prefix (its rows: every row of the
+// batch), part b + 1 the own tokens of request b. For one part and one key /
+// value head the query rows are (row of the part, head of the group), in
+// chunks of as many as the kernel holds, and the keys are in tiles of 64. A
+// unit is one tile for one chunk; the units of a part are ordered (head,
+// chunk, tile), the parts follow each other, and CTA c of G (at
+// most W) takes units [c W / G, (c + 1) W / G) of all W: every CTA streams the same number of
+// tiles, however ragged the lengths are. The tiles of one (head, chunk) that
+// one CTA takes are a piece. A piece that holds the first tile is kept by its
+// rows (`start`); any other is the first piece of its CTA and is kept by the
+// CTA (`rest`). The whole plan follows from the lengths in device memory, so
+// nothing of it depends on the host.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace dec {
+
+constexpr int kTileKeys = 64;
+constexpr int kMaxParts = 65;
+
+// Unnormalised sums [rows][dim] with their (maximum, sum) pairs, maxima in
+// units of log2.
+struct Pieces {
+  float* o = nullptr;
+  float2* ml = nullptr;
+};
+
+// One launch's share of the plan.
+struct Plan {
+  int prefix, own;  // which parts the launch takes
+  int rows;         // query rows of a chunk
+  int ctas;
+  Pieces rest;      // [ctas][rows]
+};
+
+struct AttentionLaunch {
+  AttentionParams a;
+  Plan plan;
+  Pieces start[2];  // prefix, own: [M][q_heads]
+  float scale_log2;
+  int* err;
+  unsigned long long wait_ns;
+};
+
+struct PartTable {
+  long long first[kMaxParts + 1];  // first unit; first[n] = all units
+  short row0[kMaxParts], rows[kMaxParts];
+  int len[kMaxParts];
+  int last[kMaxParts];  // keys that the part's first row sees; each further row sees one more (own parts)
+};
+
+// CTAs that take part: none without a unit, so that the pieces of a (head,
+// chunk) lie in consecutive CTAs.
+__device__ __forceinline__ long long plan_ctas(long long W, int ctas) { return W < 1 ? 1 : W < ctas ? W : ctas; }
+__device__ __forceinline__ long long unit_start(long long c, long long W, long long G) { return c * W / G; }
+__device__ __forceinline__ long long cta_of_unit(long long u, long long W, long long G) { return ((u + 1) * G - 1) / W; }
+
+// Fills the table with one warp (all 32 lanes). Lengths are brought into
+// range: rows into [0, M] and not decreasing, keys to at most max_blocks blocks.
+__device__ __forceinline__ void build_parts(PartTable& t, const AttentionParams& a, const Plan& p) {
+  const int lane = threadIdx.x & 31, n = a.requests + 1;
+  const int group = a.q_heads / a.kv_heads;
+  long long carry = 0;
+  for (int base = 0; base < n; base += 32) {
+    const int i = base + lane;
+    long long units = 0;
+    if (i < n) {
+      const int b = i - 1;
+      const int lo = i == 0 ? 0 : b, hi = i == 0 ? a.requests : b + 1;
+      const int r0 = min(max(ld_act_s32(a.row_start + lo), 0), a.M);
+      const int r1 = min(max(ld_act_s32(a.row_start + hi), r0), a.M);
+      const int rows = r1 - r0;
+      int len = a.prefix_len, last = a.prefix_len;
+      if (i > 0) {
+        const int own = ld_act_s32(a.own_len + b);
+        len = max(0, (int)min((long long)own, (long long)a.max_blocks << a.shift));
+        last = (int)max((long long)own - rows + 1, -1000LL);
+      }
+      t.row0[i] = (short)r0;
+      t.rows[i] = (short)rows;
+      t.len[i] = len;
+      t.last[i] = last;
+      if (i == 0 ? p.prefix : p.own) {
+        const int chunks = (rows * group + p.rows - 1) / p.rows;
+        units = (long long)a.kv_heads * chunks * (((long long)len + kTileKeys - 1) / kTileKeys);
+      }
+    }
+    long long inc = units;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    if (i < n) t.first[i] = carry + inc - units;
+    carry += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  if (lane == 0) t.first[n] = carry;
+}
+
+// The piece that starts at unit u and ends before u_end at the latest.
+struct Piece {
+  int part, kvh, chunk, tile0, tile1, tiles;
+};
+__device__ __forceinline__ Piece piece_at(const PartTable& t, const AttentionParams& a, const Plan& p, long long u,
+                                          long long u_end, int& part) {
+  while (t.first[part + 1] <= u) ++part;
+  const int chunks = (t.rows[part] * (a.q_heads / a.kv_heads) + p.rows - 1) / p.rows;
+  const int tiles = (int)(((long long)t.len[part] + kTileKeys - 1) / kTileKeys);
+  const long long at = u - t.first[part];
+  const int hc = (int)(at / tiles);
+  Piece q;
+  q.part = part;
+  q.kvh = hc / chunks;
+  q.chunk = hc % chunks;
+  q.tile0 = (int)(at - (long long)hc * tiles);
+  q.tile1 = (int)min((long long)tiles, q.tile0 + (u_end - u));
+  q.tiles = tiles;
+  return q;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 2^(m - top), 0 for a part that saw nothing (m = -inf, whatever top is).
+__device__ __forceinline__ float ex2_from(float m, float top) { return m == -INFINITY ? 0.f : ex2(m - top); }
+
+// Two floats rounded to nearest-even bf16, the first in the low half.
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// Cache ids of a part's blocks, read 32 at a time by a whole warp, the next 32 ahead.
+struct BlockIds {
+  const int32_t* table;
+  int count;  // entries that may be read
+  int base = -64, cur = -1, next = -1;
+  __device__ __forceinline__ BlockIds(const int32_t* t, int n) : table(t), count(n) {}
+  __device__ __forceinline__ int load(int i) const { return i < count ? ld_act_s32(table + i) : -1; }
+  // Makes the 32 entries around i present (the same i in every lane; a tile's
+  // entries lie in one aligned group of 32, and i never falls).
+  __device__ __forceinline__ void advance(int i) {
+    const int want = i & ~31;
+    if (want == base) return;
+    cur = want == base + 32 ? next : load(want + (threadIdx.x & 31));
+    base = want;
+    next = load(want + 32 + (threadIdx.x & 31));
+  }
+  __device__ __forceinline__ int get(int i) const { return __shfl_sync(0xffffffffu, cur, i & 31); }
+};
+
+}  // namespace dec

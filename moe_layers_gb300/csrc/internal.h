@@ -200,7 +200,7 @@ struct AttentionParams {
   float scale;
 };
 size_t attention_ws_bytes(const dec_handle* h, int M, int q_heads, const dec_kv_cache& cache, const dec_batch& batch);
-cudaError_t launch_attention(dec_handle* h, const AttentionParams& P, int M, cudaStream_t s);
+cudaError_t launch_attention(dec_handle* h, const AttentionParams& P, void* ws, cudaStream_t s);
 
 // Checked by the callers (api_attention.cu): shapes and pointers of an attention call.
 bool cache_ok(const dec_kv_cache* c);
