@@ -18,27 +18,34 @@
 namespace dec {
 
 constexpr int kAttnThreads = 160;  // 4 multiplying warps, 1 copying warp
-constexpr int kAttnSmem = 232448;
+// Two CTAs an SM: one warp per scheduler leaves the products' latency exposed
+// (870 cycles a tile against the 1370 that an SM's share of the memory rate
+// takes for one), and a CTA between two pieces does not stop the SM's stream.
+constexpr int kAttnCtasPerSm = 2;
+constexpr int kAttnSmem = 115712;
 
-// WK warps share a tile's keys, 4 / WK groups of 16 rows share its rows.
-template <int D, int WK>
+// WK warps share a tile's keys, 4 / WK groups of 16 rows share its rows. HALF:
+// chunks of 8 rows (the lower half of each 16-row product is not used).
+template <int D, int WK, bool HALF>
 struct AttnShape {
   static constexpr int kWM = 4 / WK;
-  static constexpr int kRows = 16 * kWM;
-  static constexpr int kKeys = kTileKeys / WK;             // keys of one warp
-  static constexpr int kHalf = kTileKeys * D * 2;          // K or V bytes of a stage
+  static constexpr int kRows = HALF ? 8 : 16 * kWM;
+  static constexpr int kKeys = kTileKeys / WK;  // keys of one warp
+  static constexpr int kHalf = kTileKeys * D * 2;  // K or V bytes of a stage
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kMerge = WK > 1 ? 4 * 16 * D * 4 : 0;  // the warps' sums, joined at the end of a piece
-  static constexpr int kFixed = 1024 + 2048;               // alignment, barriers and tables
+  // sums of the warps that join another at the end of a piece, 8 rows at a time
+  static constexpr int kMerge = (WK - 1) * kWM * 8 * D * 4;
+  static constexpr int kFixed = 1024 + 2048;  // alignment, barriers and tables
   static constexpr int kStages = std::min(12, (kAttnSmem - kFixed - kMerge) / kStage);
   static constexpr int kTotal = kStages * kStage + kMerge + kFixed;
   static_assert(kStages >= 3 && kTotal <= kAttnSmem, "shared memory");
+  static_assert(!HALF || WK == 4, "a chunk of 8 rows has one group of warps");
 };
 
 struct AttnShared {
   uint64_t full[12], empty[12];
   PartTable parts;
-  float2 ml[4][16];
+  float2 ml[4][8];
   uint8_t valid[12];  // per stage: which 16-key quarters lie in blocks of the cache
   int abort;
 };
@@ -66,20 +73,19 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // sub-tile of 128-byte rows with the 128-byte swizzle.
 __device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-template <int D, int WK>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+template <int D, int WK, bool HALF>
+__global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
     attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-                     const AttentionLaunch L) {
-  using S = AttnShape<D, WK>;
+                     const __grid_constant__ AttentionLaunch L) {
+  using S = AttnShape<D, WK, HALF>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* s_merge = reinterpret_cast<float*>(smem + S::kStages * S::kStage);  // [4][16][D], column ^ 8 (row % 8)
+  float2* s_merge = reinterpret_cast<float2*>(smem + S::kStages * S::kStage);  // [warp][D / 8][lane]
   AttnShared& sh = *reinterpret_cast<AttnShared*>(smem + S::kStages * S::kStage + S::kMerge);
   const AttentionParams& a = L.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = a.q_heads / a.kv_heads;
 
-  pdl_trigger();
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&sh.full[i], 1);
@@ -91,30 +97,31 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tmap_prefetch(&tv);
   }
   pdl_wait();
+  // Dependents start only now, when every earlier launch of the stream is
+  // complete: the joining kernel reads the lengths before its own wait.
+  pdl_trigger();
   if (warp == 0) build_parts(sh.parts, a, L.plan);
   __syncthreads();
   const long long W = sh.parts.first[a.requests + 1], G = plan_ctas(W, L.plan.ctas), c = blockIdx.x;
   const long long u0 = c < G ? unit_start(c, W, G) : 0, u1 = c < G ? unit_start(c + 1, W, G) : 0;
   const WaitCtl wc{&sh.abort, L.err, L.wait_ns};
+  Piece q;
+  if (u0 < u1) q.begin(sh.parts, a, L.plan, u0, u1);
 
   if (warp == 4) {
     // ------------------------------------------------------------ copies
     const int box = min(1 << a.shift, kTileKeys);  // keys of one box
     const int per = kTileKeys / box;               // boxes (blocks) of a tile
     constexpr int kSub = D / 64;
-    long long issued = 0;
-    int part = 0;
-    bool ok = true;
-    for (long long u = u0; ok && u < u1;) {
-      const Piece q = piece_at(sh.parts, a, L.plan, u, u1, part);
-      u += q.tile1 - q.tile0;
-      const int len = sh.parts.len[part];
-      const int32_t* table = part == 0 ? a.prefix_table : a.block_table + (long long)(part - 1) * a.max_blocks;
+    uint32_t issued = 0;
+    int s = 0;
+    uint32_t phase = 1;
+    for (long long u = u0; u < u1;) {
+      const int len = sh.parts.len[q.part];
+      const int32_t* table = q.part == 0 ? a.prefix_table : a.block_table + (long long)(q.part - 1) * a.max_blocks;
       BlockIds ids(table, (int)(((long long)len + (1 << a.shift) - 1) >> a.shift));
-      for (int t = q.tile0; t < q.tile1; ++t, ++issued) {
-        const int s = (int)(issued % S::kStages);
-        ok = __all_sync(0xffffffffu, mbar_wait(&sh.empty[s], (uint32_t)((issued / S::kStages) & 1) ^ 1u, wc));
-        if (!ok) break;
+      bool ok = true;
+      for (int t = q.tile0; t < q.tile1; ++t) {
         const int key0 = t * kTileKeys;
         const int boxes = min(per, (len - key0 + box - 1) / box);  // boxes with keys of the part
         ids.advance(key0 >> a.shift);
@@ -125,6 +132,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const bool load = b < boxes;
         const bool there = load && id >= 0 && id < a.blocks;
         const uint32_t mask = __ballot_sync(0xffffffffu, there && lane % (2 * kSub) == 0);
+        ok = warp_wait(&sh.empty[s], phase, wc);
+        if (!ok) break;
         if (lane == 0) {
           int quarters = 0;  // 16-key quarters in blocks of the cache
           for (int i = 0; i < 4; ++i) quarters |= ((mask >> ((i * 16 / box) * 2 * kSub)) & 1) << i;
@@ -135,54 +144,63 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (load) {
           uint8_t* dst = smem + s * S::kStage + (lane & 1) * S::kHalf + half * (kTileKeys * 128) + b * box * 128;
           // a block that is not there reads zeros from past the end of the cache
-          tma_load_3d(dst, (lane & 1) ? &tv : &tk, &sh.full[s], half * 64, (q.kvh << a.shift) + (key & ((1 << a.shift) - 1)),
-                      there ? id : a.blocks);
+          tma_load_3d(dst, (lane & 1) ? &tv : &tk, &sh.full[s], half * 64,
+                      (q.kvh << a.shift) + (key & ((1 << a.shift) - 1)), there ? id : a.blocks);
         }
+        ++issued;
+        if (++s == S::kStages) s = 0, phase ^= 1u;
       }
+      if (!ok) break;
+      u += q.tile1 - q.tile0;
+      if (u < u1) q.next(sh.parts, a, L.plan, u, u1);
     }
     // No copy may be in flight when the CTA exits.
     if (lane == 0)
-      for (long long i = max(0LL, issued - S::kStages); i < issued; ++i)
-        mbar_wait_drain(&sh.full[i % S::kStages], (uint32_t)((i / S::kStages) & 1), L.err, L.wait_ns);
+      for (uint32_t i = issued > (uint32_t)S::kStages ? issued - S::kStages : 0; i < issued; ++i)
+        mbar_wait_drain(&sh.full[i % S::kStages], (i / S::kStages) & 1, L.err, L.wait_ns);
   } else {
     // ------------------------------------------------------------ products
     const int wk = warp % WK, wm = warp / WK;  // which keys of a tile, which 16 rows of a chunk
     const int g = lane >> 2, t4 = lane & 3;
     constexpr int NK = S::kKeys / 8;           // 8-key columns of S
-    long long seen = 0;
-    int part = 0;
-    for (long long u = u0; u < u1;) {
-      const Piece q = piece_at(sh.parts, a, L.plan, u, u1, part);
-      u += q.tile1 - q.tile0;
-      const int len = sh.parts.len[part], rows = sh.parts.rows[part] * group;
-      const int r0 = q.chunk * S::kRows + wm * 16;
-      // this thread's two rows: g and g + 8 of the warp's 16
-      uint32_t qf[D / 16][4];
-      int sees[2];
+    constexpr int NE = HALF ? 1 : 2;           // this thread's rows: g and g + 8 of the warp's 16
+    int s = 0;
+    uint32_t phase = 0;
+    uint32_t qf[D / 16][4];
+    int sees[NE];
+    // the query fragments of a piece, and the keys that this thread's rows see
+    auto load_q = [&]() {
+      const int len = sh.parts.len[q.part], rows = sh.parts.rows[q.part] * group;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = r0 + g + 8 * e;
-        const bool in = r < rows;
-        const int row = in ? r / group : 0;
-        sees[e] = in ? min(len, part == 0 ? len : sh.parts.last[part] + row) : 0;
-        const uint16_t* src = a.q + (long long)(sh.parts.row0[part] + row) * a.ldq +
-                              (long long)(q.kvh * group + (in ? r % group : 0)) * D + 2 * t4;
+        const int r = q.chunk * S::kRows + wm * 16 + g + 8 * e;
+        const bool in = e < NE && r < rows;
+        const int row = in ? div_group(r, L.group_mul) : 0;
+        if (e < NE) sees[e] = in ? min(len, q.part == 0 ? len : sh.parts.last[q.part] + row) : 0;
+        const uint16_t* src = a.q + (long long)(sh.parts.row0[q.part] + row) * a.ldq +
+                              (long long)(q.kvh * group + (in ? r - row * group : 0)) * D + 2 * t4;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           qf[i][e] = in ? (uint32_t)ld_act_s32(src + i * 16) : 0u;
           qf[i][e + 2] = in ? (uint32_t)ld_act_s32(src + i * 16 + 8) : 0u;
         }
       }
-      float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    };
+    if (u0 < u1) load_q();
+    for (long long u = u0; u < u1;) {
+      const int len = sh.parts.len[q.part], rows = sh.parts.rows[q.part] * group;
+      float o[D / 8][4], m[NE], l[NE];
+#pragma unroll
+      for (int e = 0; e < NE; ++e) m[e] = -INFINITY, l[e] = 0.f;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
       // the fewest keys that any row of the chunk sees
-      const int fewest = part == 0 ? len : min(len, sh.parts.last[part] + (q.chunk * S::kRows) / group);
+      const int fewest =
+          q.part == 0 ? len : min(len, sh.parts.last[q.part] + div_group(q.chunk * S::kRows, L.group_mul));
 
       bool ok = true;
-      for (int t = q.tile0; t < q.tile1; ++t, ++seen) {
-        const int s = (int)(seen % S::kStages);
-        ok = __all_sync(0xffffffffu, mbar_wait(&sh.full[s], (uint32_t)((seen / S::kStages) & 1), wc));
+      for (int t = q.tile0; t < q.tile1; ++t) {
+        ok = warp_wait(&sh.full[s], phase, wc);
         if (!ok) break;
         const uint32_t kb = smem_u32(smem + s * S::kStage), vb = kb + S::kHalf;
         const int valid = sh.valid[s];
@@ -191,33 +209,53 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         float p[NK][4];
 #pragma unroll
         for (int j = 0; j < NK; ++j) p[j][0] = p[j][1] = p[j][2] = p[j][3] = 0.f;
+        if (NK == 2) {
+          // few independent sums: even and odd steps apart, half the chain
+          float p2[NK][4];
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
+          for (int j = 0; j < NK; ++j) p2[j][0] = p2[j][1] = p2[j][2] = p2[j][3] = 0.f;
 #pragma unroll
-          for (int j = 0; j < NK / 2; ++j) {
-            // matrices: keys 0-7 and 8-15 by elements 0-7 and 8-15 of step i
+          for (int i = 0; i < D / 16; ++i) {
             uint32_t b[4];
-            const int kr = wk * S::kKeys + j * 16 + ((lane >> 4) << 3) + (lane & 7);
+            const int kr = wk * S::kKeys + ((lane >> 4) << 3) + (lane & 7);
             const int cv = i * 2 + ((lane >> 3) & 1);
             ldsm4(b, kb + (cv >> 3) * (kTileKeys * 128) + swz(kr, cv & 7));
-            mma16816(p[2 * j], qf[i], b[0], b[1]);
-            mma16816(p[2 * j + 1], qf[i], b[2], b[3]);
+            mma16816(i & 1 ? p2[0] : p[0], qf[i], b[0], b[1]);
+            mma16816(i & 1 ? p2[NK - 1] : p[NK - 1], qf[i], b[2], b[3]);
           }
+#pragma unroll
+          for (int j = 0; j < NK; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[j][e] += p2[j][e];
+        } else {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int j = 0; j < NK / 2; ++j) {
+              // matrices: keys 0-7 and 8-15 by elements 0-7 and 8-15 of step i
+              uint32_t b[4];
+              const int kr = wk * S::kKeys + j * 16 + ((lane >> 4) << 3) + (lane & 7);
+              const int cv = i * 2 + ((lane >> 3) & 1);
+              ldsm4(b, kb + (cv >> 3) * (kTileKeys * 128) + swz(kr, cv & 7));
+              mma16816(p[2 * j], qf[i], b[0], b[1]);
+              mma16816(p[2 * j + 1], qf[i], b[2], b[3]);
+            }
+        }
         if (edge) {
 #pragma unroll
           for (int j = 0; j < NK; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 2 * NE; ++e) {
               const int kk = wk * S::kKeys + j * 8 + 2 * t4 + (e & 1);  // key within the tile
               const bool see = t * kTileKeys + kk < sees[e >> 1] && ((valid >> (kk >> 4)) & 1);
               p[j][e] = see ? p[j][e] : -INFINITY;
             }
         }
         // running maximum (log2 units), shared by the four threads of a row
-        float ref[2], up[2];
+        float ref[NE], up[NE];
         bool grew = false;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < NE; ++e) {
           float x = -INFINITY;
 #pragma unroll
           for (int j = 0; j < NK; ++j) x = fmaxf(x, fmaxf(p[j][2 * e], p[j][2 * e + 1]));
@@ -231,27 +269,30 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) l[e] *= up[e];
+          for (int e = 0; e < NE; ++e) {
+            l[e] *= up[e];
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            o[i][0] *= up[0];
-            o[i][1] *= up[0];
-            o[i][2] *= up[1];
-            o[i][3] *= up[1];
+            for (int i = 0; i < D / 8; ++i) {
+              o[i][2 * e] *= up[e];
+              o[i][2 * e + 1] *= up[e];
+            }
           }
         }
         uint32_t pf[NK / 2][4];
 #pragma unroll
-        for (int j = 0; j < NK; ++j) {
-          float w[4];
+        for (int j = 0; j < NK; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = ex2(fmaf(p[j][e], L.scale_log2, -ref[e >> 1]));
-          l[0] += w[0] + w[1];
-          l[1] += w[2] + w[3];
-          // P is rounded to bf16 for the product with V (fp32 sums; l keeps the unrounded weights)
-          pf[j >> 1][(j & 1) * 2] = pack_bf16x2(w[0], w[1]);
-          pf[j >> 1][(j & 1) * 2 + 1] = pack_bf16x2(w[2], w[3]);
-        }
+          for (int e = 0; e < 2; ++e) {
+            if (e >= NE) {
+              pf[j >> 1][(j & 1) * 2 + e] = 0u;
+              continue;
+            }
+            const float w0 = ex2(fmaf(p[j][2 * e], L.scale_log2, -ref[e % NE]));
+            const float w1 = ex2(fmaf(p[j][2 * e + 1], L.scale_log2, -ref[e % NE]));
+            l[e % NE] += w0 + w1;
+            // P is rounded to bf16 for the product with V (fp32 sums; l keeps the unrounded weights)
+            pf[j >> 1][(j & 1) * 2 + e] = pack_bf16x2(w0, w1);
+          }
 #pragma unroll
         for (int j = 0; j < NK / 2; ++j) {
           // Keys behind the part's last one hold anything (NaN too): their V is
@@ -281,91 +322,82 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.empty[s]);
+        if (++s == S::kStages) s = 0, phase ^= 1u;
       }
-      // the warps that join their sums leave together; this barrier also ends the
-      // reads of the previous piece's sums
-      if (WK > 1 ? !named_bar_and(1, 128, ok) : !ok) break;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-      }
+      // The warps that join their sums leave together if a wait gave up; this
+      // barrier also ends the reads of the previous piece's sums.
+      if (WK > 1 ? !named_bar_and(1 + wm, WK * 32, ok) : !ok) break;
 
       // ---------------------------------------------------------- the piece's rows
-      const bool whole = q.tile0 == 0 && q.tile1 == q.tiles;
-      const bool direct = whole && part > 0 && a.prefix_len == 0;
-      const bool begins = q.tile0 == 0;
-      const int in_chunk = min(S::kRows, rows - q.chunk * S::kRows);
-      // where row r of the chunk goes: 8 or 4 consecutive elements at column col
-      auto out_row = [&](int r) {
-        const int rr = q.chunk * S::kRows + r;
-        return (long long)(sh.parts.row0[part] + rr / group) * a.ldo + (long long)(q.kvh * group + rr % group) * D;
-      };
-      auto keep_at = [&](int r) {
-        const int rr = q.chunk * S::kRows + r;
-        return begins ? (long long)(sh.parts.row0[part] + rr / group) * a.q_heads + q.kvh * group + rr % group
-                      : c * S::kRows + r;
-      };
-      const Pieces& keep = begins ? L.start[part > 0] : L.plan.rest;
-      if (WK == 1) {
+      const Piece done = q;
+      u += q.tile1 - q.tile0;
+      if (u < u1) {  // the next piece's queries are on their way during what follows
+        q.next(sh.parts, a, L.plan, u, u1);
+        load_q();
+      }
+      const bool begins = done.tile0 == 0;
+      const bool direct = begins && done.tile1 == done.tiles && a.prefix_len == 0;
+      const int in_chunk = min(S::kRows, rows - done.chunk * S::kRows);
+      const Pieces& keep = begins ? L.start[done.part > 0] : L.plan.rest;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = wm * 16 + g + 8 * e;
-          if (r >= in_chunk) continue;
-          if (direct) {
-            const float inv = l[e] == 0.f ? 0.f : 1.f / l[e];
-            uint16_t* to = a.out + out_row(r) + 2 * t4;
+      for (int e = 0; e < NE; ++e) {
+        if (wm * 16 + 8 * e >= in_chunk) break;
+        const int r = wm * 16 + 8 * e + g;
+        float mt = m[e], lt = l[e];
+        lt += __shfl_xor_sync(0xffffffffu, lt, 1);
+        lt += __shfl_xor_sync(0xffffffffu, lt, 2);
+        if (WK > 1) {
+          // warps 1.. of the group hand their sums to warp 0, fragment by fragment
+          float2* mine = s_merge + (wm * (WK - 1) + wk - 1) * (D / 8) * 32 + lane;
+          if (e > 0) named_bar_sync(1 + wm, WK * 32);  // the first half has been read
+          if (wk > 0) {
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-              *reinterpret_cast<uint32_t*>(to + 8 * i) = pack_bf16x2(o[i][2 * e] * inv, o[i][2 * e + 1] * inv);
-          } else {
-            const long long at = keep_at(r);
-            float* to = keep.o + at * D + 2 * t4;
+            for (int i = 0; i < D / 8; ++i) mine[i * 32] = make_float2(o[i][2 * e], o[i][2 * e + 1]);
+            if (t4 == 0) sh.ml[warp][g] = make_float2(mt, lt);
+            named_bar_arrive(3 + wm, WK * 32);
+            continue;
+          }
+          named_bar_sync(3 + wm, WK * 32);
+          float f[WK], top = mt;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) *reinterpret_cast<float2*>(to + 8 * i) = make_float2(o[i][2 * e], o[i][2 * e + 1]);
-            if (t4 == 0) keep.ml[at] = make_float2(m[e], l[e]);
+          for (int w = 1; w < WK; ++w) top = fmaxf(top, sh.ml[warp + w][g].x);
+          f[0] = ex2_from(mt, top);
+          lt *= f[0];
+#pragma unroll
+          for (int w = 1; w < WK; ++w) {
+            const float2 ml = sh.ml[warp + w][g];
+            f[w] = ex2_from(ml.x, top);
+            lt = fmaf(ml.y, f[w], lt);
+          }
+          mt = top;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            o[i][2 * e] *= f[0];
+            o[i][2 * e + 1] *= f[0];
+#pragma unroll
+            for (int w = 1; w < WK; ++w) {
+              const float2 y = s_merge[((wm * (WK - 1) + w - 1) * (D / 8) + i) * 32 + lane];
+              o[i][2 * e] = fmaf(y.x, f[w], o[i][2 * e]);
+              o[i][2 * e + 1] = fmaf(y.y, f[w], o[i][2 * e + 1]);
+            }
           }
         }
-      } else {
-        // join the WK warps that hold the same rows
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = g + 8 * e;
-          if (wm * 16 + r >= in_chunk) continue;
-          float* to = s_merge + (warp * 16 + r) * D;
+        if (r >= in_chunk) continue;
+        const int rr = done.chunk * S::kRows + r, row = div_group(rr, L.group_mul);
+        const long long t = sh.parts.row0[done.part] + row;
+        const int head = done.kvh * group + rr - row * group;
+        if (direct) {
+          const float inv = lt == 0.f ? 0.f : 1.f / lt;
+          uint16_t* to = a.out + t * a.ldo + (long long)head * D + 2 * t4;
 #pragma unroll
           for (int i = 0; i < D / 8; ++i)
-            *reinterpret_cast<float2*>(to + ((8 * i + 2 * t4) ^ ((r & 7) << 3))) = make_float2(o[i][2 * e], o[i][2 * e + 1]);
-          if (t4 == 0) sh.ml[warp][r] = make_float2(m[e], l[e]);
-        }
-        named_bar_sync(1, 128);
-        for (int it = threadIdx.x; it < in_chunk * (D / 4); it += 128) {
-          const int r = it / (D / 4), col = (it % (D / 4)) * 4;
-          const int w0 = (r >> 4) * WK, rr = r & 15;
-          float top = -INFINITY, sum = 0.f;
+            *reinterpret_cast<uint32_t*>(to + 8 * i) = pack_bf16x2(o[i][2 * e] * inv, o[i][2 * e + 1] * inv);
+        } else {
+          const long long at = begins ? t * a.q_heads + head : c * S::kRows + r;
+          float* to = keep.o + at * D + 2 * t4;
 #pragma unroll
-          for (int w = 0; w < WK; ++w) top = fmaxf(top, sh.ml[w0 + w][rr].x);
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int w = 0; w < WK; ++w) {
-            const float2 ml = sh.ml[w0 + w][rr];
-            const float f = ex2_from(ml.x, top);
-            const float4 y = *reinterpret_cast<const float4*>(s_merge + ((w0 + w) * 16 + rr) * D + (col ^ ((rr & 7) << 3)));
-            sum = fmaf(ml.y, f, sum);
-            x.x = fmaf(y.x, f, x.x);
-            x.y = fmaf(y.y, f, x.y);
-            x.z = fmaf(y.z, f, x.z);
-            x.w = fmaf(y.w, f, x.w);
-          }
-          if (direct) {
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            *reinterpret_cast<uint2*>(a.out + out_row(r) + col) =
-                make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
-          } else {
-            const long long at = keep_at(r);
-            *reinterpret_cast<float4*>(keep.o + at * D + col) = x;
-            if (col == 0) keep.ml[at] = make_float2(top, sum);
-          }
+          for (int i = 0; i < D / 8; ++i) *reinterpret_cast<float2*>(to + 8 * i) = make_float2(o[i][2 * e], o[i][2 * e + 1]);
+          if (t4 == 0) keep.ml[at] = make_float2(mt, lt);
         }
       }
     }
@@ -373,69 +405,87 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 }
 
 // Joins the pieces of the rows that more than one CTA, or the prefix and the
-// own tokens, gave: out = sum O_i 2^(m_i - m) / sum l_i 2^(m_i - m). One CTA per
-// (row, head), the pieces spread over its 8 warps: what bounds it is the
-// latency of their reads from L2. A row with no piece at all gets zeros.
-template <int D>
-__global__ void __launch_bounds__(256) combine_attention_kernel(const AttentionLaunch P, const AttentionLaunch O) {
+// own tokens, gave: out = sum O_i 2^(m_i - m) / sum l_i 2^(m_i - m). A CTA
+// takes R rows (of M q_heads), 8 / R warps each, which share a row's pieces:
+// what bounds it is the latency of their reads from L2, so few rows take many
+// warps each. A row with no piece at all gets zeros. The pieces are summed in
+// a fixed order.
+template <int D, int R>
+__global__ void __launch_bounds__(256) join_attention_kernel(const __grid_constant__ AttentionLaunch P,
+                                                             const __grid_constant__ AttentionLaunch O) {
+  constexpr int NW = 8 / R, V = D / 32;
   __shared__ PartTable tp, to;
   __shared__ float s_o[8][D];
   __shared__ float2 s_ml[8];
   const AttentionParams& a = O.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = blockIdx.x, head = blockIdx.y;
-  const int group = a.q_heads / a.kv_heads, kvh = head / group;
-  pdl_trigger();
-  pdl_wait();
+  const int group = a.q_heads / a.kv_heads;
+  // The launch before this one starts its dependents after its own wait, so
+  // the lengths are final here; its pieces are not until pdl_wait().
   if (warp == 0) build_parts(to, O.a, O.plan);
   if (warp == 1) build_parts(tp, P.a, P.plan);
   __syncthreads();
+  pdl_trigger();
+  const int item = blockIdx.x * R + warp / NW, w = warp % NW;
+  const int t = item / a.q_heads, head = item - t * a.q_heads, kvh = div_group(head, O.group_mul);
   int part = 0;
-  for (int i = 1; i <= a.requests; ++i)
-    if (t >= to.row0[i] && t < to.row0[i] + to.rows[i]) part = i;
-  if (part == 0) return;  // a row of no request
-
+  if (t < a.M) {
+    // the request that has row t
+    const int n = a.requests;
+#pragma unroll
+    for (int k = 0; k < (kMaxParts + 31) / 32; ++k) {
+      const int i = 1 + k * 32 + lane;
+      const bool has = i <= n && t >= to.row0[i] && t < to.row0[i] + to.rows[i];
+      const uint32_t hit = __ballot_sync(0xffffffffu, has);
+      if (hit) part = 1 + k * 32 + __ffs(hit) - 1;
+    }
+  }
   // pieces of one part: the starting one, then one for each further CTA
   struct Span {
-    long long at;        // row of `start`
-    int c0, count, r;    // first CTA, pieces, row within the chunk
+    long long at;      // row of `start`
+    int c0, count, r;  // first CTA, pieces, row within the chunk
   };
   auto span_of = [&](const PartTable& T, const AttentionLaunch& L, int i) {
     Span s{(long long)t * a.q_heads + head, 0, 0, 0};
-    const long long W = T.first[a.requests + 1];
+    const long long W = T.first[a.requests + 1], G = plan_ctas(W, L.plan.ctas);
     const long long tiles = ((long long)T.len[i] + kTileKeys - 1) / kTileKeys;
     if (T.first[i + 1] == T.first[i]) return s;
-    const long long G = plan_ctas(W, L.plan.ctas);
     const int chunks = (T.rows[i] * group + L.plan.rows - 1) / L.plan.rows;
-    const int rr = (t - T.row0[i]) * group + head % group;
-    const long long u = T.first[i] + ((long long)kvh * chunks + rr / L.plan.rows) * tiles;
-    s.r = rr % L.plan.rows;
+    const int rr = (t - T.row0[i]) * group + head - kvh * group;
+    const int chunk = rr / L.plan.rows;
+    const long long u = T.first[i] + ((long long)kvh * chunks + chunk) * tiles;
+    s.r = rr - chunk * L.plan.rows;
     s.c0 = (int)cta_of_unit(u, W, G);
     s.count = (int)cta_of_unit(u + tiles - 1, W, G) - s.c0 + 1;
     return s;
   };
-  const Span sp = span_of(tp, P, 0), so = span_of(to, O, part);
-  if (sp.count == 0 && so.count == 1) return;  // written by the one CTA that had it
-  const int n = sp.count + so.count;
-  constexpr int V = D / 32;
+  Span sp{0, 0, 0, 0}, so{0, 0, 0, 0};
+  int n = -1;  // pieces; -1: nothing to write
+  if (part > 0) {
+    if (a.prefix_len > 0) sp = span_of(tp, P, 0);
+    so = span_of(to, O, part);
+    // a row that one CTA had whole has been written by it
+    if (sp.count > 0 || so.count != 1) n = sp.count + so.count;
+  }
+  pdl_wait();
   float x[V], m = -INFINITY, l = 0.f;
 #pragma unroll
   for (int e = 0; e < V; ++e) x[e] = 0.f;
-  constexpr int B = 4;  // pieces in flight per warp
-  for (int i0 = warp; i0 < n; i0 += 8 * B) {
+  constexpr int B = 8;  // pieces in flight per warp
+  for (int i0 = w; i0 < n; i0 += NW * B) {
     float y[B][V];
     float2 ml[B];
 #pragma unroll
     for (int k = 0; k < B; ++k) {
-      const int i = i0 + 8 * k;
+      const int i = i0 + NW * k;
       ml[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
       for (int e = 0; e < V; ++e) y[k][e] = 0.f;
       if (i < n) {
         const bool pre = i < sp.count;
         const int j = pre ? i : i - sp.count;
-        const Pieces& from = j == 0 ? O.start[pre ? 0 : 1] : (pre ? P.plan.rest : O.plan.rest);
         const Span& s = pre ? sp : so;
+        const Pieces& from = j == 0 ? O.start[pre ? 0 : 1] : (pre ? P.plan.rest : O.plan.rest);
         const long long at = j == 0 ? s.at : (long long)(s.c0 + j) * (pre ? P.plan.rows : O.plan.rows) + s.r;
         const uint2 raw = ld_act8(from.ml + at);
         ml[k] = make_float2(__uint_as_float(raw.x), __uint_as_float(raw.y));
@@ -458,32 +508,36 @@ __global__ void __launch_bounds__(256) combine_attention_kernel(const AttentionL
       for (int e = 0; e < V; ++e) x[e] = x[e] * f0 + y[k][e] * f1;
     }
   }
+  if (NW > 1) {
 #pragma unroll
-  for (int e = 0; e < V; ++e) s_o[warp][lane * V + e] = x[e];
-  if (lane == 0) s_ml[warp] = make_float2(m, l);
-  __syncthreads();
-  if (threadIdx.x < D / 2) {
-    float top = -INFINITY, sum = 0.f, v0 = 0.f, v1 = 0.f;
+    for (int e = 0; e < V; ++e) s_o[warp][lane * V + e] = x[e];
+    if (lane == 0) s_ml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (w == 0) {
 #pragma unroll
-    for (int w = 0; w < 8; ++w) top = fmaxf(top, s_ml[w].x);
+      for (int v = 1; v < NW; ++v) {
+        const float2 ml = s_ml[warp + v];
+        const float top = fmaxf(m, ml.x);
+        const float f0 = ex2_from(m, top), f1 = ex2_from(ml.x, top);
+        m = top;
+        l = l * f0 + ml.y * f1;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      const float f = ex2_from(s_ml[w].x, top);
-      sum = fmaf(s_ml[w].y, f, sum);
-      v0 = fmaf(s_o[w][2 * threadIdx.x], f, v0);
-      v1 = fmaf(s_o[w][2 * threadIdx.x + 1], f, v1);
+        for (int e = 0; e < V; ++e) x[e] = x[e] * f0 + s_o[warp + v][lane * V + e] * f1;
+      }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    *reinterpret_cast<uint32_t*>(a.out + (long long)t * a.ldo + (long long)head * D + 2 * threadIdx.x) =
-        pack_bf16x2(v0 * inv, v1 * inv);
   }
+  if (n < 0 || w > 0) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint32_t* out = reinterpret_cast<uint32_t*>(a.out + (long long)t * a.ldo + (long long)head * D + lane * V);
+#pragma unroll
+  for (int e = 0; e < V / 2; ++e) out[e] = pack_bf16x2(x[2 * e] * inv, x[2 * e + 1] * inv);
 }
 
 // ---------------------------------------------------------------------------- host side
 namespace {
 
 // Rows of the smallest chunk kernel that holds `rows` query rows.
-int chunk_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+int chunk_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 struct AttnWs {
   Pieces start[2], rest[2];
@@ -509,7 +563,7 @@ AttnWs carve(const dec_handle* h, void* base, int M, int q_heads, int dim, int p
   };
   for (int i = prefix_len > 0 ? 0 : 1; i < 2; ++i) {
     w.start[i] = pieces((size_t)M * q_heads);
-    w.rest[i] = pieces((size_t)h->sms * 64);
+    w.rest[i] = pieces((size_t)h->sms * kAttnCtasPerSm * 64);
   }
   w.bytes = used;
   return w;
@@ -526,29 +580,41 @@ bool encode_cache(const dec_handle* h, CUtensorMap* m, const uint16_t* base, con
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int WK>
+template <int D, int WK, bool HALF>
 cudaError_t launch_shape(dec_handle* h, const CUtensorMap& tk, const CUtensorMap& tv, const AttentionLaunch& L,
                          cudaStream_t s) {
-  using S = AttnShape<D, WK>;
+  using S = AttnShape<D, WK, HALF>;
   static std::atomic<uint64_t> ready{0};  // devices whose function attribute is set
   const uint64_t bit = 1ull << (h->device & 63);
   if (!(ready.load() & bit)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(attention_kernel<D, WK>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kTotal);
+        cudaFuncSetAttribute(attention_kernel<D, WK, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kTotal);
     if (e != cudaSuccess) return e;
     if (h->device < 64) ready.fetch_or(bit);
   }
-  return launch_k(h, attention_kernel<D, WK>, dim3(L.plan.ctas), dim3(kAttnThreads), (size_t)S::kTotal, s, tk, tv, L);
+  return launch_k(h, attention_kernel<D, WK, HALF>, dim3(L.plan.ctas), dim3(kAttnThreads), (size_t)S::kTotal, s, tk, tv, L);
 }
 
 cudaError_t launch_chunks(dec_handle* h, const CUtensorMap& tk, const CUtensorMap& tv, const AttentionLaunch& L,
                           cudaStream_t s) {
   const bool d64 = L.a.dim == 64;
   switch (L.plan.rows) {
-    case 16: return d64 ? launch_shape<64, 4>(h, tk, tv, L, s) : launch_shape<128, 4>(h, tk, tv, L, s);
-    case 32: return d64 ? launch_shape<64, 2>(h, tk, tv, L, s) : launch_shape<128, 2>(h, tk, tv, L, s);
-    default: return d64 ? launch_shape<64, 1>(h, tk, tv, L, s) : launch_shape<128, 1>(h, tk, tv, L, s);
+    case 8: return d64 ? launch_shape<64, 4, true>(h, tk, tv, L, s) : launch_shape<128, 4, true>(h, tk, tv, L, s);
+    case 16: return d64 ? launch_shape<64, 4, false>(h, tk, tv, L, s) : launch_shape<128, 4, false>(h, tk, tv, L, s);
+    case 32: return d64 ? launch_shape<64, 2, false>(h, tk, tv, L, s) : launch_shape<128, 2, false>(h, tk, tv, L, s);
+    default: return d64 ? launch_shape<64, 1, false>(h, tk, tv, L, s) : launch_shape<128, 1, false>(h, tk, tv, L, s);
   }
+}
+
+// Rows of a joining CTA: 8 (a warp each) from 2432 rows on, where one wave of
+// CTAs holds them all, fewer rows and more warps to each below.
+template <int D>
+cudaError_t launch_join(dec_handle* h, const AttentionLaunch& pre, const AttentionLaunch& own, cudaStream_t s) {
+  const int rows = own.a.M * own.a.q_heads, wave = 4 * h->sms;
+  if (rows <= wave) return launch_k(h, join_attention_kernel<D, 1>, dim3(rows), dim3(256), 0, s, pre, own);
+  if (rows <= 2 * wave) return launch_k(h, join_attention_kernel<D, 2>, dim3((rows + 1) / 2), dim3(256), 0, s, pre, own);
+  if (rows <= 4 * wave) return launch_k(h, join_attention_kernel<D, 4>, dim3((rows + 3) / 4), dim3(256), 0, s, pre, own);
+  return launch_k(h, join_attention_kernel<D, 8>, dim3((rows + 7) / 8), dim3(256), 0, s, pre, own);
 }
 
 }  // namespace
@@ -567,11 +633,12 @@ cudaError_t launch_attention(dec_handle* h, const AttentionParams& P, void* ws, 
   own.start[0] = w.start[0];
   own.start[1] = w.start[1];
   own.scale_log2 = P.scale * 1.4426950408889634f;
+  own.group_mul = (uint32_t)(((1 << 20) + group - 1) / group);
   own.err = h->d_err;
   own.wait_ns = h->wait_ns;
-  own.plan = Plan{0, 1, chunk_rows(std::min(P.max_new, P.M) * group), h->sms, w.rest[1]};
+  own.plan = Plan{0, 1, chunk_rows(std::min(P.max_new, P.M) * group), h->sms * kAttnCtasPerSm, w.rest[1]};
   AttentionLaunch pre = own;
-  pre.plan = Plan{P.prefix_len > 0 ? 1 : 0, 0, chunk_rows(P.M * group), h->sms, w.rest[0]};
+  pre.plan = Plan{P.prefix_len > 0 ? 1 : 0, 0, chunk_rows(P.M * group), h->sms * kAttnCtasPerSm, w.rest[0]};
   cudaError_t e = cudaSuccess;
   if (P.prefix_len > 0) {
     if (pre.plan.rows == own.plan.rows) {
@@ -590,9 +657,7 @@ cudaError_t launch_attention(dec_handle* h, const AttentionParams& P, void* ws, 
     if (e != cudaSuccess) return e;
   }
   LaunchScope scope(h, "attention_join", s);
-  const dim3 grid(P.M, P.q_heads);
-  if (P.dim == 64) return launch_k(h, combine_attention_kernel<64>, grid, dim3(256), 0, s, pre, own);
-  return launch_k(h, combine_attention_kernel<128>, grid, dim3(256), 0, s, pre, own);
+  return P.dim == 64 ? launch_join<64>(h, pre, own, s) : launch_join<128>(h, pre, own, s);
 }
 
 }  // namespace dec

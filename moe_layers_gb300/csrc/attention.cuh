@@ -44,6 +44,7 @@ struct AttentionLaunch {
   Plan plan;
   Pieces start[2];  // prefix, own: [M][q_heads]
   float scale_log2;
+  uint32_t group_mul;  // ceil(2^20 / group)
   int* err;
   unsigned long long wait_ns;
 };
@@ -61,28 +62,39 @@ __device__ __forceinline__ long long plan_ctas(long long W, int ctas) { return W
 __device__ __forceinline__ long long unit_start(long long c, long long W, long long G) { return c * W / G; }
 __device__ __forceinline__ long long cta_of_unit(long long u, long long W, long long G) { return ((u + 1) * G - 1) / W; }
 
+// r / group for 0 <= r < 64 group, group <= 128, by a product: mul = ceil(2^20 / group).
+__device__ __forceinline__ int div_group(int r, uint32_t mul) { return (int)(((uint32_t)r * mul) >> 20); }
+
 // Fills the table with one warp (all 32 lanes). Lengths are brought into
 // range: rows into [0, M] and not decreasing, keys to at most max_blocks blocks.
 __device__ __forceinline__ void build_parts(PartTable& t, const AttentionParams& a, const Plan& p) {
+  constexpr int kRounds = (kMaxParts + 31) / 32;
   const int lane = threadIdx.x & 31, n = a.requests + 1;
   const int group = a.q_heads / a.kv_heads;
+  int r0[kRounds], r1[kRounds], own[kRounds];
+#pragma unroll
+  for (int k = 0; k < kRounds; ++k) {  // every load before any use
+    const int i = k * 32 + lane;
+    r0[k] = r1[k] = own[k] = 0;
+    if (i < n) {
+      r0[k] = ld_act_s32(a.row_start + (i == 0 ? 0 : i - 1));
+      r1[k] = ld_act_s32(a.row_start + (i == 0 ? a.requests : i));
+      if (i > 0) own[k] = ld_act_s32(a.own_len + i - 1);
+    }
+  }
   long long carry = 0;
-  for (int base = 0; base < n; base += 32) {
-    const int i = base + lane;
+#pragma unroll
+  for (int k = 0; k < kRounds; ++k) {
+    const int i = k * 32 + lane;
     long long units = 0;
     if (i < n) {
-      const int b = i - 1;
-      const int lo = i == 0 ? 0 : b, hi = i == 0 ? a.requests : b + 1;
-      const int r0 = min(max(ld_act_s32(a.row_start + lo), 0), a.M);
-      const int r1 = min(max(ld_act_s32(a.row_start + hi), r0), a.M);
-      const int rows = r1 - r0;
+      const int first = min(max(r0[k], 0), a.M), rows = min(max(r1[k], first), a.M) - first;
       int len = a.prefix_len, last = a.prefix_len;
       if (i > 0) {
-        const int own = ld_act_s32(a.own_len + b);
-        len = max(0, (int)min((long long)own, (long long)a.max_blocks << a.shift));
-        last = (int)max((long long)own - rows + 1, -1000LL);
+        len = max(0, (int)min((long long)own[k], (long long)a.max_blocks << a.shift));
+        last = (int)max((long long)own[k] - rows + 1, -1000LL);
       }
-      t.row0[i] = (short)r0;
+      t.row0[i] = (short)first;
       t.rows[i] = (short)rows;
       t.len[i] = len;
       t.last[i] = last;
@@ -103,26 +115,40 @@ __device__ __forceinline__ void build_parts(PartTable& t, const AttentionParams&
   if (lane == 0) t.first[n] = carry;
 }
 
-// The piece that starts at unit u and ends before u_end at the latest.
+// Walks the pieces of units [u, u_end).
 struct Piece {
-  int part, kvh, chunk, tile0, tile1, tiles;
+  int part = 0, kvh = 0, chunk = 0, chunks = 1, tiles = 0, tile0 = 0, tile1 = 0;
+  __device__ __forceinline__ void enter(const PartTable& t, const AttentionParams& a, const Plan& p) {
+    chunks = (t.rows[part] * (a.q_heads / a.kv_heads) + p.rows - 1) / p.rows;
+    tiles = (int)(((long long)t.len[part] + kTileKeys - 1) / kTileKeys);
+  }
+  __device__ __forceinline__ void begin(const PartTable& t, const AttentionParams& a, const Plan& p, long long u,
+                                        long long u_end) {
+    while (t.first[part + 1] <= u) ++part;
+    enter(t, a, p);
+    const long long at = u - t.first[part];
+    const int hc = (at >> 32) == 0 ? (int)((uint32_t)at / (uint32_t)tiles) : (int)(at / tiles);
+    kvh = hc / chunks;
+    chunk = hc - kvh * chunks;
+    tile0 = (int)(at - (long long)hc * tiles);
+    tile1 = (int)min((long long)tiles, tile0 + (u_end - u));
+  }
+  // the next piece, which starts at unit u
+  __device__ __forceinline__ void next(const PartTable& t, const AttentionParams& a, const Plan& p, long long u,
+                                       long long u_end) {
+    if (++chunk == chunks) {
+      chunk = 0;
+      if (++kvh == a.kv_heads) {
+        kvh = 0;
+        do ++part;
+        while (t.first[part + 1] <= u);
+        enter(t, a, p);
+      }
+    }
+    tile0 = 0;
+    tile1 = (int)min((long long)tiles, u_end - u);
+  }
 };
-__device__ __forceinline__ Piece piece_at(const PartTable& t, const AttentionParams& a, const Plan& p, long long u,
-                                          long long u_end, int& part) {
-  while (t.first[part + 1] <= u) ++part;
-  const int chunks = (t.rows[part] * (a.q_heads / a.kv_heads) + p.rows - 1) / p.rows;
-  const int tiles = (int)(((long long)t.len[part] + kTileKeys - 1) / kTileKeys);
-  const long long at = u - t.first[part];
-  const int hc = (int)(at / tiles);
-  Piece q;
-  q.part = part;
-  q.kvh = hc / chunks;
-  q.chunk = hc % chunks;
-  q.tile0 = (int)(at - (long long)hc * tiles);
-  q.tile1 = (int)min((long long)tiles, q.tile0 + (u_end - u));
-  q.tiles = tiles;
-  return q;
-}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -137,6 +163,16 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// A warp's bounded wait: true in every lane, or false in every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& wc) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc));
+}
+
+__device__ __forceinline__ void named_bar_arrive(int id, int count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1, int c2) {
