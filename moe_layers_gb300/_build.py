@@ -19,7 +19,7 @@ LIB = os.path.join(HERE, "libmoedecode.so")
 ARCH = os.environ.get("MOE_DECODE_ARCH", "103a")
 
 SOURCES = ["api.cu", "gemv.cu", "umma.cu", "router.cu", "misc.cu", "noalloc.cu", "gemv_moe.cu", "route_shared.cu",
-           "batch.cu", "attention.cu", "api_attention.cu"]
+           "batch.cu", "attention.cu", "attention_tc.cu", "api_attention.cu"]
 HEADERS = ["common.cuh", "internal.h", "attention.cuh"]
 PUBLIC = os.path.join(ROOT, "include", "moe_decode.h")
 

@@ -17,12 +17,17 @@
 
 namespace dec {
 
-constexpr int kAttnThreads = 160;  // 4 multiplying warps, 1 copying warp
+constexpr int kTileKeys = 64;
+constexpr int kAttnThreads = 192;  // 4 multiplying warps, one copying K, one copying V
 // Two CTAs an SM: one warp per scheduler leaves the products' latency exposed
 // (870 cycles a tile against the 1370 that an SM's share of the memory rate
 // takes for one), and a CTA between two pieces does not stop the SM's stream.
 constexpr int kAttnCtasPerSm = 2;
 constexpr int kAttnSmem = 115712;
+// Tiles that beginning and ending a (head, chunk) costs as much as (61 ragged
+// requests of 1..4096 tokens: 75.5 us with 0, 57.0 with 1, 55.0 with 2, 55.9
+// with 3; without ragged lengths no difference).
+constexpr int kPieceLead = 2;
 
 // WK warps share a tile's keys, 4 / WK groups of 16 rows share its rows. HALF:
 // chunks of 8 rows (the lower half of each 16-row product is not used).
@@ -88,7 +93,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.full[i], 2);
       mbar_init(&sh.empty[i], 4);
     }
     sh.abort = 0;
@@ -108,15 +113,31 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
   Piece q;
   if (u0 < u1) q.begin(sh.parts, a, L.plan, u0, u1);
 
-  if (warp == 4) {
+  if (warp >= 4) {
     // ------------------------------------------------------------ copies
+    const bool keys = warp == 4;  // this warp copies K, the other V
     const int box = min(1 << a.shift, kTileKeys);  // keys of one box
     const int per = kTileKeys / box;               // boxes (blocks) of a tile
     constexpr int kSub = D / 64;
     uint32_t issued = 0;
     int s = 0;
     uint32_t phase = 1;
-    for (long long u = u0; u < u1;) {
+    for (long long u = u0; u < u1 && !q.empty();) {
+      {
+        // The queries of the next piece into L2 (this warp is a few tiles ahead of
+        // the products): read from DRAM under load they took 2.5 us of each piece.
+        Piece n = q;
+        if (keys && u + q.units < u1) {
+          n.next(sh.parts, a, L.plan, u + q.units, u1);
+          const int rows = n.empty() ? 0 : min(S::kRows, sh.parts.rows[n.part] * group - n.chunk * S::kRows);
+          for (int i = lane; i < rows * kSub; i += 32) {
+            const int rr = n.chunk * S::kRows + i / kSub, row = div_group(rr, L.group_mul);
+            const uint16_t* src = a.q + (long long)(sh.parts.row0[n.part] + row) * a.ldq +
+                                  (long long)(n.kvh * group + rr - row * group) * D + (i % kSub) * 64;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+          }
+        }
+      }
       const int len = sh.parts.len[q.part];
       const int32_t* table = q.part == 0 ? a.prefix_table : a.block_table + (long long)(q.part - 1) * a.max_blocks;
       BlockIds ids(table, (int)(((long long)len + (1 << a.shift) - 1) >> a.shift));
@@ -125,33 +146,33 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
         const int key0 = t * kTileKeys;
         const int boxes = min(per, (len - key0 + box - 1) / box);  // boxes with keys of the part
         ids.advance(key0 >> a.shift);
-        // lane: box (lane / (2 kSub)), 64-element half, k or v
-        const int b = lane / (2 * kSub), half = (lane >> 1) % kSub;
+        // lane: box (lane / kSub), 64-element half
+        const int b = lane / kSub, half = lane % kSub;
         const int key = key0 + b * box;
         const int id = ids.get(key >> a.shift);
         const bool load = b < boxes;
         const bool there = load && id >= 0 && id < a.blocks;
-        const uint32_t mask = __ballot_sync(0xffffffffu, there && lane % (2 * kSub) == 0);
+        const uint32_t mask = __ballot_sync(0xffffffffu, there);
         ok = warp_wait(&sh.empty[s], phase, wc);
         if (!ok) break;
         if (lane == 0) {
           int quarters = 0;  // 16-key quarters in blocks of the cache
-          for (int i = 0; i < 4; ++i) quarters |= ((mask >> ((i * 16 / box) * 2 * kSub)) & 1) << i;
-          sh.valid[s] = (uint8_t)quarters;
-          mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(boxes * box * D * 4));
+          for (int i = 0; i < 4; ++i) quarters |= ((mask >> ((i * 16 / box) * kSub)) & 1) << i;
+          if (keys) sh.valid[s] = (uint8_t)quarters;
+          mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(boxes * box * D * 2));
         }
         __syncwarp();
         if (load) {
-          uint8_t* dst = smem + s * S::kStage + (lane & 1) * S::kHalf + half * (kTileKeys * 128) + b * box * 128;
+          uint8_t* dst = smem + s * S::kStage + (keys ? 0 : S::kHalf) + half * (kTileKeys * 128) + b * box * 128;
           // a block that is not there reads zeros from past the end of the cache
-          tma_load_3d(dst, (lane & 1) ? &tv : &tk, &sh.full[s], half * 64,
+          tma_load_3d(dst, keys ? &tk : &tv, &sh.full[s], half * 64,
                       (q.kvh << a.shift) + (key & ((1 << a.shift) - 1)), there ? id : a.blocks);
         }
         ++issued;
         if (++s == S::kStages) s = 0, phase ^= 1u;
       }
       if (!ok) break;
-      u += q.tile1 - q.tile0;
+      u += q.units;
       if (u < u1) q.next(sh.parts, a, L.plan, u, u1);
     }
     // No copy may be in flight when the CTA exits.
@@ -187,7 +208,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
       }
     };
     if (u0 < u1) load_q();
-    for (long long u = u0; u < u1;) {
+    for (long long u = u0; u < u1 && !q.empty();) {
       const int len = sh.parts.len[q.part], rows = sh.parts.rows[q.part] * group;
       float o[D / 8][4], m[NE], l[NE];
 #pragma unroll
@@ -330,7 +351,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
 
       // ---------------------------------------------------------- the piece's rows
       const Piece done = q;
-      u += q.tile1 - q.tile0;
+      u += q.units;
       if (u < u1) {  // the next piece's queries are on their way during what follows
         q.next(sh.parts, a, L.plan, u, u1);
         load_q();
@@ -448,12 +469,12 @@ __global__ void __launch_bounds__(256) join_attention_kernel(const __grid_consta
   auto span_of = [&](const PartTable& T, const AttentionLaunch& L, int i) {
     Span s{(long long)t * a.q_heads + head, 0, 0, 0};
     const long long W = T.first[a.requests + 1], G = plan_ctas(W, L.plan.ctas);
-    const long long tiles = ((long long)T.len[i] + kTileKeys - 1) / kTileKeys;
+    const long long tiles = ((long long)T.len[i] + (1 << L.plan.tile_shift) - 1) >> L.plan.tile_shift;
     if (T.first[i + 1] == T.first[i]) return s;
     const int chunks = (T.rows[i] * group + L.plan.rows - 1) / L.plan.rows;
     const int rr = (t - T.row0[i]) * group + head - kvh * group;
     const int chunk = rr / L.plan.rows;
-    const long long u = T.first[i] + ((long long)kvh * chunks + chunk) * tiles;
+    const long long u = T.first[i] + ((long long)kvh * chunks + chunk) * (tiles + L.plan.lead) + L.plan.lead;
     s.r = rr - chunk * L.plan.rows;
     s.c0 = (int)cta_of_unit(u, W, G);
     s.count = (int)cta_of_unit(u + tiles - 1, W, G) - s.c0 + 1;
@@ -536,8 +557,17 @@ __global__ void __launch_bounds__(256) join_attention_kernel(const __grid_consta
 // ---------------------------------------------------------------------------- host side
 namespace {
 
-// Rows of the smallest chunk kernel that holds `rows` query rows.
-int chunk_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+// The chunk kernel for `rows` query rows of a key head: the smallest that holds
+// them. Above 64 rows (and from DEC_TC_ROWS on) the tcgen05 kernel.
+#ifndef DEC_TC_ROWS
+#define DEC_TC_ROWS 65
+#endif
+Plan chunk_plan(const dec_handle* h, int rows, bool prefix, bool own, const Pieces& rest) {
+  const int kPieceLeadTc = 3;
+  if (rows >= DEC_TC_ROWS) return Plan{prefix, own, rows <= 128 ? 128 : 256, kPieceLeadTc, 7, h->sms, rest};
+  return Plan{prefix, own, rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64, kPieceLead, 6,
+              h->sms * kAttnCtasPerSm, rest};
+}
 
 struct AttnWs {
   Pieces start[2], rest[2];
@@ -563,7 +593,7 @@ AttnWs carve(const dec_handle* h, void* base, int M, int q_heads, int dim, int p
   };
   for (int i = prefix_len > 0 ? 0 : 1; i < 2; ++i) {
     w.start[i] = pieces((size_t)M * q_heads);
-    w.rest[i] = pieces((size_t)h->sms * kAttnCtasPerSm * 64);
+    w.rest[i] = pieces((size_t)h->sms * std::max(kAttnCtasPerSm * 64, 256));
   }
   w.bytes = used;
   return w;
@@ -602,6 +632,8 @@ cudaError_t launch_chunks(dec_handle* h, const CUtensorMap& tk, const CUtensorMa
     case 8: return d64 ? launch_shape<64, 4, true>(h, tk, tv, L, s) : launch_shape<128, 4, true>(h, tk, tv, L, s);
     case 16: return d64 ? launch_shape<64, 4, false>(h, tk, tv, L, s) : launch_shape<128, 4, false>(h, tk, tv, L, s);
     case 32: return d64 ? launch_shape<64, 2, false>(h, tk, tv, L, s) : launch_shape<128, 2, false>(h, tk, tv, L, s);
+    case 128:
+    case 256: return launch_attention_tc(h, tk, tv, L, s);
     default: return d64 ? launch_shape<64, 1, false>(h, tk, tv, L, s) : launch_shape<128, 1, false>(h, tk, tv, L, s);
   }
 }
@@ -636,14 +668,14 @@ cudaError_t launch_attention(dec_handle* h, const AttentionParams& P, void* ws, 
   own.group_mul = (uint32_t)(((1 << 20) + group - 1) / group);
   own.err = h->d_err;
   own.wait_ns = h->wait_ns;
-  own.plan = Plan{0, 1, chunk_rows(std::min(P.max_new, P.M) * group), h->sms * kAttnCtasPerSm, w.rest[1]};
+  own.plan = chunk_plan(h, std::min(P.max_new, P.M) * group, false, true, w.rest[1]);
   AttentionLaunch pre = own;
-  pre.plan = Plan{P.prefix_len > 0 ? 1 : 0, 0, chunk_rows(P.M * group), h->sms * kAttnCtasPerSm, w.rest[0]};
+  pre.plan = chunk_plan(h, P.M * group, P.prefix_len > 0, false, w.rest[0]);
   cudaError_t e = cudaSuccess;
   if (P.prefix_len > 0) {
     if (pre.plan.rows == own.plan.rows) {
       // the same kernel: one launch takes both
-      own.plan.prefix = 1;
+      own.plan.prefix = true;
       pre.plan = own.plan;
     } else {
       LaunchScope scope(h, "attention_prefix", s);

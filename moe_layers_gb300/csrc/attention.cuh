@@ -5,11 +5,12 @@
 // A step has parts: part 0 is the shared prefix (its rows: every row of the
 // batch), part b + 1 the own tokens of request b. For one part and one key /
 // value head the query rows are (row of the part, head of the group), in
-// chunks of as many as the kernel holds, and the keys are in tiles of 64. A
-// unit is one tile for one chunk; the units of a part are ordered (head,
-// chunk, tile), the parts follow each other, and CTA c of G (at
-// most W) takes units [c W / G, (c + 1) W / G) of all W: every CTA streams the same number of
-// tiles, however ragged the lengths are. The tiles of one (head, chunk) that
+// chunks of as many as the kernel holds, and the keys are in tiles of 64 or 128. A
+// (head, chunk) is as many units as it has tiles, behind `lead` units that
+// stand for the cost of beginning and ending it; the units of a part are
+// ordered (head, chunk, tile), the parts follow each other, and CTA c of G (at
+// most W) takes units [c W / G, (c + 1) W / G) of all W: every CTA has the same
+// work, however ragged the lengths are. The tiles of one (head, chunk) that
 // one CTA takes are a piece. A piece that holds the first tile is kept by its
 // rows (`start`); any other is the first piece of its CTA and is kept by the
 // CTA (`rest`). The whole plan follows from the lengths in device memory, so
@@ -21,7 +22,6 @@
 
 namespace dec {
 
-constexpr int kTileKeys = 64;
 constexpr int kMaxParts = 65;
 
 // Unnormalised sums [rows][dim] with their (maximum, sum) pairs, maxima in
@@ -33,8 +33,10 @@ struct Pieces {
 
 // One launch's share of the plan.
 struct Plan {
-  int prefix, own;  // which parts the launch takes
+  bool prefix, own;  // which parts the launch takes
   int rows;         // query rows of a chunk
+  int lead;         // units a (head, chunk) counts for besides its tiles
+  int tile_shift;   // a tile is 1 << tile_shift keys
   int ctas;
   Pieces rest;      // [ctas][rows]
 };
@@ -85,6 +87,7 @@ __device__ __forceinline__ void build_parts(PartTable& t, const AttentionParams&
   long long carry = 0;
 #pragma unroll
   for (int k = 0; k < kRounds; ++k) {
+    if (k * 32 >= n) break;
     const int i = k * 32 + lane;
     long long units = 0;
     if (i < n) {
@@ -100,7 +103,8 @@ __device__ __forceinline__ void build_parts(PartTable& t, const AttentionParams&
       t.last[i] = last;
       if (i == 0 ? p.prefix : p.own) {
         const int chunks = (rows * group + p.rows - 1) / p.rows;
-        units = (long long)a.kv_heads * chunks * (((long long)len + kTileKeys - 1) / kTileKeys);
+        const long long tiles = ((long long)len + (1 << p.tile_shift) - 1) >> p.tile_shift;
+        units = tiles > 0 ? (long long)a.kv_heads * chunks * (tiles + p.lead) : 0;
       }
     }
     long long inc = units;
@@ -115,23 +119,30 @@ __device__ __forceinline__ void build_parts(PartTable& t, const AttentionParams&
   if (lane == 0) t.first[n] = carry;
 }
 
-// Walks the pieces of units [u, u_end).
+// Walks the pieces of units [u, u_end). A piece without tiles (its units are
+// leading ones) can only be the last.
 struct Piece {
-  int part = 0, kvh = 0, chunk = 0, chunks = 1, tiles = 0, tile0 = 0, tile1 = 0;
+  int part = 0, kvh = 0, chunk = 0, chunks = 1, tiles = 0, tile0 = 0, tile1 = 0, units = 0;
+  __device__ __forceinline__ bool empty() const { return tile1 <= tile0; }
   __device__ __forceinline__ void enter(const PartTable& t, const AttentionParams& a, const Plan& p) {
     chunks = (t.rows[part] * (a.q_heads / a.kv_heads) + p.rows - 1) / p.rows;
-    tiles = (int)(((long long)t.len[part] + kTileKeys - 1) / kTileKeys);
+    tiles = (int)(((long long)t.len[part] + (1 << p.tile_shift) - 1) >> p.tile_shift);
+  }
+  __device__ __forceinline__ void cut(const Plan& p, int x0, long long room) {
+    units = (int)min((long long)(tiles + p.lead - x0), room);
+    tile0 = max(0, x0 - p.lead);
+    tile1 = max(0, x0 + units - p.lead);
   }
   __device__ __forceinline__ void begin(const PartTable& t, const AttentionParams& a, const Plan& p, long long u,
                                         long long u_end) {
     while (t.first[part + 1] <= u) ++part;
     enter(t, a, p);
     const long long at = u - t.first[part];
-    const int hc = (at >> 32) == 0 ? (int)((uint32_t)at / (uint32_t)tiles) : (int)(at / tiles);
+    const int each = tiles + p.lead;
+    const int hc = (at >> 32) == 0 ? (int)((uint32_t)at / (uint32_t)each) : (int)(at / each);
     kvh = hc / chunks;
     chunk = hc - kvh * chunks;
-    tile0 = (int)(at - (long long)hc * tiles);
-    tile1 = (int)min((long long)tiles, tile0 + (u_end - u));
+    cut(p, (int)(at - (long long)hc * each), u_end - u);
   }
   // the next piece, which starts at unit u
   __device__ __forceinline__ void next(const PartTable& t, const AttentionParams& a, const Plan& p, long long u,
@@ -145,8 +156,7 @@ struct Piece {
         enter(t, a, p);
       }
     }
-    tile0 = 0;
-    tile1 = (int)min((long long)tiles, u_end - u);
+    cut(p, 0, u_end - u);
   }
 };
 
@@ -201,5 +211,9 @@ struct BlockIds {
   }
   __device__ __forceinline__ int get(int i) const { return __shfl_sync(0xffffffffu, cur, i & 31); }
 };
+
+// The tcgen05 kernel (attention_tc.cu), for chunks of 128 or 256 rows.
+cudaError_t launch_attention_tc(dec_handle* h, const CUtensorMap& tk, const CUtensorMap& tv, const AttentionLaunch& L,
+                                cudaStream_t s);
 
 }  // namespace dec

@@ -1,0 +1,468 @@
+// Attention for many query rows to a key head (a batch on a shared prefix, long
+// runs of new tokens): the products on tcgen05.
+//
+// 64 rows of 4 heads on one prefix are 256 flops to a byte of the cache, near
+// the ridge of the tensor cores (280), where mma.sync stops at a third of
+// their rate. A CTA holds 128 or 256 query rows and streams 128-key tiles;
+// each 128 rows are one stream of
+//   S = Q K^T (128 x 128, fp32 in TMEM)           tcgen05.mma, Q and K in shared memory
+//   P = 2^(S - m), bf16, over S in TMEM            a thread per row: no shuffles
+//   O += P V (128 x D, fp32 in TMEM)               tcgen05.mma, P from TMEM, V in shared memory
+// with its own issuing warp, so that one stream's products run under the other
+// one's exponentials. The running maximum is raised only when a row's scores
+// pass it by more than 2^8 (P <= 256 then, exact in fp32 sums), so O is read
+// and rescaled a few times, not every tile. K is a K-major operand as it lies
+// in the cache, V an MN-major one: both come by TMA with the 128-byte swizzle,
+// in separate rings that two warps fill.
+#include <atomic>
+
+#include "attention.cuh"
+
+namespace dec {
+
+namespace {
+
+constexpr int kTcTile = 128;
+constexpr int kTcThreads = 384;  // warps 0-7 softmax (4 a stream), 8 copies K, 9 copies V, 10-11 issue products
+constexpr int kTcSmem = 232448;
+constexpr float kRaise = 8.f;    // log2 of the growth of the scores that is left in P
+
+template <int D, int NT>
+struct TcShape {
+  static constexpr int kTileBytes = kTcTile * D * 2;       // K or V of a tile; also 128 query rows
+  static constexpr int kQ = NT * kTileBytes;
+  static constexpr int kFixed = 1024 + 2048;
+  static constexpr int kSlots = (kTcSmem - kFixed - kQ) / kTileBytes;
+  static constexpr int kK = kSlots >= 12 ? 6 : (kSlots + 1) / 2, kV = kSlots >= 12 ? 6 : kSlots / 2;
+  static constexpr int kTotal = (kK + kV) * kTileBytes + kQ + kFixed;
+  static_assert(kK >= 2 && kV >= 2 && kTotal <= kTcSmem, "shared memory");
+  // TMEM columns: S (P over it) and O of each stream
+  static constexpr uint32_t kS = 0, kO = NT * 128;
+  static constexpr uint32_t kCols = NT == 2 ? 512 : 256;
+};
+
+struct TcShared {
+  uint64_t kfull[6], kempty[6], vfull[6], vempty[6];
+  uint64_t sfull[2], pfull[2], pvdone[2], qfull, done[2];
+  PartTable parts;
+  uint8_t valid[8];  // per tile (modulo 8): which 16-key eighths lie in blocks of the cache
+  uint32_t tmem;
+  int abort;
+};
+static_assert(sizeof(TcShared) <= 2048, "attention tables");
+
+// Descriptor of an MN-major operand with the 128-byte swizzle: rows (one k
+// each) of 64 contiguous elements, 8-row groups 1024 bytes apart (SBO), the
+// next 64 elements lbo bytes on.
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t smem_addr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(lbo >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], issued by one thread.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+#define DEC_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), \
+                     "=r"(r[i + 6]), "=r"(r[i + 7])
+#define DEC_W8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), \
+                     "r"(r[i + 6]), "r"(r[i + 7])
+
+// 32 consecutive columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : DEC_R8(r, 0), DEC_R8(r, 8), DEC_R8(r, 16), DEC_R8(r, 24)
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::DEC_W8(r, 0),
+      DEC_W8(r, 8), DEC_W8(r, 16), DEC_W8(r, 24), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::DEC_W8(
+          r, 0),
+      DEC_W8(r, 8), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    attention_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                        const __grid_constant__ AttentionLaunch L) {
+  using S = TcShape<D, NT>;
+  constexpr int kRows = NT * 128, kSub = D / 64;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* s_q = smem;                                  // [NT][kSub][128 rows][128 bytes], swizzled
+  uint8_t* s_k = smem + S::kQ;                          // [kK][kSub][128 keys][128 bytes]
+  uint8_t* s_v = s_k + S::kK * S::kTileBytes;           // [kV][the same]
+  TcShared& sh = *reinterpret_cast<TcShared*>(s_v + S::kV * S::kTileBytes);
+  const AttentionParams& a = L.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = a.q_heads / a.kv_heads;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 6; ++i) {
+      mbar_init(&sh.kfull[i], 1);
+      mbar_init(&sh.vfull[i], 1);
+      mbar_init(&sh.kempty[i], NT);
+      mbar_init(&sh.vempty[i], NT);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.sfull[i], 1);
+      mbar_init(&sh.pfull[i], 128);
+      mbar_init(&sh.pvdone[i], 1);
+      mbar_init(&sh.done[i], 1);
+    }
+    mbar_init(&sh.qfull, kRows);
+    sh.abort = 0;
+    fence_mbar_init();
+    tmap_prefetch(&tk);
+    tmap_prefetch(&tv);
+  }
+  if (warp == 11) {
+    tmem_alloc(&sh.tmem, S::kCols);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_trigger();  // after the wait: see the joining kernel
+  if (warp == 0) build_parts(sh.parts, a, L.plan);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const long long W = sh.parts.first[a.requests + 1], G = plan_ctas(W, L.plan.ctas), c = blockIdx.x;
+  const long long u0 = c < G ? unit_start(c, W, G) : 0, u1 = c < G ? unit_start(c + 1, W, G) : 0;
+  const WaitCtl wc{&sh.abort, L.err, L.wait_ns};
+  Piece q;
+  if (u0 < u1) q.begin(sh.parts, a, L.plan, u0, u1);
+
+  if (warp == 8 || warp == 9) {
+    // ------------------------------------------------------------ copies
+    const bool keys = warp == 8;
+    uint64_t* full = keys ? sh.kfull : sh.vfull;
+    uint64_t* empty = keys ? sh.kempty : sh.vempty;
+    uint8_t* ring = keys ? s_k : s_v;
+    const int slots = keys ? S::kK : S::kV;
+    const int box = min(1 << a.shift, 64);  // keys of one box
+    const int per = kTcTile / box;
+    uint32_t issued = 0;
+    int s = 0;
+    uint32_t phase = 1;
+    for (long long u = u0; u < u1 && !q.empty();) {
+      const int len = sh.parts.len[q.part];
+      const int32_t* table = q.part == 0 ? a.prefix_table : a.block_table + (long long)(q.part - 1) * a.max_blocks;
+      BlockIds ids(table, (int)(((long long)len + (1 << a.shift) - 1) >> a.shift));
+      bool ok = true;
+      for (int t = q.tile0; t < q.tile1; ++t) {
+        const int key0 = t * kTcTile;
+        const int boxes = min(per, (len - key0 + box - 1) / box);
+        ids.advance(key0 >> a.shift);
+        const int b = lane / kSub, half = lane % kSub;
+        const int key = key0 + b * box;
+        const int id = ids.get(key >> a.shift);
+        const bool load = b < boxes;
+        const bool there = load && id >= 0 && id < a.blocks;
+        const uint32_t mask = __ballot_sync(0xffffffffu, there);
+        ok = warp_wait(&empty[s], phase, wc);
+        if (!ok) break;
+        if (lane == 0) {
+          if (keys) {
+            int eighths = 0;
+            for (int i = 0; i < 8; ++i) eighths |= ((mask >> ((i * 16 / box) * kSub)) & 1) << i;
+            sh.valid[issued & 7] = (uint8_t)eighths;
+          }
+          mbar_arrive_expect_tx(&full[s], (uint32_t)(boxes * box * D * 2));
+        }
+        __syncwarp();
+        if (load)
+          // a block that is not there reads zeros from past the end of the cache
+          tma_load_3d(ring + s * S::kTileBytes + half * (kTcTile * 128) + b * box * 128, keys ? &tk : &tv, &full[s],
+                      half * 64, (q.kvh << a.shift) + (key & ((1 << a.shift) - 1)), there ? id : a.blocks);
+        ++issued;
+        if (++s == slots) s = 0, phase ^= 1u;
+      }
+      if (!ok) break;
+      u += q.units;
+      if (u < u1) q.next(sh.parts, a, L.plan, u, u1);
+    }
+    if (lane == 0)
+      for (uint32_t i = issued > (uint32_t)slots ? issued - slots : 0; i < issued; ++i)
+        mbar_wait_drain(&full[i % slots], (i / slots) & 1, L.err, L.wait_ns);
+  } else if (warp >= 10) {
+    // ------------------------------------------------------------ products of stream j
+    const int j = warp - 10;
+    if (j < NT) {
+      int ks = 0, vs = 0;
+      uint32_t kph = 0, vph = 0, qph = 0, ph = 0;
+      constexpr uint32_t idesc_s = umma_idesc_bf16(128, kTcTile);
+      constexpr uint32_t idesc_o = umma_idesc_bf16(128, D) | (1u << 16);  // B is MN-major
+      const uint32_t qa = smem_u32(s_q + j * S::kTileBytes);
+      const uint32_t ts = tmem + S::kS + j * 128, to = tmem + S::kO + j * D;
+      bool ok = true;
+      for (long long u = u0; ok && u < u1 && !q.empty();) {
+        ok = warp_wait(&sh.qfull, qph, wc);  // the queries are there, and O has been read
+        qph ^= 1u;
+        for (int t = q.tile0; ok && t < q.tile1; ++t) {
+          ok = warp_wait(&sh.kfull[ks], kph, wc);
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t kb = smem_u32(s_k + ks * S::kTileBytes);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              const uint32_t off = (i >> 2) * (kTcTile * 128) + (i & 3) * 32;
+              umma_bf16(ts, sw128_desc(qa + off), sw128_desc(kb + off), idesc_s, i > 0);
+            }
+            umma_commit(&sh.sfull[j]);
+            umma_commit(&sh.kempty[ks]);
+          }
+          __syncwarp();
+          if (++ks == S::kK) ks = 0, kph ^= 1u;
+          ok = warp_wait(&sh.pfull[j], ph, wc) && warp_wait(&sh.vfull[vs], vph, wc);
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t vb = smem_u32(s_v + vs * S::kTileBytes);
+#pragma unroll
+            for (int i = 0; i < kTcTile / 16; ++i)
+              umma_bf16_ts(to, ts + i * 8, sw128_mn_desc(vb + i * 2048, kTcTile * 128), idesc_o,
+                           t > q.tile0 || i > 0);
+            umma_commit(&sh.pvdone[j]);
+            umma_commit(&sh.vempty[vs]);
+          }
+          __syncwarp();
+          if (++vs == S::kV) vs = 0, vph ^= 1u;
+          // S of the next tile goes where P is: only once P has been multiplied
+          ok = warp_wait(&sh.pvdone[j], ph, wc);
+          ph ^= 1u;
+        }
+        u += q.units;
+        if (u < u1) q.next(sh.parts, a, L.plan, u, u1);
+      }
+      // every product issued must be complete before TMEM is released
+      if (lane == 0) {
+        umma_commit(&sh.done[j]);
+        mbar_wait_drain(&sh.done[j], 0, L.err, L.wait_ns);
+      }
+    }
+  } else if (warp / 4 < NT) {
+    // ------------------------------------------------------------ softmax of stream j, one thread a row
+    const int j = warp >> 2, r = threadIdx.x;  // row of the chunk
+    const int rj = r & 127;
+    const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + S::kS + j * 128 + quarter, to = tmem + S::kO + j * D + quarter;
+    uint32_t ph = 0, tiles = 0;
+    int vs = 0;
+    uint32_t vph = 0;
+    int sees = 0;
+    auto load_q = [&]() {
+      const int rr = q.chunk * kRows + r;
+      const bool in = rr < sh.parts.rows[q.part] * group;
+      const int row = in ? div_group(rr, L.group_mul) : 0;
+      const int len = sh.parts.len[q.part];
+      sees = in ? min(len, q.part == 0 ? len : sh.parts.last[q.part] + row) : 0;
+      const uint16_t* src = a.q + (long long)(sh.parts.row0[q.part] + row) * a.ldq +
+                            (long long)(q.kvh * group + (in ? rr - row * group : 0)) * D;
+#pragma unroll
+      for (int h = 0; h < kSub; ++h) {
+        uint8_t* dst = s_q + j * S::kTileBytes + h * (128 * 128) + rj * 128;
+#pragma unroll
+        for (int v = 0; v < 8; ++v)
+          *reinterpret_cast<uint4*>(dst + ((v ^ (rj & 7)) << 4)) =
+              in ? ld_act16(src + h * 64 + v * 8) : make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_async_smem();
+      tc_fence_before();
+      mbar_arrive(&sh.qfull);
+    };
+    if (u0 < u1 && !q.empty()) load_q();
+    bool ok = true;
+    for (long long u = u0; ok && u < u1 && !q.empty();) {
+      const int len = sh.parts.len[q.part], rows = sh.parts.rows[q.part] * group;
+      // the fewest keys that any row of the chunk sees
+      const int fewest =
+          q.part == 0 ? len : min(len, sh.parts.last[q.part] + div_group(q.chunk * kRows, L.group_mul));
+      float m = -INFINITY, l = 0.f;
+      for (int t = q.tile0; t < q.tile1; ++t, ++tiles) {
+        ok = warp_wait(&sh.sfull[j], ph, wc);
+        if (!ok) break;
+        tc_fence_after();
+        const int key0 = t * kTcTile;
+        const int valid = sh.valid[tiles & 7];
+        const bool edge = key0 + kTcTile > fewest || valid != 255;
+        const int see = sees - key0;  // columns of the tile that the row sees
+        auto hide = [&](uint32_t (&x)[32], int col) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (col + i >= see || !((valid >> ((col + i) >> 4)) & 1)) x[i] = 0xff800000u;  // -inf
+        };
+        float top = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          uint32_t x[32];
+          tmem_ld32(ts + h * 32, x);
+          if (edge) hide(x, h * 32);
+          float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            t0 = fmaxf(t0, __uint_as_float(x[i]));
+            t1 = fmaxf(t1, __uint_as_float(x[i + 1]));
+          }
+          top = fmaxf(top, fmaxf(t0, t1));
+        }
+        const float mn = top * L.scale_log2;
+        const bool raise = mn > m + kRaise || (m == -INFINITY && mn > -INFINITY);
+        if (__any_sync(0xffffffffu, raise)) {
+          const float f = raise ? ex2_from(m, mn) : 1.f;
+          if (raise) m = mn;
+          l *= f;
+          if (t > q.tile0) {
+#pragma unroll
+            for (int h = 0; h < D / 32; ++h) {
+              uint32_t x[32];
+              tmem_ld32(to + h * 32, x);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+              tmem_st32(to + h * 32, x);
+            }
+          }
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          uint32_t x[32], p[16];
+          tmem_ld32(ts + h * 32, x);
+          if (edge) hide(x, h * 32);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float w0 = ex2(fmaf(__uint_as_float(x[2 * i]), L.scale_log2, -ref));
+            const float w1 = ex2(fmaf(__uint_as_float(x[2 * i + 1]), L.scale_log2, -ref));
+            l0 += w0;
+            l1 += w1;
+            // P is rounded to bf16 for the product with V (fp32 sums; l keeps the unrounded weights)
+            p[i] = pack_bf16x2(w0, w1);
+          }
+          tmem_st16(ts + h * 16, p);
+        }
+        l += l0 + l1;
+        if (key0 + kTcTile > len) {
+          // Keys behind the part's last one hold anything (NaN too): their V is
+          // made zero, as 0 * NaN would not be.
+          ok = warp_wait(&sh.vfull[vs], vph, wc);
+          if (!ok) break;
+          for (int i = rj; i < (key0 + kTcTile - len) * kSub * 8; i += 128) {
+            const int key = len - key0 + i / (kSub * 8), h = (i >> 3) % kSub, v = i & 7;
+            *reinterpret_cast<uint4*>(s_v + vs * S::kTileBytes + h * (kTcTile * 128) + key * 128 + v * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_async_smem();
+        }
+        if (++vs == S::kV) vs = 0, vph ^= 1u;
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&sh.pfull[j]);
+        ph ^= 1u;
+      }
+      if (!ok) break;
+      // the last product of the piece (its phase is the one before ph)
+      ok = warp_wait(&sh.pvdone[j], ph ^ 1u, wc);
+      if (!ok) break;
+      tc_fence_after();
+      const Piece done = q;
+      const bool begins = done.tile0 == 0;
+      const bool direct = begins && done.tile1 == done.tiles && a.prefix_len == 0;
+      const int rr = done.chunk * kRows + r, row = div_group(rr, L.group_mul);
+      const bool in = rr < rows;
+      const long long t = sh.parts.row0[done.part] + row;
+      const int head = done.kvh * group + rr - row * group;
+      const Pieces& keep = begins ? L.start[done.part > 0] : L.plan.rest;
+      const long long at = begins ? t * a.q_heads + head : c * kRows + r;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+      for (int h = 0; h < D / 32; ++h) {
+        uint32_t x[32];
+        __syncwarp();
+        tmem_ld32(to + h * 32, x);
+        if (in && direct) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + t * a.ldo + (long long)head * D + h * 32);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = pack_bf16x2(__uint_as_float(x[8 * i + 2 * e]) * inv, __uint_as_float(x[8 * i + 2 * e + 1]) * inv);
+            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else if (in) {
+          uint4* dst = reinterpret_cast<uint4*>(keep.o + at * D + h * 32);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        }
+      }
+      if (in && !direct) keep.ml[at] = make_float2(m, l);
+      __syncwarp();
+      u += q.units;
+      if (u < u1) {
+        q.next(sh.parts, a, L.plan, u, u1);
+        if (!q.empty()) load_q();
+      }
+    }
+  }
+
+  // ------------------------------------------------------------ teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 11) {
+    tc_fence_after();
+    tmem_dealloc(tmem, S::kCols);
+  }
+}
+
+template <int D, int NT>
+cudaError_t launch_shape(dec_handle* h, const CUtensorMap& tk, const CUtensorMap& tv, const AttentionLaunch& L,
+                         cudaStream_t s) {
+  using S = TcShape<D, NT>;
+  static std::atomic<uint64_t> ready{0};  // devices whose function attribute is set
+  const uint64_t bit = 1ull << (h->device & 63);
+  if (!(ready.load() & bit)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(attention_tc_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kTotal);
+    if (e != cudaSuccess) return e;
+    if (h->device < 64) ready.fetch_or(bit);
+  }
+  return launch_k(h, attention_tc_kernel<D, NT>, dim3(L.plan.ctas), dim3(kTcThreads), (size_t)S::kTotal, s, tk, tv, L);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_tc(dec_handle* h, const CUtensorMap& tk, const CUtensorMap& tv, const AttentionLaunch& L,
+                                cudaStream_t s) {
+  const bool two = L.plan.rows > 128;
+  if (L.a.dim == 64) return two ? launch_shape<64, 2>(h, tk, tv, L, s) : launch_shape<64, 1>(h, tk, tv, L, s);
+  return two ? launch_shape<128, 2>(h, tk, tv, L, s) : launch_shape<128, 1>(h, tk, tv, L, s);
+}
+
+}  // namespace dec
