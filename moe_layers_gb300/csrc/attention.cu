@@ -101,9 +101,11 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
     tmap_prefetch(&tk);
     tmap_prefetch(&tv);
   }
-  pdl_wait();
-  // Dependents start only now, when every earlier launch of the stream is
-  // complete: the joining kernel reads the lengths before its own wait.
+  // Dependents start only behind this wait, when every earlier launch of the
+  // stream is complete: the joining kernel reads the lengths before its own
+  // wait, and the own tokens' launch behind a prefix launch (late_wait) does not
+  // need that one's results: it waits at its end, so that its completion is both.
+  if (!L.late_wait) pdl_wait();
   pdl_trigger();
   if (warp == 0) build_parts(sh.parts, a, L.plan);
   __syncthreads();
@@ -423,6 +425,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
       }
     }
   }
+  if (L.late_wait) pdl_wait();
 }
 
 // Joins the pieces of the rows that more than one CTA, or the prefix and the
@@ -664,6 +667,7 @@ cudaError_t launch_attention(dec_handle* h, const AttentionParams& P, void* ws, 
   own.a = P;
   own.start[0] = w.start[0];
   own.start[1] = w.start[1];
+  own.late_wait = false;
   own.scale_log2 = P.scale * 1.4426950408889634f;
   own.group_mul = (uint32_t)(((1 << 20) + group - 1) / group);
   own.err = h->d_err;
@@ -681,6 +685,7 @@ cudaError_t launch_attention(dec_handle* h, const AttentionParams& P, void* ws, 
       LaunchScope scope(h, "attention_prefix", s);
       e = launch_chunks(h, tk, tv, pre, s);
       if (e != cudaSuccess) return e;
+      own.late_wait = own.plan.tile_shift == 6;
     }
   }
   {

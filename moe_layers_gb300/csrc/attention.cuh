@@ -46,6 +46,7 @@ struct AttentionLaunch {
   Plan plan;
   Pieces start[2];  // prefix, own: [M][q_heads]
   float scale_log2;
+  bool late_wait;      // the launch before it on the stream is the same call's prefix launch
   uint32_t group_mul;  // ceil(2^20 / group)
   int* err;
   unsigned long long wait_ns;

@@ -8,8 +8,9 @@
 //   S = Q K^T (128 x 128, fp32 in TMEM)           tcgen05.mma, Q and K in shared memory
 //   P = 2^(S - m), bf16, over S in TMEM            a thread per row: no shuffles
 //   O += P V (128 x D, fp32 in TMEM)               tcgen05.mma, P from TMEM, V in shared memory
-// with its own issuing warp, so that one stream's products run under the other
-// one's exponentials. The running maximum is raised only when a row's scores
+// and one warp issues the streams' products in turn, so that one stream's
+// products run under the other one's exponentials (with a warp per stream the
+// two fell into step and took turns as a pair: 100 us against N us). The running maximum is raised only when a row's scores
 // pass it by more than 2^8 (P <= 256 then, exact in fp32 sums), so O is read
 // and rescaled a few times, not every tile. K is a K-major operand as it lies
 // in the cache, V an MN-major one: both come by TMA with the 128-byte swizzle,
@@ -23,7 +24,7 @@ namespace dec {
 namespace {
 
 constexpr int kTcTile = 128;
-constexpr int kTcThreads = 384;  // warps 0-7 softmax (4 a stream), 8 copies K, 9 copies V, 10-11 issue products
+constexpr int kTcThreads = 384;  // warps 0-7 softmax (4 a stream), 8 copies K, 9 copies V, 10 issues products
 constexpr int kTcSmem = 232448;
 constexpr float kRaise = 8.f;    // log2 of the growth of the scores that is left in P
 
@@ -43,7 +44,7 @@ struct TcShape {
 
 struct TcShared {
   uint64_t kfull[6], kempty[6], vfull[6], vempty[6];
-  uint64_t sfull[2], pfull[2], pvdone[2], qfull, done[2];
+  uint64_t sfull[2], pfull[2], pvdone[2], qfull, done;
   PartTable parts;
   uint8_t valid[8];  // per tile (modulo 8): which 16-key eighths lie in blocks of the cache
   uint32_t tmem;
@@ -90,12 +91,22 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+// The same without the wait; the values may be used behind tmem_wait_ld(), which
+// takes them so that no use moves above it.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
-      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::DEC_W8(r, 0),
-      DEC_W8(r, 8), DEC_W8(r, 16), DEC_W8(r, 24), "r"(taddr)
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : DEC_R8(r, 0), DEC_R8(r, 8), DEC_R8(r, 16), DEC_R8(r, 24)
+      : "r"(taddr)
       : "memory");
+}
+#define DEC_RW8(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), \
+                      "+r"(r[i + 6]), "+r"(r[i + 7])
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&x)[32], uint32_t (&y)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  asm volatile("" : DEC_RW8(x, 0), DEC_RW8(x, 8), DEC_RW8(x, 16), DEC_RW8(x, 24));
+  asm volatile("" : DEC_RW8(y, 0), DEC_RW8(y, 8), DEC_RW8(y, 16), DEC_RW8(y, 24));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -126,15 +137,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int i = 0; i < 6; ++i) {
       mbar_init(&sh.kfull[i], 1);
       mbar_init(&sh.vfull[i], 1);
-      mbar_init(&sh.kempty[i], NT);
-      mbar_init(&sh.vempty[i], NT);
+      mbar_init(&sh.kempty[i], 1);
+      mbar_init(&sh.vempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.sfull[i], 1);
       mbar_init(&sh.pfull[i], 128);
       mbar_init(&sh.pvdone[i], 1);
-      mbar_init(&sh.done[i], 1);
     }
+    mbar_init(&sh.done, 1);
     mbar_init(&sh.qfull, kRows);
     sh.abort = 0;
     fence_mbar_init();
@@ -146,7 +157,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tmem_relinquish();
   }
   pdl_wait();
-  pdl_trigger();  // after the wait: see the joining kernel
+  pdl_trigger();  // after the wait: see the joining kernel and the launch of the own tokens
   if (warp == 0) build_parts(sh.parts, a, L.plan);
   tc_fence_before();
   __syncthreads();
@@ -210,52 +221,61 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (lane == 0)
       for (uint32_t i = issued > (uint32_t)slots ? issued - slots : 0; i < issued; ++i)
         mbar_wait_drain(&full[i % slots], (i / slots) & 1, L.err, L.wait_ns);
-  } else if (warp >= 10) {
-    // ------------------------------------------------------------ products of stream j
-    const int j = warp - 10;
-    if (j < NT) {
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------ products
+    if (warp == 10) {
       int ks = 0, vs = 0;
       uint32_t kph = 0, vph = 0, qph = 0, ph = 0;
       constexpr uint32_t idesc_s = umma_idesc_bf16(128, kTcTile);
       constexpr uint32_t idesc_o = umma_idesc_bf16(128, D) | (1u << 16);  // B is MN-major
-      const uint32_t qa = smem_u32(s_q + j * S::kTileBytes);
-      const uint32_t ts = tmem + S::kS + j * 128, to = tmem + S::kO + j * D;
+      auto issue_s = [&](int j, int slot) {
+        if (lane == 0) {
+          const uint32_t qa = smem_u32(s_q + j * S::kTileBytes), kb = smem_u32(s_k + slot * S::kTileBytes);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t off = (i >> 2) * (kTcTile * 128) + (i & 3) * 32;
+            umma_bf16(tmem + S::kS + j * 128, sw128_desc(qa + off), sw128_desc(kb + off), idesc_s, i > 0);
+          }
+          umma_commit(&sh.sfull[j]);
+          if (j == NT - 1) umma_commit(&sh.kempty[slot]);
+        }
+        __syncwarp();
+      };
       bool ok = true;
       for (long long u = u0; ok && u < u1 && !q.empty();) {
-        ok = warp_wait(&sh.qfull, qph, wc);  // the queries are there, and O has been read
+        // the queries are there, and O has been read; the first tile's scores
+        ok = warp_wait(&sh.qfull, qph, wc) && warp_wait(&sh.kfull[ks], kph, wc);
+        if (!ok) break;
         qph ^= 1u;
+        tc_fence_after();
+        for (int j = 0; j < NT; ++j) issue_s(j, ks);
+        if (++ks == S::kK) ks = 0, kph ^= 1u;
         for (int t = q.tile0; ok && t < q.tile1; ++t) {
-          ok = warp_wait(&sh.kfull[ks], kph, wc);
-          if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t kb = smem_u32(s_k + ks * S::kTileBytes);
+          const bool more = t + 1 < q.tile1;
+          for (int j = 0; ok && j < NT; ++j) {
+            ok = warp_wait(&sh.pfull[j], ph, wc) && (j > 0 || warp_wait(&sh.vfull[vs], vph, wc));
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+              const uint32_t vb = smem_u32(s_v + vs * S::kTileBytes);
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              const uint32_t off = (i >> 2) * (kTcTile * 128) + (i & 3) * 32;
-              umma_bf16(ts, sw128_desc(qa + off), sw128_desc(kb + off), idesc_s, i > 0);
+              for (int i = 0; i < kTcTile / 16; ++i)
+                umma_bf16_ts(tmem + S::kO + j * D, tmem + S::kS + j * 128 + i * 8,
+                             sw128_mn_desc(vb + i * 2048, kTcTile * 128), idesc_o, t > q.tile0 || i > 0);
+              umma_commit(&sh.pvdone[j]);
+              if (j == NT - 1) umma_commit(&sh.vempty[vs]);
             }
-            umma_commit(&sh.sfull[j]);
-            umma_commit(&sh.kempty[ks]);
+            __syncwarp();
+            if (more) {
+              // the next scores go where P is: only once P has been multiplied
+              ok = (j > 0 || warp_wait(&sh.kfull[ks], kph, wc)) && warp_wait(&sh.pvdone[j], ph, wc);
+              if (!ok) break;
+              tc_fence_after();
+              issue_s(j, ks);
+            }
           }
-          __syncwarp();
-          if (++ks == S::kK) ks = 0, kph ^= 1u;
-          ok = warp_wait(&sh.pfull[j], ph, wc) && warp_wait(&sh.vfull[vs], vph, wc);
-          if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t vb = smem_u32(s_v + vs * S::kTileBytes);
-#pragma unroll
-            for (int i = 0; i < kTcTile / 16; ++i)
-              umma_bf16_ts(to, ts + i * 8, sw128_mn_desc(vb + i * 2048, kTcTile * 128), idesc_o,
-                           t > q.tile0 || i > 0);
-            umma_commit(&sh.pvdone[j]);
-            umma_commit(&sh.vempty[vs]);
-          }
-          __syncwarp();
+          if (more && ++ks == S::kK) ks = 0, kph ^= 1u;
           if (++vs == S::kV) vs = 0, vph ^= 1u;
-          // S of the next tile goes where P is: only once P has been multiplied
-          ok = warp_wait(&sh.pvdone[j], ph, wc);
           ph ^= 1u;
         }
         u += q.units;
@@ -263,8 +283,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       // every product issued must be complete before TMEM is released
       if (lane == 0) {
-        umma_commit(&sh.done[j]);
-        mbar_wait_drain(&sh.done[j], 0, L.err, L.wait_ns);
+        umma_commit(&sh.done);
+        mbar_wait_drain(&sh.done, 0, L.err, L.wait_ns);
       }
     }
   } else if (warp / 4 < NT) {
@@ -277,21 +297,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int vs = 0;
     uint32_t vph = 0;
     int sees = 0;
+    // The stream's 128 query rows into shared memory (16 bytes a thread, rows
+    // contiguous over lanes, every load before any store), and the keys that
+    // this thread's row sees.
     auto load_q = [&]() {
-      const int rr = q.chunk * kRows + r;
-      const bool in = rr < sh.parts.rows[q.part] * group;
-      const int row = in ? div_group(rr, L.group_mul) : 0;
-      const int len = sh.parts.len[q.part];
-      sees = in ? min(len, q.part == 0 ? len : sh.parts.last[q.part] + row) : 0;
-      const uint16_t* src = a.q + (long long)(sh.parts.row0[q.part] + row) * a.ldq +
-                            (long long)(q.kvh * group + (in ? rr - row * group : 0)) * D;
+      const int rows = sh.parts.rows[q.part] * group, len = sh.parts.len[q.part], r0 = q.chunk * kRows;
+      const int mine = r0 + r;
+      sees = mine < rows ? min(len, q.part == 0 ? len : sh.parts.last[q.part] + div_group(mine, L.group_mul)) : 0;
+      constexpr int kVec = D / 8;  // 16-byte vectors of a row; 128 / kVec rows a step
 #pragma unroll
-      for (int h = 0; h < kSub; ++h) {
-        uint8_t* dst = s_q + j * S::kTileBytes + h * (128 * 128) + rj * 128;
+      for (int h = 0; h < kVec; h += 8) {
+        uint4 x[8];
 #pragma unroll
-        for (int v = 0; v < 8; ++v)
-          *reinterpret_cast<uint4*>(dst + ((v ^ (rj & 7)) << 4)) =
-              in ? ld_act16(src + h * 64 + v * 8) : make_uint4(0u, 0u, 0u, 0u);
+        for (int k = 0; k < 8; ++k) {
+          const int at = (h + k) * 128 + rj, rr = r0 + j * 128 + at / kVec;
+          const bool in = rr < rows;
+          const int row = in ? div_group(rr, L.group_mul) : 0;
+          x[k] = make_uint4(0u, 0u, 0u, 0u);
+          if (in)
+            x[k] = ld_act16(a.q + (long long)(sh.parts.row0[q.part] + row) * a.ldq +
+                            (long long)(q.kvh * group + rr - row * group) * D + (at % kVec) * 8);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int at = (h + k) * 128 + rj, qr = at / kVec, v = at % kVec;
+          *reinterpret_cast<uint4*>(s_q + j * S::kTileBytes + (v >> 3) * (128 * 128) + qr * 128 +
+                                    (((v & 7) ^ (qr & 7)) << 4)) = x[k];
+        }
       }
       fence_async_smem();
       tc_fence_before();
@@ -313,25 +345,34 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int valid = sh.valid[tiles & 7];
         const bool edge = key0 + kTcTile > fewest || valid != 255;
         const int see = sees - key0;  // columns of the tile that the row sees
-        auto hide = [&](uint32_t (&x)[32], int col) {
+        // Columns 64.. first, then 0..63, which stay in registers; 64.. are read
+        // again while those are worked on (128 scores and their weights would not
+        // fit the registers). P lies over the columns already used.
+        auto hide = [&](uint32_t (&x)[32], int h) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (col + i >= see || !((valid >> ((col + i) >> 4)) & 1)) x[i] = 0xff800000u;  // -inf
+            if (h * 32 + i >= see || !((valid >> (h * 2 + (i >> 4))) & 1)) x[i] = 0xff800000u;  // -inf
         };
-        float top = -INFINITY;
+        auto largest = [&](const uint32_t (&x)[32]) {
+          float t0 = __uint_as_float(x[0]), t1 = __uint_as_float(x[1]);
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          uint32_t x[32];
-          tmem_ld32(ts + h * 32, x);
-          if (edge) hide(x, h * 32);
-          float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
+          for (int i = 2; i < 32; i += 2) {
             t0 = fmaxf(t0, __uint_as_float(x[i]));
             t1 = fmaxf(t1, __uint_as_float(x[i + 1]));
           }
-          top = fmaxf(top, fmaxf(t0, t1));
-        }
+          return fmaxf(t0, t1);
+        };
+        uint32_t x0[32], x1[32], x2[32];
+        tmem_ld32_async(ts + 64, x0);
+        tmem_ld32_async(ts + 96, x1);
+        tmem_wait_ld(x0, x1);
+        if (edge) hide(x0, 2), hide(x1, 3);
+        float top = fmaxf(largest(x0), largest(x1));
+        tmem_ld32_async(ts, x0);
+        tmem_ld32_async(ts + 32, x1);
+        tmem_wait_ld(x0, x1);
+        if (edge) hide(x0, 0), hide(x1, 1);
+        top = fmaxf(top, fmaxf(largest(x0), largest(x1)));
         const float mn = top * L.scale_log2;
         const bool raise = mn > m + kRaise || (m == -INFINITY && mn > -INFINITY);
         if (__any_sync(0xffffffffu, raise)) {
@@ -340,22 +381,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           l *= f;
           if (t > q.tile0) {
 #pragma unroll
-            for (int h = 0; h < D / 32; ++h) {
-              uint32_t x[32];
-              tmem_ld32(to + h * 32, x);
+            for (int h = 0; h < D / 16; ++h) {
+              float o[16];
+              tmem_ld16(to + h * 16, o);
+              uint32_t y[16];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-              tmem_st32(to + h * 32, x);
+              for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(o[i] * f);
+              tmem_st16(to + h * 16, y);
             }
           }
         }
         const float ref = m == -INFINITY ? 0.f : m;
         float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          uint32_t x[32], p[16];
-          tmem_ld32(ts + h * 32, x);
-          if (edge) hide(x, h * 32);
+        auto weigh = [&](const uint32_t (&x)[32], int h) {
+          uint32_t p[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float w0 = ex2(fmaf(__uint_as_float(x[2 * i]), L.scale_log2, -ref));
@@ -366,7 +405,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             p[i] = pack_bf16x2(w0, w1);
           }
           tmem_st16(ts + h * 16, p);
-        }
+        };
+        tmem_ld32_async(ts + 64, x2);
+        weigh(x0, 0);
+        tmem_wait_ld(x2, x1);
+        tmem_ld32_async(ts + 96, x0);
+        if (edge) hide(x2, 2);
+        weigh(x1, 1);
+        weigh(x2, 2);
+        tmem_wait_ld(x0, x1);
+        if (edge) hide(x0, 3);
+        weigh(x0, 3);
         l += l0 + l1;
         if (key0 + kTcTile > len) {
           // Keys behind the part's last one hold anything (NaN too): their V is
