@@ -148,28 +148,34 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
         const int key0 = t * kTileKeys;
         const int boxes = min(per, (len - key0 + box - 1) / box);  // boxes with keys of the part
         ids.advance(key0 >> a.shift);
-        // lane: box (lane / kSub), 64-element half
-        const int b = lane / kSub, half = lane % kSub;
-        const int key = key0 + b * box;
-        const int id = ids.get(key >> a.shift);
-        const bool load = b < boxes;
-        const bool there = load && id >= 0 && id < a.blocks;
+        // lane b < per: the cache block of box b, a.blocks if it is not there
+        const int id = ids.get((key0 >> a.shift) + min(lane, per - 1));
+        const bool there = lane < boxes && id >= 0 && id < a.blocks;
         const uint32_t mask = __ballot_sync(0xffffffffu, there);
+        const int from = there ? id : a.blocks;  // past the end of the cache: reads zeros
         ok = warp_wait(&sh.empty[s], phase, wc);
         if (!ok) break;
-        if (lane == 0) {
-          int quarters = 0;  // 16-key quarters in blocks of the cache
-          for (int i = 0; i < 4; ++i) quarters |= ((mask >> ((i * 16 / box) * kSub)) & 1) << i;
-          if (keys) sh.valid[s] = (uint8_t)quarters;
-          mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(boxes * box * D * 2));
+        const int su = uniform(s);
+        uint8_t* dst = smem + su * S::kStage + (keys ? 0 : S::kHalf);
+        const int row = uniform((q.kvh << a.shift) + (key0 & ((1 << a.shift) - 1)));
+        if (elect_one()) {
+          if (keys) {
+            int quarters = 0;  // 16-key quarters in blocks of the cache
+            for (int i = 0; i < 4; ++i) quarters |= ((mask >> (i * 16 / box)) & 1) << i;
+            sh.valid[su] = (uint8_t)quarters;
+          }
+          mbar_arrive_expect_tx(&sh.full[su], (uint32_t)(boxes * box * D * 2));
+        }
+        for (int b = 0; b < boxes; ++b) {
+          const int block = __shfl_sync(0xffffffffu, from, b);
+          if (elect_one()) {
+#pragma unroll
+            for (int half = 0; half < kSub; ++half)
+              tma_load_3d(dst + half * (kTileKeys * 128) + b * box * 128, keys ? &tk : &tv, &sh.full[su], half * 64, row,
+                          block);
+          }
         }
         __syncwarp();
-        if (load) {
-          uint8_t* dst = smem + s * S::kStage + (keys ? 0 : S::kHalf) + half * (kTileKeys * 128) + b * box * 128;
-          // a block that is not there reads zeros from past the end of the cache
-          tma_load_3d(dst, keys ? &tk : &tv, &sh.full[s], half * 64,
-                      (q.kvh << a.shift) + (key & ((1 << a.shift) - 1)), there ? id : a.blocks);
-        }
         ++issued;
         if (++s == S::kStages) s = 0, phase ^= 1u;
       }

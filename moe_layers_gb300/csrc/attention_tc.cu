@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = (uint32_t)uniform((int)sh.tmem);
   const long long W = sh.parts.first[a.requests + 1], G = plan_ctas(W, L.plan.ctas), c = blockIdx.x;
   const long long u0 = c < G ? unit_start(c, W, G) : 0, u1 = c < G ? unit_start(c + 1, W, G) : 0;
   const WaitCtl wc{&sh.abort, L.err, L.wait_ns};
@@ -190,27 +190,35 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int key0 = t * kTcTile;
         const int boxes = min(per, (len - key0 + box - 1) / box);
         ids.advance(key0 >> a.shift);
-        const int b = lane / kSub, half = lane % kSub;
-        const int key = key0 + b * box;
-        const int id = ids.get(key >> a.shift);
-        const bool load = b < boxes;
-        const bool there = load && id >= 0 && id < a.blocks;
+        // lane b < per: the cache block of box b, a.blocks if it is not there
+        const int id = ids.get((key0 + min(lane, per - 1) * box) >> a.shift);
+        const bool there = lane < boxes && id >= 0 && id < a.blocks;
         const uint32_t mask = __ballot_sync(0xffffffffu, there);
+        const int from = there ? id : a.blocks;  // past the end of the cache: reads zeros
         ok = warp_wait(&empty[s], phase, wc);
         if (!ok) break;
-        if (lane == 0) {
+        const int su = uniform(s);
+        uint8_t* dst = ring + su * S::kTileBytes;
+        const int row = uniform((q.kvh << a.shift) + (key0 & ((1 << a.shift) - 1)));
+        if (elect_one()) {
           if (keys) {
             int eighths = 0;
-            for (int i = 0; i < 8; ++i) eighths |= ((mask >> ((i * 16 / box) * kSub)) & 1) << i;
+            for (int i = 0; i < 8; ++i) eighths |= ((mask >> (i * 16 / box)) & 1) << i;
             sh.valid[issued & 7] = (uint8_t)eighths;
           }
-          mbar_arrive_expect_tx(&full[s], (uint32_t)(boxes * box * D * 2));
+          mbar_arrive_expect_tx(&full[su], (uint32_t)(boxes * box * D * 2));
+        }
+        for (int b = 0; b < boxes; ++b) {
+          const int block = __shfl_sync(0xffffffffu, from, b);
+          // a 128-token block is two boxes
+          const int at = a.shift == 7 ? row + b * 64 : row;
+          if (elect_one()) {
+#pragma unroll
+            for (int half = 0; half < kSub; ++half)
+              tma_load_3d(dst + half * (kTcTile * 128) + b * box * 128, keys ? &tk : &tv, &full[su], half * 64, at, block);
+          }
         }
         __syncwarp();
-        if (load)
-          // a block that is not there reads zeros from past the end of the cache
-          tma_load_3d(ring + s * S::kTileBytes + half * (kTcTile * 128) + b * box * 128, keys ? &tk : &tv, &full[s],
-                      half * 64, (q.kvh << a.shift) + (key & ((1 << a.shift) - 1)), there ? id : a.blocks);
         ++issued;
         if (++s == slots) s = 0, phase ^= 1u;
       }
@@ -229,15 +237,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       constexpr uint32_t idesc_s = umma_idesc_bf16(128, kTcTile);
       constexpr uint32_t idesc_o = umma_idesc_bf16(128, D) | (1u << 16);  // B is MN-major
       auto issue_s = [&](int j, int slot) {
-        if (lane == 0) {
-          const uint32_t qa = smem_u32(s_q + j * S::kTileBytes), kb = smem_u32(s_k + slot * S::kTileBytes);
+        const int su = uniform(slot);
+        const uint64_t qd = sw128_desc(smem_u32(s_q) + j * S::kTileBytes);
+        const uint64_t kd = sw128_desc(smem_u32(s_k) + su * S::kTileBytes);
+        const uint32_t ts = tmem + S::kS + j * 128;
+        if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
-            const uint32_t off = (i >> 2) * (kTcTile * 128) + (i & 3) * 32;
-            umma_bf16(tmem + S::kS + j * 128, sw128_desc(qa + off), sw128_desc(kb + off), idesc_s, i > 0);
+            const uint64_t off = ((i >> 2) * (kTcTile * 128) + (i & 3) * 32) >> 4;  // the descriptors' address unit
+            umma_bf16(ts, qd + off, kd + off, idesc_s, i > 0);
           }
           umma_commit(&sh.sfull[j]);
-          if (j == NT - 1) umma_commit(&sh.kempty[slot]);
+          if (j == NT - 1) umma_commit(&sh.kempty[su]);
         }
         __syncwarp();
       };
@@ -248,22 +259,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!ok) break;
         qph ^= 1u;
         tc_fence_after();
+#pragma unroll
         for (int j = 0; j < NT; ++j) issue_s(j, ks);
         if (++ks == S::kK) ks = 0, kph ^= 1u;
         for (int t = q.tile0; ok && t < q.tile1; ++t) {
           const bool more = t + 1 < q.tile1;
-          for (int j = 0; ok && j < NT; ++j) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            if (!ok) break;
             ok = warp_wait(&sh.pfull[j], ph, wc) && (j > 0 || warp_wait(&sh.vfull[vs], vph, wc));
             if (!ok) break;
             tc_fence_after();
-            if (lane == 0) {
-              const uint32_t vb = smem_u32(s_v + vs * S::kTileBytes);
+            const int su = uniform(vs);
+            const uint64_t vd = sw128_mn_desc(smem_u32(s_v) + su * S::kTileBytes, kTcTile * 128);
+            const uint32_t ts = tmem + S::kS + j * 128, to = tmem + S::kO + j * D;
+            const uint32_t first = uniform(t > q.tile0);
+            if (elect_one()) {
 #pragma unroll
               for (int i = 0; i < kTcTile / 16; ++i)
-                umma_bf16_ts(tmem + S::kO + j * D, tmem + S::kS + j * 128 + i * 8,
-                             sw128_mn_desc(vb + i * 2048, kTcTile * 128), idesc_o, t > q.tile0 || i > 0);
+                umma_bf16_ts(to, ts + i * 8, vd + i * (2048 >> 4), idesc_o, i > 0 ? 1u : first);
               umma_commit(&sh.pvdone[j]);
-              if (j == NT - 1) umma_commit(&sh.vempty[vs]);
+              if (j == NT - 1) umma_commit(&sh.vempty[su]);
             }
             __syncwarp();
             if (more) {
@@ -282,10 +298,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (u < u1) q.next(sh.parts, a, L.plan, u, u1);
       }
       // every product issued must be complete before TMEM is released
-      if (lane == 0) {
+      __syncwarp();
+      if (elect_one()) {
         umma_commit(&sh.done);
         mbar_wait_drain(&sh.done, 0, L.err, L.wait_ns);
       }
+      __syncwarp();
     }
   } else if (warp / 4 < NT) {
     // ------------------------------------------------------------ softmax of stream j, one thread a row
