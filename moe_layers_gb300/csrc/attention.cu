@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
     tmap_prefetch(&tk);
     tmap_prefetch(&tv);
   }
+  warm_l2(a);
   // Dependents start only behind this wait, when every earlier launch of the
   // stream is complete: the joining kernel reads the lengths before its own
   // wait, and the own tokens' launch behind a prefix launch (late_wait) does not

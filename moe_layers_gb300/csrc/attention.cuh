@@ -182,6 +182,24 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc));
 }
 
+// Requests the lengths, tables and query rows into L2 while the launch before
+// drains (a hint: nothing is read). Each CTA takes a share of the lines.
+__device__ __forceinline__ void warm_l2(const AttentionParams& a) {
+  const int i = blockIdx.x * blockDim.x + threadIdx.x, n = gridDim.x * blockDim.x;
+  auto want = [](const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); };
+  const int row_lines = (a.q_heads * a.dim * 2 + 127) / 128;
+  for (int k = i; k < a.M * row_lines; k += n) {
+    const int t = k / row_lines;
+    want(a.q + t * a.ldq + (k - t * row_lines) * 64);
+  }
+  for (int k = i; k * 32 <= a.requests; k += n) {
+    want(a.row_start + k * 32);
+    if (k * 32 < a.requests) want(a.own_len + k * 32);
+  }
+  const int blocks = (int)(((long long)a.prefix_len + (1 << a.shift) - 1) >> a.shift);
+  for (int k = i; k * 32 < blocks; k += n) want(a.prefix_table + k * 32);
+}
+
 // One lane of a converged warp. Copies and products are issued behind it from
 // values that are the same in every lane: the instructions take their operands
 // from uniform registers, and a lane that diverges to issue them moves each

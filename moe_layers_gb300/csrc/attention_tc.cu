@@ -81,18 +81,8 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
 #define DEC_W8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), \
                      "r"(r[i + 6]), "r"(r[i + 7])
 
-// 32 consecutive columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : DEC_R8(r, 0), DEC_R8(r, 8), DEC_R8(r, 16), DEC_R8(r, 24)
-      : "r"(taddr)
-      : "memory");
-}
-// The same without the wait; the values may be used behind tmem_wait_ld(), which
-// takes them so that no use moves above it.
+// 32 consecutive columns of this thread's TMEM lane. The values may be used
+// behind tmem_wait_ld(), which takes them so that no use moves above it.
 __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
@@ -156,6 +146,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tmem_alloc(&sh.tmem, S::kCols);
     tmem_relinquish();
   }
+  warm_l2(a);
   pdl_wait();
   pdl_trigger();  // after the wait: see the joining kernel and the launch of the own tokens
   if (warp == 0) build_parts(sh.parts, a, L.plan);
@@ -363,14 +354,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int valid = sh.valid[tiles & 7];
         const bool edge = key0 + kTcTile > fewest || valid != 255;
         const int see = sees - key0;  // columns of the tile that the row sees
+        if (edge) {
+          // Scores that the row does not see become -inf in TMEM (one pass apart, so
+          // that the code of all other tiles stays short).
+#pragma unroll 1
+          for (int h = 0; h < 8; ++h) {
+            float x[16];
+            uint32_t y[16];
+            tmem_ld16(ts + h * 16, x);
+            const bool there = (valid >> h) & 1;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] = there && h * 16 + i < see ? __float_as_uint(x[i]) : 0xff800000u;
+            tmem_st16(ts + h * 16, y);
+          }
+          tmem_wait_st();
+        }
         // Columns 64.. first, then 0..63, which stay in registers; 64.. are read
         // again while those are worked on (128 scores and their weights would not
         // fit the registers). P lies over the columns already used.
-        auto hide = [&](uint32_t (&x)[32], int h) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (h * 32 + i >= see || !((valid >> (h * 2 + (i >> 4))) & 1)) x[i] = 0xff800000u;  // -inf
-        };
         auto largest = [&](const uint32_t (&x)[32]) {
           float t0 = __uint_as_float(x[0]), t1 = __uint_as_float(x[1]);
 #pragma unroll
@@ -384,12 +385,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tmem_ld32_async(ts + 64, x0);
         tmem_ld32_async(ts + 96, x1);
         tmem_wait_ld(x0, x1);
-        if (edge) hide(x0, 2), hide(x1, 3);
         float top = fmaxf(largest(x0), largest(x1));
         tmem_ld32_async(ts, x0);
         tmem_ld32_async(ts + 32, x1);
         tmem_wait_ld(x0, x1);
-        if (edge) hide(x0, 0), hide(x1, 1);
         top = fmaxf(top, fmaxf(largest(x0), largest(x1)));
         const float mn = top * L.scale_log2;
         const bool raise = mn > m + kRaise || (m == -INFINITY && mn > -INFINITY);
@@ -398,7 +397,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (raise) m = mn;
           l *= f;
           if (t > q.tile0) {
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < D / 16; ++h) {
               float o[16];
               tmem_ld16(to + h * 16, o);
@@ -428,11 +427,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         weigh(x0, 0);
         tmem_wait_ld(x2, x1);
         tmem_ld32_async(ts + 96, x0);
-        if (edge) hide(x2, 2);
         weigh(x1, 1);
         weigh(x2, 2);
         tmem_wait_ld(x0, x1);
-        if (edge) hide(x0, 3);
         weigh(x0, 3);
         l += l0 + l1;
         if (key0 + kTcTile > len) {
@@ -453,44 +450,63 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_arrive(&sh.pfull[j]);
         ph ^= 1u;
       }
-      if (!ok) break;
-      // the last product of the piece (its phase is the one before ph)
-      ok = warp_wait(&sh.pvdone[j], ph ^ 1u, wc);
+      // the last product of the piece (its phase is the one before ph); the
+      // stream's warps leave together if a wait gave up
+      if (ok) ok = warp_wait(&sh.pvdone[j], ph ^ 1u, wc);
+      ok = named_bar_and(1 + j, 128, ok);
       if (!ok) break;
       tc_fence_after();
       const Piece done = q;
       const bool begins = done.tile0 == 0;
       const bool direct = begins && done.tile1 == done.tiles && a.prefix_len == 0;
-      const int rr = done.chunk * kRows + r, row = div_group(rr, L.group_mul);
-      const bool in = rr < rows;
-      const long long t = sh.parts.row0[done.part] + row;
-      const int head = done.kvh * group + rr - row * group;
       const Pieces& keep = begins ? L.start[done.part > 0] : L.plan.rest;
-      const long long at = begins ? t * a.q_heads + head : c * kRows + r;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      // O leaves through the stream's query rows (every product that read them is
+      // complete), 64 columns at a time, so that a row's 256 bytes are written by 16
+      // neighbouring threads: from the threads that hold the rows, each store
+      // touched 32 rows and the piece took 4 us. 16-byte vector v of row i lies at
+      // v ^ (i & 15).
+      uint8_t* stage = s_q + j * S::kTileBytes;
+      constexpr int kPass = D == 64 ? 32 : 64;  // columns that fit 128 rows of fp32
+      const float inv = direct ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+      constexpr int kV = kPass / 4;
+      const int r0 = done.chunk * kRows + j * 128;
+#pragma unroll 1
+      for (int h = 0; h < D / kPass; ++h) {
 #pragma unroll
-      for (int h = 0; h < D / 32; ++h) {
-        uint32_t x[32];
-        __syncwarp();
-        tmem_ld32(to + h * 32, x);
-        if (in && direct) {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + t * a.ldo + (long long)head * D + h * 32);
+        for (int w = 0; w < kPass / 16; ++w) {
+          float x[16];
+          tmem_ld16(to + h * kPass + w * 16, x);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = pack_bf16x2(__uint_as_float(x[8 * i + 2 * e]) * inv, __uint_as_float(x[8 * i + 2 * e + 1]) * inv);
-            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        } else if (in) {
-          uint4* dst = reinterpret_cast<uint4*>(keep.o + at * D + h * 32);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) dst[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4*>(stage + rj * (kPass * 4) + (((w * 4 + i) ^ (rj & (kV - 1))) << 4)) =
+                make_float4(x[4 * i] * inv, x[4 * i + 1] * inv, x[4 * i + 2] * inv, x[4 * i + 3] * inv);
         }
+        named_bar_sync(1 + j, 128);
+#pragma unroll 4
+        for (int k = 0; k < kV; ++k) {
+          const int at = k * 128 + rj, i = at / kV, v = at % kV, rr = r0 + i;
+          if (rr < rows) {
+            const float4 x = *reinterpret_cast<const float4*>(stage + i * (kPass * 4) + ((v ^ (i & (kV - 1))) << 4));
+            const int row = div_group(rr, L.group_mul);
+            const long long t = sh.parts.row0[done.part] + row;
+            const int head = done.kvh * group + rr - row * group;
+            if (direct)
+              *reinterpret_cast<uint2*>(a.out + t * a.ldo + (long long)head * D + h * kPass + v * 4) =
+                  make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+            else
+              *reinterpret_cast<float4*>(keep.o + (begins ? t * a.q_heads + head : c * kRows + j * 128 + i) * D +
+                                         h * kPass + v * 4) = x;
+          }
+        }
+        named_bar_sync(1 + j, 128);
       }
-      if (in && !direct) keep.ml[at] = make_float2(m, l);
-      __syncwarp();
+      const int rr = done.chunk * kRows + r;
+      if (rr < rows && !direct) {
+        const int row = div_group(rr, L.group_mul);
+        const long long at = begins ? (long long)(sh.parts.row0[done.part] + row) * a.q_heads + done.kvh * group + rr - row * group
+                                    : c * kRows + r;
+        keep.ml[at] = make_float2(m, l);
+      }
       u += q.units;
       if (u < u1) {
         q.next(sh.parts, a, L.plan, u, u1);
