@@ -19,6 +19,7 @@ DEC_OK, DEC_ERR_INVALID_ARG, DEC_ERR_UNSUPPORTED, DEC_ERR_CUDA, DEC_ERR_TIMEOUT 
 VARIANT_AUTO, VARIANT_SMALL_M, VARIANT_SPLIT_K = 0, 1, 2
 
 _lib = None
+_bf16 = _i32 = _raw_stream = None  # set by _load
 
 
 class DecodeError(RuntimeError):
@@ -140,6 +141,10 @@ def _load():
     lib.dec_last_expert_variant.restype = ctypes.c_int
     lib.dec_launch_count.argtypes = [P]
     lib.dec_launch_count.restype = ctypes.c_uint64
+    import torch
+    global _bf16, _i32, _raw_stream
+    _bf16, _i32 = torch.bfloat16, torch.int32
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     _lib = lib
     return lib
 
@@ -190,6 +195,7 @@ class Handle:
         self.device = int(device)
         self._ws = {}
         self._stream_ws = {}
+        self._attention_ws = {}  # workspace bytes by shape
 
     @property
     def ptr(self):
@@ -544,8 +550,35 @@ def _int32(t, name: str, ndim: int = 1):
 
 def _stream_of(h: Handle, stream) -> int:
     """The given stream, else the current one of the handle's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:  # a microsecond less than a Stream object
+        return _raw_stream(h.device)
     import torch
-    return (torch.cuda.current_stream(h.device) if stream is None else stream).cuda_stream
+    return torch.cuda.current_stream(h.device).cuda_stream
+
+
+def _rows_of(t, name: str, device: int):
+    """(rows, width, row stride) of a 2-D bf16 tensor with contiguous rows on the device."""
+    if t.dtype is not _bf16 or t.dim() != 2 or t.get_device() != device:
+        _require(t, _bf16, name, 2)
+        raise ValueError(f"{name} must be on the handle's device, cuda:{device}")
+    rows, width = t.shape
+    ld, step = t.stride()
+    if step != 1 and width > 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    # the stride of a single row means nothing
+    return rows, width, ld if rows > 1 else max(ld, -(-width // 8) * 8)
+
+
+def _ints_of(t, name: str, device: int, count: Optional[int] = None) -> int:
+    """Address of a contiguous 1-D int32 tensor on the device with `count` elements."""
+    if t.dtype is not _i32 or t.dim() != 1 or t.get_device() != device or not t.is_contiguous():
+        _int32(t, name)
+        raise ValueError(f"{name} must be on the handle's device, cuda:{device}")
+    if count is not None and t.numel() != count:
+        raise ValueError(f"{name} must have {count} elements")
+    return t.data_ptr()
 
 
 class KvCache:
@@ -567,7 +600,7 @@ class KvCache:
         stride = k.stride(0) if blocks > 1 else heads * size * dim
         self._c = _KvCache(k.data_ptr(), v.data_ptr(), stride, blocks, size, heads, dim)
         self._ref = ctypes.byref(self._c)
-        self.head_dim, self.device_index = dim, k.device.index
+        self.block_size, self.kv_heads, self.head_dim, self.device_index = size, heads, dim, k.get_device()
 
 
 class StepTables:
@@ -585,7 +618,7 @@ class StepTables:
         self.row_start, self.own_len, self.positions, self.slots, self.left = row_start, own_len, positions, slots, left
         self._c = _StepTables(*(t.data_ptr() for t in (row_start, own_len, positions, slots, left)))
         self._ref = ctypes.byref(self._c)
-        self.requests, self.rows, self.device_index = own_len.numel(), positions.numel(), row_start.device.index
+        self.requests, self.rows, self.device_index = own_len.numel(), positions.numel(), row_start.get_device()
 
     @classmethod
     def empty(cls, requests: int, rows: int, device="cuda"):
@@ -615,7 +648,7 @@ class Batch:
                          block_table.data_ptr(), block_table.shape[1], prefix_table.data_ptr() if prefix_len > 0 else None,
                          self.prefix_len)
         self._ref = ctypes.byref(self._c)
-        self.device_index = own_len.device.index
+        self.device_index = own_len.get_device()
 
 
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
@@ -643,6 +676,12 @@ class Rope:
                                            float(high), _stream_of(h, stream)), "dec_rope_phases")
         self._c = _Rope(int(rotary_dim), 1 if interleaved else 0, float(magnitude), _ptr(self.phases))
         self._ref = ctypes.byref(self._c)
+        self.device_index = h.device
+
+
+def _described(h: Handle, thing, name: str) -> None:
+    if thing.device_index != h.device:
+        raise ValueError(f"{name} must be on the handle's device, cuda:{h.device}")
 
 
 def dec_batch_tables(h: Handle, ctx_len, new_len, free_blocks, free_count, block_table, block_size: int,
@@ -651,66 +690,60 @@ def dec_batch_tables(h: Handle, ctx_len, new_len, free_blocks, free_count, block
     """Positions, slots and block-table entries of one step from the requests'
     lengths (int32 tensors); block_table [requests, max_blocks] is updated in
     place. `out` gives the output tensors, else they are made for `rows` rows."""
-    for n, t in (("ctx_len", ctx_len), ("new_len", new_len), ("free_blocks", free_blocks), ("free_count", free_count)):
-        _int32(t, n)
-    _int32(block_table, "block_table", 2)
+    dev = h.device
     n = ctx_len.numel()
     if out is None:
         if rows is None:
             raise ValueError("rows is required without out")
         out = StepTables.empty(n, rows, ctx_len.device)
-    if new_len.numel() != n or block_table.shape[0] != n or out.requests != n or free_count.numel() < 1:
-        raise ValueError("ctx_len, new_len, block_table and out must be of as many requests, free_count of one value")
-    if rows is not None and rows != out.rows:
+    elif rows is not None and rows != out.rows:
         raise ValueError("rows differs from out's")
-    _same_device(h, ctx_len, new_len, free_blocks, free_count, block_table, out)
-    _check(_load().dec_batch_tables(h.ptr, ctx_len.data_ptr(), new_len.data_ptr(), n, free_blocks.data_ptr(),
-                                    free_count.data_ptr(), block_table.data_ptr(), block_table.shape[1],
-                                    int(block_size), int(position_offset), out.rows, out._ref, _stream_of(h, stream)),
-           "dec_batch_tables")
+    _int32(block_table, "block_table", 2)
+    width = block_table.shape[1]
+    if block_table.shape[0] != n or out.requests != n or free_count.numel() < 1 or block_table.get_device() != dev:
+        raise ValueError("block_table and out must be of as many requests as ctx_len, free_count of one value, all on "
+                         "the handle's device")
+    _described(h, out, "out")
+    st = _load().dec_batch_tables(h.ptr, _ints_of(ctx_len, "ctx_len", dev), _ints_of(new_len, "new_len", dev, n), n,
+                                  _ints_of(free_blocks, "free_blocks", dev), _ints_of(free_count, "free_count", dev),
+                                  block_table.data_ptr(), width, block_size, position_offset, out.rows, out._ref,
+                                  _stream_of(h, stream))
+    if st:
+        _check(st, "dec_batch_tables")
     return out
-
-
-def _same_device(h: Handle, *things) -> None:
-    for t in things:
-        index = t.device_index if hasattr(t, "device_index") else t.device.index
-        if index != h.device:
-            raise ValueError(f"every tensor must be on the handle's device, cuda:{h.device}")
 
 
 def dec_rope_append(h: Handle, rope: Rope, q, k, v, positions, slots, cache: KvCache, q_out=None, stream=None):
     """Turn q and k (bf16 [rows, heads * head_dim], rows may be strided) by their
     positions, write k and v into the cache at their slots; returns the turned
     q (q_out, which may be q; None with q None: only the cache is written)."""
-    import torch
-    for n, t in (("k", k), ("v", v)):
-        _require(t, torch.bfloat16, n, 2)
-    _int32(positions, "positions")
-    _int32(slots, "slots")
-    rows, d = k.shape[0], cache.head_dim
-    if k.shape != v.shape or k.shape[1] != cache.k.shape[1] * d:
+    dev, d = h.device, cache.head_dim
+    rows, width, ldk = _rows_of(k, "k", dev)
+    rows_v, width_v, ldv = _rows_of(v, "v", dev)
+    if rows_v != rows or width_v != width or width != cache.kv_heads * d:
         raise ValueError("k and v must be [rows, kv_heads * head_dim]")
-    if positions.numel() != rows or slots.numel() != rows:
-        raise ValueError("positions and slots must have one element per row")
-    heads = 0
+    heads, ldq, ldqo, pq, pqo = 0, 0, 0, None, None
     if q is not None:
-        _require(q, torch.bfloat16, "q", 2)
-        if q.shape[0] != rows or q.shape[1] % d != 0:
+        rows_q, width_q, ldq = _rows_of(q, "q", dev)
+        if rows_q != rows or width_q % d != 0:
             raise ValueError("q must be [rows, q_heads * head_dim]")
-        heads = q.shape[1] // d
+        heads = width_q // d
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        _require(q_out, torch.bfloat16, "q_out", 2)
-        if q_out.shape != q.shape:
+            import torch
+            q_out = torch.empty((rows, width_q), dtype=q.dtype, device=q.device)
+        rows_o, width_o, ldqo = _rows_of(q_out, "q_out", dev)
+        if rows_o != rows or width_o != width_q:
             raise ValueError("q_out must have q's shape")
-        _same_device(h, q, q_out)
+        pq, pqo = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _same_device(h, k, v, positions, slots, cache)
-    _check(_load().dec_rope_append(h.ptr, rope._ref, _ptr(q), 0 if q is None else _rows(q, "q"), k.data_ptr(),
-                                   _rows(k, "k"), v.data_ptr(), _rows(v, "v"), _ptr(q_out),
-                                   0 if q is None else _rows(q_out, "q_out"), rows, heads, positions.data_ptr(),
-                                   slots.data_ptr(), cache._ref, _stream_of(h, stream)), "dec_rope_append")
+    _described(h, cache, "cache")
+    _described(h, rope, "rope")
+    st = _load().dec_rope_append(h.ptr, rope._ref, pq, ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, pqo, ldqo, rows,
+                                 heads, _ints_of(positions, "positions", dev, rows),
+                                 _ints_of(slots, "slots", dev, rows), cache._ref, _stream_of(h, stream))
+    if st:
+        _check(st, "dec_rope_append")
     return q_out
 
 
@@ -725,25 +758,32 @@ def dec_attention(h: Handle, q, cache: KvCache, batch: Batch, scale: float, out=
     """Attention of a step's rows q (bf16 [M, q_heads * head_dim], rows may be
     strided) over the batch's shared prefix and own tokens in the cache. Without
     `out`, rows that belong to no request are zero."""
-    import torch
-    _require(q, torch.bfloat16, "q", 2)
-    M, width = q.shape
+    dev = h.device
+    M, width, ldq = _rows_of(q, "q", dev)
     if width % cache.head_dim != 0:
         raise ValueError("q must be [M, q_heads * head_dim]")
+    heads = width // cache.head_dim
     if out is None:
-        out = torch.zeros((M, width), dtype=torch.bfloat16, device=q.device)
-    _require(out, torch.bfloat16, "out", 2)
-    if out.shape != q.shape:
+        import torch
+        out = torch.zeros((M, width), dtype=q.dtype, device=q.device)
+    M_o, width_o, ldo = _rows_of(out, "out", dev)
+    if M_o != M or width_o != width:
         raise ValueError("out must have q's shape")
-    if batch.prefix_len > 0 and batch.prefix_table.numel() * cache.k.shape[2] < batch.prefix_len:
+    if batch.prefix_len > 0 and batch.prefix_table.numel() * cache.block_size < batch.prefix_len:
         raise ValueError("prefix_table holds fewer blocks than prefix_len tokens need")
-    _same_device(h, q, out, cache, batch)
-    heads, sp = width // cache.head_dim, _stream_of(h, stream)
+    _described(h, cache, "cache")
+    _described(h, batch, "batch")
+    sp = _stream_of(h, stream)
     if ws is None:
-        ws = h.stream_workspace("attention", sp, dec_attention_workspace_size(h, M, heads, cache, batch))
-    _check(_load().dec_attention(h.ptr, q.data_ptr(), _rows(q, "q"), cache._ref, batch._ref, float(scale),
-                                 out.data_ptr(), _rows(out, "out"), M, heads, ws.data_ptr(), ws.numel(), sp),
-           "dec_attention")
+        shape = (M, heads, cache.head_dim, cache.kv_heads, batch.prefix_len > 0)
+        size = h._attention_ws.get(shape)
+        if size is None:
+            size = h._attention_ws[shape] = dec_attention_workspace_size(h, M, heads, cache, batch)
+        ws = h.stream_workspace("attention", sp, size)
+    st = _load().dec_attention(h.ptr, q.data_ptr(), ldq, cache._ref, batch._ref, scale, out.data_ptr(), ldo, M, heads,
+                               ws.data_ptr(), ws.numel(), sp)
+    if st:
+        _check(st, "dec_attention")
     return out
 
 

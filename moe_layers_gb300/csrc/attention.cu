@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
 // warps each. A row with no piece at all gets zeros. The pieces are summed in
 // a fixed order.
 template <int D, int R>
-__global__ void __launch_bounds__(256) join_attention_kernel(const __grid_constant__ AttentionLaunch P,
+__global__ void __launch_bounds__(256, 4) join_attention_kernel(const __grid_constant__ AttentionLaunch P,
                                                              const __grid_constant__ AttentionLaunch O) {
   constexpr int NW = 8 / R, V = D / 32;
   __shared__ PartTable tp, to;
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(256) join_attention_kernel(const __grid_consta
   float x[V], m = -INFINITY, l = 0.f;
 #pragma unroll
   for (int e = 0; e < V; ++e) x[e] = 0.f;
-  constexpr int B = 8;  // pieces in flight per warp
+  constexpr int B = 6;  // pieces in flight per warp
   for (int i0 = w; i0 < n; i0 += NW * B) {
     float y[B][V];
     float2 ml[B];

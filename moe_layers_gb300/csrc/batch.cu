@@ -4,6 +4,8 @@
 #include <climits>
 #include <cmath>
 
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -14,7 +16,7 @@ constexpr int kTableThreads = 1024;
 
 // Exclusive sum over the block's threads (one value each); *total gets the sum.
 __device__ __forceinline__ int block_exclusive_sum(int v, int* warp_sums, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   int inc = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -23,20 +25,17 @@ __device__ __forceinline__ int block_exclusive_sum(int v, int* warp_sums, int* t
   }
   if (lane == 31) warp_sums[warp] = inc;
   __syncthreads();
-  if (warp == 0) {
-    int w = warp_sums[lane];
+  // every warp adds up the sums itself
+  int w = lane < warps ? warp_sums[lane] : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += u;
-    }
-    warp_sums[lane] = w;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += u;
   }
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  const int before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
   __syncthreads();
-  const int before = warp > 0 ? warp_sums[warp - 1] : 0;
-  *total = warp_sums[31];
-  __syncthreads();
-  return before + inc - v;
+  return (warp > 0 ? before : 0) + inc - v;
 }
 
 // Last index i in [0, n) with first[i] <= x (first[0] <= x).
@@ -52,18 +51,25 @@ __device__ __forceinline__ int last_at_most(const int* first, int n, int x) {
   return lo;
 }
 
-// One CTA, thread b for request b: two running sums (rows and new blocks)
-// place every row and every new block; then the threads take the new blocks
-// and the rows one by one, finding each one's request by bisection in shared
-// memory. Nothing is written before every length has been read.
+// Thread b for request b: two running sums (rows and new blocks) place every
+// row and every new block; then the threads take the new blocks and the rows,
+// four rows at a time, finding a row's request by bisection in shared memory.
+// A few hundred rows are one CTA, bound by the latency of a launch and three
+// dependent reads (2.4 us for 64 requests). Prompts take a cluster of 8 CTAs that
+// each repeat the sums and share the rows: no output may be written before
+// every CTA has read the lengths, as own_len and left may lie over inputs, and a
+// cluster can wait for that without a workspace.
+template <bool CLUSTER>
 __global__ void __launch_bounds__(kTableThreads) tables_kernel(const int32_t* ctx_len, const int32_t* new_len, int n,
                                                                const int32_t* free_blocks, const int32_t* free_count,
                                                                int32_t* table, int max_blocks, int shift, int offset,
                                                                int rows, dec_step_tables out) {
-  __shared__ int s_row[kTableThreads + 1], s_base[kTableThreads + 1], s_ctx[kTableThreads], s_held[kTableThreads];
+  namespace cg = cooperative_groups;
+  __shared__ int s_row[kTableThreads + 1], s_base[kTableThreads], s_ctx[kTableThreads], s_held[kTableThreads];
   __shared__ int s_warp[32];
   __shared__ int s_missing;
   const int b = threadIdx.x, size = 1 << shift;
+  const int first = blockIdx.x * blockDim.x + b, step = gridDim.x * blockDim.x;
   pdl_trigger();
   pdl_wait();
   if (b == 0) s_missing = 0;
@@ -82,43 +88,74 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(const int32_t* ct
   s_base[b] = base;
   s_ctx[b] = c;
   s_held[b] = held;
+  if (b == n - 1) s_row[n] = r1;
   __syncthreads();
-  if (b < n) {
-    out.row_start[b] = r0;
-    out.own_len[b] = (int)min((long long)c + (r1 - r0), (long long)INT_MAX);
-  }
-  if (b == 0) {
-    out.row_start[n] = used;
-    out.left[0] = max(have - fresh, 0);
+  if (CLUSTER) cg::this_cluster().sync();  // every CTA has read the lengths and the count
+  if (blockIdx.x == 0) {
+    if (b < n) {
+      out.row_start[b] = r0;
+      out.own_len[b] = (int)min((long long)c + (r1 - r0), (long long)INT_MAX);
+    }
+    if (b == 0) {
+      out.row_start[n] = used;
+      out.left[0] = max(have - fresh, 0);
+    }
   }
   auto fresh_block = [&](int i) { return i < have ? ld_act_s32(free_blocks + (have - 1 - i)) : -1; };
-  for (int i = threadIdx.x; i < fresh; i += blockDim.x) {
+  for (int i = first; i < fresh; i += step) {
     const int q = last_at_most(s_base, n, i);
     table[(long long)q * max_blocks + s_held[q] + (i - s_base[q])] = fresh_block(i);
   }
   int missing = 0;
-  for (int t = threadIdx.x; t < rows; t += blockDim.x) {
-    int slot = -1, position = 0;
-    if (t < used) {
-      const int q = last_at_most(s_row, n, t);
-      const long long j = (long long)s_ctx[q] + (t - s_row[q]);
-      const long long blk = j >> shift;
-      int id = -1;
-      if (blk < s_held[q])
-        id = ld_act_s32(table + (long long)q * max_blocks + blk);
-      else if (blk < max_blocks)
-        id = fresh_block(s_base[q] + (int)(blk - s_held[q]));
-      const long long sl = (long long)id * size + (j & (size - 1));
-      slot = id >= 0 && sl <= INT_MAX ? (int)sl : -1;
-      missing += slot < 0;
-      position = (int)min((long long)offset + j, (long long)INT_MAX);
+  // position and slot of row t of request q
+  auto place = [&](int q, int t, int& position, int& slot) {
+    const long long j = (long long)s_ctx[q] + (t - s_row[q]);
+    const long long blk = j >> shift;
+    int id = -1;
+    if (blk < s_held[q])
+      id = ld_act_s32(table + (long long)q * max_blocks + blk);
+    else if (blk < max_blocks)
+      id = fresh_block(s_base[q] + (int)(blk - s_held[q]));
+    const long long sl = (long long)id * size + (j & (size - 1));
+    slot = id >= 0 && sl <= INT_MAX ? (int)sl : -1;
+    missing += slot < 0;
+    position = (int)min((long long)offset + j, (long long)INT_MAX);
+  };
+  const bool wide = ((reinterpret_cast<uintptr_t>(out.positions) | reinterpret_cast<uintptr_t>(out.slots)) & 15) == 0;
+  if (CLUSTER && wide) {
+    for (int t0 = 4 * first; t0 < rows; t0 += 4 * step) {
+      int slot[4] = {-1, -1, -1, -1}, position[4] = {0, 0, 0, 0};
+      int q = t0 < used ? last_at_most(s_row, n, t0) : 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (t0 + k < used) {
+          while (s_row[q + 1] <= t0 + k) ++q;
+          place(q, t0 + k, position[k], slot[k]);
+        }
+      if (t0 + 4 <= rows) {
+        *reinterpret_cast<int4*>(out.positions + t0) = make_int4(position[0], position[1], position[2], position[3]);
+        *reinterpret_cast<int4*>(out.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      } else {
+        for (int k = 0; t0 + k < rows; ++k) out.positions[t0 + k] = position[k], out.slots[t0 + k] = slot[k];
+      }
     }
-    out.positions[t] = position;
-    out.slots[t] = slot;
+  } else {
+    for (int t = first; t < rows; t += step) {
+      int slot = -1, position = 0;
+      if (t < used) place(last_at_most(s_row, n, t), t, position, slot);
+      out.positions[t] = position;
+      out.slots[t] = slot;
+    }
   }
-  if (missing) atomicAdd(&s_missing, missing);
-  __syncthreads();
-  if (b == 0) out.left[1] = s_missing;
+  if (CLUSTER) {
+    cg::cluster_group cluster = cg::this_cluster();
+    if (missing) atomicAdd(cluster.map_shared_rank(&s_missing, 0), missing);
+    cluster.sync();
+  } else {
+    if (missing) atomicAdd(&s_missing, missing);
+    __syncthreads();
+  }
+  if (first == 0) out.left[1] = s_missing;
 }
 
 cudaError_t launch_tables(dec_handle* h, const int32_t* ctx_len, const int32_t* new_len, int n,
@@ -126,8 +163,23 @@ cudaError_t launch_tables(dec_handle* h, const int32_t* ctx_len, const int32_t* 
                           int block_size, int offset, int rows, const dec_step_tables& out, cudaStream_t s) {
   int shift = 0;
   while ((1 << shift) < block_size) ++shift;
-  return launch_k(h, tables_kernel, dim3(1), dim3(kTableThreads), 0, s, ctx_len, new_len, n, free_blocks, free_count,
-                  table, max_blocks, shift, offset, rows, out);
+  cudaLaunchConfig_t cfg = {};
+  // The cluster from 4096 rows on, where one CTA's rows take longer than the
+  // two cluster barriers.
+  const int ctas = rows >= 4096 ? 8 : 1;
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(n <= 128 && rows <= 512 ? 128 : kTableThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = h->pdl ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, ctas > 1 ? tables_kernel<true> : tables_kernel<false>, ctx_len, new_len, n, free_blocks, free_count, table, max_blocks, shift,
+                            offset, rows, out);
 }
 
 // ---------------------------------------------------------------- rotary positions
@@ -182,77 +234,109 @@ struct RopeParams {
   const int32_t *positions, *slots;
   const uint64_t* phases;
   float magnitude;
-  int q_heads, kv_heads, dim, rot, interleaved, shift, slots_n;
+  int rows, q_heads, kv_heads, dim, rot, interleaved, shift, slots_n;
 };
 
-__device__ __forceinline__ uint32_t pack_bf(float a, float b) { return (uint32_t)f2bf(a) | ((uint32_t)f2bf(b) << 16); }
+// Two floats rounded to nearest-even bf16, the first in the low half.
+__device__ __forceinline__ uint32_t pack_bf(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
 
-// One CTA per row. The row's cosines and sines are computed once into shared
-// memory; a work item is 8 elements of a head (16 with the half layout's
-// partners), read, turned and written by one thread, so q may be turned in
-// place.
-__global__ void __launch_bounds__(256) rope_kernel(const RopeParams P) {
-  __shared__ float s_cos[64], s_sin[64];
-  const int t = blockIdx.x;
+// A row's heads are cut into items of 8 elements (with the half layout, of 8
+// and their 8 partners); a thread reads, turns and writes whole items, so q may
+// be turned in place. Bound by the copy. A CTA has 128 NI of a row's items for
+// one row after another: where an item lies within its row is worked out once,
+// the reads of a row are all issued before any is used, and its cosines and
+// sines are computed under them. NI = 2 for many rows; few rows take NI = 1, so
+// that a row is spread over several CTAs, as the latency of one CTA's reads is
+// then all there is.
+constexpr int kRopeThreads = 128;
+
+template <int NI, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams P) {
+  __shared__ alignas(16) float s_cos[2][64], s_sin[2][64];
+  const int d8 = P.dim / 8, turn8 = INTER ? P.rot / 8 : P.rot / 16;  // items of a head that turn
+  const int per_head = INTER ? d8 : d8 - P.rot / 16;
+  const int half = P.rot / 2;
+  const int nq = P.q_heads * per_head, nk = P.kv_heads * per_head, n = nq + nk + P.kv_heads * d8;
+  int src[NI], dst[NI], kind[NI], turn[NI];  // kind: 0 q, 1 k, 2 v, -1 none; turn: first pair, -1 for a copy
+#pragma unroll
+  for (int k = 0; k < NI; ++k) {
+    const int it = (blockIdx.x * NI + k) * kRopeThreads + threadIdx.x;
+    kind[k] = it >= n ? -1 : it >= nq + nk ? 2 : it >= nq ? 1 : 0;
+    const int at = it - (kind[k] == 2 ? nq + nk : kind[k] == 1 ? nq : 0), each = kind[k] == 2 ? d8 : per_head;
+    const int head = at / each, i = at - head * each;
+    const bool turns = kind[k] < 2 && i < turn8;
+    const int e = (INTER || kind[k] == 2 || turns ? i : i + P.rot / 16) * 8;
+    src[k] = head * P.dim + e;
+    dst[k] = kind[k] == 0 ? src[k] : head * (P.dim << P.shift) + e;
+    turn[k] = turns ? i * (INTER ? 4 : 8) : -1;
+  }
   pdl_trigger();
   pdl_wait();
-  const int pos = ld_act_s32(P.positions + t), slot = ld_act_s32(P.slots + t);
-  if (threadIdx.x < P.rot / 2) {
-    float c, s;
-    rope_angle(P.phases[threadIdx.x], pos, P.magnitude, &c, &s);
-    s_cos[threadIdx.x] = c;
-    s_sin[threadIdx.x] = s;
-  }
-  __syncthreads();
-  const int d8 = P.dim / 8, turn8 = P.interleaved ? P.rot / 8 : P.rot / 16;  // items that turn
-  const int per_head = P.interleaved ? d8 : d8 - P.rot / 16;
-  const bool write = slot >= 0 && slot < P.slots_n;
-  const long long dst = write ? (long long)(slot >> P.shift) * P.block_stride +
-                                    (long long)(slot & ((1 << P.shift) - 1)) * P.dim
-                              : 0;
-  const long long head_step = (long long)P.dim << P.shift;
-  const int nq = P.q_heads * per_head, nk = write ? P.kv_heads * per_head : 0, nv = write ? P.kv_heads * d8 : 0;
-  for (int it = threadIdx.x; it < nq + nk + nv; it += blockDim.x) {
-    if (it >= nq + nk) {
-      const int head = (it - nq - nk) / d8, i = (it - nq - nk) % d8;
-      *reinterpret_cast<uint4*>(P.cv + dst + head * head_step + i * 8) =
-          ld_act16(P.v + t * P.ldv + (long long)head * P.dim + i * 8);
-      continue;
-    }
-    const int at = it < nq ? it : it - nq;
-    const int head = at / per_head, i = at % per_head;
-    const uint16_t* src = it < nq ? P.q + t * P.ldq + (long long)head * P.dim
-                                  : P.k + t * P.ldk + (long long)head * P.dim;
-    uint16_t* to = it < nq ? P.qo + t * P.ldqo + (long long)head * P.dim : P.ck + dst + head * head_step;
-    if (i >= turn8) {  // an element behind the rotary part
-      const int e = (P.interleaved ? i : i + P.rot / 16) * 8;
-      *reinterpret_cast<uint4*>(to + e) = ld_act16(src + e);
-    } else if (P.interleaved) {
-      const uint4 x = ld_act16(src + i * 8);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      uint32_t o[4];
+  const uint64_t phase = threadIdx.x < half ? P.phases[threadIdx.x] : 0;
+  int t = blockIdx.y, pos = ld_act_s32(P.positions + t), slot = ld_act_s32(P.slots + t);
+  for (int buf = 0; t < P.rows; buf ^= 1) {
+    uint4 xa[NI], xb[NI];
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const float a = bf_lo(w[p]), b = bf_hi(w[p]), c = s_cos[i * 4 + p], s = s_sin[i * 4 + p];
-        o[p] = pack_bf(a * c - b * s, b * c + a * s);
-      }
-      *reinterpret_cast<uint4*>(to + i * 8) = make_uint4(o[0], o[1], o[2], o[3]);
-    } else {
-      const int half = P.rot / 2;
-      const uint4 xa = ld_act16(src + i * 8), xb = ld_act16(src + half + i * 8);
-      const uint32_t wa[4] = {xa.x, xa.y, xa.z, xa.w}, wb[4] = {xb.x, xb.y, xb.z, xb.w};
-      uint32_t oa[4], ob[4];
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const float c0 = s_cos[i * 8 + 2 * p], s0 = s_sin[i * 8 + 2 * p];
-        const float c1 = s_cos[i * 8 + 2 * p + 1], s1 = s_sin[i * 8 + 2 * p + 1];
-        const float a0 = bf_lo(wa[p]), a1 = bf_hi(wa[p]), b0 = bf_lo(wb[p]), b1 = bf_hi(wb[p]);
-        oa[p] = pack_bf(a0 * c0 - b0 * s0, a1 * c1 - b1 * s1);
-        ob[p] = pack_bf(b0 * c0 + a0 * s0, b1 * c1 + a1 * s1);
-      }
-      *reinterpret_cast<uint4*>(to + i * 8) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
-      *reinterpret_cast<uint4*>(to + half + i * 8) = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+    for (int k = 0; k < NI; ++k) {
+      if (kind[k] < 0) continue;
+      const uint16_t* from = (kind[k] == 0 ? P.q + t * P.ldq : kind[k] == 1 ? P.k + t * P.ldk : P.v + t * P.ldv) + src[k];
+      xa[k] = ld_act16(from);
+      if (!INTER && turn[k] >= 0) xb[k] = ld_act16(from + half);
     }
+    const int next = t + gridDim.y;
+    int next_pos = 0, next_slot = 0;
+    if (next < P.rows) next_pos = ld_act_s32(P.positions + next), next_slot = ld_act_s32(P.slots + next);
+    if (threadIdx.x < half) rope_angle(phase, pos, P.magnitude, &s_cos[buf][threadIdx.x], &s_sin[buf][threadIdx.x]);
+    __syncthreads();  // one a row: the other buffer is written only behind the next one
+    const bool write = slot >= 0 && slot < P.slots_n;
+    const long long at = (long long)(slot >> P.shift) * P.block_stride + (slot & ((1 << P.shift) - 1)) * P.dim;
+#pragma unroll
+    for (int k = 0; k < NI; ++k) {
+      if (kind[k] < 0 || (kind[k] > 0 && !write)) continue;
+      uint16_t* to = (kind[k] == 0 ? P.qo + t * P.ldqo : (kind[k] == 1 ? P.ck : P.cv) + at) + dst[k];
+      if (turn[k] < 0) {
+        *reinterpret_cast<uint4*>(to) = xa[k];
+        continue;
+      }
+      const float* cs = s_cos[buf] + turn[k];
+      const float* sn = s_sin[buf] + turn[k];
+      if (INTER) {
+        const uint32_t w[4] = {xa[k].x, xa[k].y, xa[k].z, xa[k].w};
+        const float4 c4 = *reinterpret_cast<const float4*>(cs), s4 = *reinterpret_cast<const float4*>(sn);
+        const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const float a = bf_lo(w[p]), b = bf_hi(w[p]);
+          o[p] = pack_bf(a * c[p] - b * s[p], b * c[p] + a * s[p]);
+        }
+        *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
+      } else {
+        const uint32_t wa[4] = {xa[k].x, xa[k].y, xa[k].z, xa[k].w}, wb[4] = {xb[k].x, xb[k].y, xb[k].z, xb[k].w};
+        uint32_t oa[4], ob[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4 c4 = *reinterpret_cast<const float4*>(cs + 4 * h), s4 = *reinterpret_cast<const float4*>(sn + 4 * h);
+          const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const uint32_t va = wa[2 * h + p], vb = wb[2 * h + p];
+            const float a0 = bf_lo(va), a1 = bf_hi(va), b0 = bf_lo(vb), b1 = bf_hi(vb);
+            oa[2 * h + p] = pack_bf(a0 * c[2 * p] - b0 * s[2 * p], a1 * c[2 * p + 1] - b1 * s[2 * p + 1]);
+            ob[2 * h + p] = pack_bf(b0 * c[2 * p] + a0 * s[2 * p], b1 * c[2 * p + 1] + a1 * s[2 * p + 1]);
+          }
+        }
+        *reinterpret_cast<uint4*>(to) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+        *reinterpret_cast<uint4*>(to + half) = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+      }
+    }
+    t = next;
+    pos = next_pos;
+    slot = next_slot;
   }
 }
 
@@ -284,7 +368,24 @@ cudaError_t launch_rope_append(dec_handle* h, const dec_rope& rope, const uint16
   P.shift = 0;
   while ((1 << P.shift) < cache.block_size) ++P.shift;
   P.slots_n = cache.blocks << P.shift;
-  return launch_k(h, rope_kernel, dim3(rows), dim3(256), 0, s, P);
+  P.rows = rows;
+  const int d8 = P.dim / 8, per_head = P.interleaved ? d8 : d8 - P.rot / 16;
+  const int items = (P.q_heads + P.kv_heads) * per_head + P.kv_heads * d8;
+  // One item a thread while a wave (2048 threads an SM) holds them all. Above,
+  // two a thread and up to 60 CTAs an SM: more than are resident (18), so that
+  // those that begin overlap those that end, and few enough to take several rows
+  // each (8192 rows of 64 + 16 + 16 heads of 128: 60.2 us; with one wave of
+  // CTAs 73, a CTA for every row 63, four items a thread 65, one 66).
+  const bool few = (long long)rows * items <= 2048LL * h->sms;
+  const int ni = few ? 1 : 2;
+  const int chunks = (items + kRopeThreads * ni - 1) / (kRopeThreads * ni);
+  const int wave = (few ? 16 : 60) * h->sms;
+  const dim3 grid(chunks, std::max(1, std::min(rows, wave / chunks)));
+  if (P.interleaved)
+    return few ? launch_k(h, rope_kernel<1, true>, grid, dim3(kRopeThreads), 0, s, P)
+               : launch_k(h, rope_kernel<2, true>, grid, dim3(kRopeThreads), 0, s, P);
+  return few ? launch_k(h, rope_kernel<1, false>, grid, dim3(kRopeThreads), 0, s, P)
+             : launch_k(h, rope_kernel<2, false>, grid, dim3(kRopeThreads), 0, s, P);
 }
 
 }  // namespace dec
