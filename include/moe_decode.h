@@ -494,6 +494,35 @@ dec_status dec_attention(dec_handle* h, const dec_bf16* q, int64_t ldq, const de
                          const dec_batch* batch, float scale, dec_bf16* out, int64_t ldo, int M, int q_heads,
                          void* ws, size_t ws_bytes, cudaStream_t stream);
 
+/* The attention core of one decode layer. */
+typedef struct dec_layer_attention {
+  int q_heads;               /* q_heads * head_dim = K_out */
+  float scale;               /* factor on the scores, > 0 */
+  const dec_rope* rope;      /* rotary positions, or NULL for none */
+  const dec_kv_cache* cache; /* the layer's cache */
+  const dec_batch* batch;
+  const int32_t* positions;  /* [M], from dec_batch_tables */
+  const int32_t* slots;      /* [M] */
+} dec_layer_attention;
+
+dec_status decode_layer_attention_workspace_size(const dec_handle* h, const dec_layer_weights* Wt,
+                                                 const dec_layer_attention* A, int M, size_t* bytes);
+
+/* decode_layer with attention in place of the identity:
+ *   y = RMSNorm(h; gamma1) W_in^T = [q | k | v | rest],
+ *       q_heads, kv_heads and kv_heads heads of head_dim columns
+ *   q, k turned by their positions, k and v written to the cache
+ *   h1 = h + attention(q) W_o^T, and the rest of the layer as it is there.
+ * Wt->K_out = q_heads * head_dim, Wt->N_in >= (q_heads + 2 kv_heads) *
+ * head_dim. The rows' own tokens must be counted in batch->own_len already (as
+ * dec_batch_tables does). Rows of no request pass with an attention output of
+ * zero. Everything else (workspace, trace, prefetch) as in decode_layer; the
+ * shape that a workspace is zeroed for includes q_heads, kv_heads, head_dim
+ * and whether there is a prefix. */
+dec_status decode_layer_attention(dec_handle* h, const dec_layer_weights* Wt, const dec_layer_attention* A,
+                                  dec_bf16* hidden, int M, const dec_layer_trace* trace, void* ws, size_t ws_bytes,
+                                  cudaStream_t stream);
+
 /* ------------------------------------------------------------------ measurement */
 
 /* Per-kernel timing record returned by dec_profile_read. */

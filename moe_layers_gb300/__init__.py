@@ -70,6 +70,11 @@ class _Rope(ctypes.Structure):
                 ("phases", ctypes.c_void_p)]
 
 
+class _LayerAttention(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int), ("scale", ctypes.c_float)] + \
+               [(n, ctypes.c_void_p) for n in ("rope", "cache", "batch", "positions", "slots")]
+
+
 class _KernelTime(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 32), ("launches", ctypes.c_int), ("total_ms", ctypes.c_double)]
 
@@ -121,6 +126,10 @@ def _load():
                             ctypes.POINTER(_KvCache), P],
         "dec_attention_workspace_size": [P, I, I, ctypes.POINTER(_KvCache), ctypes.POINTER(_Batch),
                                          ctypes.POINTER(Z)],
+        "decode_layer_attention_workspace_size": [P, ctypes.POINTER(_LayerWeights), ctypes.POINTER(_LayerAttention), I,
+                                                  ctypes.POINTER(Z)],
+        "decode_layer_attention": [P, ctypes.POINTER(_LayerWeights), ctypes.POINTER(_LayerAttention), P, I,
+                                   ctypes.POINTER(_LayerTrace), P, Z, P],
         "dec_attention": [P, P, I64, ctypes.POINTER(_KvCache), ctypes.POINTER(_Batch), F, P, I64, I, I, P, Z, P],
         "dec_test_wait_timeout": [P, P],
         "dec_test_routing_wait_timeout": [P, I, P],
@@ -784,6 +793,70 @@ def dec_attention(h: Handle, q, cache: KvCache, batch: Batch, scale: float, out=
                                ws.data_ptr(), ws.numel(), sp)
     if st:
         _check(st, "dec_attention")
+    return out
+
+
+class LayerAttention:
+    """The attention core of one decode layer (see dec_layer_attention):
+    positions and slots are int32 [M] (StepTables), rope None turns nothing."""
+
+    def __init__(self, q_heads: int, scale: float, cache: KvCache, batch: Batch, positions, slots,
+                 rope: Optional[Rope] = None):
+        for n, t in (("positions", positions), ("slots", slots)):
+            _int32(t, n)
+        if positions.numel() != slots.numel() or positions.device != slots.device:
+            raise ValueError("positions and slots must be of the same rows")
+        if any(x is not None and x.device_index != positions.get_device() for x in (cache, batch, rope)):
+            raise ValueError("cache, batch, rope, positions and slots must be on one device")
+        if batch.prefix_len > 0 and batch.prefix_table.numel() * cache.block_size < batch.prefix_len:
+            raise ValueError("prefix_table holds fewer blocks than prefix_len tokens need")
+        self.q_heads, self.cache, self.batch, self.rope = int(q_heads), cache, batch, rope
+        self.positions, self.slots = positions, slots
+        self.rows, self.device_index = positions.numel(), positions.get_device()
+        at = ctypes.addressof
+        self._c = _LayerAttention(self.q_heads, float(scale), None if rope is None else at(rope._c), at(cache._c),
+                                  at(batch._c), positions.data_ptr(), slots.data_ptr())
+        self._ref = ctypes.byref(self._c)
+
+
+def decode_layer_attention_workspace_size(h: Handle, weights: LayerWeights, attention: LayerAttention, M: int) -> int:
+    nb = ctypes.c_size_t()
+    cw = weights.c_struct()
+    _check(_load().decode_layer_attention_workspace_size(h.ptr, ctypes.byref(cw), attention._ref, int(M),
+                                                         ctypes.byref(nb)), "decode_layer_attention_workspace_size")
+    return nb.value
+
+
+def decode_layer_attention(h: Handle, weights: LayerWeights, attention: LayerAttention, hidden, trace=False,
+                           stream=None, ws=None, _cw=None):
+    """decode_layer with attention between the projections, in place on hidden
+    bf16 [M,H]; trace as in decode_layer."""
+    import torch
+    _require(hidden, torch.bfloat16, "hidden", 2)
+    _described(h, attention, "attention")
+    M = hidden.shape[0]
+    if hidden.get_device() != h.device or not hidden.is_contiguous() or attention.rows != M:
+        raise ValueError("hidden must be contiguous on the handle's device, with as many rows as attention's positions")
+    cw = weights.c_struct() if _cw is None else _cw
+    sp = _stream_of(h, stream)
+    if ws is None:
+        c = attention.cache
+        ws = h.workspace(("layer_attention", sp), decode_layer_attention_workspace_size(h, weights, attention, M),
+                         ("layer_attention", M, cw.H, cw.N_in, cw.K_out, cw.E, cw.k, cw.I, attention.q_heads, c.kv_heads,
+                          c.head_dim, attention.batch.prefix_len > 0))
+    out = trace if isinstance(trace, dict) else None
+    if trace is True:
+        out = dict(h1=torch.empty_like(hidden),
+                   idx=torch.empty((M, cw.k), dtype=torch.int32, device=hidden.device),
+                   w=torch.empty((M, cw.k), dtype=torch.float32, device=hidden.device),
+                   scores=torch.empty((M, cw.E), dtype=torch.float32, device=hidden.device))
+    tr = None
+    if out is not None:
+        tr = _LayerTrace()
+        tr.h1, tr.idx, tr.w, tr.scores = (_ptr(out.get(n)) for n in ("h1", "idx", "w", "scores"))
+    _check(_load().decode_layer_attention(h.ptr, ctypes.byref(cw), attention._ref, _ptr(hidden), M,
+                                          ctypes.byref(tr) if tr is not None else None, _ptr(ws), ws.numel(), sp),
+           "decode_layer_attention")
     return out
 
 

@@ -460,6 +460,9 @@ struct LayerWs {
   uint16_t* a = nullptr;
   uint16_t* yin = nullptr;
   uint16_t* h1 = nullptr;
+  uint16_t* att = nullptr;  // decode_layer_attention: the attention output
+  void* att_ws = nullptr;
+  size_t att_ws_bytes = 0;
   MoeLayerWs ml;
 };
 
@@ -486,7 +489,14 @@ bool layer_ok(const dec_layer_weights* L, int M) {
   return moe_shape_ok(M, L->k, L->E, L->H, L->I);
 }
 
-void carve_layer(Carver& c, const dec_handle* h, const dec_layer_weights* L, int M, LayerWs* w) {
+bool layer_attention_ok(const dec_layer_weights* L, const dec_layer_attention* A, int M) {
+  if (A == nullptr || !attention_shape_ok(M, A->q_heads, A->cache, A->batch)) return false;
+  const long long q = (long long)A->q_heads * A->cache->head_dim, kv = (long long)A->cache->kv_heads * A->cache->head_dim;
+  return L->K_out == q && L->N_in >= q + 2 * kv && (A->rope == nullptr || rope_ok(A->rope, A->cache->head_dim));
+}
+
+void carve_layer(Carver& c, const dec_handle* h, const dec_layer_weights* L, int M, LayerWs* w,
+                 const dec_layer_attention* A = nullptr) {
   const int H = L->H;
   const long long dense_tiles = std::max<long long>((L->N_in + kTileN - 1) / kTileN, H / kTileN);
   carve_moe_layer_head(c, L->E, H, L->I, dense_tiles, &w->ml);
@@ -494,6 +504,11 @@ void carve_layer(Carver& c, const dec_handle* h, const dec_layer_weights* L, int
   w->yin = c.take<uint16_t>((size_t)M * L->N_in);
   w->h1 = c.take<uint16_t>((size_t)M * H);
   carve_moe_layer_data(c, h, M, L->k, L->E, H, L->I, &w->ml);
+  if (A != nullptr) {
+    w->att = c.take<uint16_t>((size_t)M * L->K_out);
+    w->att_ws_bytes = attention_ws_bytes(h, M, A->q_heads, *A->cache, *A->batch);
+    w->att_ws = c.take<char>(w->att_ws_bytes);
+  }
 }
 
 // ---------------------------------------------------------------- MoE layer
@@ -894,8 +909,11 @@ dec_status decode_layer_workspace_size(const dec_handle* h, const dec_layer_weig
   return DEC_OK;
 }
 
-dec_status decode_layer(dec_handle* h, const dec_layer_weights* Wt, dec_bf16* hidden, int M,
-                        const dec_layer_trace* trace, void* ws, size_t ws_bytes, cudaStream_t s) {
+// The layer with the attention core A, or without one (null) the identity on
+// the first K_out columns of the input projection.
+static dec_status layer_entry(dec_handle* h, const dec_layer_weights* Wt, const dec_layer_attention* A,
+                              dec_bf16* hidden, int M, const dec_layer_trace* trace, void* ws, size_t ws_bytes,
+                              cudaStream_t s) {
   if (h == nullptr || Wt == nullptr || hidden == nullptr || !layer_ok(Wt, M)) return DEC_ERR_INVALID_ARG;
   const dec_layer_weights& L = *Wt;
   if (!L.gamma1 || !L.W_in || !L.W_o || !L.gamma2 || !L.W_r || !L.Wg || !L.Wu || !L.Wd) return DEC_ERR_INVALID_ARG;
@@ -913,12 +931,11 @@ dec_status decode_layer(dec_handle* h, const dec_layer_weights* Wt, dec_bf16* hi
                           (const void*)trace->scores})
       if (p != nullptr && !al16(p)) return DEC_ERR_INVALID_ARG;
   }
-  size_t need = 0;
-  decode_layer_workspace_size(h, Wt, M, &need);
-  if (ws == nullptr || ws_bytes < need) return DEC_ERR_INVALID_ARG;
-  Carver c(ws);
+  Carver measure(nullptr), c(ws);
   LayerWs w;
-  carve_layer(c, h, Wt, M, &w);
+  carve_layer(measure, h, Wt, M, &w, A);
+  if (ws == nullptr || ws_bytes < measure.used) return DEC_ERR_INVALID_ARG;
+  carve_layer(c, h, Wt, M, &w, A);
   uint16_t* h1 = (trace && trace->h1) ? trace->h1 : w.h1;
   const int H = L.H;
 
@@ -934,33 +951,66 @@ dec_status decode_layer(dec_handle* h, const dec_layer_weights* Wt, dec_bf16* hi
                                            L.gamma1, L.eps)
                              : linear_impl(h, w.a, H, L.W_in, nullptr, w.yin, M, L.N_in, H, dense, s, "in_proj");
   if (st != DEC_OK) return st;
-  st = linear_impl(h, w.yin, L.N_in, L.W_o, hidden, h1, M, H, L.K_out, dense, s, "out_proj");
+  const uint16_t* core = w.yin;
+  int ld_core = L.N_in;
+  if (A != nullptr) {
+    st = layer_attention(h, *A, w.yin, L.N_in, w.att, L.K_out, M, w.att_ws, s);
+    if (st != DEC_OK) return st;
+    core = w.att;
+    ld_core = L.K_out;
+  }
+  st = linear_impl(h, core, ld_core, L.W_o, hidden, h1, M, H, L.K_out, dense, s, "out_proj");
   if (st != DEC_OK) return st;
   // The MoE block, pre-norm with its own residual: hidden = h1 + MoE(RMSNorm(h1)).
-  MoeLayerArgs A;
-  A.x = h1;
-  A.gamma = L.gamma2;
-  A.eps = L.eps;
-  A.Wr = L.W_r;
-  A.M = M;
-  A.k = L.k;
-  A.E = L.E;
-  A.H = H;
-  A.I = L.I;
-  A.Wg = L.Wg;
-  A.Wu = L.Wu;
-  A.Wd = L.Wd;
-  A.Wg_s = L.Wg_s;
-  A.Wu_s = L.Wu_s;
-  A.Wd_s = L.Wd_s;
-  A.residual = h1;
-  A.out = hidden;
-  A.idx = (trace && trace->idx) ? trace->idx : w.ml.idx;
-  A.w = (trace && trace->w) ? trace->w : w.ml.w;
-  A.scores = trace ? trace->scores : nullptr;
-  A.pf = L.prefetch_next;
-  A.pf_bytes = L.prefetch_next != nullptr ? L.prefetch_bytes : 0;
-  return moe_layer_impl(h, A, w.ml, s);
+  MoeLayerArgs B;
+  B.x = h1;
+  B.gamma = L.gamma2;
+  B.eps = L.eps;
+  B.Wr = L.W_r;
+  B.M = M;
+  B.k = L.k;
+  B.E = L.E;
+  B.H = H;
+  B.I = L.I;
+  B.Wg = L.Wg;
+  B.Wu = L.Wu;
+  B.Wd = L.Wd;
+  B.Wg_s = L.Wg_s;
+  B.Wu_s = L.Wu_s;
+  B.Wd_s = L.Wd_s;
+  B.residual = h1;
+  B.out = hidden;
+  B.idx = (trace && trace->idx) ? trace->idx : w.ml.idx;
+  B.w = (trace && trace->w) ? trace->w : w.ml.w;
+  B.scores = trace ? trace->scores : nullptr;
+  B.pf = L.prefetch_next;
+  B.pf_bytes = L.prefetch_next != nullptr ? L.prefetch_bytes : 0;
+  return moe_layer_impl(h, B, w.ml, s);
+}
+
+dec_status decode_layer(dec_handle* h, const dec_layer_weights* Wt, dec_bf16* hidden, int M,
+                        const dec_layer_trace* trace, void* ws, size_t ws_bytes, cudaStream_t s) {
+  return layer_entry(h, Wt, nullptr, hidden, M, trace, ws, ws_bytes, s);
+}
+
+dec_status decode_layer_attention_workspace_size(const dec_handle* h, const dec_layer_weights* Wt,
+                                                 const dec_layer_attention* A, int M, size_t* bytes) {
+  if (h == nullptr || bytes == nullptr || !layer_ok(Wt, M) || !layer_attention_ok(Wt, A, M)) return DEC_ERR_INVALID_ARG;
+  Carver c(nullptr);
+  LayerWs w;
+  carve_layer(c, h, Wt, M, &w, A);
+  *bytes = c.used;
+  return DEC_OK;
+}
+
+dec_status decode_layer_attention(dec_handle* h, const dec_layer_weights* Wt, const dec_layer_attention* A,
+                                  dec_bf16* hidden, int M, const dec_layer_trace* trace, void* ws, size_t ws_bytes,
+                                  cudaStream_t s) {
+  if (h == nullptr || !layer_ok(Wt, M) || !layer_attention_ok(Wt, A, M)) return DEC_ERR_INVALID_ARG;
+  if (A->positions == nullptr || A->slots == nullptr || !(A->scale > 0.f) || !std::isfinite(A->scale))
+    return DEC_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(A->positions) | reinterpret_cast<uintptr_t>(A->slots)) & 3) return DEC_ERR_INVALID_ARG;
+  return layer_entry(h, Wt, A, hidden, M, trace, ws, ws_bytes, s);
 }
 
 dec_status moe_layer_workspace_size(const dec_handle* h, const dec_moe_weights* Wt, int M, size_t* bytes) {

@@ -52,6 +52,52 @@ bool attention_shape_ok(int M, int q_heads, const dec_kv_cache* c, const dec_bat
          (long long)b->max_blocks * c->block_size <= 0x7fffffffLL;
 }
 
+static AttentionParams attention_params(const uint16_t* q, long long ldq, const dec_kv_cache& cache,
+                                        const dec_batch& batch, float scale, uint16_t* out, long long ldo, int M,
+                                        int q_heads, bool zero_idle) {
+  AttentionParams P;
+  P.q = q;
+  P.ldq = ldq;
+  P.out = out;
+  P.ldo = ldo;
+  P.k = cache.k;
+  P.v = cache.v;
+  P.block_stride = cache.block_stride;
+  P.blocks = cache.blocks;
+  P.shift = 0;
+  while ((1 << P.shift) < cache.block_size) ++P.shift;
+  P.kv_heads = cache.kv_heads;
+  P.q_heads = q_heads;
+  P.dim = cache.head_dim;
+  P.requests = batch.requests;
+  P.max_new = batch.max_new;
+  P.max_blocks = batch.max_blocks;
+  P.prefix_len = batch.prefix_len;
+  P.M = M;
+  P.row_start = batch.row_start;
+  P.own_len = batch.own_len;
+  P.block_table = batch.block_table;
+  P.prefix_table = batch.prefix_table;
+  P.scale = scale;
+  P.zero_idle = zero_idle;
+  return P;
+}
+
+dec_status layer_attention(dec_handle* h, const dec_layer_attention& A, uint16_t* y, long long ldy, uint16_t* out,
+                           long long ldo, int M, void* ws, cudaStream_t s) {
+  const dec_kv_cache& c = *A.cache;
+  const long long q = (long long)A.q_heads * c.head_dim, kv = (long long)c.kv_heads * c.head_dim;
+  const dec_rope none = {0, 0, 1.f, nullptr};
+  {
+    LaunchScope scope(h, "rope_append", s);
+    if (launch_rope_append(h, A.rope ? *A.rope : none, y, ldy, y + q, ldy, y + q + kv, ldy, y, ldy, M, A.q_heads,
+                           A.positions, A.slots, c, s) != cudaSuccess)
+      return DEC_ERR_CUDA;
+  }
+  return status(
+      launch_attention(h, attention_params(y, ldy, c, *A.batch, A.scale, out, ldo, M, A.q_heads, true), ws, s));
+}
+
 }  // namespace dec
 
 extern "C" {
@@ -137,31 +183,8 @@ dec_status dec_attention(dec_handle* h, const dec_bf16* q, int64_t ldq, const de
   if (need > 0 && (ws == nullptr || !al(ws, 16) || ws_bytes < need)) return DEC_ERR_INVALID_ARG;
   DeviceGuard dev(h->device);
   if (!dev.ok) return DEC_ERR_CUDA;
-  AttentionParams P;
-  P.q = q;
-  P.ldq = ldq;
-  P.out = out;
-  P.ldo = ldo;
-  P.k = cache->k;
-  P.v = cache->v;
-  P.block_stride = cache->block_stride;
-  P.blocks = cache->blocks;
-  P.shift = 0;
-  while ((1 << P.shift) < cache->block_size) ++P.shift;
-  P.kv_heads = cache->kv_heads;
-  P.q_heads = q_heads;
-  P.dim = cache->head_dim;
-  P.requests = batch->requests;
-  P.max_new = batch->max_new;
-  P.max_blocks = batch->max_blocks;
-  P.prefix_len = batch->prefix_len;
-  P.M = M;
-  P.row_start = batch->row_start;
-  P.own_len = batch->own_len;
-  P.block_table = batch->block_table;
-  P.prefix_table = batch->prefix_table;
-  P.scale = scale;
-  return status(launch_attention(h, P, ws, stream));
+  return status(launch_attention(
+      h, attention_params(q, ldq, *cache, *batch, scale, out, ldo, M, q_heads, false), ws, stream));
 }
 
 }  // extern "C"

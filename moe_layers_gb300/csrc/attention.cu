@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(256, 4) join_attention_kernel(const __grid_con
     return s;
   };
   Span sp{0, 0, 0, 0}, so{0, 0, 0, 0};
-  int n = -1;  // pieces; -1: nothing to write
+  int n = part == 0 && t < a.M && a.zero_idle ? 0 : -1;  // pieces; -1: nothing to write
   if (part > 0) {
     if (a.prefix_len > 0) sp = span_of(tp, P, 0);
     so = span_of(to, O, part);

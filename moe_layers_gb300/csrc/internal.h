@@ -198,11 +198,17 @@ struct AttentionParams {
   int requests, max_new, max_blocks, prefix_len, M;
   const int32_t *row_start, *own_len, *block_table, *prefix_table;
   float scale;
+  bool zero_idle;  // rows of no request become zeros (else they are left)
 };
 size_t attention_ws_bytes(const dec_handle* h, int M, int q_heads, const dec_kv_cache& cache, const dec_batch& batch);
 cudaError_t launch_attention(dec_handle* h, const AttentionParams& P, void* ws, cudaStream_t s);
 
-// Checked by the callers (api_attention.cu): shapes and pointers of an attention call.
+// q and k of the input projection's rows y turned in place, k and v written to
+// the cache, attention into out (rows of no request: zeros). Checked by the caller.
+dec_status layer_attention(dec_handle* h, const dec_layer_attention& A, uint16_t* y, long long ldy, uint16_t* out,
+                           long long ldo, int M, void* ws, cudaStream_t s);
+
+// Shapes and pointers of an attention call.
 bool cache_ok(const dec_kv_cache* c);
 bool batch_ok(const dec_batch* b);
 bool rope_ok(const dec_rope* r, int head_dim);

@@ -234,10 +234,12 @@ def moe_layer(x, gamma, Wr, k: int, expert: ExpertFn, shared: Optional[Sequence]
 # ----------------------------------------------------------------------------- decode layer
 def decode_layer(h, gamma1, W_in, W_o, gamma2, Wr, k: int, expert: ExpertFn, shared: Optional[Sequence],
                  k_out: Optional[int] = None, eps: float = RMS_EPS, tokens: Optional[Sequence[int]] = None,
-                 storage: str = "bf16"):
+                 storage: str = "bf16", core: Optional[Callable] = None):
     """One decode layer: RMSNorm -> input projection -> out-projection + residual
     -> RMSNorm -> MoE (+ residual).
 
+    ``core``: maps the stored input projection [rows, N_in] to the input of the
+    out-projection [rows, k_out] (an attention core); without one, as follows.
     The pages omit the attention core between the input projection and the
     out-projection; the plainest reading that keeps the data dependency is to
     feed the first ``k_out`` columns of the input projection (K of the
@@ -269,7 +271,7 @@ def decode_layer(h, gamma1, W_in, W_o, gamma2, Wr, k: int, expert: ExpertFn, sha
     a = st(a_x)
     y_x = linear(a, W_in)
     y_in = st(y_x)
-    h1_x = linear_residual(y_in[:, :k_out], W_o64, h)
+    h1_x = linear_residual(y_in[:, :k_out] if core is None else core(y_in), W_o64, h)
     h1 = st(h1_x)
     m = moe_layer(h1, gamma2, Wr, k, expert, shared, residual=h1, eps=eps, storage=storage)
     return dict(a=a, y_in=y_in, h1=h1, b=m["b"], logits=m["logits"], scores=m["scores"], idx=m["idx"], w=m["w"],

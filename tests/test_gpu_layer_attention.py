@@ -1,0 +1,183 @@
+"""The decode layer with attention (decode_layer_attention): steps of a small
+batch from tables to hidden state against the oracle's layer, stage by stage."""
+import numpy as np
+import pytest
+
+import oracle
+import synth
+from _util import SEED, assert_bf16_close, dev_bf16, dev_f32, host_bits
+
+pytestmark = pytest.mark.gpu
+
+H, E, I, K = 256, 16, 128, 4
+
+
+@pytest.fixture(scope="module")
+def h():
+    import torch
+    import moe_layers_gb300 as M
+    assert torch.cuda.is_available()
+    M.build()
+    with M.Handle(0) as hd:
+        yield hd
+        assert hd.check_device_error() == M.DEC_OK
+
+
+def i32(a):
+    import torch
+    return torch.tensor(np.ascontiguousarray(a, dtype=np.int32), device="cuda")
+
+
+class Layer:
+    def __init__(self, heads, kv, d, rest, shared):
+        import moe_layers_gb300 as ML
+        self.heads, self.kv, self.d = heads, kv, d
+        n_in, k_out = (heads + 2 * kv) * d + rest, heads * d
+        mk = lambda tid, *shape, s=0.05: synth.bf16(int(np.prod(shape)), SEED, 7000 + tid, 0, s).reshape(shape)  # noqa: E731
+        one = (np.asarray(1.0, np.float32).view(np.uint32) >> 16).astype(np.uint16)
+        self.g1, self.g2 = np.full(H, one), np.full(H, one)
+        self.W_in, self.W_o = mk(0, n_in, H, s=0.1), mk(1, H, k_out)
+        self.Wr = synth.f32(E * H, SEED, 7002, 0, 0.05).reshape(E, H)
+        self.bank = [mk(3, E, I, H), mk(4, E, I, H), mk(5, E, H, I)]
+        self.shared = [mk(6, I, H), mk(7, I, H), mk(8, H, I)] if shared else None
+        dev = lambda a: dev_bf16(a, a.shape)  # noqa: E731
+        sh = [dev(a) for a in self.shared] if shared else [None] * 3
+        self.w = ML.LayerWeights(gamma1=dev(self.g1), W_in=dev(self.W_in), W_o=dev(self.W_o), gamma2=dev(self.g2),
+                                 W_r=dev_f32(self.Wr), Wg=dev(self.bank[0]), Wu=dev(self.bank[1]), Wd=dev(self.bank[2]),
+                                 Wg_s=sh[0], Wu_s=sh[1], Wd_s=sh[2], k=K, k_out=k_out)
+
+
+@pytest.mark.parametrize("shared", [True, False])
+@pytest.mark.parametrize("heads,kv,d,rest", [(4, 2, 64, 8), (2, 1, 128, 0), (6, 6, 64, 64)])
+@pytest.mark.parametrize("news,prefix,pad", [([[1], [1]], 0, 0), ([[1, 1], [1, 1]], 20, 0), ([[3, 1], [1, 1]], 37, 1),
+                                             ([[2, 0, 5, 1], [1, 1, 1, 1]], 0, 2), ([[16, 20, 9, 11], [1] * 4], 65, 3)])
+def test_steps(h, heads, kv, d, rest, news, prefix, pad, shared):
+    import torch
+    import moe_layers_gb300 as ML
+    L = Layer(heads, kv, d, rest, shared)
+    size, blocks, n = 16, 40, len(news[0])
+    rng = np.random.default_rng(len(news[0]) + prefix)
+    kc, vc = (torch.tensor(rng.standard_normal((blocks, kv, size, d)), dtype=torch.float32).to(torch.bfloat16).cuda()
+              for _ in range(2))
+    ids = [int(x) for x in rng.permutation(blocks)]
+    prefix_table = ids[:-(-prefix // size)]
+    free = ids[len(prefix_table):]
+    table, ctx, count = np.full((n, 4), -1), np.zeros(n, int), len(free)
+    d_table, d_free = i32(table), i32(free)
+    rope, freq = ML.Rope(h, 32, base=10000.0), oracle.rope_frequencies(32, 10000.0)
+    for step, new in enumerate(news):
+        M = sum(new) + pad
+        tables = ML.dec_batch_tables(h, i32(ctx), i32(new), d_free, i32([count]), d_table, size, rows=M,
+                                     position_offset=prefix)
+        batch = ML.Batch(tables.row_start, tables.own_len, d_table, max_new=max(new),
+                         prefix_table=i32(prefix_table) if prefix else None, prefix_len=prefix)
+        att = ML.LayerAttention(heads, d ** -0.5, ML.KvCache(kc, vc), batch, tables.positions, tables.slots, rope)
+        hb = synth.bf16(M * H, SEED, 7100 + step, 0, 1.0).reshape(M, H)
+        hidden = dev_bf16(hb, (M, H))
+        k0, v0 = host_bits(kc), host_bits(vc)
+        tr = ML.decode_layer_attention(h, L.w, att, hidden, trace=True)
+        torch.cuda.synchronize()
+        want = oracle.batch_tables(ctx, new, free, count, table, size, prefix, M)
+        table, ctx, count = want["table"], want["own_len"], int(want["left"][0])
+
+        def core(y):
+            y = y.reshape(M, -1)
+            q, k, v = (y[:, a * d:b * d].reshape(M, b - a, d) for a, b in ((0, heads), (heads, heads + kv),
+                                                                          (heads + kv, heads + 2 * kv)))
+            q, k = (oracle.round_bf16(oracle.rope(x, want["positions"], freq)) for x in (q, k))
+            ck, cv = oracle.as_f64(k0).copy(), oracle.as_f64(v0).copy()
+            for t in range(sum(new)):
+                b, o = want["slots"][t] // size, want["slots"][t] % size
+                ck[b, :, o], cv[b, :, o] = k[t], v[t]
+            core.cache = ck, cv
+            out, _, _ = oracle.attention(q, ck, cv, want["row_start"], ctx, table, d ** -0.5, prefix_table, prefix)
+            return oracle.round_bf16(np.nan_to_num(out)).reshape(M, heads * d)
+
+        expert = lambda e: tuple(oracle.bf16_to_f64(b[e]) for b in L.bank)  # noqa: E731
+        ref = oracle.decode_layer(hb, L.g1, L.W_in, L.W_o, L.g2, L.Wr, K, expert, L.shared, k_out=heads * d, core=core)
+        # against the sum before its storage rounding: the rule allows the stored value one
+        # half-ulp, and a reference that had been rounded as well could lie another one off
+        assert_bf16_close(host_bits(tr["h1"]), ref["unrounded"]["h1"], "h1")
+        # the cache: the step's tokens to a rounding of the projection and of the turn, the rest untouched
+        for got, exp, before in zip((host_bits(kc), host_bits(vc)), core.cache, (k0, v0)):
+            touched = np.zeros(got.shape, bool)
+            for t in range(sum(new)):
+                touched[want["slots"][t] // size, :, want["slots"][t] % size] = True
+            assert np.array_equal(got[~touched], before[~touched])
+            assert np.all(np.abs(oracle.as_f64(got) - exp)[touched] <= 2.0 ** -6 * np.abs(exp)[touched] + 2e-2)
+        # rows of no request pass without attention
+        assert np.array_equal(host_bits(tr["h1"])[sum(new):], hb[sum(new):])
+        # the MoE block on the stored h1 with the routing it chose
+        h1 = oracle.as_f64(host_bits(tr["h1"]))
+        b = oracle.round_bf16(oracle.rmsnorm(h1, L.g2))
+        out = h1 + oracle.moe(b, tr["idx"].cpu().numpy(), tr["w"].cpu().numpy().astype(np.float64), expert, L.shared)
+        assert_bf16_close(host_bits(hidden), out, "out")
+
+
+def test_layer_attention_under_a_graph(h):
+    """A captured step replayed with the tables' own outputs as the next lengths gives the eager steps' bits."""
+    import torch
+    import moe_layers_gb300 as ML
+    heads, kv, d, size, n = 4, 2, 64, 16, 3
+    L = Layer(heads, kv, d, 0, True)
+    rng = np.random.default_rng(1)
+    init = torch.tensor(rng.standard_normal((2, 20, kv, size, d)), dtype=torch.float32).to(torch.bfloat16).cuda()
+    x0 = dev_bf16(synth.bf16(n * H, SEED, 7200, 0, 1.0).reshape(n, H), (n, H))
+    rope = ML.Rope(h, 64)
+
+    def run(graph):
+        pool = init.clone()
+        ctx, new, free, count = i32([0, 3, 15]), i32([1, 1, 1]), i32(range(3, 20)), i32([17, 0])
+        table = i32([[-1] * 4, [0] + [-1] * 3, [1] + [-1] * 3])
+        out = ML.StepTables(torch.zeros(n + 1, dtype=torch.int32, device="cuda"), ctx,
+                            torch.zeros(n, dtype=torch.int32, device="cuda"),
+                            torch.zeros(n, dtype=torch.int32, device="cuda"), count)
+        batch = ML.Batch(out.row_start, out.own_len, table)
+        att = ML.LayerAttention(heads, 0.125, ML.KvCache(pool[0], pool[1]), batch, out.positions, out.slots, rope)
+        x = x0.clone()
+        ws = torch.zeros(ML.decode_layer_attention_workspace_size(h, L.w, att, n), dtype=torch.uint8, device="cuda")
+
+        def step():
+            ML.dec_batch_tables(h, ctx, new, free, count, table, size, out)
+            ML.decode_layer_attention(h, L.w, att, x, ws=ws)
+
+        if graph:
+            g = torch.cuda.CUDAGraph()
+            side = torch.cuda.Stream()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.graph(g, stream=side):
+                step()
+            for _ in range(20):
+                g.replay()
+        else:
+            for _ in range(20):
+                step()
+        torch.cuda.synchronize()
+        return host_bits(x), host_bits(pool), ctx.cpu().numpy(), table.cpu().numpy()
+
+    for a, b in zip(run(False), run(True)):
+        assert np.array_equal(a, b)
+
+
+def test_layer_attention_refuses(h):
+    import torch
+    import moe_layers_gb300 as ML
+    L = Layer(4, 2, 64, 0, True)
+    pool = torch.zeros((4, 2, 16, 64), dtype=torch.bfloat16, device="cuda")
+    batch = ML.Batch(i32([0, 1]), i32([1]), i32([[0]]))
+    one = i32([0])
+    x = torch.zeros((1, H), dtype=torch.bfloat16, device="cuda")
+
+    def call(heads=4, scale=0.125, cache=pool, rope=None):
+        ML.decode_layer_attention(h, L.w, ML.LayerAttention(heads, scale, ML.KvCache(cache, cache), batch, one, one, rope), x)
+
+    for bad in (dict(heads=3), dict(heads=2), dict(scale=0.0), dict(scale=float("inf")),
+                dict(cache=torch.zeros((4, 4, 16, 64), dtype=torch.bfloat16, device="cuda")),
+                dict(rope=ML.Rope(h, 128))):
+        with pytest.raises(ML.DecodeError) as e:
+            call(**bad)
+        assert e.value.status == ML.DEC_ERR_INVALID_ARG
+    with pytest.raises(ValueError):
+        ML.decode_layer_attention(h, L.w, ML.LayerAttention(4, 0.125, ML.KvCache(pool, pool), batch, one, one),
+                                  torch.zeros((2, H), dtype=torch.bfloat16, device="cuda"))
+    torch.cuda.synchronize()
