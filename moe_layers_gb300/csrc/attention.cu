@@ -12,6 +12,7 @@
 // took are joined by the combine kernel.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "attention.cuh"
 
@@ -28,23 +29,34 @@ constexpr int kAttnSmem = 115712;
 // requests of 1..4096 tokens: 75.5 us with 0, 57.0 with 1, 55.0 with 2, 55.9
 // with 3; without ragged lengths no difference).
 constexpr int kPieceLead = 2;
+constexpr int kPieceLeadTc = 3;  // 128-key tiles of the tcgen05 kernel
 
-// WK warps share a tile's keys, 4 / WK groups of 16 rows share its rows. HALF:
-// chunks of 8 rows (the lower half of each 16-row product is not used).
-template <int D, int WK, bool HALF>
-struct AttnShape {
-  static constexpr int kWM = 4 / WK;
-  static constexpr int kRows = HALF ? 8 : 16 * kWM;
+// How the four warps share a chunk: WK of them split a tile's keys, 4 / WK
+// groups of 16 rows split its rows. HALF: chunks of 8 rows (the lower half of
+// each 16-row product is not used).
+template <int WK_, bool HALF_>
+struct Rows {
+  static constexpr int WK = WK_, WM = 4 / WK_;
+  static constexpr bool HALF = HALF_;
+  static constexpr int kRows = HALF ? 8 : 16 * WM;
   static constexpr int kKeys = kTileKeys / WK;  // keys of one warp
+  static_assert(!HALF || WK == 4, "a chunk of 8 rows has one group of warps");
+};
+using Rows8 = Rows<4, true>;
+using Rows16 = Rows<4, false>;
+using Rows32 = Rows<2, false>;
+
+// Shared memory of the kernel with chunks RP for the prefix and RO for own tokens.
+template <int D, class RP, class RO>
+struct AttnShape {
   static constexpr int kHalf = kTileKeys * D * 2;  // K or V bytes of a stage
   static constexpr int kStage = 2 * kHalf;
   // sums of the warps that join another at the end of a piece, 8 rows at a time
-  static constexpr int kMerge = (WK - 1) * kWM * 8 * D * 4;
+  static constexpr int kMerge = std::max((RP::WK - 1) * RP::WM, (RO::WK - 1) * RO::WM) * 8 * D * 4;
   static constexpr int kFixed = 1024 + 2048;  // alignment, barriers and tables
   static constexpr int kStages = std::min(12, (kAttnSmem - kFixed - kMerge) / kStage);
   static constexpr int kTotal = kStages * kStage + kMerge + kFixed;
   static_assert(kStages >= 3 && kTotal <= kAttnSmem, "shared memory");
-  static_assert(!HALF || WK == 4, "a chunk of 8 rows has one group of warps");
 };
 
 struct AttnShared {
@@ -78,11 +90,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // sub-tile of 128-byte rows with the 128-byte swizzle.
 __device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-template <int D, int WK, bool HALF>
+template <int D, class RP, class RO>
 __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
     attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                      const __grid_constant__ AttentionLaunch L) {
-  using S = AttnShape<D, WK, HALF>;
+  using S = AttnShape<D, RP, RO>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float2* s_merge = reinterpret_cast<float2*>(smem + S::kStages * S::kStage);  // [warp][D / 8][lane]
@@ -132,9 +144,10 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
         Piece n = q;
         if (keys && u + q.units < u1) {
           n.next(sh.parts, a, L.plan, u + q.units, u1);
-          const int rows = n.empty() ? 0 : min(S::kRows, sh.parts.rows[n.part] * group - n.chunk * S::kRows);
+          const int each = n.part == 0 ? RP::kRows : RO::kRows;
+          const int rows = n.empty() ? 0 : min(each, sh.parts.rows[n.part] * group - n.chunk * each);
           for (int i = lane; i < rows * kSub; i += 32) {
-            const int rr = n.chunk * S::kRows + i / kSub, row = div_group(rr, L.group_mul);
+            const int rr = n.chunk * each + i / kSub, row = div_group(rr, L.group_mul);
             const uint16_t* src = a.q + (long long)(sh.parts.row0[n.part] + row) * a.ldq +
                                   (long long)(n.kvh * group + rr - row * group) * D + (i % kSub) * 64;
             asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
@@ -190,23 +203,37 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
         mbar_wait_drain(&sh.full[i % S::kStages], (i / S::kStages) & 1, L.err, L.wait_ns);
   } else {
     // ------------------------------------------------------------ products
-    const int wk = warp % WK, wm = warp / WK;  // which keys of a tile, which 16 rows of a chunk
     const int g = lane >> 2, t4 = lane & 3;
-    constexpr int NK = S::kKeys / 8;           // 8-key columns of S
-    constexpr int NE = HALF ? 1 : 2;           // this thread's rows: g and g + 8 of the warp's 16
     int s = 0;
     uint32_t phase = 0;
+    long long u = u0;
+    // Every piece from u on in chunks of `shape`: all that are left, or those of the
+    // prefix (which come first); false if a wait gave up.
+    auto run = [&](auto shape, auto prefix_only) -> bool {
+    using R = decltype(shape);
+    constexpr bool kPrefixOnly = decltype(prefix_only)::value;
+    auto mine = [&]() { return u < u1 && !q.empty() && (!kPrefixOnly || q.part == 0); };
+    constexpr int WK = R::WK;
+    constexpr int NK = R::kKeys / 8;       // 8-key columns of S
+    constexpr int NE = R::HALF ? 1 : 2;    // this thread's rows
+    const int wk = warp % WK, wm = warp / WK;  // which keys of a tile, which 16 rows of a chunk
+    // Barriers of the warps that join their sums, apart for the two groupings: a
+    // warp may be in its first own piece while others end their last prefix piece.
+    // (Pieces of the prefix come first, so the sums' memory changes hands only
+    // behind the barrier of all four warps that ends an own piece.)
+    const int bar_end = WK == 4 ? 1 : 3 + wm, bar_sums = WK == 4 ? 2 : 5 + wm;
     uint32_t qf[D / 16][4];
     int sees[NE];
-    // the query fragments of a piece, and the keys that this thread's rows see
+    // the query fragments of a piece (rows g and g + 8 of the warp's 16), and the
+    // keys that this thread's rows see
     auto load_q = [&]() {
       const int len = sh.parts.len[q.part], rows = sh.parts.rows[q.part] * group;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = q.chunk * S::kRows + wm * 16 + g + 8 * e;
+        const int r = q.chunk * R::kRows + wm * 16 + g + 8 * e;
         const bool in = e < NE && r < rows;
         const int row = in ? div_group(r, L.group_mul) : 0;
-        if (e < NE) sees[e] = in ? min(len, q.part == 0 ? len : sh.parts.last[q.part] + row) : 0;
+        if (e < NE) sees[e % NE] = in ? min(len, q.part == 0 ? len : sh.parts.last[q.part] + row) : 0;
         const uint16_t* src = a.q + (long long)(sh.parts.row0[q.part] + row) * a.ldq +
                               (long long)(q.kvh * group + (in ? r - row * group : 0)) * D + 2 * t4;
 #pragma unroll
@@ -216,8 +243,8 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
         }
       }
     };
-    if (u0 < u1) load_q();
-    for (long long u = u0; u < u1 && !q.empty();) {
+    if (mine()) load_q();
+    while (mine()) {
       const int len = sh.parts.len[q.part], rows = sh.parts.rows[q.part] * group;
       float o[D / 8][4], m[NE], l[NE];
 #pragma unroll
@@ -226,16 +253,23 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
       for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
       // the fewest keys that any row of the chunk sees
       const int fewest =
-          q.part == 0 ? len : min(len, sh.parts.last[q.part] + div_group(q.chunk * S::kRows, L.group_mul));
+          q.part == 0 ? len : min(len, sh.parts.last[q.part] + div_group(q.chunk * R::kRows, L.group_mul));
 
+      const int in_chunk = min(R::kRows, rows - q.chunk * R::kRows);
+      const bool busy = wm * 16 < in_chunk;  // else the warp has no row in this chunk
       bool ok = true;
       for (int t = q.tile0; t < q.tile1; ++t) {
         ok = warp_wait(&sh.full[s], phase, wc);
         if (!ok) break;
+        if (WK == 1 && !busy) {
+          if (lane == 0) mbar_arrive(&sh.empty[s]);
+          if (++s == S::kStages) s = 0, phase ^= 1u;
+          continue;
+        }
         const uint32_t kb = smem_u32(smem + s * S::kStage), vb = kb + S::kHalf;
         const int valid = sh.valid[s];
-        const int key0 = t * kTileKeys + wk * S::kKeys;  // the warp's first key
-        const bool edge = key0 + S::kKeys > fewest || valid != 15;
+        const int key0 = t * kTileKeys + wk * R::kKeys;  // the warp's first key
+        const bool edge = key0 + R::kKeys > fewest || valid != 15;
         float p[NK][4];
 #pragma unroll
         for (int j = 0; j < NK; ++j) p[j][0] = p[j][1] = p[j][2] = p[j][3] = 0.f;
@@ -247,7 +281,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             uint32_t b[4];
-            const int kr = wk * S::kKeys + ((lane >> 4) << 3) + (lane & 7);
+            const int kr = wk * R::kKeys + ((lane >> 4) << 3) + (lane & 7);
             const int cv = i * 2 + ((lane >> 3) & 1);
             ldsm4(b, kb + (cv >> 3) * (kTileKeys * 128) + swz(kr, cv & 7));
             mma16816(i & 1 ? p2[0] : p[0], qf[i], b[0], b[1]);
@@ -264,7 +298,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
             for (int j = 0; j < NK / 2; ++j) {
               // matrices: keys 0-7 and 8-15 by elements 0-7 and 8-15 of step i
               uint32_t b[4];
-              const int kr = wk * S::kKeys + j * 16 + ((lane >> 4) << 3) + (lane & 7);
+              const int kr = wk * R::kKeys + j * 16 + ((lane >> 4) << 3) + (lane & 7);
               const int cv = i * 2 + ((lane >> 3) & 1);
               ldsm4(b, kb + (cv >> 3) * (kTileKeys * 128) + swz(kr, cv & 7));
               mma16816(p[2 * j], qf[i], b[0], b[1]);
@@ -276,7 +310,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
           for (int j = 0; j < NK; ++j)
 #pragma unroll
             for (int e = 0; e < 2 * NE; ++e) {
-              const int kk = wk * S::kKeys + j * 8 + 2 * t4 + (e & 1);  // key within the tile
+              const int kk = wk * R::kKeys + j * 8 + 2 * t4 + (e & 1);  // key within the tile
               const bool see = t * kTileKeys + kk < sees[e >> 1] && ((valid >> (kk >> 4)) & 1);
               p[j][e] = see ? p[j][e] : -INFINITY;
             }
@@ -337,7 +371,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
           for (int i = 0; i < D / 16; ++i) {
             // matrices (transposed): keys 0-7 and 8-15 by elements 0-7 and 8-15 of pair i
             uint32_t b[4];
-            const int kr = wk * S::kKeys + j * 16 + (lane & 15);
+            const int kr = wk * R::kKeys + j * 16 + (lane & 15);
             const int cv = i * 2 + (lane >> 4);
             ldsm4_t(b, vb + (cv >> 3) * (kTileKeys * 128) + swz(kr, cv & 7));
             if (edge) {
@@ -356,18 +390,17 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
       }
       // The warps that join their sums leave together if a wait gave up; this
       // barrier also ends the reads of the previous piece's sums.
-      if (WK > 1 ? !named_bar_and(1 + wm, WK * 32, ok) : !ok) break;
+      if (WK > 1 ? !named_bar_and(bar_end, WK * 32, ok) : !ok) return false;
 
       // ---------------------------------------------------------- the piece's rows
       const Piece done = q;
       u += q.units;
       if (u < u1) {  // the next piece's queries are on their way during what follows
         q.next(sh.parts, a, L.plan, u, u1);
-        load_q();
+        if (mine()) load_q();
       }
       const bool begins = done.tile0 == 0;
       const bool direct = begins && done.tile1 == done.tiles && a.prefix_len == 0;
-      const int in_chunk = min(S::kRows, rows - done.chunk * S::kRows);
       const Pieces& keep = begins ? L.start[done.part > 0] : L.plan.rest;
 #pragma unroll
       for (int e = 0; e < NE; ++e) {
@@ -379,15 +412,15 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
         if (WK > 1) {
           // warps 1.. of the group hand their sums to warp 0, fragment by fragment
           float2* mine = s_merge + (wm * (WK - 1) + wk - 1) * (D / 8) * 32 + lane;
-          if (e > 0) named_bar_sync(1 + wm, WK * 32);  // the first half has been read
+          if (e > 0) named_bar_sync(bar_end, WK * 32);  // the first half has been read
           if (wk > 0) {
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) mine[i * 32] = make_float2(o[i][2 * e], o[i][2 * e + 1]);
             if (t4 == 0) sh.ml[warp][g] = make_float2(mt, lt);
-            named_bar_arrive(3 + wm, WK * 32);
+            named_bar_arrive(bar_sums, WK * 32);
             continue;
           }
-          named_bar_sync(3 + wm, WK * 32);
+          named_bar_sync(bar_sums, WK * 32);
           float f[WK], top = mt;
 #pragma unroll
           for (int w = 1; w < WK; ++w) top = fmaxf(top, sh.ml[warp + w][g].x);
@@ -413,7 +446,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
           }
         }
         if (r >= in_chunk) continue;
-        const int rr = done.chunk * S::kRows + r, row = div_group(rr, L.group_mul);
+        const int rr = done.chunk * R::kRows + r, row = div_group(rr, L.group_mul);
         const long long t = sh.parts.row0[done.part] + row;
         const int head = done.kvh * group + rr - row * group;
         if (direct) {
@@ -423,13 +456,20 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
           for (int i = 0; i < D / 8; ++i)
             *reinterpret_cast<uint32_t*>(to + 8 * i) = pack_bf16x2(o[i][2 * e] * inv, o[i][2 * e + 1] * inv);
         } else {
-          const long long at = begins ? t * a.q_heads + head : c * S::kRows + r;
+          const long long at = begins ? t * a.q_heads + head : c * L.plan.rest_rows + r;
           float* to = keep.o + at * D + 2 * t4;
 #pragma unroll
           for (int i = 0; i < D / 8; ++i) *reinterpret_cast<float2*>(to + 8 * i) = make_float2(o[i][2 * e], o[i][2 * e + 1]);
           if (t4 == 0) keep.ml[at] = make_float2(mt, lt);
         }
       }
+    }
+    return true;
+    };
+    if constexpr (std::is_same<RP, RO>::value) {
+      run(RO(), std::false_type());
+    } else {
+      if (run(RP(), std::true_type())) run(RO(), std::false_type());
     }
   }
   if (L.late_wait) pdl_wait();
@@ -481,11 +521,12 @@ __global__ void __launch_bounds__(256, 4) join_attention_kernel(const __grid_con
     const long long W = T.first[a.requests + 1], G = plan_ctas(W, L.plan.ctas);
     const long long tiles = ((long long)T.len[i] + (1 << L.plan.tile_shift) - 1) >> L.plan.tile_shift;
     if (T.first[i + 1] == T.first[i]) return s;
-    const int chunks = (T.rows[i] * group + L.plan.rows - 1) / L.plan.rows;
+    const int each = L.plan.rows[i > 0];
+    const int chunks = (T.rows[i] * group + each - 1) / each;
     const int rr = (t - T.row0[i]) * group + head - kvh * group;
-    const int chunk = rr / L.plan.rows;
+    const int chunk = rr / each;
     const long long u = T.first[i] + ((long long)kvh * chunks + chunk) * (tiles + L.plan.lead) + L.plan.lead;
-    s.r = rr - chunk * L.plan.rows;
+    s.r = rr - chunk * each;
     s.c0 = (int)cta_of_unit(u, W, G);
     s.count = (int)cta_of_unit(u + tiles - 1, W, G) - s.c0 + 1;
     return s;
@@ -517,7 +558,7 @@ __global__ void __launch_bounds__(256, 4) join_attention_kernel(const __grid_con
         const int j = pre ? i : i - sp.count;
         const Span& s = pre ? sp : so;
         const Pieces& from = j == 0 ? O.start[pre ? 0 : 1] : (pre ? P.plan.rest : O.plan.rest);
-        const long long at = j == 0 ? s.at : (long long)(s.c0 + j) * (pre ? P.plan.rows : O.plan.rows) + s.r;
+        const long long at = j == 0 ? s.at : (long long)(s.c0 + j) * (pre ? P.plan.rest_rows : O.plan.rest_rows) + s.r;
         const uint2 raw = ld_act8(from.ml + at);
         ml[k] = make_float2(__uint_as_float(raw.x), __uint_as_float(raw.y));
         if (V == 4) {
@@ -567,17 +608,7 @@ __global__ void __launch_bounds__(256, 4) join_attention_kernel(const __grid_con
 // ---------------------------------------------------------------------------- host side
 namespace {
 
-// The chunk kernel for `rows` query rows of a key head: the smallest that holds
-// them. Above 64 rows (and from DEC_TC_ROWS on) the tcgen05 kernel.
-#ifndef DEC_TC_ROWS
-#define DEC_TC_ROWS 65
-#endif
-Plan chunk_plan(const dec_handle* h, int rows, bool prefix, bool own, const Pieces& rest) {
-  const int kPieceLeadTc = 3;
-  if (rows >= DEC_TC_ROWS) return Plan{prefix, own, rows <= 128 ? 128 : 256, kPieceLeadTc, 7, h->sms, rest};
-  return Plan{prefix, own, rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64, kPieceLead, 6,
-              h->sms * kAttnCtasPerSm, rest};
-}
+int chunk_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 
 struct AttnWs {
   Pieces start[2], rest[2];
@@ -620,32 +651,47 @@ bool encode_cache(const dec_handle* h, CUtensorMap* m, const uint16_t* base, con
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int WK, bool HALF>
+template <int D, class RP, class RO>
 cudaError_t launch_shape(dec_handle* h, const CUtensorMap& tk, const CUtensorMap& tv, const AttentionLaunch& L,
                          cudaStream_t s) {
-  using S = AttnShape<D, WK, HALF>;
+  using S = AttnShape<D, RP, RO>;
   static std::atomic<uint64_t> ready{0};  // devices whose function attribute is set
   const uint64_t bit = 1ull << (h->device & 63);
   if (!(ready.load() & bit)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(attention_kernel<D, WK, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kTotal);
+        cudaFuncSetAttribute(attention_kernel<D, RP, RO>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kTotal);
     if (e != cudaSuccess) return e;
     if (h->device < 64) ready.fetch_or(bit);
   }
-  return launch_k(h, attention_kernel<D, WK, HALF>, dim3(L.plan.ctas), dim3(kAttnThreads), (size_t)S::kTotal, s, tk, tv, L);
+  return launch_k(h, attention_kernel<D, RP, RO>, dim3(L.plan.ctas), dim3(kAttnThreads), (size_t)S::kTotal, s, tk, tv, L);
+}
+
+// Own chunks RO; the prefix in the same chunks or in those that hold more rows.
+template <int D, class RO>
+cudaError_t launch_own(dec_handle* h, const CUtensorMap& tk, const CUtensorMap& tv, const AttentionLaunch& L,
+                       cudaStream_t s) {
+  const int pre = L.plan.prefix ? L.plan.rows[0] : RO::kRows;
+  if constexpr (RO::kRows < 16)
+    if (pre == 16) return launch_shape<D, Rows16, RO>(h, tk, tv, L, s);
+  if constexpr (RO::kRows < 32)
+    if (pre == 32) return launch_shape<D, Rows32, RO>(h, tk, tv, L, s);
+  return launch_shape<D, RO, RO>(h, tk, tv, L, s);
+}
+
+template <int D>
+cudaError_t launch_mma(dec_handle* h, const CUtensorMap& tk, const CUtensorMap& tv, const AttentionLaunch& L,
+                       cudaStream_t s) {
+  switch (L.plan.rows[1]) {
+    case 8: return launch_own<D, Rows8>(h, tk, tv, L, s);
+    case 16: return launch_own<D, Rows16>(h, tk, tv, L, s);
+    default: return launch_own<D, Rows32>(h, tk, tv, L, s);
+  }
 }
 
 cudaError_t launch_chunks(dec_handle* h, const CUtensorMap& tk, const CUtensorMap& tv, const AttentionLaunch& L,
                           cudaStream_t s) {
-  const bool d64 = L.a.dim == 64;
-  switch (L.plan.rows) {
-    case 8: return d64 ? launch_shape<64, 4, true>(h, tk, tv, L, s) : launch_shape<128, 4, true>(h, tk, tv, L, s);
-    case 16: return d64 ? launch_shape<64, 4, false>(h, tk, tv, L, s) : launch_shape<128, 4, false>(h, tk, tv, L, s);
-    case 32: return d64 ? launch_shape<64, 2, false>(h, tk, tv, L, s) : launch_shape<128, 2, false>(h, tk, tv, L, s);
-    case 128:
-    case 256: return launch_attention_tc(h, tk, tv, L, s);
-    default: return d64 ? launch_shape<64, 1, false>(h, tk, tv, L, s) : launch_shape<128, 1, false>(h, tk, tv, L, s);
-  }
+  if (L.plan.tile_shift == 7) return launch_attention_tc(h, tk, tv, L, s);
+  return L.a.dim == 64 ? launch_mma<64>(h, tk, tv, L, s) : launch_mma<128>(h, tk, tv, L, s);
 }
 
 // Rows of a joining CTA: 8 (a warp each) from 2432 rows on, where one wave of
@@ -679,21 +725,40 @@ cudaError_t launch_attention(dec_handle* h, const AttentionParams& P, void* ws, 
   own.group_mul = (uint32_t)(((1 << 20) + group - 1) / group);
   own.err = h->d_err;
   own.wait_ns = h->wait_ns;
-  own.plan = chunk_plan(h, std::min(P.max_new, P.M) * group, false, true, w.rest[1]);
+  // Query rows of a key head: of all requests on the prefix, and of one request.
+  const int rows_p = P.M * group, rows_o = std::min(P.max_new, P.M) * group;
+  const long long prefix_tiles = (long long)P.kv_heads * (((long long)P.prefix_len + 63) / 64);
+  // tcgen05 for requests of more than 32 query rows to a key head (4 requests of 16
+  // drafts by 4 heads, 16000 tokens each: 96 us, in chunks of 32 rows 162 us; 1000
+  // tokens each: 19.3 and 18.3 us), and for a prefix of more than 32 rows and 40
+  // 64-key tiles of 32 rows an SM (64 heads on 16, own tokens 500 each, tcgen05
+  // against chunks of 32 in one launch with the own tokens: 16 requests, 8192
+  // tokens 41 and 36 us, 32768 tokens 72 and 97; 32 requests, 2048 tokens 46 and
+  // 39, 8192 tokens 56 and 60; 64 requests, 2048 tokens 72 and 68, 8192 82 and 109).
+  const bool tc_own = rows_o > 32;
+  const bool tc_prefix =
+      P.prefix_len > 0 && rows_p > 32 && (tc_own || prefix_tiles * ((rows_p + 31) / 32) >= 40LL * h->sms);
+  auto mma_plan = [&](bool prefix, bool own, const Pieces& rest) {
+    Plan p{prefix, own, {0, chunk_rows(rows_o)}, 0, kPieceLead, 6, h->sms * kAttnCtasPerSm, rest};
+    p.rows[0] = std::max(p.rows[1], chunk_rows(rows_p));
+    p.rest_rows = prefix ? p.rows[0] : p.rows[1];
+    return p;
+  };
+  auto tc_plan = [&](bool prefix, bool own, const Pieces& rest) {
+    const int rows = (prefix ? rows_p : rows_o) <= 128 ? 128 : 256;
+    return Plan{prefix, own, {rows, rows}, rows, kPieceLeadTc, 7, h->sms, rest};
+  };
   AttentionLaunch pre = own;
-  pre.plan = chunk_plan(h, P.M * group, P.prefix_len > 0, false, w.rest[0]);
   cudaError_t e = cudaSuccess;
-  if (P.prefix_len > 0) {
-    if (pre.plan.rows == own.plan.rows) {
-      // the same kernel: one launch takes both
-      own.plan.prefix = true;
-      pre.plan = own.plan;
-    } else {
-      LaunchScope scope(h, "attention_prefix", s);
-      e = launch_chunks(h, tk, tv, pre, s);
-      if (e != cudaSuccess) return e;
-      own.late_wait = own.plan.tile_shift == 6;
-    }
+  const bool apart = tc_prefix && !tc_own;  // a launch for the prefix, one for the own tokens
+  own.plan = tc_own ? tc_plan(P.prefix_len > 0, true, w.rest[1]) : mma_plan(P.prefix_len > 0 && !apart, true, w.rest[1]);
+  pre.plan = own.plan;
+  if (apart) {
+    pre.plan = tc_plan(true, false, w.rest[0]);
+    LaunchScope scope(h, "attention_prefix", s);
+    e = launch_chunks(h, tk, tv, pre, s);
+    if (e != cudaSuccess) return e;
+    own.late_wait = true;
   }
   {
     LaunchScope scope(h, "attention", s);

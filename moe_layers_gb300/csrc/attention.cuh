@@ -34,11 +34,12 @@ struct Pieces {
 // One launch's share of the plan.
 struct Plan {
   bool prefix, own;  // which parts the launch takes
-  int rows;         // query rows of a chunk
+  int rows[2];      // query rows of a chunk: prefix, own
+  int rest_rows;    // rows of a piece in `rest`
   int lead;         // units a (head, chunk) counts for besides its tiles
   int tile_shift;   // a tile is 1 << tile_shift keys
   int ctas;
-  Pieces rest;      // [ctas][rows]
+  Pieces rest;      // [ctas][rest_rows]
 };
 
 struct AttentionLaunch {
@@ -103,7 +104,7 @@ __device__ __forceinline__ void build_parts(PartTable& t, const AttentionParams&
       t.len[i] = len;
       t.last[i] = last;
       if (i == 0 ? p.prefix : p.own) {
-        const int chunks = (rows * group + p.rows - 1) / p.rows;
+        const int each = p.rows[i > 0], chunks = (rows * group + each - 1) / each;
         const long long tiles = ((long long)len + (1 << p.tile_shift) - 1) >> p.tile_shift;
         units = tiles > 0 ? (long long)a.kv_heads * chunks * (tiles + p.lead) : 0;
       }
@@ -126,7 +127,8 @@ struct Piece {
   int part = 0, kvh = 0, chunk = 0, chunks = 1, tiles = 0, tile0 = 0, tile1 = 0, units = 0;
   __device__ __forceinline__ bool empty() const { return tile1 <= tile0; }
   __device__ __forceinline__ void enter(const PartTable& t, const AttentionParams& a, const Plan& p) {
-    chunks = (t.rows[part] * (a.q_heads / a.kv_heads) + p.rows - 1) / p.rows;
+    const int each = p.rows[part > 0];
+    chunks = (t.rows[part] * (a.q_heads / a.kv_heads) + each - 1) / each;
     tiles = (int)(((long long)t.len[part] + (1 << p.tile_shift) - 1) >> p.tile_shift);
   }
   __device__ __forceinline__ void cut(const Plan& p, int x0, long long room) {

@@ -543,7 +543,7 @@ cudaError_t launch_shape(dec_handle* h, const CUtensorMap& tk, const CUtensorMap
 
 cudaError_t launch_attention_tc(dec_handle* h, const CUtensorMap& tk, const CUtensorMap& tv, const AttentionLaunch& L,
                                 cudaStream_t s) {
-  const bool two = L.plan.rows > 128;
+  const bool two = L.plan.rows[0] > 128;
   if (L.a.dim == 64) return two ? launch_shape<64, 2>(h, tk, tv, L, s) : launch_shape<64, 1>(h, tk, tv, L, s);
   return two ? launch_shape<128, 2>(h, tk, tv, L, s) : launch_shape<128, 1>(h, tk, tv, L, s);
 }
