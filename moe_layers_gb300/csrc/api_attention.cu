@@ -68,6 +68,7 @@ static AttentionParams attention_params(const uint16_t* q, long long ldq, const 
   while ((1 << P.shift) < cache.block_size) ++P.shift;
   P.kv_heads = cache.kv_heads;
   P.q_heads = q_heads;
+  P.group = q_heads / cache.kv_heads;
   P.dim = cache.head_dim;
   P.requests = batch.requests;
   P.max_new = batch.max_new;

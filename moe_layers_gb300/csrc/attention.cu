@@ -53,14 +53,15 @@ struct AttnShape {
   static constexpr int kStage = 2 * kHalf;
   // sums of the warps that join another at the end of a piece, 8 rows at a time
   static constexpr int kMerge = std::max((RP::WK - 1) * RP::WM, (RO::WK - 1) * RO::WM) * 8 * D * 4;
+  static constexpr int kQ = RO::HALF ? 8 * D * 2 : 0;  // query rows of 8-row chunks
   static constexpr int kFixed = 1024 + 2048;  // alignment, barriers and tables
-  static constexpr int kStages = std::min(12, (kAttnSmem - kFixed - kMerge) / kStage);
-  static constexpr int kTotal = kStages * kStage + kMerge + kFixed;
+  static constexpr int kStages = std::min(12, (kAttnSmem - kFixed - kMerge - kQ) / kStage);
+  static constexpr int kTotal = kStages * kStage + kMerge + kQ + kFixed;
   static_assert(kStages >= 3 && kTotal <= kAttnSmem, "shared memory");
 };
 
 struct AttnShared {
-  uint64_t full[12], empty[12];
+  uint64_t full[12], empty[12], qfull;
   PartTable parts;
   float2 ml[4][8];
   uint8_t valid[12];  // per stage: which 16-key quarters lie in blocks of the cache
@@ -98,16 +99,18 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float2* s_merge = reinterpret_cast<float2*>(smem + S::kStages * S::kStage);  // [warp][D / 8][lane]
-  AttnShared& sh = *reinterpret_cast<AttnShared*>(smem + S::kStages * S::kStage + S::kMerge);
+  uint8_t* s_q = smem + S::kStages * S::kStage + S::kMerge;  // [D / 64][8 rows][128 bytes], swizzled
+  AttnShared& sh = *reinterpret_cast<AttnShared*>(s_q + S::kQ);
   const AttentionParams& a = L.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int group = a.q_heads / a.kv_heads;
+  const int group = a.group;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&sh.full[i], 2);
       mbar_init(&sh.empty[i], 4);
     }
+    mbar_init(&sh.qfull, 128);
     sh.abort = 0;
     fence_mbar_init();
     tmap_prefetch(&tk);
@@ -224,24 +227,66 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
     const int bar_end = WK == 4 ? 1 : 3 + wm, bar_sums = WK == 4 ? 2 : 5 + wm;
     uint32_t qf[D / 16][4];
     int sees[NE];
-    // the query fragments of a piece (rows g and g + 8 of the warp's 16), and the
-    // keys that this thread's rows see
-    auto load_q = [&]() {
+    // the keys that this thread's rows (g and g + 8 of the warp's 16) see
+    auto look = [&]() {
       const int len = sh.parts.len[q.part], rows = sh.parts.rows[q.part] * group;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < NE; ++e) {
         const int r = q.chunk * R::kRows + wm * 16 + g + 8 * e;
-        const bool in = e < NE && r < rows;
-        const int row = in ? div_group(r, L.group_mul) : 0;
-        if (e < NE) sees[e % NE] = in ? min(len, q.part == 0 ? len : sh.parts.last[q.part] + row) : 0;
-        const uint16_t* src = a.q + (long long)(sh.parts.row0[q.part] + row) * a.ldq +
-                              (long long)(q.kvh * group + (in ? r - row * group : 0)) * D + 2 * t4;
+        sees[e] = r >= rows ? 0 : min(len, q.part == 0 ? len : sh.parts.last[q.part] + div_group(r, L.group_mul));
+      }
+    };
+    auto q_row = [&](int r) {  // row r of the part
+      const int row = div_group(r, L.group_mul);
+      return a.q + (long long)(sh.parts.row0[q.part] + row) * a.ldq + (long long)(q.kvh * group + r - row * group) * D;
+    };
+    // A piece's queries on their way: to fragments in registers (4 bytes a read),
+    // or for 8 rows by one asynchronous 16-byte copy a thread to shared memory,
+    // which all four warps read as fragments (fetch_q): 32 reads a thread fewer
+    // in every piece.
+    auto load_q = [&]() {
+      const int rows = sh.parts.rows[q.part] * group;
+      if constexpr (R::HALF) {
+        if (threadIdx.x < D) {
+          const int i = threadIdx.x / (D / 8), v = threadIdx.x % (D / 8), r = q.chunk * 8 + i;
+          const bool in = r < rows;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                           smem_u32(s_q + (v >> 3) * 1024) + swz(i, v & 7)),
+                       "l"(q_row(in ? r : 0) + v * 8), "r"(in ? 16 : 0)
+                       : "memory");
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sh.qfull)) : "memory");
+      } else {
+        look();
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          qf[i][e] = in ? (uint32_t)ld_act_s32(src + i * 16) : 0u;
-          qf[i][e + 2] = in ? (uint32_t)ld_act_s32(src + i * 16 + 8) : 0u;
+        for (int e = 0; e < 2; ++e) {
+          const int r = q.chunk * R::kRows + wm * 16 + g + 8 * e;
+          const bool in = r < rows;
+          const uint16_t* src = q_row(in ? r : 0) + 2 * t4;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            qf[i][e] = in ? (uint32_t)ld_act_s32(src + i * 16) : 0u;
+            qf[i][e + 2] = in ? (uint32_t)ld_act_s32(src + i * 16 + 8) : 0u;
+          }
         }
       }
+    };
+    uint32_t qphase = 0;
+    auto fetch_q = [&]() -> bool {
+      if constexpr (R::HALF) {
+        look();
+        if (!warp_wait(&sh.qfull, qphase, wc)) return false;
+        qphase ^= 1u;
+#pragma unroll
+        for (int i = 0; i < D / 16; i += 2) {
+          uint32_t b[4];  // elements 0-7 and 8-15 of steps i and i + 1
+          const int cv = 2 * i + (lane >> 3);
+          ldsm4(b, smem_u32(s_q + (cv >> 3) * 1024) + swz(lane & 7, cv & 7));
+          qf[i][0] = b[0], qf[i][2] = b[1], qf[i][1] = qf[i][3] = 0u;
+          qf[i + 1][0] = b[2], qf[i + 1][2] = b[3], qf[i + 1][1] = qf[i + 1][3] = 0u;
+        }
+      }
+      return true;
     };
     if (mine()) load_q();
     while (mine()) {
@@ -256,16 +301,10 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
           q.part == 0 ? len : min(len, sh.parts.last[q.part] + div_group(q.chunk * R::kRows, L.group_mul));
 
       const int in_chunk = min(R::kRows, rows - q.chunk * R::kRows);
-      const bool busy = wm * 16 < in_chunk;  // else the warp has no row in this chunk
-      bool ok = true;
-      for (int t = q.tile0; t < q.tile1; ++t) {
+      bool ok = fetch_q();
+      for (int t = q.tile0; ok && t < q.tile1; ++t) {
         ok = warp_wait(&sh.full[s], phase, wc);
         if (!ok) break;
-        if (WK == 1 && !busy) {
-          if (lane == 0) mbar_arrive(&sh.empty[s]);
-          if (++s == S::kStages) s = 0, phase ^= 1u;
-          continue;
-        }
         const uint32_t kb = smem_u32(smem + s * S::kStage), vb = kb + S::kHalf;
         const int valid = sh.valid[s];
         const int key0 = t * kTileKeys + wk * R::kKeys;  // the warp's first key
@@ -471,6 +510,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
     } else {
       if (run(RP(), std::true_type())) run(RO(), std::false_type());
     }
+    cp_async_wait_all();  // none in flight at exit
   }
   if (L.late_wait) pdl_wait();
 }
@@ -490,7 +530,7 @@ __global__ void __launch_bounds__(256, 4) join_attention_kernel(const __grid_con
   __shared__ float2 s_ml[8];
   const AttentionParams& a = O.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int group = a.q_heads / a.kv_heads;
+  const int group = a.group;
   // The launch before this one starts its dependents after its own wait, so
   // the lengths are final here; its pieces are not until pdl_wait().
   if (warp == 0) build_parts(to, O.a, O.plan);
@@ -521,14 +561,13 @@ __global__ void __launch_bounds__(256, 4) join_attention_kernel(const __grid_con
     const long long W = T.first[a.requests + 1], G = plan_ctas(W, L.plan.ctas);
     const long long tiles = ((long long)T.len[i] + (1 << L.plan.tile_shift) - 1) >> L.plan.tile_shift;
     if (T.first[i + 1] == T.first[i]) return s;
-    const int each = L.plan.rows[i > 0];
-    const int chunks = (T.rows[i] * group + each - 1) / each;
+    const int shift = L.plan.row_shift[i > 0];
     const int rr = (t - T.row0[i]) * group + head - kvh * group;
-    const int chunk = rr / each;
-    const long long u = T.first[i] + ((long long)kvh * chunks + chunk) * (tiles + L.plan.lead) + L.plan.lead;
-    s.r = rr - chunk * each;
-    s.c0 = (int)cta_of_unit(u, W, G);
-    s.count = (int)cta_of_unit(u + tiles - 1, W, G) - s.c0 + 1;
+    const int chunk = rr >> shift;
+    const long long u = T.first[i] + ((long long)kvh * T.chunks[i] + chunk) * (tiles + L.plan.lead) + L.plan.lead;
+    s.r = rr - (chunk << shift);
+    s.c0 = cta_of_unit(u, W, G);
+    s.count = cta_of_unit(u + tiles - 1, W, G) - s.c0 + 1;
     return s;
   };
   Span sp{0, 0, 0, 0}, so{0, 0, 0, 0};
@@ -608,7 +647,7 @@ __global__ void __launch_bounds__(256, 4) join_attention_kernel(const __grid_con
 // ---------------------------------------------------------------------------- host side
 namespace {
 
-int chunk_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+int chunk_shift(int rows) { return rows <= 8 ? 3 : rows <= 16 ? 4 : 5; }
 
 struct AttnWs {
   Pieces start[2], rest[2];
@@ -670,7 +709,7 @@ cudaError_t launch_shape(dec_handle* h, const CUtensorMap& tk, const CUtensorMap
 template <int D, class RO>
 cudaError_t launch_own(dec_handle* h, const CUtensorMap& tk, const CUtensorMap& tv, const AttentionLaunch& L,
                        cudaStream_t s) {
-  const int pre = L.plan.prefix ? L.plan.rows[0] : RO::kRows;
+  const int pre = L.plan.prefix ? 1 << L.plan.row_shift[0] : RO::kRows;
   if constexpr (RO::kRows < 16)
     if (pre == 16) return launch_shape<D, Rows16, RO>(h, tk, tv, L, s);
   if constexpr (RO::kRows < 32)
@@ -681,7 +720,7 @@ cudaError_t launch_own(dec_handle* h, const CUtensorMap& tk, const CUtensorMap& 
 template <int D>
 cudaError_t launch_mma(dec_handle* h, const CUtensorMap& tk, const CUtensorMap& tv, const AttentionLaunch& L,
                        cudaStream_t s) {
-  switch (L.plan.rows[1]) {
+  switch (1 << L.plan.row_shift[1]) {
     case 8: return launch_own<D, Rows8>(h, tk, tv, L, s);
     case 16: return launch_own<D, Rows16>(h, tk, tv, L, s);
     default: return launch_own<D, Rows32>(h, tk, tv, L, s);
@@ -739,14 +778,14 @@ cudaError_t launch_attention(dec_handle* h, const AttentionParams& P, void* ws, 
   const bool tc_prefix =
       P.prefix_len > 0 && rows_p > 32 && (tc_own || prefix_tiles * ((rows_p + 31) / 32) >= 40LL * h->sms);
   auto mma_plan = [&](bool prefix, bool own, const Pieces& rest) {
-    Plan p{prefix, own, {0, chunk_rows(rows_o)}, 0, kPieceLead, 6, h->sms * kAttnCtasPerSm, rest};
-    p.rows[0] = std::max(p.rows[1], chunk_rows(rows_p));
-    p.rest_rows = prefix ? p.rows[0] : p.rows[1];
+    Plan p{prefix, own, {chunk_shift(std::max(rows_o, rows_p)), chunk_shift(rows_o)}, 0, kPieceLead, 6,
+           h->sms * kAttnCtasPerSm, rest};
+    p.rest_rows = 1 << p.row_shift[!prefix];
     return p;
   };
   auto tc_plan = [&](bool prefix, bool own, const Pieces& rest) {
-    const int rows = (prefix ? rows_p : rows_o) <= 128 ? 128 : 256;
-    return Plan{prefix, own, {rows, rows}, rows, kPieceLeadTc, 7, h->sms, rest};
+    const int shift = (prefix ? rows_p : rows_o) <= 128 ? 7 : 8;
+    return Plan{prefix, own, {shift, shift}, 1 << shift, kPieceLeadTc, 7, h->sms, rest};
   };
   AttentionLaunch pre = own;
   cudaError_t e = cudaSuccess;

@@ -34,7 +34,7 @@ struct Pieces {
 // One launch's share of the plan.
 struct Plan {
   bool prefix, own;  // which parts the launch takes
-  int rows[2];      // query rows of a chunk: prefix, own
+  int row_shift[2]; // a chunk is 1 << row_shift query rows: prefix, own
   int rest_rows;    // rows of a piece in `rest`
   int lead;         // units a (head, chunk) counts for besides its tiles
   int tile_shift;   // a tile is 1 << tile_shift keys
@@ -55,7 +55,7 @@ struct AttentionLaunch {
 
 struct PartTable {
   long long first[kMaxParts + 1];  // first unit; first[n] = all units
-  short row0[kMaxParts], rows[kMaxParts];
+  short row0[kMaxParts], rows[kMaxParts], chunks[kMaxParts];
   int len[kMaxParts];
   int last[kMaxParts];  // keys that the part's first row sees; each further row sees one more (own parts)
 };
@@ -63,8 +63,23 @@ struct PartTable {
 // CTAs that take part: none without a unit, so that the pieces of a (head,
 // chunk) lie in consecutive CTAs.
 __device__ __forceinline__ long long plan_ctas(long long W, int ctas) { return W < 1 ? 1 : W < ctas ? W : ctas; }
-__device__ __forceinline__ long long unit_start(long long c, long long W, long long G) { return c * W / G; }
-__device__ __forceinline__ long long cta_of_unit(long long u, long long W, long long G) { return ((u + 1) * G - 1) / W; }
+// c W / G, rounded down (an approximate quotient and exact products).
+__device__ __forceinline__ long long unit_start(long long c, long long W, long long G) {
+  const long long x = c * W;
+  if (x >> 40) return x / G;
+  long long q = (long long)((float)x / (float)G);  // off by at most x / G 2^-22 + 1
+  const long long e = x - q * G;
+  if (e < 0 || e >= G) q += e >= 0 ? (int)((uint32_t)e / (uint32_t)G) : -(int)((uint32_t)(G - 1 - e) / (uint32_t)G);
+  return q;
+}
+// The c with unit_start(c) <= u < unit_start(c + 1), that is c W < (u + 1) G <= (c + 1) W.
+__device__ __forceinline__ int cta_of_unit(long long u, long long W, long long G) {
+  const long long x = (u + 1) * G;
+  int c = (int)((float)x / (float)W);
+  while (c * W >= x) --c;
+  while ((c + 1) * W < x) ++c;
+  return c;
+}
 
 // r / group for 0 <= r < 64 group, group <= 128, by a product: mul = ceil(2^20 / group).
 __device__ __forceinline__ int div_group(int r, uint32_t mul) { return (int)(((uint32_t)r * mul) >> 20); }
@@ -74,7 +89,6 @@ __device__ __forceinline__ int div_group(int r, uint32_t mul) { return (int)(((u
 __device__ __forceinline__ void build_parts(PartTable& t, const AttentionParams& a, const Plan& p) {
   constexpr int kRounds = (kMaxParts + 31) / 32;
   const int lane = threadIdx.x & 31, n = a.requests + 1;
-  const int group = a.q_heads / a.kv_heads;
   int r0[kRounds], r1[kRounds], own[kRounds];
 #pragma unroll
   for (int k = 0; k < kRounds; ++k) {  // every load before any use
@@ -104,7 +118,8 @@ __device__ __forceinline__ void build_parts(PartTable& t, const AttentionParams&
       t.len[i] = len;
       t.last[i] = last;
       if (i == 0 ? p.prefix : p.own) {
-        const int each = p.rows[i > 0], chunks = (rows * group + each - 1) / each;
+        const int shift = p.row_shift[i > 0], chunks = (rows * a.group + (1 << shift) - 1) >> shift;
+        t.chunks[i] = (short)chunks;
         const long long tiles = ((long long)len + (1 << p.tile_shift) - 1) >> p.tile_shift;
         units = tiles > 0 ? (long long)a.kv_heads * chunks * (tiles + p.lead) : 0;
       }
@@ -126,9 +141,8 @@ __device__ __forceinline__ void build_parts(PartTable& t, const AttentionParams&
 struct Piece {
   int part = 0, kvh = 0, chunk = 0, chunks = 1, tiles = 0, tile0 = 0, tile1 = 0, units = 0;
   __device__ __forceinline__ bool empty() const { return tile1 <= tile0; }
-  __device__ __forceinline__ void enter(const PartTable& t, const AttentionParams& a, const Plan& p) {
-    const int each = p.rows[part > 0];
-    chunks = (t.rows[part] * (a.q_heads / a.kv_heads) + each - 1) / each;
+  __device__ __forceinline__ void enter(const PartTable& t, const Plan& p) {
+    chunks = t.chunks[part];
     tiles = (int)(((long long)t.len[part] + (1 << p.tile_shift) - 1) >> p.tile_shift);
   }
   __device__ __forceinline__ void cut(const Plan& p, int x0, long long room) {
@@ -138,12 +152,18 @@ struct Piece {
   }
   __device__ __forceinline__ void begin(const PartTable& t, const AttentionParams& a, const Plan& p, long long u,
                                         long long u_end) {
-    while (t.first[part + 1] <= u) ++part;
-    enter(t, a, p);
+    // the part that holds unit u (all lanes of a warp, the same u)
+#pragma unroll
+    for (int k = 0; k < (kMaxParts + 31) / 32; ++k) {
+      const int i = k * 32 + (threadIdx.x & 31);
+      const uint32_t hit = __ballot_sync(0xffffffffu, i <= a.requests && t.first[i] <= u && u < t.first[i + 1]);
+      if (hit) part = k * 32 + __ffs(hit) - 1;
+    }
+    enter(t, p);
     const long long at = u - t.first[part];
     const int each = tiles + p.lead;
     const int hc = (at >> 32) == 0 ? (int)((uint32_t)at / (uint32_t)each) : (int)(at / each);
-    kvh = hc / chunks;
+    kvh = chunks == 1 ? hc : hc / chunks;
     chunk = hc - kvh * chunks;
     cut(p, (int)(at - (long long)hc * each), u_end - u);
   }
@@ -156,7 +176,7 @@ struct Piece {
         kvh = 0;
         do ++part;
         while (t.first[part + 1] <= u);
-        enter(t, a, p);
+        enter(t, p);
       }
     }
     cut(p, 0, u_end - u);

@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   TcShared& sh = *reinterpret_cast<TcShared*>(s_v + S::kV * S::kTileBytes);
   const AttentionParams& a = L.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int group = a.q_heads / a.kv_heads;
+  const int group = a.group;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 6; ++i) {
@@ -543,7 +543,7 @@ cudaError_t launch_shape(dec_handle* h, const CUtensorMap& tk, const CUtensorMap
 
 cudaError_t launch_attention_tc(dec_handle* h, const CUtensorMap& tk, const CUtensorMap& tv, const AttentionLaunch& L,
                                 cudaStream_t s) {
-  const bool two = L.plan.rows[0] > 128;
+  const bool two = L.plan.rest_rows > 128;
   if (L.a.dim == 64) return two ? launch_shape<64, 2>(h, tk, tv, L, s) : launch_shape<64, 1>(h, tk, tv, L, s);
   return two ? launch_shape<128, 2>(h, tk, tv, L, s) : launch_shape<128, 1>(h, tk, tv, L, s);
 }

@@ -194,7 +194,7 @@ struct AttentionParams {
   const uint16_t *k, *v;
   long long block_stride;
   int blocks, shift;  // block_size = 1 << shift
-  int kv_heads, q_heads, dim;
+  int kv_heads, q_heads, dim, group;  // group = q_heads / kv_heads
   int requests, max_new, max_blocks, prefix_len, M;
   const int32_t *row_start, *own_len, *block_table, *prefix_table;
   float scale;
