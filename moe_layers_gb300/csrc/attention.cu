@@ -29,7 +29,10 @@ constexpr int kAttnSmem = 115712;
 // requests of 1..4096 tokens: 75.5 us with 0, 57.0 with 1, 55.0 with 2, 55.9
 // with 3; without ragged lengths no difference).
 constexpr int kPieceLead = 2;
-constexpr int kPieceLeadTc = 3;  // 128-key tiles of the tcgen05 kernel
+// The same of the tcgen05 kernel, in its 128-key tiles (64 requests on 32768
+// shared tokens: 104 us with 3, 101 with 5 and 6; 4 requests of 16 drafts at 1000
+// tokens: 19.2, 19.9 and 20.4).
+constexpr int kPieceLeadTc = 5;
 
 // How the four warps share a chunk: WK of them split a tile's keys, 4 / WK
 // groups of 16 rows split its rows. HALF: chunks of 8 rows (the lower half of
@@ -137,6 +140,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
     const int box = min(1 << a.shift, kTileKeys);  // keys of one box
     const int per = kTileKeys / box;               // boxes (blocks) of a tile
     constexpr int kSub = D / 64;
+    const uint64_t first = policy_evict_first(), normal = policy_evict_normal();
     uint32_t issued = 0;
     int s = 0;
     uint32_t phase = 1;
@@ -159,6 +163,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
       }
       const int len = sh.parts.len[q.part];
       const int32_t* table = q.part == 0 ? a.prefix_table : a.block_table + (long long)(q.part - 1) * a.max_blocks;
+      const uint64_t policy = q.chunks == 1 ? first : normal;
       BlockIds ids(table, (int)(((long long)len + (1 << a.shift) - 1) >> a.shift));
       bool ok = true;
       for (int t = q.tile0; t < q.tile1; ++t) {
@@ -189,7 +194,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
 #pragma unroll
             for (int half = 0; half < kSub; ++half)
               tma_load_3d(dst + half * (kTileKeys * 128) + b * box * 128, keys ? &tk : &tv, &sh.full[su], half * 64, row,
-                          block);
+                          block, policy);
           }
         }
         __syncwarp();

@@ -169,12 +169,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int slots = keys ? S::kK : S::kV;
     const int box = min(1 << a.shift, 64);  // keys of one box
     const int per = kTcTile / box;
+    const uint64_t first = policy_evict_first(), normal = policy_evict_normal();
     uint32_t issued = 0;
     int s = 0;
     uint32_t phase = 1;
     for (long long u = u0; u < u1 && !q.empty();) {
       const int len = sh.parts.len[q.part];
       const int32_t* table = q.part == 0 ? a.prefix_table : a.block_table + (long long)(q.part - 1) * a.max_blocks;
+      const uint64_t policy = q.chunks == 1 ? first : normal;
       BlockIds ids(table, (int)(((long long)len + (1 << a.shift) - 1) >> a.shift));
       bool ok = true;
       for (int t = q.tile0; t < q.tile1; ++t) {
@@ -206,7 +208,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (elect_one()) {
 #pragma unroll
             for (int half = 0; half < kSub; ++half)
-              tma_load_3d(dst + half * (kTcTile * 128) + b * box * 128, keys ? &tk : &tv, &full[su], half * 64, at, block);
+              tma_load_3d(dst + half * (kTcTile * 128) + b * box * 128, keys ? &tk : &tv, &full[su], half * 64, at, block,
+                          policy);
           }
         }
         __syncwarp();
