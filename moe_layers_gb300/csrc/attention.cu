@@ -25,10 +25,10 @@ constexpr int kAttnThreads = 192;  // 4 multiplying warps, one copying K, one co
 // takes for one), and a CTA between two pieces does not stop the SM's stream.
 constexpr int kAttnCtasPerSm = 2;
 constexpr int kAttnSmem = 115712;
-// Tiles that beginning and ending a (head, chunk) costs as much as (61 ragged
-// requests of 1..4096 tokens: 75.5 us with 0, 57.0 with 1, 55.0 with 2, 55.9
-// with 3; without ragged lengths no difference).
-constexpr int kPieceLead = 2;
+// Tiles that beginning and ending a (head, chunk) costs as much as: 0.5 us
+// against 0.78 a tile (61 ragged requests of 1..4096 tokens: 60.9 us with 0, 44.6
+// with 1, 44.8 with 2; without ragged lengths no difference).
+constexpr int kPieceLead = 1;
 // The same of the tcgen05 kernel, in its 128-key tiles (64 requests on 32768
 // shared tokens: 104 us with 3, 101 with 5 and 6; 4 requests of 16 drafts at 1000
 // tokens: 19.2, 19.9 and 20.4).

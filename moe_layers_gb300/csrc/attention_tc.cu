@@ -8,13 +8,17 @@
 //   S = Q K^T (128 x 128, fp32 in TMEM)           tcgen05.mma, Q and K in shared memory
 //   P = 2^(S - m), bf16, over S in TMEM            a thread per row: no shuffles
 //   O += P V (128 x D, fp32 in TMEM)               tcgen05.mma, P from TMEM, V in shared memory
-// and one warp issues the streams' products in turn, so that one stream's
-// products run under the other one's exponentials (with a warp per stream the
-// two fell into step and took turns as a pair: 100 us against N us). The running maximum is raised only when a row's scores
-// pass it by more than 2^8 (P <= 256 then, exact in fp32 sums), so O is read
-// and rescaled a few times, not every tile. K is a K-major operand as it lies
-// in the cache, V an MN-major one: both come by TMA with the 128-byte swizzle,
-// in separate rings that two warps fill.
+// One warp issues the products. With two streams (all of TMEM) it takes them in
+// turn, so that one's products run under the other one's exponentials; with a
+// warp per stream the two fell into step and took turns as a pair (64 requests
+// on 32768 shared tokens: 147 and 124 us). One stream has two buffers of S, and
+// the next tile's scores are there when a softmax ends. (64-key tiles with two
+// buffers for both streams: 113 us where this takes 93; a product of 64 columns
+// reads as much of Q as one of 128.) The running maximum is raised only when a
+// row's scores pass it by more than 2^8 (P <= 256 then, exact in fp32 sums), so O
+// is read and rescaled a few times, not every tile. K is a K-major operand as it
+// lies in the cache, V an MN-major one: both come by TMA with the 128-byte
+// swizzle, in separate rings that two warps fill.
 #include <atomic>
 
 #include "attention.cuh"
@@ -37,16 +41,21 @@ struct TcShape {
   static constexpr int kK = kSlots >= 12 ? 6 : (kSlots + 1) / 2, kV = kSlots >= 12 ? 6 : kSlots / 2;
   static constexpr int kTotal = (kK + kV) * kTileBytes + kQ + kFixed;
   static_assert(kK >= 2 && kV >= 2 && kTotal <= kTcSmem, "shared memory");
-  // TMEM columns: S (P over it) and O of each stream
-  static constexpr uint32_t kS = 0, kO = NT * 128;
-  static constexpr uint32_t kCols = NT == 2 ? 512 : 256;
+  // TMEM columns: S (P over it) in kBuf buffers and O of each stream
+  static constexpr uint32_t kBuf = NT == 1 ? 2 : 1;
+  static constexpr uint32_t kO = 256;
+  static constexpr uint32_t kCols = 512;
+  __device__ static constexpr uint32_t s_col(uint32_t j, uint32_t b) { return (j * kBuf + b) * 128; }
+  // buffer of the c-th tile, and the parity of its barriers' phase
+  __device__ static constexpr uint32_t buf(uint32_t c) { return kBuf == 2 ? c & 1 : 0; }
+  __device__ static constexpr uint32_t phase(uint32_t c) { return kBuf == 2 ? (c >> 1) & 1 : c & 1; }
 };
 
 struct TcShared {
   uint64_t kfull[6], kempty[6], vfull[6], vempty[6];
-  uint64_t sfull[2], pfull[2], pvdone[2], qfull, done;
+  uint64_t sfull[2][2], pfull[2][2], pvdone[2], qfull, done;  // [stream][buffer], [stream]
   PartTable parts;
-  uint8_t valid[8];  // per tile (modulo 8): which 16-key eighths lie in blocks of the cache
+  uint8_t valid[16];  // per tile (modulo 16): which 16-key eighths lie in blocks of the cache
   uint32_t tmem;
   int abort;
 };
@@ -131,8 +140,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&sh.vempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.sfull[i], 1);
-      mbar_init(&sh.pfull[i], 128);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&sh.sfull[i][b], 1);
+        mbar_init(&sh.pfull[i][b], 128);
+      }
       mbar_init(&sh.pvdone[i], 1);
     }
     mbar_init(&sh.done, 1);
@@ -197,7 +208,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (keys) {
             int eighths = 0;
             for (int i = 0; i < 8; ++i) eighths |= ((mask >> (i * 16 / box)) & 1) << i;
-            sh.valid[issued & 7] = (uint8_t)eighths;
+            sh.valid[issued & 15] = (uint8_t)eighths;
           }
           mbar_arrive_expect_tx(&full[su], (uint32_t)(boxes * box * D * 2));
         }
@@ -227,21 +238,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // ------------------------------------------------------------ products
     if (warp == 10) {
       int ks = 0, vs = 0;
-      uint32_t kph = 0, vph = 0, qph = 0, ph = 0;
+      uint32_t kph = 0, vph = 0, qph = 0;
+      uint32_t n = 0;  // tiles so far
       constexpr uint32_t idesc_s = umma_idesc_bf16(128, kTcTile);
       constexpr uint32_t idesc_o = umma_idesc_bf16(128, D) | (1u << 16);  // B is MN-major
-      auto issue_s = [&](int j, int slot) {
-        const int su = uniform(slot);
+      auto issue_s = [&](int j, int slot, uint32_t tile) {
+        const int su = uniform(slot), b = uniform((int)S::buf(tile));
         const uint64_t qd = sw128_desc(smem_u32(s_q) + j * S::kTileBytes);
         const uint64_t kd = sw128_desc(smem_u32(s_k) + su * S::kTileBytes);
-        const uint32_t ts = tmem + S::kS + j * 128;
+        const uint32_t ts = tmem + S::s_col(j, b);
         if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             const uint64_t off = ((i >> 2) * (kTcTile * 128) + (i & 3) * 32) >> 4;  // the descriptors' address unit
             umma_bf16(ts, qd + off, kd + off, idesc_s, i > 0);
           }
-          umma_commit(&sh.sfull[j]);
+          umma_commit(&sh.sfull[j][b]);
           if (j == NT - 1) umma_commit(&sh.kempty[su]);
         }
         __syncwarp();
@@ -254,19 +266,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         qph ^= 1u;
         tc_fence_after();
 #pragma unroll
-        for (int j = 0; j < NT; ++j) issue_s(j, ks);
+        for (int j = 0; j < NT; ++j) issue_s(j, ks, n);
         if (++ks == S::kK) ks = 0, kph ^= 1u;
-        for (int t = q.tile0; ok && t < q.tile1; ++t) {
+        for (int t = q.tile0; ok && t < q.tile1; ++t, ++n) {
           const bool more = t + 1 < q.tile1;
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
             if (!ok) break;
-            ok = warp_wait(&sh.pfull[j], ph, wc) && (j > 0 || warp_wait(&sh.vfull[vs], vph, wc));
+            // The next tile's scores go where P of kBuf - 1 tiles ago is: only once it
+            // has been multiplied (before a piece's first tile, all have been).
+            auto next_scores = [&](bool wait, uint32_t after) {
+              ok = (j > 0 || warp_wait(&sh.kfull[ks], kph, wc)) && (!wait || warp_wait(&sh.pvdone[j], after & 1, wc));
+              if (!ok) return;
+              tc_fence_after();
+              issue_s(j, ks, n + 1);
+            };
+            if (S::kBuf == 2 && more) next_scores(t > q.tile0, n - 1);
+            ok = ok && warp_wait(&sh.pfull[j][S::buf(n)], S::phase(n), wc) && (j > 0 || warp_wait(&sh.vfull[vs], vph, wc));
             if (!ok) break;
             tc_fence_after();
             const int su = uniform(vs);
             const uint64_t vd = sw128_mn_desc(smem_u32(s_v) + su * S::kTileBytes, kTcTile * 128);
-            const uint32_t ts = tmem + S::kS + j * 128, to = tmem + S::kO + j * D;
+            const uint32_t ts = tmem + S::s_col(j, uniform((int)S::buf(n))), to = tmem + S::kO + j * D;
             const uint32_t first = uniform(t > q.tile0);
             if (elect_one()) {
 #pragma unroll
@@ -276,17 +297,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               if (j == NT - 1) umma_commit(&sh.vempty[su]);
             }
             __syncwarp();
-            if (more) {
-              // the next scores go where P is: only once P has been multiplied
-              ok = (j > 0 || warp_wait(&sh.kfull[ks], kph, wc)) && warp_wait(&sh.pvdone[j], ph, wc);
-              if (!ok) break;
-              tc_fence_after();
-              issue_s(j, ks);
-            }
+            if (S::kBuf == 1 && more) next_scores(true, n);
           }
           if (more && ++ks == S::kK) ks = 0, kph ^= 1u;
           if (++vs == S::kV) vs = 0, vph ^= 1u;
-          ph ^= 1u;
         }
         u += q.units;
         if (u < u1) q.next(sh.parts, a, L.plan, u, u1);
@@ -304,8 +318,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int j = warp >> 2, r = threadIdx.x;  // row of the chunk
     const int rj = r & 127;
     const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + S::kS + j * 128 + quarter, to = tmem + S::kO + j * D + quarter;
-    uint32_t ph = 0, tiles = 0;
+    const uint32_t to = tmem + S::kO + j * D + quarter;
+    uint32_t n = 0;  // tiles so far
     int vs = 0;
     uint32_t vph = 0;
     int sees = 0;
@@ -349,12 +363,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int fewest =
           q.part == 0 ? len : min(len, sh.parts.last[q.part] + div_group(q.chunk * kRows, L.group_mul));
       float m = -INFINITY, l = 0.f;
-      for (int t = q.tile0; t < q.tile1; ++t, ++tiles) {
-        ok = warp_wait(&sh.sfull[j], ph, wc);
+      for (int t = q.tile0; t < q.tile1; ++t, ++n) {
+        const uint32_t ts = tmem + S::s_col(j, S::buf(n)) + quarter;
+        ok = warp_wait(&sh.sfull[j][S::buf(n)], S::phase(n), wc);
         if (!ok) break;
         tc_fence_after();
         const int key0 = t * kTcTile;
-        const int valid = sh.valid[tiles & 7];
+        const int valid = sh.valid[n & 15];
         const bool edge = key0 + kTcTile > fewest || valid != 255;
         const int see = sees - key0;  // columns of the tile that the row sees
         if (edge) {
@@ -400,6 +415,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (raise) m = mn;
           l *= f;
           if (t > q.tile0) {
+            // O is still until this tile's P is there, once the tile before is added
+            ok = warp_wait(&sh.pvdone[j], (n - 1) & 1, wc);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll 1
             for (int h = 0; h < D / 16; ++h) {
               float o[16];
@@ -450,12 +469,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (++vs == S::kV) vs = 0, vph ^= 1u;
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&sh.pfull[j]);
-        ph ^= 1u;
+        mbar_arrive(&sh.pfull[j][S::buf(n)]);
       }
-      // the last product of the piece (its phase is the one before ph); the
-      // stream's warps leave together if a wait gave up
-      if (ok) ok = warp_wait(&sh.pvdone[j], ph ^ 1u, wc);
+      // the last product of the piece; the stream's warps leave together if a wait gave up
+      if (ok) ok = warp_wait(&sh.pvdone[j], (n - 1) & 1, wc);
       ok = named_bar_and(1 + j, 128, ok);
       if (!ok) break;
       tc_fence_after();
