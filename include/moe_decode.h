@@ -374,9 +374,9 @@ typedef struct dec_batch {
   const int32_t* row_start;   /* [requests + 1] first row of each request, not decreasing */
   const int32_t* own_len;     /* [requests] own tokens in the cache, this step's included */
   const int32_t* block_table; /* [requests][max_blocks] cache blocks of the own tokens, in order */
-  int max_blocks;             /* at least 1 */
+  int max_blocks;             /* at least 1; max_blocks * block_size <= 2^31 - 256 */
   const int32_t* prefix_table; /* [ceil(prefix_len / block_size)] blocks of the shared prefix; NULL if none */
-  int prefix_len;             /* 0: no shared prefix */
+  int prefix_len;             /* 0: no shared prefix; at most 2^31 - 256 */
 } dec_batch;
 
 /* Outputs of dec_batch_tables (device memory). */
@@ -487,7 +487,7 @@ dec_status dec_attention_workspace_size(const dec_handle* h, int M, int q_heads,
  * matter (they may hold infinities and NaN).
  * q [M][q_heads * head_dim] with row stride ldq, out the same with ldo; out
  * must not overlap q. 1 <= M <= 64, q_heads a multiple of kv_heads, at most
- * 1024 in all and 128 to a key head, scale > 0 and finite. Scores, softmax
+ * 1024 in all and 128 to a key head, scale in [1e-30, 1e30]. Scores, softmax
  * statistics and sums are fp32; the weights p are rounded to bf16 for the
  * product with v. */
 dec_status dec_attention(dec_handle* h, const dec_bf16* q, int64_t ldq, const dec_kv_cache* cache,
@@ -497,7 +497,7 @@ dec_status dec_attention(dec_handle* h, const dec_bf16* q, int64_t ldq, const de
 /* The attention core of one decode layer. */
 typedef struct dec_layer_attention {
   int q_heads;               /* q_heads * head_dim = K_out */
-  float scale;               /* factor on the scores, > 0 */
+  float scale;               /* factor on the scores, in [1e-30, 1e30] */
   const dec_rope* rope;      /* rotary positions, or NULL for none */
   const dec_kv_cache* cache; /* the layer's cache */
   const dec_batch* batch;

@@ -567,6 +567,13 @@ def _stream_of(h: Handle, stream) -> int:
     return torch.cuda.current_stream(h.device).cuda_stream
 
 
+def _on_stream(stream):
+    """Context in which new tensors belong to the stream of the call (None: the current one)."""
+    import contextlib
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _rows_of(t, name: str, device: int):
     """(rows, width, row stride) of a 2-D bf16 tensor with contiguous rows on the device."""
     if t.dtype is not _bf16 or t.dim() != 2 or t.get_device() != device:
@@ -577,7 +584,7 @@ def _rows_of(t, name: str, device: int):
     if step != 1 and width > 1:
         raise ValueError(f"{name}: rows must be contiguous")
     # the stride of a single row means nothing
-    return rows, width, ld if rows > 1 else max(ld, -(-width // 8) * 8)
+    return rows, width, ld if rows > 1 else -(-width // 8) * 8
 
 
 def _ints_of(t, name: str, device: int, count: Optional[int] = None) -> int:
@@ -679,7 +686,8 @@ class Rope:
         high = (4.0 if scaling == "bands" else 32.0) if high is None else high
         self.phases = None
         if rotary_dim:
-            self.phases = torch.empty(max(rotary_dim // 2, 1), dtype=torch.int64, device=f"cuda:{h.device}")
+            with _on_stream(stream):
+                self.phases = torch.empty(max(rotary_dim // 2, 1), dtype=torch.int64, device=f"cuda:{h.device}")
             _check(_load().dec_rope_phases(h.ptr, self.phases.data_ptr(), int(rotary_dim), float(base),
                                            ROPE_SCALING[scaling], float(factor), float(original_len), float(low),
                                            float(high), _stream_of(h, stream)), "dec_rope_phases")
@@ -704,7 +712,8 @@ def dec_batch_tables(h: Handle, ctx_len, new_len, free_blocks, free_count, block
     if out is None:
         if rows is None:
             raise ValueError("rows is required without out")
-        out = StepTables.empty(n, rows, ctx_len.device)
+        with _on_stream(stream):
+            out = StepTables.empty(n, rows, ctx_len.device)
     elif rows is not None and rows != out.rows:
         raise ValueError("rows differs from out's")
     _int32(block_table, "block_table", 2)
@@ -739,7 +748,8 @@ def dec_rope_append(h: Handle, rope: Rope, q, k, v, positions, slots, cache: KvC
         heads = width_q // d
         if q_out is None:
             import torch
-            q_out = torch.empty((rows, width_q), dtype=q.dtype, device=q.device)
+            with _on_stream(stream):
+                q_out = torch.empty((rows, width_q), dtype=q.dtype, device=q.device)
         rows_o, width_o, ldqo = _rows_of(q_out, "q_out", dev)
         if rows_o != rows or width_o != width_q:
             raise ValueError("q_out must have q's shape")
@@ -774,7 +784,8 @@ def dec_attention(h: Handle, q, cache: KvCache, batch: Batch, scale: float, out=
     heads = width // cache.head_dim
     if out is None:
         import torch
-        out = torch.zeros((M, width), dtype=q.dtype, device=q.device)
+        with _on_stream(stream):
+            out = torch.zeros((M, width), dtype=q.dtype, device=q.device)
     M_o, width_o, ldo = _rows_of(out, "out", dev)
     if M_o != M or width_o != width:
         raise ValueError("out must have q's shape")

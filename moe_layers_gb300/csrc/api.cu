@@ -1007,7 +1007,7 @@ dec_status decode_layer_attention(dec_handle* h, const dec_layer_weights* Wt, co
                                   dec_bf16* hidden, int M, const dec_layer_trace* trace, void* ws, size_t ws_bytes,
                                   cudaStream_t s) {
   if (h == nullptr || !layer_ok(Wt, M) || !layer_attention_ok(Wt, A, M)) return DEC_ERR_INVALID_ARG;
-  if (A->positions == nullptr || A->slots == nullptr || !(A->scale > 0.f) || !std::isfinite(A->scale))
+  if (A->positions == nullptr || A->slots == nullptr || !scale_ok(A->scale))
     return DEC_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(A->positions) | reinterpret_cast<uintptr_t>(A->slots)) & 3) return DEC_ERR_INVALID_ARG;
   return layer_entry(h, Wt, A, hidden, M, trace, ws, ws_bytes, s);

@@ -12,6 +12,7 @@ constexpr int kMaxAttentionRows = 64;
 constexpr int kMaxBatchRequests = 64;
 constexpr int kMaxTableRequests = 1024;
 constexpr int kMaxTokens = 1 << 20;
+constexpr int kMaxKeys = 0x7fffff00;  // a tile's end past the last key stays an int
 
 inline bool al(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline bool block_size_ok(int s) { return s == 16 || s == 32 || s == 64 || s == 128; }
@@ -46,10 +47,14 @@ bool rope_ok(const dec_rope* r, int head_dim) {
          (r->interleaved == 0 || r->interleaved == 1);
 }
 
+// Far enough from 0 and infinity that a masked score times it is minus infinity
+// and a score of zero stays zero.
+bool scale_ok(float s) { return s >= 1e-30f && s <= 1e30f; }
+
 bool attention_shape_ok(int M, int q_heads, const dec_kv_cache* c, const dec_batch* b) {
   return M >= 1 && M <= kMaxAttentionRows && cache_ok(c) && batch_ok(b) && q_heads >= c->kv_heads &&
          q_heads % c->kv_heads == 0 && q_heads / c->kv_heads <= 128 && q_heads <= 1024 &&
-         (long long)b->max_blocks * c->block_size <= 0x7fffffffLL;
+         (long long)b->max_blocks * c->block_size <= kMaxKeys && b->prefix_len <= kMaxKeys;
 }
 
 static AttentionParams attention_params(const uint16_t* q, long long ldq, const dec_kv_cache& cache,
@@ -179,7 +184,7 @@ dec_status dec_attention(dec_handle* h, const dec_bf16* q, int64_t ldq, const de
   const int64_t w = (int64_t)q_heads * cache->head_dim, most = (int64_t)1 << 31;
   if (!al(q, 16) || !al(out, 16) || ldq < w || ldo < w || ldq % 8 != 0 || ldo % 8 != 0 || ldq > most || ldo > most)
     return DEC_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return DEC_ERR_INVALID_ARG;
+  if (!scale_ok(scale)) return DEC_ERR_INVALID_ARG;
   const size_t need = attention_ws_bytes(h, M, q_heads, *cache, *batch);
   if (need > 0 && (ws == nullptr || !al(ws, 16) || ws_bytes < need)) return DEC_ERR_INVALID_ARG;
   DeviceGuard dev(h->device);

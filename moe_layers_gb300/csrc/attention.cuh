@@ -111,7 +111,7 @@ __device__ __forceinline__ void build_parts(PartTable& t, const AttentionParams&
       int len = a.prefix_len, last = a.prefix_len;
       if (i > 0) {
         len = max(0, (int)min((long long)own[k], (long long)a.max_blocks << a.shift));
-        last = (int)max((long long)own[k] - rows + 1, -1000LL);
+        last = (int)min(max((long long)own[k] - rows + 1, -1000LL), 0x7fffff00LL);  // room for the rows on top
       }
       t.row0[i] = (short)first;
       t.rows[i] = (short)rows;

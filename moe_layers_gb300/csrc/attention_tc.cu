@@ -416,6 +416,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           l *= f;
           if (t > q.tile0) {
             // O is still until this tile's P is there, once the tile before is added
+            // (the one before that is: these scores were issued behind it)
             ok = warp_wait(&sh.pvdone[j], (n - 1) & 1, wc);
             if (!ok) break;
             tc_fence_after();
@@ -471,7 +472,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_fence_before();
         mbar_arrive(&sh.pfull[j][S::buf(n)]);
       }
-      // the last product of the piece; the stream's warps leave together if a wait gave up
+      // The last product of the piece. With two buffers the one before it may still
+      // be under way, and a wait for a phase's parity passes while the phase before
+      // is open: that one first. The stream's warps leave together if a wait gave up.
+      if (ok && S::kBuf == 2 && q.tile1 - q.tile0 > 1) ok = warp_wait(&sh.pvdone[j], n & 1, wc);
       if (ok) ok = warp_wait(&sh.pvdone[j], (n - 1) & 1, wc);
       ok = named_bar_and(1 + j, 128, ok);
       if (!ok) break;

@@ -212,6 +212,7 @@ dec_status layer_attention(dec_handle* h, const dec_layer_attention& A, uint16_t
 bool cache_ok(const dec_kv_cache* c);
 bool batch_ok(const dec_batch* b);
 bool rope_ok(const dec_rope* r, int head_dim);
+bool scale_ok(float scale);
 bool attention_shape_ok(int M, int q_heads, const dec_kv_cache* c, const dec_batch* b);
 
 // Makes the handle's device current for the lifetime of the object.

@@ -42,11 +42,11 @@ BAD_CACHE = [dict(k=None), dict(v=None), dict(k=A + 8), dict(v=A + 2), dict(bloc
              dict(head_dim=96), dict(head_dim=0), dict(block_stride=2 * 16 * 64 - 8), dict(block_stride=2 * 16 * 64 + 4),
              dict(blocks=1 << 27), dict(block_stride=1 << 38)]
 BAD_BATCH = [dict(requests=0), dict(requests=65), dict(max_new=0), dict(max_new=65), dict(row_start=None),
-             dict(own_len=None), dict(block_table=None), dict(max_blocks=0), dict(max_blocks=1 << 25),
+             dict(own_len=None), dict(block_table=None), dict(max_blocks=0), dict(max_blocks=1 << 25), dict(max_blocks=(1 << 24), block_size=128), dict(prefix_len=(1 << 31) - 1, prefix_table=A),
              dict(prefix_len=-1), dict(prefix_len=5), dict(row_start=A + 2)]
 BAD_CALL = [dict(q=None), dict(out=None), dict(q=A + 8), dict(out=A + 8), dict(M=0), dict(M=65), dict(q_heads=0),
             dict(q_heads=3), dict(q_heads=2 * 129), dict(ldq=255), dict(ldq=252), dict(ldo=248), dict(scale=0.0),
-            dict(scale=-1.0), dict(scale=float("inf")), dict(scale=float("nan")), dict(out=2 * A),
+            dict(scale=-1.0), dict(scale=1e-31), dict(scale=1e31), dict(scale=float("inf")), dict(scale=float("nan")), dict(out=2 * A),
             dict(ldq=(1 << 31) + 8)]
 
 

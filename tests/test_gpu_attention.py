@@ -300,8 +300,8 @@ class Case:
         return oracle.attention(host_bits(self.q).reshape(-1, self.heads, self.d), host_bits(self.k), host_bits(self.v),
                                 self.row_start, self.own, self.table, self.scale, self.prefix_table, self.prefix)
 
-    def check(self, bits):
-        want, spread, reach = self.want()
+    def check(self, bits, reference=None):
+        want, spread, reach = (reference or Case.want)(self)
         got = oracle.as_f64(bits)
         used = ~np.isnan(want[:, 0, 0])
         assert np.all(got[~used] == 7.5)  # rows of no request
@@ -311,6 +311,34 @@ class Case:
         err = np.abs(got - want)
         assert np.all(err[used] <= tol[used] * 1.01), float(np.max(err[used] - tol[used]))
         return got, want
+
+
+def reference64(c):
+    """Like oracle.attention, in float64 on the GPU (elementary operations, one request at a time), for
+    cases that are long for a loop over rows on the host. Returns (out, sum p |v|, reach)."""
+    import torch
+    k, v = (torch.nan_to_num(t.double(), 0.0, 0.0, 0.0) for t in (c.k, c.v))
+    q = c.q.double().reshape(-1, c.kv, c.heads // c.kv, c.d)
+    shape = (q.shape[0], c.heads, c.d)
+    out, spread = np.full(shape, np.nan), np.zeros(shape)
+    reach = np.zeros(shape[:2])
+    for b, n in enumerate(c.new):
+        if not n:
+            continue
+        place = [(int(c.prefix_table[j // c.size]), j % c.size, -1) for j in range(c.prefix)]
+        place += [(int(c.table[b][j // c.size]), j % c.size, j) for j in range(c.own[b])]
+        blk, off, own = torch.tensor([p for p in place if 0 <= p[0] < c.blocks], device="cuda").T
+        first = int(c.row_start[b])
+        kk, vv, qq = k[blk, :, off], v[blk, :, off], q[first:first + n]
+        s = torch.einsum("tkgd,nkd->tkgn", qq, kk) * c.scale
+        last = c.own[b] - n + torch.arange(n, device="cuda")
+        s = s.masked_fill((own[None, :] > last[:, None])[:, None, None, :], -np.inf)
+        p = torch.softmax(s, -1)
+        out[first:first + n] = torch.einsum("tkgn,nkd->tkgd", p, vv).reshape(n, c.heads, c.d).cpu().numpy()
+        spread[first:first + n] = torch.einsum("tkgn,nkd->tkgd", p, vv.abs()).reshape(n, c.heads, c.d).cpu().numpy()
+        far = torch.einsum("tkgd,nkd->tkgn", qq.abs(), kk.abs()).amax(-1) * c.scale
+        reach[first:first + n] = far.reshape(n, c.heads).cpu().numpy()
+    return out, spread, reach
 
 
 LAYOUTS = [(8, 2, 64), (8, 2, 128), (4, 4, 128), (6, 1, 64), (20, 1, 128), (3, 3, 64), (40, 2, 128)]
@@ -509,6 +537,95 @@ def test_attention_long_context_offsets(h):
     assert np.array_equal(host_bits(out).reshape(1, 4, d), want)
     del k, v
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("heads,kv,d,M,prefix", [(64, 32, 64, 32, 6100), (32, 32, 128, 64, 6085), (128, 8, 64, 64, 1600),
+                                                 (64, 8, 128, 40, 5003), (16, 16, 128, 64, 16000), (64, 16, 128, 24, 20000),
+                                                 (64, 16, 128, 64, 12345), (32, 4, 64, 63, 30001)])
+def test_attention_large_prefix_work(h, heads, kv, d, M, prefix):
+    """Enough prefix for the tensor-memory kernel and a launch apart for the own tokens: one and two streams,
+    a few tiles a CTA and many; the same bits every time."""
+    rng = np.random.default_rng(M)
+    c = Case([1] * (M - 1) + [0], [int(x) for x in rng.integers(1, 70, M)], heads, kv, d, 16, prefix=prefix, pad=1, seed=M,
+             sharp=2.5)
+    c.prefix_table[3] = c.blocks + 5  # one block of the prefix is not there
+    first = c.run(h)
+    got, want = c.check(first, reference64)
+    used = slice(0, M - 1)
+    # both roundings are independent and at most 2^-8 of each term: 2^0.5 2^-8 in the 2-norm
+    assert np.linalg.norm((got - want)[used]) <= 2.0 ** -7.5 * np.linalg.norm(want[used])
+    for _ in range(5):
+        assert np.array_equal(c.run(h), first)
+
+
+@pytest.mark.parametrize("heads,kv,d,new,own", [(64, 32, 128, [24], [8000]), (64, 16, 128, [64], [9000]),
+                                                (40, 1, 64, [1] * 16, [5000 + 77 * i for i in range(16)]),
+                                                (64, 8, 64, [16, 9, 0, 20], [12000, 30, 500, 7000])])
+def test_attention_many_rows_on_long_contexts(h, heads, kv, d, new, own):
+    """More than 32 rows of one request to a key head: the tensor-memory kernel on own tokens, many tiles a CTA."""
+    c = Case(new, own, heads, kv, d, 32, seed=sum(new), sharp=2.5)
+    first = c.run(h)
+    c.check(first, reference64)
+    for _ in range(5):
+        assert np.array_equal(c.run(h), first)
+
+
+@pytest.mark.parametrize("heads,kv,d,M", [(1024, 128, 64, 2), (128, 1, 64, 3), (128, 1, 128, 64), (1024, 8, 64, 1)])
+def test_attention_many_heads(h, heads, kv, d, M):
+    c = Case([1] * M, [40 + i for i in range(M)], heads, kv, d, 32, prefix=70, seed=heads + M)
+    c.check(c.run(h))
+
+
+def test_attention_row_lengths_at_the_int_limit(h):
+    """own_len near 2^31 with several rows: each sees the whole table."""
+    c = Case([4], [64], 4, 2, 64, 16, seed=2)
+    c.own = [2 ** 31 - 1]
+    got = oracle.as_f64(c.run(h))
+    want, spread, reach = c.want()
+    tol = 2.0 ** -8 * np.abs(want) + spread * (2.0 ** -8 + 2.0 ** -12)
+    assert np.all(np.abs(got - want) <= tol)
+
+
+def test_attention_without_dependent_launches_and_while_profiling(h):
+    """The same bits with kernels strictly one after another."""
+    for prefix, heads, M in ((0, 8, 9), (90, 8, 9), (6085, 32, 64)):
+        c = Case([1] * M, [30 + 5 * i for i in range(M)], heads, 32 if heads == 32 else 2, 64, 16, prefix=prefix, seed=M)
+        first = c.run(h)
+        h.set_pdl(False)
+        assert np.array_equal(c.run(h), first)
+        h.set_pdl(True)
+        h.set_profiling(True)
+        assert np.array_equal(c.run(h), first)
+        tags = h.profile_read()
+        h.set_profiling(False)
+        assert "attention" in tags and ("attention_prefix" in tags) == (prefix == 6085)
+
+
+def test_attention_single_row_of_any_stride(h):
+    import torch
+    import moe_layers_gb300 as ML
+    c = Case([1], [50], 4, 2, 64, 16, seed=3)
+    want = c.run(h)
+    odd = torch.zeros((1, 4 * 64 + 3), dtype=torch.bfloat16, device="cuda")
+    odd[:, :256] = c.q
+    got = ML.dec_attention(h, odd[:, :256], c.cache, c.batch, c.scale)
+    torch.cuda.synchronize()
+    assert np.array_equal(host_bits(got).reshape(1, 4, 64), want)
+
+
+def test_outputs_made_on_the_stream_of_the_call(h):
+    """Without an output tensor, the zeros of idle rows and the result belong to the call's stream."""
+    import torch
+    import moe_layers_gb300 as ML
+    c = Case([1, 0, 1], [500, 7, 300], 8, 2, 64, 16, pad=2, seed=7)
+    want = c.run(h)
+    want[2:] = 0
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    ML.test_occupy_sms(h, 8, 20_000_000)  # the current stream is busy meanwhile
+    got = ML.dec_attention(h, c.q, c.cache, c.batch, c.scale, stream=s)
+    s.synchronize()
+    assert np.array_equal(host_bits(got).reshape(want.shape), want)
 
 
 def test_operators_together(h):
