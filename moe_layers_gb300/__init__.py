@@ -205,6 +205,7 @@ class Handle:
         self._ws = {}
         self._stream_ws = {}
         self._attention_ws = {}  # workspace bytes by shape
+        self._layer_ws = {}      # decode_layer_attention's workspaces by stream and shape
 
     @property
     def ptr(self):
@@ -216,6 +217,7 @@ class Handle:
             self._h = ctypes.c_void_p()
             self._ws.clear()
             self._stream_ws.clear()
+            self._layer_ws.clear()
 
     def __enter__(self):
         return self
@@ -776,7 +778,9 @@ def dec_attention_workspace_size(h: Handle, M: int, q_heads: int, cache: KvCache
 def dec_attention(h: Handle, q, cache: KvCache, batch: Batch, scale: float, out=None, stream=None, ws=None):
     """Attention of a step's rows q (bf16 [M, q_heads * head_dim], rows may be
     strided) over the batch's shared prefix and own tokens in the cache. Without
-    `out`, rows that belong to no request are zero."""
+    `out`, rows that belong to no request are zero. Without `ws`, the calls of one
+    stream share a workspace: give graphs that may run at the same time one each
+    (dec_attention_workspace_size bytes, any contents)."""
     dev = h.device
     M, width, ldq = _rows_of(q, "q", dev)
     if width % cache.head_dim != 0:
@@ -841,7 +845,8 @@ def decode_layer_attention_workspace_size(h: Handle, weights: LayerWeights, atte
 def decode_layer_attention(h: Handle, weights: LayerWeights, attention: LayerAttention, hidden, trace=False,
                            stream=None, ws=None, _cw=None):
     """decode_layer with attention between the projections, in place on hidden
-    bf16 [M,H]; trace as in decode_layer."""
+    bf16 [M,H]; trace as in decode_layer. Without `ws`, a workspace is made at the
+    first call of a stream and shape, which cannot be one that is captured."""
     import torch
     _require(hidden, torch.bfloat16, "hidden", 2)
     _described(h, attention, "attention")
@@ -851,10 +856,20 @@ def decode_layer_attention(h: Handle, weights: LayerWeights, attention: LayerAtt
     cw = weights.c_struct() if _cw is None else _cw
     sp = _stream_of(h, stream)
     if ws is None:
+        # one per stream and shape, kept until the handle closes: a captured graph may
+        # hold its address, and its counters must stay as its own calls leave them
         c = attention.cache
-        ws = h.workspace(("layer_attention", sp), decode_layer_attention_workspace_size(h, weights, attention, M),
-                         ("layer_attention", M, cw.H, cw.N_in, cw.K_out, cw.E, cw.k, cw.I, attention.q_heads, c.kv_heads,
-                          c.head_dim, attention.batch.prefix_len > 0))
+        key = (sp, M, cw.H, cw.N_in, cw.K_out, cw.E, cw.k, cw.I, cw.Wg_s is not None, attention.q_heads, c.kv_heads,
+               c.head_dim, attention.batch.prefix_len > 0)
+        ws = h._layer_ws.get(key)
+        if ws is None:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("decode_layer_attention: the first call of a shape makes its zeroed workspace; make it "
+                                   "before the capture, or pass ws")
+            with _on_stream(stream):
+                ws = torch.zeros(decode_layer_attention_workspace_size(h, weights, attention, M), dtype=torch.uint8,
+                                 device=hidden.device)
+            h._layer_ws[key] = ws
     out = trace if isinstance(trace, dict) else None
     if trace is True:
         out = dict(h1=torch.empty_like(hidden),

@@ -5,11 +5,14 @@
 // P = 2^(S - m'), l = l 2^(m - m') + sum P, the scale and log2 e folded into
 // one factor on S. What bounds it is the read of the cache: 4 query rows to a
 // key row make 4 flops a byte. The cache therefore streams through a ring of
-// TMA copies (one box per block and 64 elements, 128-byte swizzle) that one
-// warp keeps full, while four warps multiply with mma.sync m16n8k16, whose
-// fragments come from the ring by ldmatrix without bank conflicts. Each CTA
-// streams one equal share of all tiles (attention.cuh); rows that several CTAs
-// took are joined by the combine kernel.
+// TMA copies (one box per block and 64 elements, 128-byte swizzle) that two
+// warps keep full, one with K and one with V, while four warps multiply with
+// mma.sync m16n8k16, whose fragments come from the ring by ldmatrix without bank
+// conflicts; up to 32 rows the multiplications are no limit. Each CTA streams one
+// equal share of all tiles (attention.cuh); rows that several CTAs took are
+// joined by a second kernel. Measured (64 heads on 16, head dim 128): one request
+// of 131000 tokens 156 us, 6.9 TB/s, the copy rate; 61 requests of 1..4096 tokens
+// 44 us, 6.3 TB/s; 8 requests of 8 drafts on 2000..16000 tokens 80 us, 6.0 TB/s.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -434,7 +437,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
       }
       // The warps that join their sums leave together if a wait gave up; this
       // barrier also ends the reads of the previous piece's sums.
-      if (WK > 1 ? !named_bar_and(bar_end, WK * 32, ok) : !ok) return false;
+      if (!named_bar_and(bar_end, WK * 32, ok)) return false;
 
       // ---------------------------------------------------------- the piece's rows
       const Piece done = q;
@@ -453,40 +456,38 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
         float mt = m[e], lt = l[e];
         lt += __shfl_xor_sync(0xffffffffu, lt, 1);
         lt += __shfl_xor_sync(0xffffffffu, lt, 2);
-        if (WK > 1) {
-          // warps 1.. of the group hand their sums to warp 0, fragment by fragment
-          float2* mine = s_merge + (wm * (WK - 1) + wk - 1) * (D / 8) * 32 + lane;
-          if (e > 0) named_bar_sync(bar_end, WK * 32);  // the first half has been read
-          if (wk > 0) {
+        // warps 1.. of the group hand their sums to warp 0, fragment by fragment
+        float2* mine = s_merge + (wm * (WK - 1) + wk - 1) * (D / 8) * 32 + lane;
+        if (e > 0) named_bar_sync(bar_end, WK * 32);  // the first half has been read
+        if (wk > 0) {
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) mine[i * 32] = make_float2(o[i][2 * e], o[i][2 * e + 1]);
-            if (t4 == 0) sh.ml[warp][g] = make_float2(mt, lt);
-            named_bar_arrive(bar_sums, WK * 32);
-            continue;
-          }
-          named_bar_sync(bar_sums, WK * 32);
-          float f[WK], top = mt;
+          for (int i = 0; i < D / 8; ++i) mine[i * 32] = make_float2(o[i][2 * e], o[i][2 * e + 1]);
+          if (t4 == 0) sh.ml[warp][g] = make_float2(mt, lt);
+          named_bar_arrive(bar_sums, WK * 32);
+          continue;
+        }
+        named_bar_sync(bar_sums, WK * 32);
+        float f[WK], top = mt;
 #pragma unroll
-          for (int w = 1; w < WK; ++w) top = fmaxf(top, sh.ml[warp + w][g].x);
-          f[0] = ex2_from(mt, top);
-          lt *= f[0];
+        for (int w = 1; w < WK; ++w) top = fmaxf(top, sh.ml[warp + w][g].x);
+        f[0] = ex2_from(mt, top);
+        lt *= f[0];
+#pragma unroll
+        for (int w = 1; w < WK; ++w) {
+          const float2 ml = sh.ml[warp + w][g];
+          f[w] = ex2_from(ml.x, top);
+          lt = fmaf(ml.y, f[w], lt);
+        }
+        mt = top;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          o[i][2 * e] *= f[0];
+          o[i][2 * e + 1] *= f[0];
 #pragma unroll
           for (int w = 1; w < WK; ++w) {
-            const float2 ml = sh.ml[warp + w][g];
-            f[w] = ex2_from(ml.x, top);
-            lt = fmaf(ml.y, f[w], lt);
-          }
-          mt = top;
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            o[i][2 * e] *= f[0];
-            o[i][2 * e + 1] *= f[0];
-#pragma unroll
-            for (int w = 1; w < WK; ++w) {
-              const float2 y = s_merge[((wm * (WK - 1) + w - 1) * (D / 8) + i) * 32 + lane];
-              o[i][2 * e] = fmaf(y.x, f[w], o[i][2 * e]);
-              o[i][2 * e + 1] = fmaf(y.y, f[w], o[i][2 * e + 1]);
-            }
+            const float2 y = s_merge[((wm * (WK - 1) + w - 1) * (D / 8) + i) * 32 + lane];
+            o[i][2 * e] = fmaf(y.x, f[w], o[i][2 * e]);
+            o[i][2 * e + 1] = fmaf(y.y, f[w], o[i][2 * e + 1]);
           }
         }
         if (r >= in_chunk) continue;

@@ -515,6 +515,44 @@ def test_attention_under_a_graph_with_new_lengths(h):
         c.check(host_bits(out).reshape(9, 8, 64))
 
 
+@pytest.mark.parametrize("heads,kv,d,M", [(32, 32, 128, 64), (128, 8, 64, 64), (8, 2, 64, 9)])
+def test_two_graphs_at_once(h, heads, kv, d, M):
+    """Captured calls with a workspace each, replayed on two streams at the same time, many times."""
+    import torch
+    import moe_layers_gb300 as ML
+    prefix = 6085 if kv == 32 else 1600
+    cs = [Case([1] * M, [3 + (7 * i + s) % 60 for i in range(M)], heads, kv, d, 16, prefix=prefix, seed=s) for s in (0, 1)]
+    alone = [c.run(h) for c in cs]
+    # a graph keeps addresses, not tensors: its workspace and output stay alive here
+    outs, spaces, graphs, streams = [], [], [], [torch.cuda.Stream() for _ in cs]
+    for c in cs:
+        out = torch.zeros((M, heads * d), dtype=torch.bfloat16, device="cuda")
+        ws = torch.empty(ML.dec_attention_workspace_size(h, M, heads, c.cache, c.batch), dtype=torch.uint8, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ML.dec_attention(h, c.q, c.cache, c.batch, c.scale, out=out, ws=ws)
+        outs.append(out)
+        spaces.append(ws)
+        graphs.append(g)
+    for _ in range(20):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for o, want in zip(outs, alone):
+            assert np.array_equal(host_bits(o).reshape(want.shape), want)
+
+
+@pytest.mark.parametrize("prefix", [0, 40])
+def test_attention_of_an_idle_batch(h, prefix):
+    """No request has a row: nothing is written."""
+    c = Case([0, 0, 0], [5, 0, 90], 8, 2, 64, 16, prefix=prefix, pad=3, seed=1)
+    assert np.all(oracle.as_f64(c.run(h)) == 7.5)
+
+
 def test_attention_long_context_offsets(h):
     """A cache whose blocks lie past 2^32 elements."""
     import torch

@@ -159,6 +159,47 @@ def test_layer_attention_under_a_graph(h):
         assert np.array_equal(a, b)
 
 
+def test_layer_attention_workspace_and_captures(h):
+    """A capture that would have to make the workspace is refused; one made before keeps it, whatever other
+    shapes run in between."""
+    import torch
+    import moe_layers_gb300 as ML
+    L = Layer(4, 2, 64, 0, True)
+    pool = torch.zeros((40, 2, 16, 64), dtype=torch.bfloat16, device="cuda")
+
+    def layer(M):
+        step = ML.StepTables.empty(M, M)
+        table = torch.full((M, 2), -1, dtype=torch.int32, device="cuda")
+        ML.dec_batch_tables(h, i32([0] * M), i32([1] * M), i32(range(40)), i32([40]), table, 16, step)
+        batch = ML.Batch(step.row_start, step.own_len, table)
+        return ML.LayerAttention(4, 0.125, ML.KvCache(pool, pool.clone()), batch, step.positions, step.slots)
+
+    x0 = {M: dev_bf16(synth.bf16(M * H, SEED, 7300 + M, 0, 1.0).reshape(M, H), (M, H)) for M in (3, 8, 33)}
+    att = {M: layer(M) for M in x0}
+    s = torch.cuda.Stream()
+    x = x0[3].clone()
+    with pytest.raises(RuntimeError, match="before the capture"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=s):
+            ML.decode_layer_attention(h, L.w, att[3], x)
+    torch.cuda.synchronize()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        want = x0[3].clone()
+        ML.decode_layer_attention(h, L.w, att[3], want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        ML.decode_layer_attention(h, L.w, att[3], x)
+    for M in (8, 33, 8):
+        with torch.cuda.stream(s):
+            ML.decode_layer_attention(h, L.w, att[M], x0[M].clone())
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        x.copy_(x0[3])
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(x.view(torch.int16), want.view(torch.int16))
+
+
 def test_layer_attention_refuses(h):
     import torch
     import moe_layers_gb300 as ML
