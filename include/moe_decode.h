@@ -483,8 +483,9 @@ dec_status dec_attention_workspace_size(const dec_handle* h, int M, int q_heads,
  * prefix is read once for all rows, not once a request. Tokens in a block
  * whose table entry is outside [0, blocks), or past max_blocks blocks, are
  * not there. A row that sees no token gets zeros; rows of no request are left
- * as they were. Places of the cache that hold none of these tokens do not
- * matter (they may hold infinities and NaN).
+ * as they were. A row follows from the tokens that it sees alone: the rows
+ * behind it and places of the cache that hold none of these tokens may hold
+ * infinities and NaN.
  * q [M][q_heads * head_dim] with row stride ldq, out the same with ldo; out
  * must not overlap q. 1 <= M <= 64, q_heads a multiple of kv_heads, at most
  * 1024 in all and 128 to a key head, scale in [1e-30, 1e30]. Scores, softmax

@@ -404,6 +404,47 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
             // P is rounded to bf16 for the product with V (fp32 sums; l keeps the unrounded weights)
             pf[j >> 1][(j & 1) * 2 + e] = pack_bf16x2(w0, w1);
           }
+        int stop = len;
+        if (edge && fewest < len) {
+          // Keys that some rows see and others do not. Where one of their V is an
+          // infinity or NaN, the product would carry it to the others as 0 * V: these
+          // keys are then added row by row.
+          const int lo = max(fewest, key0), hi = min(len, key0 + R::kKeys), kr0 = lo - t * kTileKeys;
+          bool bad = false;
+          for (int i = lane; i < (hi - lo) * (D / 8); i += 32) {
+            const int cv = i % (D / 8);
+            const uint4 x = *reinterpret_cast<const uint4*>(smem + s * S::kStage + S::kHalf + (cv >> 3) * (kTileKeys * 128) +
+                                                            swz(kr0 + i / (D / 8), cv & 7));
+            bad = bad || not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w);
+          }
+          if (__any_sync(0xffffffffu, bad)) {
+            stop = lo;
+#pragma unroll
+            for (int j = 0; j < NK; ++j)
+#pragma unroll 1
+              for (int k = 0; k < 8; ++k) {
+                float w[NE];
+#pragma unroll
+                for (int e = 0; e < NE; ++e) {
+                  const uint32_t pair = __shfl_sync(0xffffffffu, pf[j >> 1][(j & 1) * 2 + e], (lane & ~3) | (k >> 1));
+                  w[e] = k & 1 ? bf_hi(pair) : bf_lo(pair);
+                }
+                const int kk = key0 + j * 8 + k;
+                if (kk < lo || kk >= hi) continue;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                  const uint32_t x = *reinterpret_cast<const uint32_t*>(
+                      smem + s * S::kStage + S::kHalf + (i >> 3) * (kTileKeys * 128) + swz(kk - t * kTileKeys, i & 7) + 4 * t4);
+#pragma unroll
+                  for (int e = 0; e < NE; ++e)
+                    if (kk < sees[e]) {
+                      o[i][2 * e] = fmaf(w[e], bf_lo(x), o[i][2 * e]);
+                      o[i][2 * e + 1] = fmaf(w[e], bf_hi(x), o[i][2 * e + 1]);
+                    }
+                }
+              }
+          }
+        }
 #pragma unroll
         for (int j = 0; j < NK / 2; ++j) {
           // Keys behind the part's last one hold anything (NaN too): their V is
@@ -411,8 +452,8 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
           uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
           if (edge) {
             const int kk = key0 + j * 16 + 2 * t4;
-            keep0 = (kk < len ? 0xffffu : 0u) | (kk + 1 < len ? 0xffff0000u : 0u);
-            keep1 = (kk + 8 < len ? 0xffffu : 0u) | (kk + 9 < len ? 0xffff0000u : 0u);
+            keep0 = (kk < stop ? 0xffffu : 0u) | (kk + 1 < stop ? 0xffff0000u : 0u);
+            keep1 = (kk + 8 < stop ? 0xffffu : 0u) | (kk + 9 < stop ? 0xffff0000u : 0u);
           }
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {

@@ -198,6 +198,16 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return r;
 }
 
+// Whether one of two bf16 values is an infinity or NaN (its exponent is all ones).
+__device__ __forceinline__ bool not_finite(uint32_t pair) {
+  return (((pair & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0;
+}
+// The pair with zeros in place of infinities and NaN.
+__device__ __forceinline__ uint32_t finite_of(uint32_t pair) {
+  const uint32_t top = ((pair & 0x7f807f80u) + 0x00800080u) & 0x80008000u;  // the top bit of each such half
+  return pair & ~(top | (top - (top >> 15)));
+}
+
 // A warp's bounded wait: true in every lane, or false in every lane.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& wc) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;

@@ -60,6 +60,7 @@ struct TcShared {
   PartTable parts;
   uint8_t valid[16];  // per tile (modulo 16): which 16-key eighths lie in blocks of the cache
   uint32_t tmem;
+  uint32_t bad;  // 1 + the first tile (of all of the CTA's) of the last piece with a V to be added at its end
   int abort;
 };
 static_assert(sizeof(TcShared) <= 2048, "attention tables");
@@ -152,6 +153,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     mbar_init(&sh.done, 1);
     mbar_init(&sh.qfull, kRows);
     sh.abort = 0;
+    sh.bad = 0;
     fence_mbar_init();
     tmap_prefetch(&tk);
     tmap_prefetch(&tv);
@@ -366,6 +368,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int fewest =
           q.part == 0 ? len : min(len, sh.parts.last[q.part] + div_group(q.chunk * kRows, L.group_mul));
       float m = -INFINITY, l = 0.f;
+      const uint32_t id = n + 1;  // of the piece
       for (int t = q.tile0; t < q.tile1; ++t, ++n) {
         const uint32_t ts = tmem + S::s_col(j, S::buf(n)) + quarter;
         ok = warp_wait(&sh.sfull[j][S::buf(n)], S::phase(n), wc);
@@ -458,15 +461,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tmem_wait_ld(x0, x1);
         weigh(x0, 3);
         l += l0 + l1;
-        if (key0 + kTcTile > len) {
+        if (key0 + kTcTile > fewest) {
           // Keys behind the part's last one hold anything (NaN too): their V is
-          // made zero, as 0 * NaN would not be.
+          // made zero, as 0 * NaN would not be. Keys that some rows see and others
+          // do not carry an infinity or NaN to the others the same way: those
+          // elements are made zero too, and added at the end of the piece. (Both
+          // streams do this to the same tile, the one behind may find it done.)
           ok = warp_wait(&sh.vfull[vs], vph, wc);
           if (!ok) break;
-          for (int i = rj; i < (key0 + kTcTile - len) * kSub * 8; i += 128) {
-            const int key = len - key0 + i / (kSub * 8), h = (i >> 3) % kSub, v = i & 7;
-            *reinterpret_cast<uint4*>(s_v + vs * S::kTileBytes + h * (kTcTile * 128) + key * 128 + v * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
+          const int from = max(fewest - key0, 0);
+          for (int i = rj; i < (kTcTile - from) * kSub * 8; i += 128) {
+            const int key = from + i / (kSub * 8), h = (i >> 3) % kSub, v = i & 7;
+            uint4* at = reinterpret_cast<uint4*>(s_v + vs * S::kTileBytes + h * (kTcTile * 128) + key * 128 + v * 16);
+            if (key0 + key >= len) {
+              *at = make_uint4(0u, 0u, 0u, 0u);
+              continue;
+            }
+            const uint4 x = *at;
+            if (not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w)) {
+              *const_cast<volatile uint32_t*>(&sh.bad) = id;
+              __threadfence_block();
+              *at = make_uint4(finite_of(x.x), finite_of(x.y), finite_of(x.z), finite_of(x.w));
+            }
           }
           fence_async_smem();
         }
@@ -483,6 +499,31 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       ok = named_bar_and(1 + j, 128, ok);
       if (!ok) break;
       tc_fence_after();
+      if (*const_cast<volatile uint32_t*>(&sh.bad) == id) {
+        // The infinities and NaN that were left out, from the cache, to the rows that
+        // see them (their weight would not change them).
+        const int32_t* table = a.block_table + (long long)(q.part - 1) * a.max_blocks;  // the prefix has no such keys
+        for (int key = max(fewest, q.tile0 * kTcTile); key < min(len, q.tile1 * kTcTile); ++key) {
+          const int block = ld_act_s32(table + (key >> a.shift));
+          if (block < 0 || block >= a.blocks) continue;
+          const uint16_t* v = a.v + block * a.block_stride +
+                              (long long)((q.kvh << a.shift) + (key & ((1 << a.shift) - 1))) * D;
+#pragma unroll 1
+          for (int h = 0; h < D / 16; ++h) {
+            float o[16];
+            tmem_ld16(to + h * 16, o);
+            uint32_t y[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint32_t x = (uint32_t)v[h * 16 + i];
+              const float f = not_finite(x) && key < sees ? __uint_as_float(x << 16) : 0.f;
+              y[i] = __float_as_uint(o[i] + f);
+            }
+            tmem_st16(to + h * 16, y);
+          }
+          tmem_wait_st();
+        }
+      }
       const Piece done = q;
       const bool begins = done.tile0 == 0;
       const bool direct = begins && done.tile1 == done.tiles && a.prefix_len == 0;

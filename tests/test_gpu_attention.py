@@ -375,6 +375,43 @@ def test_attention_prefix_batches(h, M, heads, kv, d):
     c.check(c.run(h))
 
 
+@pytest.mark.parametrize("heads,kv,d,new", [(8, 2, 128, 2), (8, 2, 64, 4), (8, 2, 128, 8), (8, 2, 64, 8), (8, 2, 128, 16),
+                                            (4, 1, 64, 30), (8, 2, 128, 64), (16, 1, 64, 64), (2, 2, 128, 8)])
+@pytest.mark.parametrize("prefix", [0, 70])
+def test_attention_later_tokens_that_are_not_finite(h, heads, kv, d, new, prefix):
+    """Infinities and NaN in k and v of a step's own tokens reach the rows that see them alone: the rows
+    before are as without them, and in those behind, an element of v only its own column."""
+    n = min(4, 64 // new)
+    own = [127 + new, 120 + new // 2, new, 1000][:n]  # the new tokens begin and end in all parts of a tile
+    c = Case([new] * n, own, heads, kv, d, 16, prefix=prefix, seed=new + d)
+    rng = np.random.default_rng(new)
+    planted = np.zeros((c.M, heads, d), dtype=bool)
+    sick = np.zeros(c.M, dtype=bool)  # rows that see a NaN score
+    values = []
+    for b in range(n):
+        for i in {0, 1, new // 2, new - 1}:
+            j, g, col = own[b] - new + i, int(rng.integers(kv)), int(rng.integers(d))
+            at = (int(c.table[b][j // 16]), g, j % 16)
+            values.append((at, col, (np.inf, -np.inf, np.nan)[(i + b) % 3]))
+            first = int(c.row_start[b]) + i
+            planted[first:int(c.row_start[b + 1]), g * heads // kv:(g + 1) * heads // kv, col] = True
+    for at, col, _ in values:
+        c.v[at][col] = 0.0
+    want, spread, reach = c.want()
+    for at, col, x in values:
+        c.v[at][col] = x
+    j = own[-1] - 1  # the last row of the last request sees a key of NaN
+    c.k[int(c.table[-1][j // 16]), :, j % 16] = float("nan")
+    sick[-1] = True
+    got = oracle.as_f64(c.run(h))
+    assert np.all(np.isnan(got[sick]))
+    assert not np.any(np.isfinite(got[planted & ~sick[:, None, None]]))
+    ok = ~planted & ~sick[:, None, None]
+    score = d * 2.0 ** -23 * reach[..., None]
+    tol = 2.0 ** -8 * np.abs(want) + spread * (2.0 ** -8 + 2 * score + (prefix + 1000) * 2.0 ** -23 + 2.0 ** -20)
+    assert np.all((np.abs(got - want) <= tol * 1.01)[ok])
+
+
 @pytest.mark.parametrize("heads,kv,d", [(8, 2, 128), (4, 1, 64), (16, 16, 64), (64, 4, 128)])
 @pytest.mark.parametrize("new", [[8] * 8, [3, 1, 7, 0, 16], [64], [33, 31], [2] * 5, [1, 0, 0, 1]])
 @pytest.mark.parametrize("prefix", [0, 70])
