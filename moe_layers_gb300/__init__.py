@@ -244,15 +244,18 @@ class Handle:
         self._ws[key] = (t, layout)
         return t
 
-    def stream_workspace(self, key, stream: int, nbytes: int):
-        """A workspace of at least nbytes per key and stream, for calls that need no
-        zeroed memory. One that is outgrown is kept until the handle closes: a
-        captured graph may still use it."""
+    def stream_workspace(self, key, address: int, nbytes: int, stream=None):
+        """A workspace of at least nbytes per key and stream (its address; `stream` if it
+        is not the current one), for calls that need no zeroed memory. It is memory of
+        that stream: a block that another stream gave back may still be in use there.
+        One that is outgrown is kept until the handle closes: a captured graph may
+        still use it."""
         import torch
-        held = self._stream_ws.setdefault((key, stream), [])
+        held = self._stream_ws.setdefault((key, address), [])
         if not held or held[-1].numel() < nbytes:
             size = max(int(nbytes), 256, 2 * held[-1].numel() if held else 0)
-            held.append(torch.empty(size, dtype=torch.uint8, device=f"cuda:{self.device}"))
+            with _on_stream(stream):
+                held.append(torch.empty(size, dtype=torch.uint8, device=f"cuda:{self.device}"))
         return held[-1]
 
     def set_force_variant(self, v: int) -> None:
@@ -803,7 +806,7 @@ def dec_attention(h: Handle, q, cache: KvCache, batch: Batch, scale: float, out=
         size = h._attention_ws.get(shape)
         if size is None:
             size = h._attention_ws[shape] = dec_attention_workspace_size(h, M, heads, cache, batch)
-        ws = h.stream_workspace("attention", sp, size)
+        ws = h.stream_workspace("attention", sp, size, stream)
     st = _load().dec_attention(h.ptr, q.data_ptr(), ldq, cache._ref, batch._ref, scale, out.data_ptr(), ldo, M, heads,
                                ws.data_ptr(), ws.numel(), sp)
     if st:

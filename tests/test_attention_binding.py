@@ -1,0 +1,138 @@
+"""What the binding of the attention operators does around a call (where it makes
+its tensors, what it refuses, what it passes on), checked without a GPU.
+
+Tensors, streams and the library are stand-ins: a tensor remembers the stream
+that was current when it was made, and a call only records its arguments.
+"""
+import contextlib
+import types
+
+import pytest
+import torch
+
+
+class Stream:
+    def __init__(self, number, capturing=False):
+        self.cuda_stream, self.capturing = number, capturing
+
+
+class Tensor:
+    """The part of a CUDA tensor that the binding looks at."""
+    is_cuda = True
+    made = 0
+
+    def __init__(self, shape, dtype=torch.bfloat16, device=0, stride=None, stream=None):
+        self.shape, self.dtype, self.index, self.made_on = tuple(shape), dtype, device, stream
+        self.device = f"cuda:{device}"
+        if stride is None:
+            stride, n = [], 1
+            for s in reversed(self.shape):
+                stride.insert(0, n)
+                n *= s
+        self.strides = tuple(stride)
+        Tensor.made += 1
+        self.address = Tensor.made << 24 if self.numel() else 0
+
+    def stride(self, i=None):
+        return self.strides if i is None else self.strides[i]
+
+    def is_contiguous(self):
+        return self.strides == Tensor(self.shape).strides
+
+    def numel(self):
+        n = 1
+        for s in self.shape:
+            n *= s
+        return n
+
+    def dim(self):
+        return len(self.shape)
+
+    def element_size(self):
+        return torch.empty((), dtype=self.dtype, device="cpu").element_size()
+
+    def get_device(self):
+        return self.index
+
+    def data_ptr(self):
+        return self.address
+
+
+class Library:
+    """Every entry point answers OK and keeps its arguments; size queries answer `size`."""
+    size = 5000
+
+    def __init__(self):
+        self.calls = {}
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls[name] = args
+            if name.endswith("_workspace_size"):
+                args[-1]._obj.value = self.size
+            return 0
+        return call
+
+
+@pytest.fixture
+def b(monkeypatch):
+    """The binding on stand-ins: b.ml, b.lib, b.h, and b.current, the current stream."""
+    import moe_layers_gb300 as ml
+    at = types.SimpleNamespace(ml=ml, lib=Library(), current=Stream(1))
+
+    @contextlib.contextmanager
+    def stream(s):
+        before, at.current = at.current, s
+        yield
+        at.current = before
+
+    def make(*shape, dtype=None, device=None):
+        shape = shape[0] if isinstance(shape[0], (tuple, list)) else shape
+        return Tensor(shape, dtype, int(str(device).rpartition(":")[2]), stream=at.current)
+
+    real_empty = torch.empty
+
+    def empty(*shape, dtype=None, device=None):
+        return real_empty(*shape, dtype=dtype) if device == "cpu" else make(*shape, dtype=dtype, device=device)
+
+    monkeypatch.setattr(ml, "_load", lambda: at.lib)
+    monkeypatch.setattr(ml, "_bf16", torch.bfloat16)
+    monkeypatch.setattr(ml, "_i32", torch.int32)
+    monkeypatch.setattr(ml, "_raw_stream", lambda device: at.current.cuda_stream)
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(torch, "zeros", make)
+    monkeypatch.setattr(torch, "empty_like", lambda t: make(t.shape, dtype=t.dtype, device=t.device))
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: at.current)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: at.current.capturing)
+    at.h = ml.Handle(0)
+    at.h._h.value = 1
+    yield at
+    at.h._h.value = None  # nothing to destroy
+
+
+def ints(*shape, **kw):
+    return Tensor(shape, torch.int32, **kw)
+
+
+def attention_call(b, rows=2, heads=4, **kw):
+    cache = b.ml.KvCache(Tensor((10, 2, 16, 64)), Tensor((10, 2, 16, 64)))
+    batch = b.ml.Batch(ints(rows + 1), ints(rows), ints(rows, 4))
+    return b.ml.dec_attention(b.h, Tensor((rows, heads * 64)), cache, batch, 0.125, **kw)
+
+
+def test_attention_workspace_is_made_on_the_stream_of_the_call(b):
+    """A block that the current stream has just given back may still be read there: only memory of
+    the call's own stream may be written by the call."""
+    s = Stream(7)
+    attention_call(b, stream=s)
+    (ws,) = b.h._stream_ws[("attention", 7)]
+    assert ws.made_on is s and ws.numel() >= Library.size
+    attention_call(b)
+    (ws,) = b.h._stream_ws[("attention", 1)]
+    assert ws.made_on is b.current
+    # one that is outgrown, too, is replaced by one of its own stream
+    b.lib.size = 50000
+    attention_call(b, rows=3, stream=s)
+    assert len(b.h._stream_ws[("attention", 7)]) == 2
+    assert all(ws.made_on is s for ws in b.h._stream_ws[("attention", 7)])
