@@ -875,10 +875,11 @@ def decode_layer_attention(h: Handle, weights: LayerWeights, attention: LayerAtt
             h._layer_ws[key] = ws
     out = trace if isinstance(trace, dict) else None
     if trace is True:
-        out = dict(h1=torch.empty_like(hidden),
-                   idx=torch.empty((M, cw.k), dtype=torch.int32, device=hidden.device),
-                   w=torch.empty((M, cw.k), dtype=torch.float32, device=hidden.device),
-                   scores=torch.empty((M, cw.E), dtype=torch.float32, device=hidden.device))
+        with _on_stream(stream):
+            out = dict(h1=torch.empty_like(hidden),
+                       idx=torch.empty((M, cw.k), dtype=torch.int32, device=hidden.device),
+                       w=torch.empty((M, cw.k), dtype=torch.float32, device=hidden.device),
+                       scores=torch.empty((M, cw.E), dtype=torch.float32, device=hidden.device))
     tr = None
     if out is not None:
         tr = _LayerTrace()

@@ -136,3 +136,32 @@ def test_attention_workspace_is_made_on_the_stream_of_the_call(b):
     attention_call(b, rows=3, stream=s)
     assert len(b.h._stream_ws[("attention", 7)]) == 2
     assert all(ws.made_on is s for ws in b.h._stream_ws[("attention", 7)])
+
+
+class Weights:
+    """A layer of 64 columns with 6 experts, top 2."""
+
+    def __init__(self, ml):
+        self.ml = ml
+
+    def c_struct(self):
+        c = self.ml._LayerWeights()
+        c.H, c.N_in, c.K_out, c.E, c.k, c.I = 64, 512, 256, 6, 2, 128
+        return c
+
+
+def layer_call(b, M=2, hidden=None, **kw):
+    cache = b.ml.KvCache(Tensor((10, 2, 16, 64)), Tensor((10, 2, 16, 64)))
+    batch = b.ml.Batch(ints(M + 1), ints(M), ints(M, 4))
+    att = b.ml.LayerAttention(4, 0.125, cache, batch, ints(M), ints(M))
+    return b.ml.decode_layer_attention(b.h, Weights(b.ml), att, Tensor((M, 64)) if hidden is None else hidden, **kw)
+
+
+def test_layer_trace_is_made_on_the_stream_of_the_call(b):
+    s = Stream(7)
+    trace = layer_call(b, trace=True, stream=s)
+    assert sorted(trace) == ["h1", "idx", "scores", "w"]
+    assert all(t.made_on is s for t in trace.values())
+    assert all(ws.made_on is s for ws in b.h._layer_ws.values())
+    trace = layer_call(b, trace=True)
+    assert all(t.made_on is b.current for t in trace.values())

@@ -50,3 +50,30 @@ def test_attention_workspace_is_memory_of_its_stream(h):
     torch.cuda.synchronize()
     assert torch.equal(got, want)
     assert (host_bits(out).reshape(alone.shape) == alone).all()
+
+
+def test_layer_trace_is_memory_of_its_stream(h):
+    import torch
+    import moe_layers_gb300 as ML
+    from test_gpu_layer_attention import H, Layer, i32
+    M, size = 40, 16
+    L = Layer(4, 2, 64, 0, True)
+    pool = torch.randn((2, M, 2, size, 64), device="cuda").to(torch.bfloat16)
+    lens = i32([5] * M)
+    batch = ML.Batch(i32(range(M + 1)), lens, i32([[b] for b in range(M)]))
+    x0 = torch.randn((M, H), device="cuda").to(torch.bfloat16)
+    streams = [torch.cuda.current_stream(), torch.cuda.Stream()]
+    results = []
+    for s in streams:
+        # a cache of its own for each run, which writes its rows' own tokens
+        cache = ML.KvCache(pool[0].clone(), pool[1].clone())
+        att = ML.LayerAttention(4, 0.125, cache, batch, lens, i32([b * size + 4 for b in range(M)]))
+        ML.decode_layer_attention(h, L.w, att, x0.clone(), stream=s)  # makes the workspace
+        x = x0.clone()
+        want, got = read_late(h, 2 * M * H)  # the size of h1
+        trace = ML.decode_layer_attention(h, L.w, att, x, trace=True, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        results.append(dict(trace, x=x))
+    for n, t in results[0].items():
+        assert torch.equal(t, results[1][n]), n
