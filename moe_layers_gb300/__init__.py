@@ -866,10 +866,11 @@ def decode_layer_attention(h: Handle, weights: LayerWeights, attention: LayerAtt
                c.head_dim, attention.batch.prefix_len > 0)
         ws = h._layer_ws.get(key)
         if ws is None:
-            if torch.cuda.is_current_stream_capturing():
-                raise RuntimeError("decode_layer_attention: the first call of a shape makes its zeroed workspace; make it "
-                                   "before the capture, or pass ws")
-            with _on_stream(stream):
+            # on the call's stream, which is another device's than the current one if the handle is
+            with torch.cuda.stream(torch.cuda.current_stream(h.device) if stream is None else stream):
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("decode_layer_attention: the first call of a shape makes its zeroed workspace; "
+                                       "make it before the capture, or pass ws")
                 ws = torch.zeros(decode_layer_attention_workspace_size(h, weights, attention, M), dtype=torch.uint8,
                                  device=hidden.device)
             h._layer_ws[key] = ws

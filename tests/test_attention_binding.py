@@ -83,8 +83,10 @@ def b(monkeypatch):
     @contextlib.contextmanager
     def stream(s):
         before, at.current = at.current, s
-        yield
-        at.current = before
+        try:
+            yield
+        finally:
+            at.current = before
 
     def make(*shape, dtype=None, device=None):
         shape = shape[0] if isinstance(shape[0], (tuple, list)) else shape
@@ -165,3 +167,20 @@ def test_layer_trace_is_made_on_the_stream_of_the_call(b):
     assert all(ws.made_on is s for ws in b.h._layer_ws.values())
     trace = layer_call(b, trace=True)
     assert all(t.made_on is b.current for t in trace.values())
+
+
+def test_layer_workspace_is_not_made_in_a_capture_of_the_given_stream(b):
+    """The zeroes would be recorded instead of written, and the workspace kept for eager calls."""
+    s = Stream(7, capturing=True)
+    with pytest.raises(RuntimeError, match="before the capture"):
+        layer_call(b, stream=s)
+    assert not b.h._layer_ws and "decode_layer_attention" not in b.lib.calls
+    s.capturing = False
+    layer_call(b, stream=s)
+    s.capturing = True
+    layer_call(b, stream=s)  # the workspace is there
+    # a capture of the current stream does not concern a call on another one
+    b.current.capturing = True
+    layer_call(b, M=3, stream=Stream(8))
+    with pytest.raises(RuntimeError, match="before the capture"):
+        layer_call(b, M=3)

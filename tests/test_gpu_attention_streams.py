@@ -77,3 +77,33 @@ def test_layer_trace_is_memory_of_its_stream(h):
         results.append(dict(trace, x=x))
     for n, t in results[0].items():
         assert torch.equal(t, results[1][n]), n
+
+
+def test_layer_workspace_is_not_made_in_a_capture_of_the_given_stream(h):
+    import torch
+    import moe_layers_gb300 as ML
+    from test_gpu_layer_attention import H, Layer, i32
+    L = Layer(4, 2, 64, 0, True)
+    pool = torch.zeros((2, 2, 2, 16, 64), dtype=torch.bfloat16, device="cuda")
+    batch = ML.Batch(i32([0, 1]), i32([1]), i32([[0]]))
+    att = ML.LayerAttention(4, 0.125, ML.KvCache(pool[0], pool[1]), batch, i32([0]), i32([0]))
+    x0 = torch.randn((1, H), device="cuda").to(torch.bfloat16)
+    s, other = torch.cuda.Stream(), torch.cuda.Stream()
+    x = x0.clone()
+    torch.cuda.synchronize()
+    with pytest.raises(RuntimeError, match="before the capture"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=s):
+            with torch.cuda.stream(other):
+                ML.decode_layer_attention(h, L.w, att, x, stream=s)
+    torch.cuda.synchronize()
+    assert not h._layer_ws and torch.equal(x, x0)
+    want = x0.clone()
+    ML.decode_layer_attention(h, L.w, att, want, stream=s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        with torch.cuda.stream(other):
+            ML.decode_layer_attention(h, L.w, att, x, stream=s)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(x, want)
