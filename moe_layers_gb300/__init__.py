@@ -854,9 +854,10 @@ def decode_layer_attention(h: Handle, weights: LayerWeights, attention: LayerAtt
     _require(hidden, torch.bfloat16, "hidden", 2)
     _described(h, attention, "attention")
     M = hidden.shape[0]
-    if hidden.get_device() != h.device or not hidden.is_contiguous() or attention.rows != M:
-        raise ValueError("hidden must be contiguous on the handle's device, with as many rows as attention's positions")
     cw = weights.c_struct() if _cw is None else _cw
+    if hidden.get_device() != h.device or not hidden.is_contiguous() or attention.rows != M or hidden.shape[1] != cw.H:
+        raise ValueError("hidden must be contiguous on the handle's device, as wide as the weights' H and with as many "
+                         "rows as attention's positions")
     sp = _stream_of(h, stream)
     if ws is None:
         # one per stream and shape, kept until the handle closes: a captured graph may

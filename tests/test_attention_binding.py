@@ -109,6 +109,7 @@ def b(monkeypatch):
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: at.current.capturing)
     at.h = ml.Handle(0)
     at.h._h.value = 1
+    at.lib.calls.clear()
     yield at
     at.h._h.value = None  # nothing to destroy
 
@@ -184,3 +185,13 @@ def test_layer_workspace_is_not_made_in_a_capture_of_the_given_stream(b):
     layer_call(b, M=3, stream=Stream(8))
     with pytest.raises(RuntimeError, match="before the capture"):
         layer_call(b, M=3)
+
+
+@pytest.mark.parametrize("hidden", [Tensor((2, 56)), Tensor((2, 72)), Tensor((2, 64), stride=(128, 1)), Tensor((3, 64)),
+                                    Tensor((2, 64), device=1), Tensor((2, 64), torch.float16), Tensor((128,))],
+                         ids=lambda t: f"{t.shape}{t.stride()}{t.dtype}{t.device}")
+def test_layer_refuses_hidden_states_of_another_form(b, hidden):
+    """The layer's width comes from the weights: M x H values are read and written."""
+    with pytest.raises(ValueError):
+        layer_call(b, hidden=hidden)
+    assert not b.lib.calls

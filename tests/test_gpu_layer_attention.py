@@ -222,3 +222,17 @@ def test_layer_attention_refuses(h):
         ML.decode_layer_attention(h, L.w, ML.LayerAttention(4, 0.125, ML.KvCache(pool, pool), batch, one, one),
                                   torch.zeros((2, H), dtype=torch.bfloat16, device="cuda"))
     torch.cuda.synchronize()
+
+
+def test_layer_attention_refuses_another_width(h):
+    """The weights' H values of each row are read and written: a narrower or wider hidden state is refused."""
+    import torch
+    import moe_layers_gb300 as ML
+    L = Layer(4, 2, 64, 0, True)
+    pool = torch.zeros((4, 2, 16, 64), dtype=torch.bfloat16, device="cuda")
+    batch = ML.Batch(i32([0, 1]), i32([1]), i32([[0]]))
+    att = ML.LayerAttention(4, 0.125, ML.KvCache(pool, pool), batch, i32([0]), i32([0]))
+    for width in (H - 8, H + 8, 8):
+        x = torch.zeros((1, width), dtype=torch.bfloat16, device="cuda")
+        with pytest.raises(ValueError):
+            ML.decode_layer_attention(h, L.w, att, x)
