@@ -858,6 +858,13 @@ def decode_layer_attention(h: Handle, weights: LayerWeights, attention: LayerAtt
     if hidden.get_device() != h.device or not hidden.is_contiguous() or attention.rows != M or hidden.shape[1] != cw.H:
         raise ValueError("hidden must be contiguous on the handle's device, as wide as the weights' H and with as many "
                          "rows as attention's positions")
+    forms = dict(h1=(cw.H, torch.bfloat16), idx=(cw.k, torch.int32), w=(cw.k, torch.float32), scores=(cw.E, torch.float32))
+    for n, t in trace.items() if isinstance(trace, dict) else ():
+        if t is not None and n in forms:
+            width, dtype = forms[n]
+            _require(t, dtype, n, 2)
+            if t.shape[0] < M or t.shape[1] != width or not t.is_contiguous() or t.get_device() != h.device:
+                raise ValueError(f"trace: {n} must be contiguous [{M}, {width}] (or more rows) on the handle's device")
     sp = _stream_of(h, stream)
     if ws is None:
         # one per stream and shape, kept until the handle closes: a captured graph may
@@ -878,10 +885,7 @@ def decode_layer_attention(h: Handle, weights: LayerWeights, attention: LayerAtt
     out = trace if isinstance(trace, dict) else None
     if trace is True:
         with _on_stream(stream):
-            out = dict(h1=torch.empty_like(hidden),
-                       idx=torch.empty((M, cw.k), dtype=torch.int32, device=hidden.device),
-                       w=torch.empty((M, cw.k), dtype=torch.float32, device=hidden.device),
-                       scores=torch.empty((M, cw.E), dtype=torch.float32, device=hidden.device))
+            out = {n: torch.empty((M, width), dtype=dtype, device=hidden.device) for n, (width, dtype) in forms.items()}
     tr = None
     if out is not None:
         tr = _LayerTrace()

@@ -195,3 +195,36 @@ def test_layer_refuses_hidden_states_of_another_form(b, hidden):
     with pytest.raises(ValueError):
         layer_call(b, hidden=hidden)
     assert not b.lib.calls
+
+
+TRACE = dict(h1=lambda **kw: Tensor((2, 64), **kw), idx=lambda **kw: Tensor((2, 2), torch.int32, **kw),
+             w=lambda **kw: Tensor((2, 2), torch.float32, **kw), scores=lambda **kw: Tensor((2, 6), torch.float32, **kw))
+BAD_TRACE = [dict(h1=Tensor((1, 64))), dict(h1=Tensor((2, 56))), dict(h1=Tensor((2, 64), torch.float32)),
+             dict(h1=Tensor((2, 64), stride=(72, 1))), dict(h1=Tensor((2, 64), device=1)),
+             dict(idx=Tensor((2, 1), torch.int32)), dict(idx=Tensor((2, 2), torch.int64)),
+             dict(w=Tensor((2, 2))), dict(w=Tensor((1, 2), torch.float32)), dict(scores=Tensor((2, 2), torch.float32)),
+             dict(scores=Tensor((2, 6), torch.float32, stride=(1, 2))), dict(idx=torch.zeros((2, 2), dtype=torch.int32))]
+
+
+@pytest.mark.parametrize("bad", BAD_TRACE, ids=lambda d: f"{next(iter(d))}-{BAD_TRACE.index(d)}")
+def test_layer_refuses_trace_tensors_of_another_form(b, bad):
+    """M x H, M x k and M x E values are written to them."""
+    trace = {n: make() for n, make in TRACE.items()}
+    trace.update(bad)
+    with pytest.raises(ValueError):
+        layer_call(b, trace=trace)
+    with pytest.raises(ValueError):
+        layer_call(b, trace=bad)
+    assert not b.lib.calls
+
+
+def test_layer_takes_trace_tensors(b):
+    for names in ("h1", "idx w", "scores", "h1 idx w scores", ""):
+        trace = {n: TRACE[n]() for n in names.split()}
+        assert layer_call(b, trace=trace) is trace
+        given = b.lib.calls["decode_layer_attention"][5]
+        if trace:
+            for n in TRACE:
+                assert getattr(given._obj, n) == (trace[n].data_ptr() if n in trace else None)
+    layer_call(b, trace=dict(h1=Tensor((64, 64))))  # of a larger batch
+    assert layer_call(b, trace=False) is None and layer_call(b, trace=dict(h1=None, idx=TRACE["idx"]()))
