@@ -602,6 +602,13 @@ def _ints_of(t, name: str, device: int, count: Optional[int] = None) -> int:
     return t.data_ptr()
 
 
+def _ws_bytes(ws, device: int) -> int:
+    """Bytes of a caller's workspace, a contiguous tensor of any type on the device."""
+    if not ws.is_cuda or ws.get_device() != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous on the handle's device, cuda:{device}")
+    return ws.numel() * ws.element_size()
+
+
 class KvCache:
     """Paged key / value cache of one layer (see dec_kv_cache): k and v bf16
     [blocks, kv_heads, block_size, head_dim], each block contiguous (the two may
@@ -801,14 +808,17 @@ def dec_attention(h: Handle, q, cache: KvCache, batch: Batch, scale: float, out=
     _described(h, cache, "cache")
     _described(h, batch, "batch")
     sp = _stream_of(h, stream)
-    if ws is None:
+    if ws is not None:
+        nbytes = _ws_bytes(ws, dev)
+    else:
         shape = (M, heads, cache.head_dim, cache.kv_heads, batch.prefix_len > 0)
         size = h._attention_ws.get(shape)
         if size is None:
             size = h._attention_ws[shape] = dec_attention_workspace_size(h, M, heads, cache, batch)
         ws = h.stream_workspace("attention", sp, size, stream)
+        nbytes = ws.numel()
     st = _load().dec_attention(h.ptr, q.data_ptr(), ldq, cache._ref, batch._ref, scale, out.data_ptr(), ldo, M, heads,
-                               ws.data_ptr(), ws.numel(), sp)
+                               ws.data_ptr(), nbytes, sp)
     if st:
         _check(st, "dec_attention")
     return out
@@ -891,8 +901,8 @@ def decode_layer_attention(h: Handle, weights: LayerWeights, attention: LayerAtt
         tr = _LayerTrace()
         tr.h1, tr.idx, tr.w, tr.scores = (_ptr(out.get(n)) for n in ("h1", "idx", "w", "scores"))
     _check(_load().decode_layer_attention(h.ptr, ctypes.byref(cw), attention._ref, _ptr(hidden), M,
-                                          ctypes.byref(tr) if tr is not None else None, _ptr(ws), ws.numel(), sp),
-           "decode_layer_attention")
+                                          ctypes.byref(tr) if tr is not None else None, _ptr(ws),
+                                          _ws_bytes(ws, h.device), sp), "decode_layer_attention")
     return out
 
 

@@ -228,3 +228,22 @@ def test_layer_takes_trace_tensors(b):
                 assert getattr(given._obj, n) == (trace[n].data_ptr() if n in trace else None)
     layer_call(b, trace=dict(h1=Tensor((64, 64))))  # of a larger batch
     assert layer_call(b, trace=False) is None and layer_call(b, trace=dict(h1=None, idx=TRACE["idx"]()))
+
+
+BAD_WS = [torch.zeros(10000, dtype=torch.uint8), Tensor((10000,), torch.uint8, device=1),
+          Tensor((10000,), torch.uint8, stride=(0,)), Tensor((100, 100), torch.uint8, stride=(1, 100))]
+
+
+@pytest.mark.parametrize("ws", BAD_WS, ids=["host", "other device", "expanded", "not contiguous"])
+@pytest.mark.parametrize("call", [attention_call, layer_call])
+def test_workspaces_of_another_form_are_refused(b, call, ws):
+    with pytest.raises(ValueError):
+        call(b, ws=ws)
+    assert not b.lib.calls
+
+
+@pytest.mark.parametrize("call,name,size_at", [(attention_call, "dec_attention", 11), (layer_call, "decode_layer_attention", 7)])
+def test_workspaces_count_in_bytes(b, call, name, size_at):
+    for t in (Tensor((6000,), torch.uint8), Tensor((60, 100), torch.float32)):
+        call(b, ws=t)
+        assert b.lib.calls[name][size_at - 1:size_at + 1] == (t.data_ptr(), t.numel() * t.element_size())
