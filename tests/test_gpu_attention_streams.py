@@ -68,8 +68,9 @@ def test_layer_trace_is_memory_of_its_stream(h):
         # a cache of its own for each run, which writes its rows' own tokens
         cache = ML.KvCache(pool[0].clone(), pool[1].clone())
         att = ML.LayerAttention(4, 0.125, cache, batch, lens, i32([b * size + 4 for b in range(M)]))
-        ML.decode_layer_attention(h, L.w, att, x0.clone(), stream=s)  # makes the workspace
-        x = x0.clone()
+        first, x = x0.clone(), x0.clone()
+        torch.cuda.synchronize()
+        ML.decode_layer_attention(h, L.w, att, first, stream=s)  # makes the workspace
         want, got = read_late(h, 2 * M * H)  # the size of h1
         trace = ML.decode_layer_attention(h, L.w, att, x, trace=True, stream=s)
         torch.cuda.synchronize()
@@ -88,6 +89,7 @@ def test_layer_workspace_is_not_made_in_a_capture_of_the_given_stream(h):
     batch = ML.Batch(i32([0, 1]), i32([1]), i32([[0]]))
     att = ML.LayerAttention(4, 0.125, ML.KvCache(pool[0], pool[1]), batch, i32([0]), i32([0]))
     x0 = torch.randn((1, H), device="cuda").to(torch.bfloat16)
+    want = x0.clone()
     s, other = torch.cuda.Stream(), torch.cuda.Stream()
     x = x0.clone()
     torch.cuda.synchronize()
@@ -97,7 +99,6 @@ def test_layer_workspace_is_not_made_in_a_capture_of_the_given_stream(h):
                 ML.decode_layer_attention(h, L.w, att, x, stream=s)
     torch.cuda.synchronize()
     assert not h._layer_ws and torch.equal(x, x0)
-    want = x0.clone()
     ML.decode_layer_attention(h, L.w, att, want, stream=s)
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
