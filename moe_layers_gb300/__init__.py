@@ -718,7 +718,8 @@ def dec_batch_tables(h: Handle, ctx_len, new_len, free_blocks, free_count, block
                      stream=None) -> StepTables:
     """Positions, slots and block-table entries of one step from the requests'
     lengths (int32 tensors); block_table [requests, max_blocks] is updated in
-    place. `out` gives the output tensors, else they are made for `rows` rows."""
+    place. free_count is at most free_blocks' elements (0 if it has none). `out`
+    gives the output tensors, else they are made for `rows` rows."""
     dev = h.device
     n = ctx_len.numel()
     if out is None:
@@ -734,9 +735,10 @@ def dec_batch_tables(h: Handle, ctx_len, new_len, free_blocks, free_count, block
         raise ValueError("block_table and out must be of as many requests as ctx_len, free_count of one value, all on "
                          "the handle's device")
     _described(h, out, "out")
+    count = _ints_of(free_count, "free_count", dev)
     st = _load().dec_batch_tables(h.ptr, _ints_of(ctx_len, "ctx_len", dev), _ints_of(new_len, "new_len", dev, n), n,
-                                  _ints_of(free_blocks, "free_blocks", dev), _ints_of(free_count, "free_count", dev),
-                                  block_table.data_ptr(), width, block_size, position_offset, out.rows, out._ref,
+                                  _ints_of(free_blocks, "free_blocks", dev) or count,  # no address without elements
+                                  count, block_table.data_ptr(), width, block_size, position_offset, out.rows, out._ref,
                                   _stream_of(h, stream))
     if st:
         _check(st, "dec_batch_tables")

@@ -247,3 +247,24 @@ def test_workspaces_count_in_bytes(b, call, name, size_at):
     for t in (Tensor((6000,), torch.uint8), Tensor((60, 100), torch.float32)):
         call(b, ws=t)
         assert b.lib.calls[name][size_at - 1:size_at + 1] == (t.data_ptr(), t.numel() * t.element_size())
+
+
+def tables_call(b, free, n=2, rows=3):
+    out = b.ml.StepTables(ints(n + 1), ints(n), ints(rows), ints(rows), ints(2))
+    count = ints(1)
+    b.ml.dec_batch_tables(b.h, ints(n), ints(n), free, count, ints(n, 4), 16, out)
+    return b.lib.calls["dec_batch_tables"][4:6] + (count,)
+
+
+def test_tables_take_an_empty_free_list(b):
+    """A tensor without elements has no address, which the library takes for a missing argument:
+    another one stands for it (with a count of 0 nothing is read there)."""
+    free, at, count = tables_call(b, ints(0))
+    assert free == at == count.data_ptr() != 0
+    given = ints(5)
+    free, at, count = tables_call(b, given)
+    assert free == given.data_ptr() and at == count.data_ptr()
+    with pytest.raises(ValueError):
+        tables_call(b, ints(0, device=1))
+    with pytest.raises(ValueError):
+        tables_call(b, Tensor((0,), torch.int64))

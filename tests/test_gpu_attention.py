@@ -748,3 +748,10 @@ def test_operators_together(h):
         tol = 2.0 ** -8 * np.abs(ref) + spread * (2.0 ** -8 + 2.0 ** -12 + 2 * d * 2.0 ** -23 * reach[..., None])
         assert np.all(np.abs(got - ref)[used] <= tol[used])
         assert np.all(got[sum(new):] == 0)
+
+
+def test_tables_with_an_empty_free_list(h):
+    """A free list without elements is a list that is used up: requests within their blocks go on, others get -1."""
+    check_tables(h, [3, 16, 0], [2, 1, 4], [], 0, [[1, -1], [2, -1], [-1, -1]], 16, 5, 9)
+    check_tables(h, [3], [2], [], 0, [[1, -1]], 16, 0, 2)
+    check_tables(h, [0] * 3, [3000, 1, 2000], [], 0, np.full((3, 200), 7), 16, 0, 5010)
