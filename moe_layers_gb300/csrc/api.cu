@@ -936,6 +936,8 @@ static dec_status layer_entry(dec_handle* h, const dec_layer_weights* Wt, const 
   carve_layer(measure, h, Wt, M, &w, A);
   if (ws == nullptr || ws_bytes < measure.used) return DEC_ERR_INVALID_ARG;
   carve_layer(c, h, Wt, M, &w, A);
+  DeviceGuard dev(h->device);
+  if (!dev.ok) return DEC_ERR_CUDA;
   uint16_t* h1 = (trace && trace->h1) ? trace->h1 : w.h1;
   const int H = L.H;
 

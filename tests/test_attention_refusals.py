@@ -177,3 +177,31 @@ def test_oracle_rope_is_a_rotation():
         z = rng.standard_normal((4, 2, 64))
         c, d = oracle.rope(z, [2] * 4, f, inter), oracle.rope(z, [1002] * 4, f, inter)
         assert np.allclose((a * c).sum(-1), (b * d).sum(-1))
+
+
+@pytest.mark.parametrize("M", [2, 40])
+def test_nothing_is_launched_where_the_device_is_not_there(ml, M):
+    """The entry points make the handle's device current before the first launch: on the default stream of
+    another device, kernels would take this one's addresses."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("shows by the launch count that no call reaches a device, for a machine without one")
+    handle = ctypes.create_string_buffer(4096)
+    handle[0:4] = (1000).to_bytes(4, "little")  # the device
+    lib, c, b = ml._load(), cache(ml), batch(ml)
+    rope, tables = ml._Rope(64, 0, 1.0, A), ml._StepTables(A, A, A, A, A)
+    att = ml._LayerAttention(4, 0.125, ctypes.addressof(rope), ctypes.addressof(c), ctypes.addressof(b), A, A)
+    w = ml._LayerWeights()
+    w.H, w.N_in, w.K_out, w.E, w.k, w.I, w.eps = 256, 512, 256, 16, 4, 128, 1e-6
+    for n in ("gamma1", "W_in", "W_o", "gamma2", "W_r", "Wg", "Wu", "Wd"):
+        setattr(w, n, A)
+    ref = ctypes.byref
+    answers = [
+        lib.dec_batch_tables(handle, A, A, 2, A, A, A, 4, 16, 0, 2, ref(tables), None),
+        lib.dec_rope_phases(handle, A, 64, 1e4, 0, 1.0, 8192.0, 1.0, 4.0, None),
+        lib.dec_rope_append(handle, ref(rope), 2 * A, 256, A, 128, A, 128, 3 * A, 256, M, 4, A, A, ref(c), None),
+        lib.dec_attention(handle, 2 * A, 256, ref(c), ref(b), 0.125, 3 * A, 256, M, 4, A, 1 << 40, None),
+        lib.decode_layer_attention(handle, ref(w), ref(att), A, M, None, A, 1 << 40, None),
+        lib.decode_layer(handle, ref(w), A, M, None, A, 1 << 40, None)]
+    assert answers == [3] * 6  # DEC_ERR_CUDA
+    assert lib.dec_launch_count(handle) == 0
