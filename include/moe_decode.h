@@ -489,8 +489,8 @@ dec_status dec_attention_workspace_size(const dec_handle* h, int M, int q_heads,
  * q [M][q_heads * head_dim] with row stride ldq, out the same with ldo; out
  * must not overlap q. 1 <= M <= 64, q_heads a multiple of kv_heads, at most
  * 1024 in all and 128 to a key head, scale in [1e-30, 1e30]. Scores, softmax
- * statistics and sums are fp32; the weights p are rounded to bf16 for the
- * product with v. */
+ * statistics and sums are fp32; the weights p, up to a factor that a row's
+ * keys share, are rounded to bf16 for the product with v. */
 dec_status dec_attention(dec_handle* h, const dec_bf16* q, int64_t ldq, const dec_kv_cache* cache,
                          const dec_batch* batch, float scale, dec_bf16* out, int64_t ldo, int M, int q_heads,
                          void* ws, size_t ws_bytes, cudaStream_t stream);

@@ -445,10 +445,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int i = 0; i < 16; ++i) {
             const float w0 = ex2(fmaf(__uint_as_float(x[2 * i]), L.scale_log2, -ref));
             const float w1 = ex2(fmaf(__uint_as_float(x[2 * i + 1]), L.scale_log2, -ref));
-            l0 += w0;
-            l1 += w1;
-            // P is rounded to bf16 for the product with V (fp32 sums; l keeps the unrounded weights)
+            // P is rounded to bf16 for the product with V; l sums the rounded weights too:
+            // with the maximum left behind by up to 2^8, the weight of a key that dominates
+            // is no power of two, and its rounding cancels only so
             p[i] = pack_bf16x2(w0, w1);
+            l0 += bf_lo(p[i]);
+            l1 += bf_hi(p[i]);
           }
           tmem_st16(ts + h * 16, p);
         };

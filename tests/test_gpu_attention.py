@@ -755,3 +755,20 @@ def test_tables_with_an_empty_free_list(h):
     check_tables(h, [3, 16, 0], [2, 1, 4], [], 0, [[1, -1], [2, -1], [-1, -1]], 16, 5, 9)
     check_tables(h, [3], [2], [], 0, [[1, -1]], 16, 0, 2)
     check_tables(h, [0] * 3, [3000, 1, 2000], [], 0, np.full((3, 200), 7), 16, 0, 5010)
+
+
+# own tokens, with and without a prefix, and a prefix with one own token a row; one and two streams
+@pytest.mark.parametrize("heads,kv,d,new,more,prefix", [(64, 16, 128, [16] * 3, 700, 0), (64, 16, 128, [64], 700, 500),
+                                                        (8, 2, 64, [30], 700, 0), (32, 32, 128, [1] * 64, 1, 6085)])
+def test_attention_averages_equal_values_to_that_value(h, heads, kv, d, new, more, prefix):
+    """In the tensor-memory kernel, whatever the weights are, their average of one value is that value, exactly:
+    the weights that are summed are the rounded ones that are multiplied. (fp32 sums of at most 7000 terms are
+    off by less than 2^-11, and 255/128 would round to its neighbour 2^-9 away. A single own token has weight 1.)"""
+    for seed, sharp in ((1, 1.0), (2, 4.0), (3, 12.0)):
+        rng = np.random.default_rng(seed)
+        own = [n + int(rng.integers(0, more)) for n in new]
+        c = Case(new, own, heads, kv, d, 16, prefix=prefix, seed=seed, sharp=sharp)
+        values = 255.0 / 128 * np.exp2(rng.integers(-3, 4, d)) * rng.choice([-1.0, 1.0], d)
+        c.v[:] = bf16(values)
+        wrong = np.sum(oracle.as_f64(c.run(h)) != values)
+        assert wrong == 0
