@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
               p[j][e] = see ? p[j][e] : -INFINITY;
             }
         }
-        // running maximum (log2 units), shared by the four threads of a row
+        // running maximum, shared by the four threads of a row
         float ref[NE], up[NE];
         bool grew = false;
 #pragma unroll
@@ -372,10 +372,10 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
           for (int j = 0; j < NK; ++j) x = fmaxf(x, fmaxf(p[j][2 * e], p[j][2 * e + 1]));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-          const float mn = fmaxf(m[e], x * L.scale_log2);
+          const float mn = fmaxf(m[e], x);
           grew = grew || mn > m[e];
           ref[e] = mn == -INFINITY ? 0.f : mn;
-          up[e] = ex2_from(m[e], ref[e]);
+          up[e] = ex2_from(m[e], ref[e], L.scale_log2);
           m[e] = mn;
         }
         if (__any_sync(0xffffffffu, grew)) {
@@ -398,8 +398,8 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
               pf[j >> 1][(j & 1) * 2 + e] = 0u;
               continue;
             }
-            const float w0 = ex2(fmaf(p[j][2 * e], L.scale_log2, -ref[e % NE]));
-            const float w1 = ex2(fmaf(p[j][2 * e + 1], L.scale_log2, -ref[e % NE]));
+            const float w0 = ex2((p[j][2 * e] - ref[e % NE]) * L.scale_log2);
+            const float w1 = ex2((p[j][2 * e + 1] - ref[e % NE]) * L.scale_log2);
             l[e % NE] += w0 + w1;
             // P is rounded to bf16 for the product with V (fp32 sums; l keeps the unrounded weights)
             pf[j >> 1][(j & 1) * 2 + e] = pack_bf16x2(w0, w1);
@@ -511,12 +511,12 @@ __global__ void __launch_bounds__(kAttnThreads, kAttnCtasPerSm)
         float f[WK], top = mt;
 #pragma unroll
         for (int w = 1; w < WK; ++w) top = fmaxf(top, sh.ml[warp + w][g].x);
-        f[0] = ex2_from(mt, top);
+        f[0] = ex2_from(mt, top, L.scale_log2);
         lt *= f[0];
 #pragma unroll
         for (int w = 1; w < WK; ++w) {
           const float2 ml = sh.ml[warp + w][g];
-          f[w] = ex2_from(ml.x, top);
+          f[w] = ex2_from(ml.x, top, L.scale_log2);
           lt = fmaf(ml.y, f[w], lt);
         }
         mt = top;
@@ -659,7 +659,7 @@ __global__ void __launch_bounds__(256, 4) join_attention_kernel(const __grid_con
 #pragma unroll
     for (int k = 0; k < B; ++k) {
       const float top = fmaxf(m, ml[k].x);
-      const float f0 = ex2_from(m, top), f1 = ex2_from(ml[k].x, top);
+      const float f0 = ex2_from(m, top, O.scale_log2), f1 = ex2_from(ml[k].x, top, O.scale_log2);
       m = top;
       l = l * f0 + ml[k].y * f1;
 #pragma unroll
@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(256, 4) join_attention_kernel(const __grid_con
       for (int v = 1; v < NW; ++v) {
         const float2 ml = s_ml[warp + v];
         const float top = fmaxf(m, ml.x);
-        const float f0 = ex2_from(m, top), f1 = ex2_from(ml.x, top);
+        const float f0 = ex2_from(m, top, O.scale_log2), f1 = ex2_from(ml.x, top, O.scale_log2);
         m = top;
         l = l * f0 + ml.y * f1;
 #pragma unroll

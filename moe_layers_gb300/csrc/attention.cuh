@@ -24,8 +24,8 @@ namespace dec {
 
 constexpr int kMaxParts = 65;
 
-// Unnormalised sums [rows][dim] with their (maximum, sum) pairs, maxima in
-// units of log2.
+// Unnormalised sums [rows][dim] with their (maximum, sum) pairs, maxima of q . k
+// as it is, without the scale.
 struct Pieces {
   float* o = nullptr;
   float2* ml = nullptr;
@@ -46,7 +46,7 @@ struct AttentionLaunch {
   AttentionParams a;
   Plan plan;
   Pieces start[2];  // prefix, own: [M][q_heads]
-  float scale_log2;
+  float scale_log2;    // the scale times log2 e
   bool late_wait;      // the launch before it on the stream is the same call's prefix launch
   uint32_t group_mul;  // ceil(2^20 / group)
   int* err;
@@ -188,8 +188,14 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// 2^(m - top), 0 for a part that saw nothing (m = -inf, whatever top is).
-__device__ __forceinline__ float ex2_from(float m, float top) { return m == -INFINITY ? 0.f : ex2(m - top); }
+// 2^(scale (m - top)), 0 for a part that saw nothing (m = -inf, whatever top is).
+// The difference comes before the scale, here and for the weights: the largest
+// score's weight is then 1 whatever its size. (With fma(score, scale, -maximum),
+// an instruction less, the rounding of the maximum remains, and from scores of
+// 2^31 on it alone passes the range of an exponential.)
+__device__ __forceinline__ float ex2_from(float m, float top, float scale) {
+  return m == -INFINITY ? 0.f : ex2((m - top) * scale);
+}
 
 // Two floats rounded to nearest-even bf16, the first in the low half.
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {

@@ -33,7 +33,7 @@ namespace {
 constexpr int kTcTile = 128;
 constexpr int kTcThreads = 384;  // warps 0-7 softmax (4 a stream), 8 copies K, 9 copies V, 10 issues products
 constexpr int kTcSmem = 232448;
-constexpr float kRaise = 8.f;    // log2 of the growth of the scores that is left in P
+constexpr float kRaise = 8.f;    // log2 of the growth of the weights that is left in P
 
 template <int D, int NT>
 struct TcShape {
@@ -119,6 +119,28 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Two fp32 values in one 64-bit register, and operations on both at once.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kTcThreads, 1)
@@ -328,6 +350,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int vs = 0;
     uint32_t vph = 0;
     int sees = 0;
+    const float room = kRaise / L.scale_log2;  // above the maximum, in scores
     // The stream's 128 query rows into shared memory (16 bytes a thread, rows
     // contiguous over lanes, every load before any store), and the keys that
     // this thread's row sees.
@@ -414,11 +437,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tmem_ld32_async(ts + 32, x1);
         tmem_wait_ld(x0, x1);
         top = fmaxf(top, fmaxf(largest(x0), largest(x1)));
-        const float mn = top * L.scale_log2;
-        const bool raise = mn > m + kRaise || (m == -INFINITY && mn > -INFINITY);
+        const bool raise = top > m + room || (m == -INFINITY && top > -INFINITY);
         if (__any_sync(0xffffffffu, raise)) {
-          const float f = raise ? ex2_from(m, mn) : 1.f;
-          if (raise) m = mn;
+          const float f = raise ? ex2_from(m, top, L.scale_log2) : 1.f;
+          if (raise) m = top;
           l *= f;
           if (t > q.tile0) {
             // O is still until this tile's P is there, once the tile before is added
@@ -438,19 +460,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
         const float ref = m == -INFINITY ? 0.f : m;
-        float l0 = 0.f, l1 = 0.f;
+        const uint64_t less = pair(-ref, -ref), scale = pair(L.scale_log2, L.scale_log2);
+        uint64_t sum = 0;  // of even and odd columns
         auto weigh = [&](const uint32_t (&x)[32], int h) {
           uint32_t p[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float w0 = ex2(fmaf(__uint_as_float(x[2 * i]), L.scale_log2, -ref));
-            const float w1 = ex2(fmaf(__uint_as_float(x[2 * i + 1]), L.scale_log2, -ref));
+            const uint64_t s2 = pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+            const float2 e = unpair(mul2(add2(s2, less), scale));
             // P is rounded to bf16 for the product with V; l sums the rounded weights too:
             // with the maximum left behind by up to 2^8, the weight of a key that dominates
             // is no power of two, and its rounding cancels only so
-            p[i] = pack_bf16x2(w0, w1);
-            l0 += bf_lo(p[i]);
-            l1 += bf_hi(p[i]);
+            p[i] = pack_bf16x2(ex2(e.x), ex2(e.y));
+            sum = add2(sum, pair(bf_lo(p[i]), bf_hi(p[i])));
           }
           tmem_st16(ts + h * 16, p);
         };
@@ -462,7 +484,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         weigh(x2, 2);
         tmem_wait_ld(x0, x1);
         weigh(x0, 3);
-        l += l0 + l1;
+        const float2 both = unpair(sum);
+        l += both.x + both.y;
         if (key0 + kTcTile > fewest) {
           // Keys behind the part's last one hold anything (NaN too): their V is
           // made zero, as 0 * NaN would not be. Keys that some rows see and others

@@ -772,3 +772,35 @@ def test_attention_averages_equal_values_to_that_value(h, heads, kv, d, new, mor
         c.v[:] = bf16(values)
         wrong = np.sum(oracle.as_f64(c.run(h)) != values)
         assert wrong == 0
+
+
+@pytest.mark.parametrize("heads,kv,d,new,prefix", [(8, 2, 128, [1] * 5, 0), (8, 2, 64, [1] * 5, 200), (16, 1, 128, [1] * 3, 0),
+                                                   (32, 1, 64, [1] * 3, 300), (8, 2, 128, [16] * 2, 100), (8, 2, 64, [30], 0),
+                                                   (32, 32, 128, [1] * 64, 6085)])
+@pytest.mark.parametrize("scale", [1e4, 1e9, 1e12, 1e30])
+def test_attention_of_huge_scores_takes_the_largest(h, heads, kv, d, new, prefix, scale):
+    """Scores far apart (a large scale): the output is the value of the largest score's key, or, where keys
+    are the same, the mean of theirs. q and k hold small whole numbers, so that scores are exact in fp32 and
+    the gap between two of them is at least 1 before the scale."""
+    rng = np.random.default_rng(len(new) + prefix)
+    own = [n + int(rng.integers(0, 400)) for n in new]
+    c = Case(new, own, heads, kv, d, 16, prefix=prefix, seed=prefix + d)
+    c.q[:] = bf16(rng.integers(-40, 41, tuple(c.q.shape)))
+    c.k[:] = bf16(rng.integers(-40, 41, tuple(c.k.shape)))
+    c.scale = scale
+    got = oracle.as_f64(c.run(h))
+    want, spread, _ = reference64(c)
+    # the mean of equally large scores: weights of 1 are exact, one rounding of the output, fp32 sums
+    assert np.all(np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + spread * 2.0 ** -20)
+
+
+def test_attention_of_large_values(h):
+    """Scores of 10^12 from large q and k, with the usual scale: as above."""
+    rng = np.random.default_rng(3)
+    for new, heads, prefix in (([1] * 4, 8, 130), ([16, 16], 16, 0)):
+        c = Case(new, [n + 150 for n in new], heads, 2, 64, 16, prefix=prefix, seed=3)
+        c.q[:] = bf16(rng.integers(-40, 41, tuple(c.q.shape)) * 2.0 ** 14)
+        c.k[:] = bf16(rng.integers(-40, 41, tuple(c.k.shape)) * 2.0 ** 14)
+        got = oracle.as_f64(c.run(h))
+        want, spread, _ = reference64(c)
+        assert np.all(np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + spread * 2.0 ** -20)
