@@ -85,7 +85,8 @@ __device__ __forceinline__ int cta_of_unit(long long u, long long W, long long G
 __device__ __forceinline__ int div_group(int r, uint32_t mul) { return (int)(((uint32_t)r * mul) >> 20); }
 
 // Fills the table with one warp (all 32 lanes). Lengths are brought into
-// range: rows into [0, M] and not decreasing, keys to at most max_blocks blocks.
+// range: rows into [0, M] and not decreasing, the requests' within part 0's (the
+// joining kernel looks each of them up in both), keys to at most max_blocks blocks.
 __device__ __forceinline__ void build_parts(PartTable& t, const AttentionParams& a, const Plan& p) {
   constexpr int kRounds = (kMaxParts + 31) / 32;
   const int lane = threadIdx.x & 31, n = a.requests + 1;
@@ -100,6 +101,8 @@ __device__ __forceinline__ void build_parts(PartTable& t, const AttentionParams&
       if (i > 0) own[k] = ld_act_s32(a.own_len + i - 1);
     }
   }
+  const int begin = min(max(__shfl_sync(0xffffffffu, r0[0], 0), 0), a.M);
+  const int end = min(max(__shfl_sync(0xffffffffu, r1[0], 0), begin), a.M);
   long long carry = 0;
 #pragma unroll
   for (int k = 0; k < kRounds; ++k) {
@@ -107,7 +110,7 @@ __device__ __forceinline__ void build_parts(PartTable& t, const AttentionParams&
     const int i = k * 32 + lane;
     long long units = 0;
     if (i < n) {
-      const int first = min(max(r0[k], 0), a.M), rows = min(max(r1[k], first), a.M) - first;
+      const int first = min(max(r0[k], begin), end), rows = min(max(r1[k], first), end) - first;
       int len = a.prefix_len, last = a.prefix_len;
       if (i > 0) {
         len = max(0, (int)min((long long)own[k], (long long)a.max_blocks << a.shift));

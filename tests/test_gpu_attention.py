@@ -804,3 +804,19 @@ def test_attention_of_large_values(h):
         got = oracle.as_f64(c.run(h))
         want, spread, _ = reference64(c)
         assert np.all(np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + spread * 2.0 ** -20)
+
+
+@pytest.mark.parametrize("prefix,heads,kv,d", [(0, 8, 2, 64), (500, 8, 2, 64), (6085, 32, 32, 128)])
+@pytest.mark.parametrize("start,same", [([0, 20, 12], [0, 12, 12]), ([5, 2, 30], [5, 5, 30]), ([4, 30, 10], [4, 10, 10]),
+                                        ([-9, 3, 99], [0, 3, 40]), ([3, 40, 39], [3, 39, 39]), ([20, 3, 0], [20, 20, 20])])
+def test_attention_row_starts_out_of_order(h, prefix, heads, kv, d, start, same):
+    """Rows at and behind row_start[requests] belong to no request, and none before row_start[0] does,
+    whatever lies between."""
+    c = Case([40, 0], [300, 200], heads, kv, d, 16, prefix=prefix, seed=1)
+    got = []
+    for s in (same, start):
+        c.row_start = s
+        got.append(c.run(h))
+    assert np.array_equal(got[0], got[1])
+    idle = oracle.as_f64(got[0]) == 7.5
+    assert np.all(idle[:max(same[0], 0)]) and np.all(idle[same[2]:]) and not np.any(np.all(idle[same[0]:same[2]], (1, 2)))
