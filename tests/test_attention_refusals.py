@@ -205,3 +205,105 @@ def test_nothing_is_launched_where_the_device_is_not_there(ml, M):
         lib.decode_layer(handle, ref(w), A, M, None, A, 1 << 40, None)]
     assert answers == [3] * 6  # DEC_ERR_CUDA
     assert lib.dec_launch_count(handle) == 0
+
+
+# Each limit by itself: everything else about the call is allowed, as the first case of each list shows by
+# passing the checks (it then ends at the device, which is not there).
+WIDE = dict(block_stride=1 << 24, ldq=1 << 20, ldo=1 << 20)
+ATTENTION_LIMITS = [
+    (dict(WIDE), dict(), None),
+    (dict(WIDE, block_size=128, max_blocks=(1 << 24) - 2), dict(max_blocks=(1 << 24) - 1), "keys"),
+    (dict(WIDE, max_blocks=1 << 24), dict(max_blocks=(1 << 24) + 1), "blocks of a request"),
+    (dict(WIDE, q_heads=2 * 128), dict(q_heads=2 * 129), "heads to a key head"),
+    (dict(WIDE, kv_heads=16, q_heads=1024), dict(q_heads=1040), "heads"),
+    (dict(WIDE, kv_heads=128, q_heads=128), dict(kv_heads=129, q_heads=129), "key heads"),
+    (dict(WIDE, head_dim=128), dict(head_dim=96), "head dim"),
+    (dict(WIDE, head_dim=64), dict(head_dim=80), "head dim"),
+    (dict(WIDE, block_size=16), dict(block_size=24), "block size"),
+    (dict(WIDE, block_size=128), dict(block_size=256), "block size"),
+    (dict(WIDE, block_size=16), dict(block_size=8), "block size"),
+    (dict(WIDE, blocks=(1 << 27) - 1), dict(blocks=1 << 27), "tokens of the cache"),
+    (dict(WIDE, block_stride=(1 << 38) - 8), dict(block_stride=1 << 38), "block stride"),
+    (dict(WIDE, prefix_table=A, prefix_len=(1 << 31) - 256), dict(prefix_len=(1 << 31) - 255), "prefix"),
+    (dict(WIDE, prefix_table=A, prefix_len=5), dict(prefix_table=A + 2), "alignment"),
+    (dict(WIDE, requests=64, M=64, max_new=64), dict(requests=65), "requests"),
+    (dict(WIDE, requests=64, M=64, max_new=64), dict(M=65), "rows"),
+    (dict(WIDE, requests=64, M=64, max_new=64), dict(max_new=65), "new rows"),
+    (dict(WIDE, scale=1e30), dict(scale=1.1e30), "scale"),
+    (dict(WIDE, scale=1.1e-30), dict(scale=0.9e-30), "scale"),
+    (dict(WIDE, ldq=1 << 31), dict(ldq=(1 << 31) + 8), "row stride"),
+    (dict(WIDE, ldo=1 << 31), dict(ldo=(1 << 31) + 8), "row stride"),
+    (dict(WIDE, ldo=256), dict(ldo=248), "row stride"),
+]
+
+
+def attention_answer(ml, handle, kw):
+    c = cache(ml, **{k: v for k, v in kw.items() if k in dict(ml._KvCache._fields_)})
+    b = batch(ml, **{k: v for k, v in kw.items() if k in dict(ml._Batch._fields_)})
+    a = dict(q=2 * A, ldq=256, scale=0.125, out=3 * A, ldo=256, M=2, q_heads=4)
+    a.update({k: v for k, v in kw.items() if k in a})
+    return ml._load().dec_attention(handle, a["q"], a["ldq"], ctypes.byref(c), ctypes.byref(b), a["scale"], a["out"],
+                                    a["ldo"], a["M"], a["q_heads"], 4 * A, 1 << 40, None)
+
+
+@pytest.fixture(scope="module")
+def nowhere():
+    """A handle of a device that no machine has: a call that passes the checks ends there, as a CUDA error."""
+    h = ctypes.create_string_buffer(4096)
+    h[0:4] = (1000).to_bytes(4, "little")
+    return h
+
+
+@pytest.mark.parametrize("good,bad,what", ATTENTION_LIMITS, ids=lambda x: x if isinstance(x, str) else "")
+def test_attention_limits_one_by_one(ml, nowhere, good, bad, what):
+    assert attention_answer(ml, nowhere, good) == 3
+    if bad:
+        assert attention_answer(ml, nowhere, dict(good, **bad)) == INVALID
+
+
+ROPE_LIMITS = [
+    (dict(q_heads=1024), dict(q_heads=1025)), (dict(head_dim=128, rotary_dim=128), dict(rotary_dim=144)),
+    (dict(head_dim=64), dict(head_dim=80)), (dict(rotary_dim=16), dict(rotary_dim=8)),
+    (dict(rotary_dim=0, phases=None), dict(rotary_dim=-16)),
+    (dict(ldk=1 << 31), dict(ldk=(1 << 31) + 8)), (dict(ldv=1 << 31), dict(ldv=(1 << 31) + 8)),
+    (dict(ldq=1 << 31), dict(ldq=(1 << 31) + 8)), (dict(ldqo=1 << 31), dict(ldqo=(1 << 31) + 8)),
+    (dict(ldk=128), dict(ldk=124)), (dict(ldk=136), dict(ldk=132)), (dict(ldv=128), dict(ldv=120)),
+    (dict(q_out=2 * A), dict(q_out=2 * A, ldqo=(1 << 20) + 8)), (dict(rows=1 << 20), dict(rows=(1 << 20) + 1)),
+    (dict(magnitude=-2.0), dict(magnitude=float("nan"))), (dict(slots=A + 4), dict(slots=A + 2)),
+    (dict(positions=A + 4), dict(positions=A + 1)), (dict(q=None, q_out=None, q_heads=0), dict(q_out=3 * A)),
+    (dict(q=None, q_out=None, q_heads=0), dict(q_heads=4)), (dict(interleaved=1), dict(interleaved=-1))]
+
+
+@pytest.mark.parametrize("good,bad", ROPE_LIMITS, ids=str)
+def test_rope_append_limits_one_by_one(ml, nowhere, good, bad):
+    def answer(kw):
+        c = cache(ml, block_stride=1 << 24, **{k: v for k, v in kw.items() if k == "head_dim"})
+        r = dict(rotary_dim=64, interleaved=0, magnitude=1.0, phases=A)
+        r.update({k: v for k, v in kw.items() if k in r})
+        rope = ml._Rope(*r.values())
+        a = dict(q=2 * A, ldq=1 << 20, k=A, ldk=256, v=A, ldv=256, q_out=3 * A, ldqo=1 << 20, rows=2, q_heads=4,
+                 positions=A, slots=A)
+        a.update({k: v for k, v in kw.items() if k in a})
+        return ml._load().dec_rope_append(nowhere, ctypes.byref(rope), *a.values(), ctypes.byref(c), None)
+
+    assert answer(good) == 3
+    assert answer(dict(good, **bad)) == INVALID
+
+
+TABLE_LIMITS = [(dict(n=1024), dict(n=1025)), (dict(max_blocks=1 << 24), dict(max_blocks=(1 << 24) + 1)),
+                (dict(size=128), dict(size=256)), (dict(size=16), dict(size=8)),
+                (dict(rows=1 << 20), dict(rows=(1 << 20) + 1)),
+                (dict(offset=(1 << 31) - 1), dict(offset=-1)), (dict(free=A + 4), dict(free=A + 2)),
+                (dict(table=A + 4), dict(table=A + 3)), (dict(new=A + 4), dict(new=A + 1)), (dict(count=A + 4), dict(count=A + 2))]
+
+
+@pytest.mark.parametrize("good,bad", TABLE_LIMITS, ids=str)
+def test_tables_limits_one_by_one(ml, nowhere, good, bad):
+    def answer(kw):
+        a = dict(TABLES, **kw)
+        out = ml._StepTables(A, A, A, A, A)
+        return ml._load().dec_batch_tables(nowhere, a["ctx"], a["new"], a["n"], a["free"], a["count"], a["table"],
+                                           a["max_blocks"], a["size"], a["offset"], a["rows"], ctypes.byref(out), None)
+
+    assert answer(good) == 3
+    assert answer(dict(good, **bad)) == INVALID
