@@ -820,3 +820,80 @@ def test_attention_row_starts_out_of_order(h, prefix, heads, kv, d, start, same)
     assert np.array_equal(got[0], got[1])
     idle = oracle.as_f64(got[0]) == 7.5
     assert np.all(idle[:max(same[0], 0)]) and np.all(idle[same[2]:]) and not np.any(np.all(idle[same[0]:same[2]], (1, 2)))
+
+
+def test_rope_places_in_a_pool_past_32_bits(h):
+    """k and v interleaved in one pool of more than 2^32 elements: both at their slots, exactly, and nothing where a
+    wrapped offset or the other one's place would be."""
+    import torch
+    import moe_layers_gb300 as ML
+    kv, size, d = 2, 16, 64
+    blocks, per = 1200000, 2 * 16 * 64  # elements of one block of k, and of v
+    pool = torch.empty((blocks, 2, kv, size, d), dtype=torch.bfloat16, device="cuda")
+    assert pool.numel() > 1 << 32
+    pool.view(torch.int16).fill_(0x1234)
+    x = bf16(np.random.default_rng(0).standard_normal((4, 2 * kv * d)))
+    far = (1 << 32) // (2 * per)  # the block that begins at element 2^32
+    slots = [blocks * size - 1, 5, far * size + 3, (far - 1) * size + 15]
+    r = ML.Rope(h, 0)
+    ML.dec_rope_append(h, r, None, x[:, :kv * d], x[:, kv * d:], i32([1, 2, 3, 4]), i32(slots),
+                       ML.KvCache(pool[:, 0], pool[:, 1]))
+    torch.cuda.synchronize()
+    for t, s in enumerate(slots):
+        place = pool[s // size, :, :, s % size].view(torch.int16)  # [k or v][head][element]
+        assert torch.equal(place.reshape(-1), x[t].view(torch.int16))
+        place.fill_(0x1234)
+    for part in pool.view(torch.int16).split(100000):
+        assert bool((part == 0x1234).all())
+    del pool, place, part
+    torch.cuda.empty_cache()
+
+
+def tables_in_place(h, rows, offsets, seed):
+    """A step whose own_len lies over ctx_len and whose left over free_count, with outputs that begin at `offsets`
+    4-byte words behind a 16-byte boundary."""
+    import torch
+    import moe_layers_gb300 as ML
+    rng = np.random.default_rng(seed)
+    n, size = 60, 16
+    ctx = rng.integers(0, 400, n)
+    new = rng.multinomial(rows - 5, np.ones(n) / n)
+    new[3] = 0
+    width = -(-int((ctx + new).max()) // size)
+    ids = rng.permutation(n * width)
+    table = np.full((n, width), -1)
+    at = 0
+    for b in range(n):
+        m = -(-int(ctx[b]) // size)
+        table[b, :m] = ids[at:at + m]
+        at += m
+    free = ids[at:]
+    count = len(free) if seed % 2 else 50  # plenty, or used up in the middle
+
+    def words(k, values, fill):
+        buf = torch.full((len(values) + 8,), fill, dtype=torch.int32, device="cuda")
+        view = buf[k:k + len(values)]
+        view.copy_(i32(values))
+        return buf, view
+
+    bufs, views = zip(*(words(k, v, -77) for k, v in zip(
+        offsets, ([0] * (n + 1), ctx, [0] * rows, [0] * rows, [count, 0]))))
+    row_start, own, positions, slots, left = views
+    t = i32(table)
+    ML.dec_batch_tables(h, own, i32(new), i32(free), left, t, size, ML.StepTables(*views), position_offset=11)
+    torch.cuda.synchronize()
+    want = oracle.batch_tables(ctx, new, free, count, table, size, 11, rows)
+    for name, v in dict(row_start=row_start, own_len=own, positions=positions, slots=slots, left=left, table=t).items():
+        assert np.array_equal(v.cpu().numpy(), want[name]), name
+    for k, buf, v in zip(offsets, bufs, views):  # nothing around the outputs
+        rest = torch.cat((buf[:k], buf[k + len(v):]))
+        assert bool((rest == -77).all())
+
+
+@pytest.mark.parametrize("rows", [6, 700, 4095, 4096, 4099, 20002])
+@pytest.mark.parametrize("offsets", [(0, 0, 0, 0, 0), (1, 2, 3, 1, 3), (0, 0, 4, 2, 1), (3, 1, 1, 4, 0)], ids=str)
+def test_tables_in_place_and_at_any_alignment(h, rows, offsets):
+    """own_len over ctx_len and left over free_count in one CTA and in the cluster, whose CTAs all have to have read
+    both before one writes; positions and slots that are not 16-byte aligned."""
+    for seed in range(4):
+        tables_in_place(h, rows, offsets, seed)
