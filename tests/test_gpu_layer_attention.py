@@ -236,3 +236,86 @@ def test_layer_attention_refuses_another_width(h):
         x = torch.zeros((1, width), dtype=torch.bfloat16, device="cuda")
         with pytest.raises(ValueError):
             ML.decode_layer_attention(h, L.w, att, x)
+
+
+@pytest.fixture(scope="module")
+def wide():
+    """The workload's projections (7168 -> 12288 -> 8192 -> 7168, 64 + 16 + 16 heads of 128) before 16 experts."""
+    import torch
+    import moe_layers_gb300 as ML
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    width, n_in, k_out, experts, inner = 7168, 12288, 8192, 16, 2048
+
+    def rand(*shape, s=0.02):
+        return (torch.randn(*shape, device="cuda", generator=g) * s).to(torch.bfloat16)
+
+    return ML.LayerWeights(gamma1=1 + rand(width, s=0.1), W_in=rand(n_in, width), W_o=rand(width, k_out),
+                           gamma2=1 + rand(width, s=0.1),
+                           W_r=torch.randn(experts, width, device="cuda", generator=g) * 0.01,
+                           Wg=rand(experts, inner, width), Wu=rand(experts, inner, width), Wd=rand(experts, width, inner),
+                           Wg_s=rand(inner, width), Wu_s=rand(inner, width), Wd_s=rand(width, inner), k=8, k_out=k_out)
+
+
+@pytest.mark.parametrize("n,new,own,prefix,pad", [(1, 1, 777, 0, 0), (1, 1, 2000, 300, 0), (2, 1, 90, 0, 0), (4, 2, 500, 0, 0),
+                                                  (1, 64, 1000, 0, 0), (60, 1, 70, 2048, 4), (7, 1, 33, 40, 2)])
+@pytest.mark.parametrize("spare", [True, False])
+def test_layer_attention_at_the_workloads_width(h, wide, n, new, own, prefix, pad, spare):
+    """One step against float64: h1 by the formulas from the hidden state on, the rest as moe_layer gives it.
+    Without spare blocks, new tokens that begin a block have no place and are not there."""
+    import torch
+    import moe_layers_gb300 as ML
+    heads, kv, d, size, M = 64, 16, 128, 16, n * new + pad
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M + prefix)
+    lens = [own + new + 3 * b for b in range(n)]  # with this step's rows
+    held, ahead = [-(-x // size) for x in lens], -(-prefix // size)
+    blocks = sum(held) + ahead + n * 5  # a request begins five blocks at most
+    pool = torch.randn((2, blocks, kv, size, d), device="cuda", generator=g).to(torch.bfloat16)
+    order = torch.randperm(blocks, device="cuda", generator=g).to(torch.int32)
+    table = torch.full((n, max(held)), -1, dtype=torch.int32, device="cuda")
+    at = ahead
+    for b in range(n):
+        table[b, :held[b]] = order[at:at + held[b]]
+        at += held[b]
+    step = ML.dec_batch_tables(h, i32([x - new for x in lens]), i32([new] * n), order[at:].contiguous(),
+                               i32([n * 5 if spare else 0]), table, size, rows=M, position_offset=prefix)
+    batch = ML.Batch(step.row_start, step.own_len, table, max_new=new,
+                     prefix_table=order[:ahead].contiguous() if prefix else None, prefix_len=prefix)
+    rope = ML.Rope(h, d, base=500000.0)
+    att = ML.LayerAttention(heads, d ** -0.5, ML.KvCache(pool[0], pool[1]), batch, step.positions, step.slots, rope)
+    x = torch.randn((M, 7168), device="cuda", generator=g).to(torch.bfloat16)
+    old, hidden = pool.clone(), x.clone()
+    trace = ML.decode_layer_attention(h, wide, att, hidden, trace=True)
+    torch.cuda.synchronize()
+
+    stored = lambda t: t.to(torch.bfloat16).double()  # noqa: E731
+    a = x.double()
+    a = stored(a * torch.rsqrt((a * a).mean(-1, keepdim=True) + wide.eps) * wide.gamma1.double())
+    y = stored(a @ wide.W_in.double().T)
+    q, k, v = (t.reshape(M, -1, d) for t in (y[:, :heads * d], y[:, heads * d:(heads + kv) * d], y[:, (heads + kv) * d:]))
+    angle = step.positions.double()[:, None] * 500000.0 ** (-2.0 * torch.arange(d // 2, device="cuda").double() / d)
+    c, s = torch.cos(angle)[:, None], torch.sin(angle)[:, None]
+    turn = lambda t: stored(torch.cat((t[..., :64] * c - t[..., 64:] * s, t[..., 64:] * c + t[..., :64] * s), -1))  # noqa: E731
+    q, k = turn(q), turn(k)
+    core = torch.zeros((M, heads, d), dtype=torch.float64, device="cuda")
+    for b in range(n):
+        keys = [torch.cat([old[i, t.long()].transpose(1, 2).reshape(-1, kv, d)[:m]
+                           for t, m in ((order[:ahead], prefix), (table[b, :held[b]], lens[b] - new))]).double() for i in (0, 1)]
+        rows = slice(b * new, (b + 1) * new)
+        kk, vv = (torch.cat((t, mine[rows])) for t, mine in zip(keys, (k, v)))
+        score = torch.einsum("tkgd,nkd->tkgn", q[rows].reshape(new, kv, heads // kv, d), kk) * d ** -0.5
+        place = torch.arange(kk.shape[0], device="cuda")
+        hidden_from = prefix + lens[b] - new + torch.arange(new, device="cuda")
+        gone = (place >= prefix) & (table[b, ((place - prefix) // size).clamp(min=0)] < 0)  # in a block that is not there
+        score = score.masked_fill(((place[None] > hidden_from[:, None]) | gone)[:, None, None], -torch.inf)
+        core[rows] = torch.einsum("tkgn,nkd->tkgd", torch.softmax(score, -1), vv).reshape(new, heads, d)
+    h1 = x.double() + stored(core.reshape(M, -1)) @ wide.W_o.double().T
+    assert_bf16_close(host_bits(trace["h1"]), h1.cpu().numpy(), "h1")
+    assert torch.equal(trace["h1"][n * new:], x[n * new:])  # rows of no request
+    moe = ML.MoeWeights(W_r=wide.W_r, Wg=wide.Wg, Wu=wide.Wu, Wd=wide.Wd, Wg_s=wide.Wg_s, Wu_s=wide.Wu_s, Wd_s=wide.Wd_s,
+                        gamma=wide.gamma2, k=wide.k)
+    out, same = ML.moe_layer(h, moe, trace["h1"], residual=trace["h1"], trace=True)
+    torch.cuda.synchronize()
+    assert torch.equal(same["idx"], trace["idx"])
+    assert_bf16_close(host_bits(hidden), out.double().cpu().numpy(), "out")
