@@ -897,3 +897,73 @@ def test_tables_in_place_and_at_any_alignment(h, rows, offsets):
     both before one writes; positions and slots that are not 16-byte aligned."""
     for seed in range(4):
         tables_in_place(h, rows, offsets, seed)
+
+
+@pytest.mark.parametrize("size", [16, 32, 64, 128])
+@pytest.mark.parametrize("heads,kv,d,new,own,prefix", [(64, 16, 128, [1] * 40, 60, 9001), (32, 32, 64, [1] * 60, 60, 8333),
+                                                       (64, 16, 128, [17, 30], 1500, 0), (8, 2, 64, [20, 0, 44], 900, 333)])
+def test_tensor_memory_kernel_with_every_block_size(h, size, heads, kv, d, new, own, prefix):
+    """Prefixes and contexts that end inside a block and a tile, blocks that are not there, requests whose last
+    block has a token of the step alone."""
+    rng = np.random.default_rng(size + d)
+    lens = [n + int(rng.integers(0, own)) for n in new]
+    lens[0] = new[0] + 3 * size
+    c = Case(new, lens, heads, kv, d, size, prefix=prefix, pad=64 - sum(new), seed=size, sharp=2.0)
+    for b in range(0, len(new), 2):
+        c.table[b, int(rng.integers(0, -(-lens[b] // size)))] = (-1, c.blocks)[b % 4 // 2]
+    if prefix:
+        c.prefix_table[[1, -(-prefix // size) // 2]] = (c.blocks, -5)
+    first = c.run(h)
+    c.check(first, reference64)
+    assert np.array_equal(c.run(h), first)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("T,heads,kv,d,rot,size", [(3000, 64, 16, 128, 128, 16), (5000, 8, 1, 128, 64, 64),
+                                                   (9001, 16, 16, 64, 48, 128), (2433, 2, 1, 64, 16, 32),
+                                                   (20000, 0, 1, 64, 64, 16), (700, 71, 1, 64, 0, 16)])
+def test_rope_of_many_rows(h, T, heads, kv, d, rot, size, inter):
+    """As many rows as one CTA turns several of, in place and not, and rows without a slot among them."""
+    import torch
+    import moe_layers_gb300 as ML
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    y = torch.randn((T, (heads + 2 * kv) * d + 8), device="cuda", generator=g).to(torch.bfloat16)
+    q, k, v = (y[:, a * d:b * d] for a, b in ((0, heads), (heads, heads + kv), (heads + kv, heads + 2 * kv)))
+    blocks = -(-T // size) + 2
+    slots = torch.randperm(blocks * size, device="cuda", generator=g)[:T].to(torch.int32)
+    slots[::7] = -1
+    slots[5::91] = blocks * size
+    positions = torch.randint(0, 1 << 20, (T,), device="cuda", generator=g).to(torch.int32)
+    pool = torch.randn((2, blocks, kv, size, d), device="cuda", generator=g).to(torch.bfloat16)
+    freq = torch.tensor(oracle.rope_frequencies(rot, 500000.0) if rot else np.zeros(0), device="cuda")
+    angle = positions.double()[:, None, None] * freq
+    x = y[:, :(heads + 2 * kv) * d].double().reshape(T, -1, d)
+    a_at, b_at = (slice(0, rot, 2), slice(1, rot, 2)) if inter else (slice(0, rot // 2), slice(rot // 2, rot))
+    want, size_of = x.clone(), torch.zeros_like(x)
+    want[..., a_at] = x[..., a_at] * torch.cos(angle) - x[..., b_at] * torch.sin(angle)
+    want[..., b_at] = x[..., b_at] * torch.cos(angle) + x[..., a_at] * torch.sin(angle)
+    size_of[..., a_at] = size_of[..., b_at] = x[..., a_at].abs() + x[..., b_at].abs()
+    near = want.abs() * 2.0 ** -8 + size_of * 2.0 ** -20
+    near[..., rot:] = 0
+    there = (slots >= 0) & (slots < blocks * size)
+    at = slots[there].long()
+    rope = ML.Rope(h, rot, base=500000.0, interleaved=inter)
+    for in_place in (False, True) if heads else (False,):
+        old_y, old = y.clone(), pool.clone()
+        cache = pool.clone()
+        out = ML.dec_rope_append(h, rope, q if heads else None, k, v, positions, slots, ML.KvCache(cache[0], cache[1]),
+                                 q_out=q if in_place else None)
+        torch.cuda.synchronize()
+        if heads:
+            assert bool(((out.double().reshape(T, heads, d) - want[:, :heads]).abs() <= near[:, :heads]).all())
+        rest = slice(heads * d if in_place else 0, None)
+        assert torch.equal(y[:, rest].view(torch.int16), old_y[:, rest].view(torch.int16))
+        for part, mine, by in ((0, want[:, heads:heads + kv], near[:, heads:heads + kv]),
+                               (1, x[:, heads + kv:], torch.zeros_like(x[:, heads + kv:]))):
+            places = cache[part].transpose(1, 2)  # [block][token][head][element]
+            got = places[at // size, at % size].double()
+            assert bool(((got - mine[there]).abs() <= by[there]).all())
+            untouched = torch.ones((blocks, size), dtype=torch.bool, device="cuda")
+            untouched[at // size, at % size] = False
+            assert torch.equal(places[untouched].view(torch.int16), old[part].transpose(1, 2)[untouched].view(torch.int16))

@@ -319,3 +319,54 @@ def test_layer_attention_at_the_workloads_width(h, wide, n, new, own, prefix, pa
     torch.cuda.synchronize()
     assert torch.equal(same["idx"], trace["idx"])
     assert_bf16_close(host_bits(hidden), out.double().cpu().numpy(), "out")
+
+
+@pytest.mark.parametrize("M", [1, 2, 4, 40])
+def test_two_layers_at_once(h, wide, M):
+    """Steps of two batches on two streams through one handle, and two captured ones replayed at the same time:
+    the bits of each alone."""
+    import torch
+    import moe_layers_gb300 as ML
+    kv, d, size, streams = 16, 128, 16, [torch.cuda.Stream() for _ in range(2)]
+    runs = []
+    for i in range(2):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(i)
+        own = 300 + 50 * i
+        pool = torch.randn((2, M * 25, kv, size, d), device="cuda", generator=g).to(torch.bfloat16)
+        table = torch.arange(M * 25, device="cuda").to(torch.int32).reshape(M, 25)
+        batch = ML.Batch(i32(range(M + 1)), i32([own] * M), table)
+        slots = table[:, (own - 1) // size].contiguous() * size + (own - 1) % size
+        att = ML.LayerAttention(64, d ** -0.5, ML.KvCache(pool[0], pool[1]), batch, i32([own - 1] * M), slots,
+                                ML.Rope(h, 128))
+        x0 = torch.randn((M, 7168), device="cuda", generator=g).to(torch.bfloat16)
+        x, alone = x0.clone(), x0.clone()
+        ws = torch.zeros(ML.decode_layer_attention_workspace_size(h, wide, att, M), dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        for _ in range(6):
+            ML.decode_layer_attention(h, wide, att, alone, ws=ws)
+        torch.cuda.synchronize()
+        runs.append((att, x0, x, ws, alone))
+    for _ in range(5):
+        for att, x0, x, ws, alone in runs:
+            x.copy_(x0)
+        torch.cuda.synchronize()
+        for _ in range(6):
+            for s, (att, x0, x, ws, alone) in zip(streams, runs):
+                ML.decode_layer_attention(h, wide, att, x, stream=s, ws=ws)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, alone) for att, x0, x, ws, alone in runs)
+    graphs = [torch.cuda.CUDAGraph() for _ in runs]
+    for g, (att, x0, x, ws, alone) in zip(graphs, runs):
+        with torch.cuda.graph(g):
+            for _ in range(6):
+                ML.decode_layer_attention(h, wide, att, x, ws=ws)
+    for _ in range(5):
+        for att, x0, x, ws, alone in runs:
+            x.copy_(x0)
+        torch.cuda.synchronize()
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, alone) for att, x0, x, ws, alone in runs)
