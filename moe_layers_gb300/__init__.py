@@ -861,7 +861,10 @@ def decode_layer_attention(h: Handle, weights: LayerWeights, attention: LayerAtt
                            stream=None, ws=None, _cw=None):
     """decode_layer with attention between the projections, in place on hidden
     bf16 [M,H]; trace as in decode_layer. Without `ws`, a workspace is made at the
-    first call of a stream and shape, which cannot be one that is captured."""
+    first call of a stream and shape, which cannot be one that is captured; the
+    calls and captured graphs of one stream and shape share it: give graphs that
+    may run at the same time one each (decode_layer_attention_workspace_size
+    bytes, zeroed)."""
     import torch
     _require(hidden, torch.bfloat16, "hidden", 2)
     _described(h, attention, "attention")

@@ -10,9 +10,10 @@
 // mma.sync m16n8k16, whose fragments come from the ring by ldmatrix without bank
 // conflicts; up to 32 rows the multiplications are no limit. Each CTA streams one
 // equal share of all tiles (attention.cuh); rows that several CTAs took are
-// joined by a second kernel. Measured (64 heads on 16, head dim 128): one request
-// of 131000 tokens 156 us, 6.9 TB/s, the copy rate; 61 requests of 1..4096 tokens
-// 44 us, 6.3 TB/s; 8 requests of 8 drafts on 2000..16000 tokens 80 us, 6.0 TB/s.
+// joined by a second kernel. Measured (64 heads on 16, head dim 128, calls back to
+// back): one request of 131000 tokens 157 us, 6.8 TB/s, the copy rate; 61 requests
+// of 1..4096 tokens 49 us, 5.6 TB/s; 8 requests of 8 drafts on 2000..16000 tokens
+// 82 us, 5.9 TB/s.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -720,7 +721,7 @@ AttnWs carve(const dec_handle* h, void* base, int M, int q_heads, int dim, int p
   };
   for (int i = prefix_len > 0 ? 0 : 1; i < 2; ++i) {
     w.start[i] = pieces((size_t)M * q_heads);
-    w.rest[i] = pieces((size_t)h->sms * std::max(kAttnCtasPerSm * 64, 256));
+    w.rest[i] = pieces((size_t)h->sms * std::max(kAttnCtasPerSm * Rows32::kRows, 256));
   }
   w.bytes = used;
   return w;

@@ -200,13 +200,6 @@ __device__ __forceinline__ float ex2_from(float m, float top, float scale) {
   return m == -INFINITY ? 0.f : ex2((m - top) * scale);
 }
 
-// Two floats rounded to nearest-even bf16, the first in the low half.
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // Whether one of two bf16 values is an infinity or NaN (its exponent is all ones).
 __device__ __forceinline__ bool not_finite(uint32_t pair) {
   return (((pair & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0;

@@ -18,10 +18,12 @@
 // row's scores pass it by more than 2^8 (P <= 256 then, exact in fp32 sums), so O
 // is read and rescaled a few times, not every tile. K is a K-major operand as it
 // lies in the cache, V an MN-major one: both come by TMA with the 128-byte
-// swizzle, in separate rings that two warps fill. What bounds it with two streams
-// is each one's chain of scores, softmax and product with the waits between
-// (1.69 us a tile, tensor pipe 50%) against 1.44 us to read the tile; 64 rows of
-// 64 heads on 32768 shared tokens: 60 us of the call's 94, 4.5 TB/s, 1.1 PFLOP/s.
+// swizzle, in separate rings that two warps fill. With two streams of head dim 128
+// a tile costs 1.71 us (32768 more tokens of the prefix: 46 us more) where its
+// read takes 1.47; the softmax is most of the difference (without one, 0.2 us a
+// tile less), and the rings' three K and two V tiles are enough (two and two: the
+// same times). What remains of a call's 96 us with 64 rows of 64 heads on 32768
+// shared tokens is the ramp and the way out, the own tokens' launch and the join.
 #include <atomic>
 
 #include "attention.cuh"

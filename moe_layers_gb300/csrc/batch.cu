@@ -259,13 +259,6 @@ struct RopeParams {
   int rows, q_heads, kv_heads, dim, rot, interleaved, shift, slots_n;
 };
 
-// Two floats rounded to nearest-even bf16, the first in the low half.
-__device__ __forceinline__ uint32_t pack_bf(float a, float b) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-  return r;
-}
-
 // A row's heads are cut into items of 8 elements (with the half layout, of 8
 // and their 8 partners); a thread reads, turns and writes whole items, so q may
 // be turned in place. Bound by the copy. A CTA has 128 NI of a row's items for
@@ -334,7 +327,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           const float a = bf_lo(w[p]), b = bf_hi(w[p]);
-          o[p] = pack_bf(a * c[p] - b * s[p], b * c[p] + a * s[p]);
+          o[p] = pack_bf16x2(a * c[p] - b * s[p], b * c[p] + a * s[p]);
         }
         *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
       } else {
@@ -348,8 +341,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
           for (int p = 0; p < 2; ++p) {
             const uint32_t va = wa[2 * h + p], vb = wb[2 * h + p];
             const float a0 = bf_lo(va), a1 = bf_hi(va), b0 = bf_lo(vb), b1 = bf_hi(vb);
-            oa[2 * h + p] = pack_bf(a0 * c[2 * p] - b0 * s[2 * p], a1 * c[2 * p + 1] - b1 * s[2 * p + 1]);
-            ob[2 * h + p] = pack_bf(b0 * c[2 * p] + a0 * s[2 * p], b1 * c[2 * p + 1] + a1 * s[2 * p + 1]);
+            oa[2 * h + p] = pack_bf16x2(a0 * c[2 * p] - b0 * s[2 * p], a1 * c[2 * p + 1] - b1 * s[2 * p + 1]);
+            ob[2 * h + p] = pack_bf16x2(b0 * c[2 * p] + a0 * s[2 * p], b1 * c[2 * p + 1] + a1 * s[2 * p + 1]);
           }
         }
         *reinterpret_cast<uint4*>(to) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
@@ -393,11 +386,12 @@ cudaError_t launch_rope_append(dec_handle* h, const dec_rope& rope, const uint16
   P.rows = rows;
   const int d8 = P.dim / 8, per_head = P.interleaved ? d8 : d8 - P.rot / 16;
   const int items = (P.q_heads + P.kv_heads) * per_head + P.kv_heads * d8;
-  // One item a thread while a wave (2048 threads an SM) holds them all. Above,
-  // two a thread and up to 60 CTAs an SM: more than are resident (18), so that
-  // those that begin overlap those that end, and few enough to take several rows
-  // each (8192 rows of 64 + 16 + 16 heads of 128: 60.2 us; with one wave of
-  // CTAs 73, a CTA for every row 63, four items a thread 65, one 66).
+  // One item a thread up to 2048 threads an SM (10 to 12 CTAs are resident, at 37
+  // to 44 registers, the rest follow). Above, two a thread and up to 60 CTAs an SM:
+  // more than the 9 or 10 that are resident (56 and 46 registers), so that those
+  // that begin overlap those that end, and few enough to take several rows each
+  // (8192 rows of 64 + 16 + 16 heads of 128: 60.6 us; with one wave of CTAs 73, a
+  // CTA for every row 63, four items a thread 65, one 66).
   const bool few = (long long)rows * items <= 2048LL * h->sms;
   const int ni = few ? 1 : 2;
   const int chunks = (items + kRopeThreads * ni - 1) / (kRopeThreads * ni);

@@ -29,6 +29,13 @@ __device__ __forceinline__ uint16_t f2bf(float f) {
   return (uint16_t)(u >> 16);
 }
 
+// Two floats rounded to nearest-even bf16, the first in the low half.
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // acc + w_lo * x_lo + w_hi * x_hi for the two bf16 lanes of 32-bit words w
 // and x, in that order: fp32 fused multiply-adds on bf16 operands (a product
 // of two bf16 values is exact in fp32, so each step is fmaf of the widened
