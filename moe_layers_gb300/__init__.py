@@ -873,7 +873,8 @@ def decode_layer_attention(h: Handle, weights: LayerWeights, attention: LayerAtt
     if hidden.get_device() != h.device or not hidden.is_contiguous() or attention.rows != M or hidden.shape[1] != cw.H:
         raise ValueError("hidden must be contiguous on the handle's device, as wide as the weights' H and with as many "
                          "rows as attention's positions")
-    forms = dict(h1=(cw.H, torch.bfloat16), idx=(cw.k, torch.int32), w=(cw.k, torch.float32), scores=(cw.E, torch.float32))
+    forms = dict(h1=(cw.H, torch.bfloat16), idx=(cw.k, torch.int32), w=(cw.k, torch.float32),
+                 scores=(cw.E, torch.float32))
     for n, t in trace.items() if isinstance(trace, dict) else ():
         if t is not None and n in forms:
             width, dtype = forms[n]
