@@ -524,6 +524,97 @@ dec_status decode_layer_attention(dec_handle* h, const dec_layer_weights* Wt, co
                                   dec_bf16* hidden, int M, const dec_layer_trace* trace, void* ws, size_t ws_bytes,
                                   cudaStream_t stream);
 
+/* ------------------------------------------------------------------ 8-bit weights and rows
+ *
+ * The layer's products with half the weight bytes. An e4m3 number (1 sign, 4
+ * exponent, 3 mantissa bits, largest value 448, no infinities) stands for
+ * itself times a 32-bit scale:
+ *   weights W[N][K]:  one scale for each block of 128 x 128,
+ *                     scales[ceil(N / 128)][ceil(K / 128)]
+ *   rows x[M][K]:     one for each 128 values of a row, from its start
+ * the last blocks of a row or matrix being what is left. A group is quantised
+ * by its largest absolute value m: scale = m / 448, q = e4m3(value * (448 / m)),
+ * nearest-even; a group with m < 2^-116 is zeros with scale 0. A group that
+ * holds a NaN or an infinity has it as its scale, so what reads it becomes NaN.
+ * Rows and reduction lengths K are multiples of 16 here. */
+
+typedef uint8_t dec_e4m3; /* bit pattern of an e4m3 value */
+
+/* Rows of 8-bit values: row t at q + t * ldq, its scales at scales + t * lds. */
+typedef struct dec_fp8_rows {
+  dec_e4m3* q;   /* 16-byte aligned */
+  int64_t ldq;   /* elements, a multiple of 16, at least the width */
+  float* scales; /* 4-byte aligned */
+  int64_t lds;   /* at least ceil(width / 128) */
+} dec_fp8_rows;
+
+/* An 8-bit weight matrix [N][K] and its block scales, both without gaps. */
+typedef struct dec_fp8_weight {
+  const dec_e4m3* q;   /* 16-byte aligned */
+  const float* scales; /* 4-byte aligned */
+} dec_fp8_weight;
+
+/* A bf16 weight matrix [N][K] to 8 bits with block scales, for load time. A
+ * bank of E experts of I rows is one matrix of E I rows if I is a multiple of
+ * 128. 1 <= N <= 2^32, K a multiple of 16 in [16, 65536]. */
+dec_status dec_quant_weight(dec_handle* h, const dec_bf16* W, int64_t N, int K, dec_e4m3* q, float* scales,
+                            cudaStream_t stream);
+
+/* The residual's addition, the RMSNorm and its rows in 8 bits, in one pass:
+ *   a = residual ? bf16(x + residual) : x       -> sum, if given
+ *   b = gamma ? a / sqrt(mean(a^2) + eps) * gamma : a   (fp32) -> y in bf16, if given
+ *   out = b in 8 bits, quantised from fp32
+ * All bf16 rows have H contiguous values and a row stride in elements, a
+ * multiple of 8. sum (only with a residual) may be x or residual itself, y too,
+ * with the same stride; apart from that no output overlaps an input or another
+ * output. y has the bits that dec_rmsnorm gives for a. gamma NULL quantises
+ * rows that need no norm, such as the attention's output.
+ * 1 <= M <= 2^20, H a multiple of 16 in [16, 65536]. */
+dec_status dec_rmsnorm_quant(dec_handle* h, const dec_bf16* x, int64_t ldx, const dec_bf16* residual, int64_t ldr,
+                             const dec_bf16* gamma, float eps, dec_bf16* sum, int64_t lds, dec_bf16* y, int64_t ldy,
+                             const dec_fp8_rows* out, int M, int H, cudaStream_t stream);
+
+dec_status dec_linear_fp8_workspace_size(const dec_handle* h, int M, int N, int K, size_t* bytes);
+
+/* y[M][N] = [residual[M][N] +] x[M][K] W[N][K]^T on 8-bit rows and weights.
+ * Within a block of 128 the products and their sum are fp32; the block's sum is
+ * scaled and added to the total in fp32, and y is rounded once. y and residual
+ * have row strides ldy, ldr >= N in elements (any, 2-byte aligned); y may be
+ * residual itself with the same stride and overlaps nothing else.
+ * 1 <= M <= 2^20 (prompts too), 1 <= N <= 2^20, K a multiple of 16 in
+ * [16, 65536] (above 24576: DEC_ERR_UNSUPPORTED). */
+dec_status dec_linear_fp8(dec_handle* h, const dec_fp8_rows* x, const dec_fp8_weight* W, const dec_bf16* residual,
+                          int64_t ldr, dec_bf16* y, int64_t ldy, int M, int N, int K, void* ws, size_t ws_bytes,
+                          cudaStream_t stream);
+
+/* Weights of an MoE layer's experts in 8 bits: gate, up [E][I][H] and down
+ * [E][H][I] with scales [E][I / 128][H / 128] and [E][H / 128][I / 128]; the
+ * shared expert's are one expert's, or all NULL. */
+typedef struct dec_moe_fp8_weights {
+  int H; /* hidden size, a multiple of 128 */
+  int E; /* routed experts, at most 1024 */
+  int I; /* expert intermediate size, a multiple of 128 */
+  dec_fp8_weight gate, up, down;
+  dec_fp8_weight gate_s, up_s, down_s;
+} dec_moe_fp8_weights;
+
+dec_status moe_experts_fp8_workspace_size(const dec_handle* h, const dec_moe_fp8_weights* Wt, int M, int k,
+                                          size_t* bytes);
+
+/* moe_experts on 8-bit rows and weights:
+ *   out_t = [residual_t +] sum_j w_tj E_{idx_tj}(x_t) [+ S(x_t)],
+ *   E(x) = Wd q(silu(Wg x) * (Wu x))
+ * where q quantises the inner row from fp32 by groups of 128, as
+ * dec_rmsnorm_quant does. Everything else is fp32 until out is rounded to bf16.
+ * x [M][H]; idx int32 [M][k] and w fp32 [M][k] as from moe_route_topk; an entry
+ * whose id is outside [0, E) is left out. residual bf16 [M][H] or NULL; out bf16
+ * [M][H], which may be residual itself and overlaps nothing else. The workspace
+ * needs no particular contents. 1 <= M <= 64, 1 <= k <= 16, H and I up to 16384
+ * (else DEC_ERR_UNSUPPORTED). */
+dec_status moe_experts_fp8(dec_handle* h, const dec_fp8_rows* x, const int32_t* idx, const float* w, int M, int k,
+                           const dec_moe_fp8_weights* Wt, const dec_bf16* residual, dec_bf16* out, void* ws,
+                           size_t ws_bytes, cudaStream_t stream);
+
 /* ------------------------------------------------------------------ measurement */
 
 /* Per-kernel timing record returned by dec_profile_read. */

@@ -19,7 +19,7 @@ DEC_OK, DEC_ERR_INVALID_ARG, DEC_ERR_UNSUPPORTED, DEC_ERR_CUDA, DEC_ERR_TIMEOUT 
 VARIANT_AUTO, VARIANT_SMALL_M, VARIANT_SPLIT_K = 0, 1, 2
 
 _lib = None
-_bf16 = _i32 = _raw_stream = None  # set by _load
+_bf16 = _i32 = _f32 = _e4m3 = _raw_stream = None  # set by _load
 
 
 class DecodeError(RuntimeError):
@@ -73,6 +73,19 @@ class _Rope(ctypes.Structure):
 class _LayerAttention(ctypes.Structure):
     _fields_ = [("q_heads", ctypes.c_int), ("scale", ctypes.c_float)] + \
                [(n, ctypes.c_void_p) for n in ("rope", "cache", "batch", "positions", "slots")]
+
+
+class _Fp8Rows(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("scales", ctypes.c_void_p), ("lds", ctypes.c_int64)]
+
+
+class _Fp8Weight(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class _MoeFp8Weights(ctypes.Structure):
+    _fields_ = [("H", ctypes.c_int), ("E", ctypes.c_int), ("I", ctypes.c_int)] + \
+               [(n, _Fp8Weight) for n in ("gate", "up", "down", "gate_s", "up_s", "down_s")]
 
 
 class _KernelTime(ctypes.Structure):
@@ -131,6 +144,12 @@ def _load():
         "decode_layer_attention": [P, ctypes.POINTER(_LayerWeights), ctypes.POINTER(_LayerAttention), P, I,
                                    ctypes.POINTER(_LayerTrace), P, Z, P],
         "dec_attention": [P, P, I64, ctypes.POINTER(_KvCache), ctypes.POINTER(_Batch), F, P, I64, I, I, P, Z, P],
+        "dec_quant_weight": [P, P, I64, I, P, P, P],
+        "dec_rmsnorm_quant": [P, P, I64, P, I64, P, F, P, I64, P, I64, ctypes.POINTER(_Fp8Rows), I, I, P],
+        "dec_linear_fp8_workspace_size": [P, I, I, I, ctypes.POINTER(Z)],
+        "dec_linear_fp8": [P, ctypes.POINTER(_Fp8Rows), ctypes.POINTER(_Fp8Weight), P, I64, P, I64, I, I, I, P, Z, P],
+        "moe_experts_fp8_workspace_size": [P, ctypes.POINTER(_MoeFp8Weights), I, I, ctypes.POINTER(Z)],
+        "moe_experts_fp8": [P, ctypes.POINTER(_Fp8Rows), P, P, I, I, ctypes.POINTER(_MoeFp8Weights), P, P, P, Z, P],
         "dec_test_wait_timeout": [P, P],
         "dec_test_routing_wait_timeout": [P, I, P],
         "dec_test_delayed_copy": [P, P, P, Z, U64, P],
@@ -151,8 +170,8 @@ def _load():
     lib.dec_launch_count.argtypes = [P]
     lib.dec_launch_count.restype = ctypes.c_uint64
     import torch
-    global _bf16, _i32, _raw_stream
-    _bf16, _i32 = torch.bfloat16, torch.int32
+    global _bf16, _i32, _f32, _e4m3, _raw_stream
+    _bf16, _i32, _f32, _e4m3 = torch.bfloat16, torch.int32, torch.float32, torch.float8_e4m3fn
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     _lib = lib
     return lib
@@ -206,6 +225,7 @@ class Handle:
         self._stream_ws = {}
         self._attention_ws = {}  # workspace bytes by shape
         self._layer_ws = {}      # decode_layer_attention's workspaces by stream and shape
+        self._fp8_ws = {}        # workspace bytes of the 8-bit operators by shape
 
     @property
     def ptr(self):
@@ -256,6 +276,21 @@ class Handle:
             size = max(int(nbytes), 256, 2 * held[-1].numel() if held else 0)
             with _on_stream(stream):
                 held.append(torch.empty(size, dtype=torch.uint8, device=f"cuda:{self.device}"))
+        return held[-1]
+
+    def zeroed_workspace(self, key, address: int, nbytes: int, stream=None):
+        """The same for calls that need zeroed memory and leave it zeroed where it
+        matters. It cannot be made in a capture, whose replays would zero it again."""
+        import torch
+        held = self._stream_ws.setdefault((key, address), [])
+        if not held or held[-1].numel() < nbytes:
+            # on the call's stream, which is another device's than the current one if the handle is
+            with torch.cuda.stream(torch.cuda.current_stream(self.device) if stream is None else stream):
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError(f"{key}: the first call of a size makes its zeroed workspace; make it before the "
+                                       "capture, or pass ws")
+                size = max(int(nbytes), 256, 2 * held[-1].numel() if held else 0)
+                held.append(torch.zeros(size, dtype=torch.uint8, device=f"cuda:{self.device}"))
         return held[-1]
 
     def set_force_variant(self, v: int) -> None:
@@ -909,6 +944,242 @@ def decode_layer_attention(h: Handle, weights: LayerWeights, attention: LayerAtt
     _check(_load().decode_layer_attention(h.ptr, ctypes.byref(cw), attention._ref, _ptr(hidden), M,
                                           ctypes.byref(tr) if tr is not None else None, _ptr(ws),
                                           _ws_bytes(ws, h.device), sp), "decode_layer_attention")
+    return out
+
+
+# ---------------------------------------------------------------------------- 8-bit weights and rows
+class Fp8Rows:
+    """Rows of 8-bit values with a scale for each 128 (see dec_fp8_rows): q
+    float8_e4m3fn [rows, width] and scale float32 [rows, ceil(width / 128)],
+    both with contiguous rows that may be strided (columns of wider ones, from a
+    multiple of 128 on). Make a new one to describe other tensors."""
+
+    def __init__(self, q, scale):
+        import torch
+        _require(q, torch.float8_e4m3fn, "q", 2)
+        _require(scale, torch.float32, "scale", 2)
+        rows, width = q.shape
+        groups = -(-width // 128)
+        if width % 16 != 0 or rows < 1 or tuple(scale.shape) != (rows, groups) or scale.device != q.device:
+            raise ValueError("q must be [rows, width], scale [rows, ceil(width / 128)] on the same device, width a "
+                             "multiple of 16")
+        if q.stride(1) != 1 or (groups > 1 and scale.stride(1) != 1):
+            raise ValueError("q and scale: rows must be contiguous")
+        self.q, self.scale, self.rows, self.width = q, scale, rows, width
+        # the stride of a single row means nothing
+        self._c = _Fp8Rows(q.data_ptr(), q.stride(0) if rows > 1 else width, scale.data_ptr(),
+                           scale.stride(0) if rows > 1 else groups)
+        self._ref = ctypes.byref(self._c)
+        self.device_index = q.get_device()
+
+    @classmethod
+    def empty(cls, rows: int, width: int, device="cuda"):
+        import torch
+        return cls(torch.empty((rows, width), dtype=torch.float8_e4m3fn, device=device),
+                   torch.empty((rows, -(-width // 128)), dtype=torch.float32, device=device))
+
+
+class Fp8Weight:
+    """8-bit weights with a scale for each block of 128 x 128 (see
+    dec_fp8_weight): q float8_e4m3fn [N, K] or a bank [E, N, K] (then N a multiple
+    of 128), scale float32 [(E,) ceil(N / 128), ceil(K / 128)], contiguous."""
+
+    def __init__(self, q, scale):
+        import torch
+        _require(q, torch.float8_e4m3fn, "q")
+        _require(scale, torch.float32, "scale")
+        if q.dim() not in (2, 3) or (q.dim() == 3 and q.shape[1] % 128 != 0):
+            raise ValueError("q must be [N, K], or a bank [E, N, K] with N a multiple of 128")
+        n, k = q.shape[-2:]
+        if tuple(scale.shape) != (*q.shape[:-2], -(-n // 128), -(-k // 128)) or scale.device != q.device:
+            raise ValueError("scale must have a value for each block of 128 x 128 of q, on its device")
+        if not q.is_contiguous() or not scale.is_contiguous():
+            raise ValueError("q and scale must be contiguous")
+        self.q, self.scale = q, scale
+        self._c = _Fp8Weight(q.data_ptr(), scale.data_ptr())
+        self._ref = ctypes.byref(self._c)
+        self.device_index = q.get_device()
+
+
+class MoeFp8Weights:
+    """8-bit weights of an MoE layer's experts (see dec_moe_fp8_weights): gate
+    and up are banks [E, I, H], down [E, H, I]; the shared expert's are [I, H],
+    [I, H] and [H, I], or all None."""
+
+    def __init__(self, gate: Fp8Weight, up: Fp8Weight, down: Fp8Weight, gate_s: Optional[Fp8Weight] = None,
+                 up_s: Optional[Fp8Weight] = None, down_s: Optional[Fp8Weight] = None):
+        if gate.q.dim() != 3:
+            raise ValueError("gate must be a bank [E, I, H]")
+        E, I, H = gate.q.shape
+        if tuple(up.q.shape) != (E, I, H) or tuple(down.q.shape) != (E, H, I):
+            raise ValueError("up must have gate's shape [E, I, H], down [E, H, I]")
+        shared = (gate_s, up_s, down_s)
+        if any(w is None for w in shared) != all(w is None for w in shared):
+            raise ValueError("the shared expert's weights must be all given or all None")
+        if gate_s is not None and [tuple(w.q.shape) for w in shared] != [(I, H), (I, H), (H, I)]:
+            raise ValueError("the shared expert's weights must be [I, H], [I, H] and [H, I]")
+        every = [w for w in (gate, up, down) + shared if w is not None]
+        if any(w.device_index != gate.device_index for w in every):
+            raise ValueError("the weights must be on one device")
+        self.gate, self.up, self.down, self.gate_s, self.up_s, self.down_s = (gate, up, down) + shared
+        self.E, self.I, self.H = E, I, H
+        self._c = _MoeFp8Weights(H, E, I, *(_Fp8Weight() if w is None else w._c for w in (gate, up, down) + shared))
+        self._ref = ctypes.byref(self._c)
+        self.device_index = gate.device_index
+
+
+def dec_quant_weight(h: Handle, W, stream=None) -> Fp8Weight:
+    """bf16 weights [N, K], or a bank [E, N, K] with N a multiple of 128, in 8
+    bits with a scale for each block of 128 x 128."""
+    import torch
+    _require(W, torch.bfloat16, "W")
+    if W.dim() not in (2, 3) or not W.is_contiguous() or W.get_device() != h.device:
+        raise ValueError(f"W must be contiguous [N, K] or [E, N, K] on the handle's device, cuda:{h.device}")
+    n, k = W.shape[-2:]
+    with _on_stream(stream):
+        out = Fp8Weight(torch.empty(W.shape, dtype=torch.float8_e4m3fn, device=W.device),
+                        torch.empty((*W.shape[:-2], -(-n // 128), -(-k // 128)), dtype=torch.float32, device=W.device))
+    _check(_load().dec_quant_weight(h.ptr, W.data_ptr(), W.numel() // k if k else 0, k, out.q.data_ptr(),
+                                    out.scale.data_ptr(), _stream_of(h, stream)), "dec_quant_weight")
+    return out
+
+
+def dec_rmsnorm_quant(h: Handle, x, gamma=None, residual=None, eps: float = 1e-6, total=None, y=None,
+                      out: Optional[Fp8Rows] = None, stream=None) -> Fp8Rows:
+    """[x + residual] -> RMSNorm (gamma None: no norm) -> rows in 8 bits (bf16
+    [rows, width], rows may be strided). total receives bf16(x + residual) and may
+    be x or residual; y receives the normed rows in bf16. Returns the 8-bit rows
+    (out, else new ones)."""
+    dev = h.device
+    rows, width, ldx = _rows_of(x, "x", dev)
+    extra = []
+    for name, t in (("residual", residual), ("total", total), ("y", y)):
+        if t is None:
+            extra += [None, 0]
+            continue
+        r, w, ld = _rows_of(t, name, dev)
+        if r != rows or w != width:
+            raise ValueError(f"{name} must have x's shape")
+        extra += [t.data_ptr(), ld]
+    pg = None
+    if gamma is not None:
+        if gamma.dtype is not _bf16 or gamma.dim() != 1 or gamma.numel() != width or not gamma.is_contiguous() or \
+                gamma.get_device() != dev:
+            raise ValueError("gamma must be a contiguous bf16 vector of x's width on the handle's device")
+        pg = gamma.data_ptr()
+    if out is None:
+        with _on_stream(stream):
+            out = Fp8Rows.empty(rows, width, x.device)
+    elif out.rows != rows or out.width != width:
+        raise ValueError("out must have x's shape")
+    _described(h, out, "out")
+    st = _load().dec_rmsnorm_quant(h.ptr, x.data_ptr(), ldx, extra[0], extra[1], pg, eps, extra[2], extra[3], extra[4],
+                                   extra[5], out._ref, rows, width, _stream_of(h, stream))
+    if st:
+        _check(st, "dec_rmsnorm_quant")
+    return out
+
+
+def dec_linear_fp8_workspace_size(h: Handle, M: int, N: int, K: int) -> int:
+    nb = ctypes.c_size_t()
+    _check(_load().dec_linear_fp8_workspace_size(h.ptr, int(M), int(N), int(K), ctypes.byref(nb)),
+           "dec_linear_fp8_workspace_size")
+    return nb.value
+
+
+def _any_rows(t, name: str, device: int, rows: int, width: int):
+    """(address, row stride) of a bf16 tensor [rows, width] on the device; rows may be strided."""
+    if t.dtype is not _bf16 or t.dim() != 2 or t.get_device() != device or t.shape[0] != rows or t.shape[1] != width or \
+            (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be bf16 [{rows}, {width}] with contiguous rows on the handle's device")
+    return t.data_ptr(), t.stride(0) if rows > 1 else width
+
+
+def dec_linear_fp8(h: Handle, x: Fp8Rows, W: Fp8Weight, residual=None, y=None, stream=None, ws=None):
+    """y = [residual +] x W^T on 8-bit rows and weights (bf16 [rows, N]; y may be
+    residual). Without `ws`, the calls of one stream share a zeroed workspace,
+    which is made at the first call that needs one of its size and cannot be made
+    in a capture: give graphs that may run at the same time one each
+    (dec_linear_fp8_workspace_size bytes, zeroed)."""
+    dev = h.device
+    _described(h, x, "x")
+    _described(h, W, "W")
+    if W.q.dim() != 2 or W.q.shape[1] != x.width:
+        raise ValueError("W must be [N, K] with K the width of x")
+    M, (N, K) = x.rows, W.q.shape
+    pr, ldr = (None, 0) if residual is None else _any_rows(residual, "residual", dev, M, N)
+    if y is None:
+        import torch
+        with _on_stream(stream):
+            y = torch.empty((M, N), dtype=torch.bfloat16, device=x.q.device)
+    py, ldy = _any_rows(y, "y", dev, M, N)
+    sp = _stream_of(h, stream)
+    if ws is not None:
+        pw, nbytes = ws.data_ptr(), _ws_bytes(ws, dev)
+    else:
+        nbytes = h._fp8_ws.get((M, N, K))
+        if nbytes is None:
+            nbytes = h._fp8_ws[(M, N, K)] = dec_linear_fp8_workspace_size(h, M, N, K)
+        pw = None
+        if nbytes:
+            ws = h.zeroed_workspace("linear_fp8", sp, nbytes, stream)
+            pw, nbytes = ws.data_ptr(), ws.numel()
+    st = _load().dec_linear_fp8(h.ptr, x._ref, W._ref, pr, ldr, py, ldy, M, N, K, pw, nbytes, sp)
+    if st:
+        _check(st, "dec_linear_fp8")
+    return y
+
+
+def moe_experts_fp8_workspace_size(h: Handle, weights: MoeFp8Weights, M: int, k: int) -> int:
+    nb = ctypes.c_size_t()
+    _check(_load().moe_experts_fp8_workspace_size(h.ptr, weights._ref, int(M), int(k), ctypes.byref(nb)),
+           "moe_experts_fp8_workspace_size")
+    return nb.value
+
+
+def moe_experts_fp8(h: Handle, x: Fp8Rows, idx, w, weights: MoeFp8Weights, residual=None, out=None, stream=None,
+                    ws=None):
+    """out = [residual +] sum_j w_j E_idx_j(x) [+ S(x)] on 8-bit rows and weights
+    (bf16 [M, H]; out may be residual); idx int32 and w float32 [M, k] as from
+    moe_route_topk. Without `ws`, the calls of one stream share a workspace: give
+    graphs that may run at the same time one each (moe_experts_fp8_workspace_size
+    bytes, any contents)."""
+    dev = h.device
+    _described(h, x, "x")
+    _described(h, weights, "weights")
+    M, H = x.rows, weights.H
+    if x.width != H:
+        raise ValueError("x must be as wide as the weights' H")
+    for name, t, dtype in (("idx", idx, _i32), ("w", w, _f32)):
+        if t.dtype is not dtype or t.dim() != 2 or t.get_device() != dev or not t.is_contiguous():
+            _require(t, dtype, name, 2)
+            raise ValueError(f"{name} must be contiguous on the handle's device, cuda:{dev}")
+    k = idx.shape[1]
+    if tuple(idx.shape) != (M, k) or w.shape != idx.shape:
+        raise ValueError("idx and w must be [M, k] with as many rows as x")
+    if out is None:
+        import torch
+        with _on_stream(stream):
+            out = torch.empty((M, H), dtype=torch.bfloat16, device=x.q.device)
+    for name, t in (("residual", residual), ("out", out)):
+        if t is not None and (t.dtype is not _bf16 or tuple(t.shape) != (M, H) or not t.is_contiguous() or
+                              t.get_device() != dev):
+            raise ValueError(f"{name} must be contiguous bf16 [{M}, {H}] on the handle's device")
+    sp = _stream_of(h, stream)
+    if ws is not None:
+        nbytes = _ws_bytes(ws, dev)
+    else:
+        shape = (M, k, weights.E, H, weights.I, weights.gate_s is not None)
+        size = h._fp8_ws.get(shape)
+        if size is None:
+            size = h._fp8_ws[shape] = moe_experts_fp8_workspace_size(h, weights, M, k)
+        ws = h.stream_workspace("experts_fp8", sp, size, stream)
+        nbytes = ws.numel()
+    st = _load().moe_experts_fp8(h.ptr, x._ref, idx.data_ptr(), w.data_ptr(), M, k, weights._ref,
+                                 None if residual is None else residual.data_ptr(), out.data_ptr(), ws.data_ptr(), nbytes,
+                                 sp)
+    if st:
+        _check(st, "moe_experts_fp8")
     return out
 
 

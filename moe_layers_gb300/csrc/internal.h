@@ -215,6 +215,73 @@ bool rope_ok(const dec_rope* r, int head_dim);
 bool scale_ok(float scale);
 bool attention_shape_ok(int M, int q_heads, const dec_kv_cache* c, const dec_batch* b);
 
+// ---------------------------------------------------------------- 8-bit numbers
+struct QuantRows {
+  const void* x;  // bf16 rows (fp32 for the wide form: no residual, no gains, no bf16 outputs)
+  long long ldx;
+  const uint16_t* res;  // or null
+  long long ldr;
+  const uint16_t* gamma;  // or null: no norm
+  float eps;
+  uint16_t* sum;  // or null
+  long long lds;
+  uint16_t* y;  // or null
+  long long ldy;
+  uint8_t* q;
+  long long ldq;
+  float* scales;
+  long long ldsc;
+  int H;
+};
+cudaError_t launch_norm_quant(dec_handle* h, const QuantRows& P, int M, bool wide, cudaStream_t s);
+cudaError_t launch_weight_quant(dec_handle* h, const uint16_t* W, long long N, int K, uint8_t* q, float* scales,
+                                cudaStream_t s);
+
+// A projection on 8-bit rows and weights.
+struct Linear8 {
+  const uint8_t* x;
+  long long ldx;
+  const float* xs;
+  long long ldxs;
+  const uint8_t* W;
+  const float* ws;
+  const uint16_t* res;
+  long long ldr;
+  uint16_t* y;
+  long long ldy;
+  int M, N, K;
+};
+// Most rows that the streaming kernel takes at this reduction length (0, 8 or 16).
+int stream8_rows(int K, bool pair);
+cudaError_t launch_stream8_linear(dec_handle* h, const Linear8& L, cudaStream_t s);
+
+// Weights of a SwiGLU pair (gate, up), or of one matrix (the first).
+struct Stream8Bank {
+  const uint8_t* W[2];
+  const float* scales[2];
+};
+struct Experts8 {
+  const uint8_t* x;
+  long long ldx;
+  const float* xs;
+  long long ldxs;
+  const int32_t* idx;
+  const float* w;
+  int M, k, E, H, I;
+  Stream8Bank gate, down, sgate, sdown;  // gate and up; sgate.W[0] null: no shared expert
+  const uint16_t* res;
+  uint16_t* out;
+};
+struct Experts8Plan {
+  int most = 0;   // rows of one problem at most (0: unsupported sizes)
+  int slots = 0;  // M k entries, then M of the shared expert
+  int P_max = 0;  // problems at most
+  int words = 0;  // of the table
+};
+Experts8Plan experts8_plan(int M, int k, int E, int H, int I, bool shared);
+cudaError_t launch_experts8(dec_handle* h, const Experts8& X, const Experts8Plan& plan, int* table, float* inner,
+                            uint8_t* hq, float* hs, float* y, cudaStream_t s);
+
 // Makes the handle's device current for the lifetime of the object.
 struct DeviceGuard {
   int prev = -1;
