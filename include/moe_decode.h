@@ -582,7 +582,7 @@ dec_status dec_linear_fp8_workspace_size(const dec_handle* h, int M, int N, int 
  * have row strides ldy, ldr >= N in elements (any, 2-byte aligned); y may be
  * residual itself with the same stride and overlaps nothing else.
  * 1 <= M <= 2^20 (prompts too), 1 <= N <= 2^20, K a multiple of 16 in
- * [16, 65536] (above 24576: DEC_ERR_UNSUPPORTED). */
+ * [16, 65536]. */
 dec_status dec_linear_fp8(dec_handle* h, const dec_fp8_rows* x, const dec_fp8_weight* W, const dec_bf16* residual,
                           int64_t ldr, dec_bf16* y, int64_t ldy, int M, int N, int K, void* ws, size_t ws_bytes,
                           cudaStream_t stream);

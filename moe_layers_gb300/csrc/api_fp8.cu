@@ -109,7 +109,6 @@ dec_status dec_linear_fp8(dec_handle* h, const dec_fp8_rows* x, const dec_fp8_we
   if (residual != nullptr && (!al(residual, 2) || ldr < N || ldr > kMaxStride || (residual == y && ldr != ldy)))
     return DEC_ERR_INVALID_ARG;
   const int most = stream8_rows(K, false);
-  if (most == 0) return DEC_ERR_UNSUPPORTED;
   DeviceGuard dev(h->device);
   if (!dev.ok) return DEC_ERR_CUDA;
   for (int m = 0; m < M; m += most) {

@@ -251,7 +251,7 @@ struct Linear8 {
   long long ldy;
   int M, N, K;
 };
-// Most rows that the streaming kernel takes at this reduction length (0, 8 or 16).
+// Most rows that the streaming kernel takes at this reduction length, up to 16.
 int stream8_rows(int K, bool pair);
 cudaError_t launch_stream8_linear(dec_handle* h, const Linear8& L, cudaStream_t s);
 

@@ -128,7 +128,6 @@ __global__ void __launch_bounds__(256) weight_quant_kernel(const uint16_t* W, lo
   const int k = blockIdx.y * 128 + c * 8;
   __shared__ uint32_t s_most;
   if (t == 0) s_most = 0;
-  pdl_trigger();
   pdl_wait();
   __syncthreads();
   uint4 v[8];

@@ -4,26 +4,32 @@
 //   y[t][n] = sum_b sx[t][b] sw[n / 128][b] sum_{k in b} xq[t][k] wq[n][k]
 //
 // over blocks b of 128 values. Every weight byte is used for a few rows only, so
-// the kernel is a stream of weights past the tensor cores. The products are
-// mma.sync's (16 weight rows x 8 activation rows x 32 values; measured 1.3 clocks
-// a warp instruction and SM, 30 times what the stream needs at 8 rows), because
-// their operands come straight from registers: a lane's 16-byte load of a weight
-// row holds the words that it feeds for two products if both operands take the
-// row's 64 bytes in the same permuted order, and a sum does not mind its order.
-// So weights pass from memory to the products with no shared memory between, as
-// deep in flight as registers allow (tcgen05's operands would have to be staged,
-// and its accumulators fetched again for each block of 128, which has a scale of
-// its own). The fp32 sum of a block is scaled and added to the total right away.
+// the kernel is a stream of weights. The products are mma.sync's (16 weight rows x
+// 8 activation rows x 32 values; measured 1.3 clocks a warp instruction and SM,
+// which is 30 times what the stream needs at 8 rows): a block's fp32 sum lies in
+// registers, where it is scaled and added to the total, while tcgen05's would have
+// to be fetched from tensor memory for every block of 128.
 //
-// Work: a problem is R weight rows for up to 8 NT activation rows; problems' rows
-// form one sequence, cut into one equal range per CTA (one CTA per SM), so that
-// every SM streams the same bytes. Inside a CTA a segment (the rows of its range
-// that belong to one problem) is a sequence of units of 16 rows x 128 bytes, cut
-// once more into one equal range per warp; a warp that holds all blocks of 16
-// rows writes them out, the pieces of rows that several warps share are added in
-// block order after the segment's one barrier. No atomics: the results follow
-// from the inputs and the shape alone.
+// One thread copies weights by TMA into a ring in shared memory, a stage with one copy
+// (of each matrix): groups of h <= 16 rows x blocks of 128 bytes, eight in all, of which
+// each of eight warps multiplies one. (A copy costs its thread about 150 clocks whatever
+// its size, and a stage has 700 at the memory's rate: eight copies of 2 KB streamed at 0.25
+// of the copy rate. Loads from global memory straight into the products' registers, which
+// touch 64 bytes of 8 rows an instruction, streamed at 0.6.) A lane reads 16 bytes of a
+// row for two products, both operands in the same permuted order, which a sum does not
+// mind. The boxes have the 128-byte swizzle; product row g is group row g / 2 + 4 (g % 2),
+// so that the two rows that are read at once lie in different halves of the banks.
+// Warps that share rows leave their sums in shared memory and take turns at adding
+// them, in block order. No atomics: the results follow from the inputs and the shape
+// alone.
+//
+// Work: a problem is R weight rows for up to 8 NT activation rows, cut into groups of h
+// rows; all problems' groups form one sequence, cut into one equal range per CTA (one
+// CTA per SM). h is chosen so that the largest range holds few rows beyond the mean. The
+// groups of a CTA's range that belong to one problem are a segment. The ring runs on from
+// one segment into the next, while the activation rows change.
 #include <algorithm>
+#include <cmath>
 
 #include "common.cuh"
 #include "fp8.cuh"
@@ -33,9 +39,30 @@ namespace dec {
 
 namespace {
 
-constexpr int kWarps = 16;
-constexpr int kThreads = kWarps * 32;
+constexpr int kWarps = 8;                   // that multiply
+constexpr int kThreads = (kWarps + 1) * 32;  // and one that copies
+constexpr int kSums = 2;                    // groups whose sums may wait for their turn
+constexpr int kMaxStages = 12;
 constexpr int kMaxSmem = 232448;
+constexpr int kBarBytes = 8 * (2 * kMaxStages + 2 * kWarps * kSums) + 16;
+
+// Shared memory by its 32-bit address: volatile, so that reads stay behind the waits.
+__device__ __forceinline__ uint4 lds16(uint32_t p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
+  return v;
+}
+__device__ __forceinline__ float2 lds8(uint32_t p) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(p));
+  return v;
+}
+
+// The fast way through a wait that is over already; the whole warp leaves together.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& wc) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc));
+}
 
 }  // namespace
 
@@ -45,222 +72,341 @@ struct Stream8Params {
   const float* xs;   // their scales
   long long ldxs;
   Stream8Bank bank, shared;  // the routed (or only) weights, and the shared expert's
-  const int* table;          // problems (grouped), see Experts8Table
-  int slots, P_max;
+  const int* table;          // problems (grouped), see experts8_table_kernel
+  int P_max;
   bool by_token;  // activation rows by the slot's token, else by the slot
   int R, K, KB, rows;
+  int height;      // rows of a group
+  int WK;          // warps that share 16 rows, a block of 128 each: 1, 2, 4 or 8
+  int stages, xrows;
   const uint16_t* res;
   long long ldr;
   void* out;
   long long ldo;
+  int* err;
+  unsigned long long wait_ns;
 };
 
-// Weights in flight ahead of the products, in units a warp.
-template <bool PAIR>
-constexpr int kDepth = PAIR ? 2 : 4;
-
-__host__ __device__ constexpr int row_pitch(int K) { return (K + 127) / 128 * 128 + 64; }  // 16-byte reads of 2 rows x 64 bytes: no bank twice
-
-template <int NT, bool PAIR>
-static size_t smem_bytes(int K) {
-  const size_t KB = (K + 127) / 128;
-  return 8 * NT * (size_t)row_pitch(K) + KB * 8 * NT * 4 + (size_t)2 * kWarps * (PAIR ? 2 : 1) * 4 * NT * 32 * 4;
+// Distance of activation rows in shared memory: 16-byte reads of 2 rows x 64 bytes then meet no bank twice.
+__host__ __device__ constexpr int pitch_of(int bytes) { return (bytes + 127) / 128 * 128 + 64; }
+// WK warps take the blocks along a group's rows, UW each, WG = kWarps / WK groups a
+// stage. A stage of the ring holds [WK UW][WG h][128] bytes of each matrix, then, if the
+// last block of a row is short, [WG h][128] of such blocks. (A stage costs its readers
+// some 500 clocks of waiting and reading beside the products, so it is large: 32 KB.)
+__host__ __device__ constexpr int blocks_each(int na) { return na == 2 ? 1 : 2; }
+__host__ __device__ constexpr int up1024(int n) { return (n + 1023) & ~1023; }
+__host__ __device__ constexpr int main_bytes(int na, int h) { return up1024(kWarps * blocks_each(na) * h * 128); }
+__host__ __device__ constexpr int warps_along(int KB, int na) {
+  return KB >= 8 * blocks_each(na) ? 8 : KB >= 4 * blocks_each(na) ? 4 : KB >= 2 * blocks_each(na) ? 2 : 1;
+}
+__host__ __device__ constexpr int stage_bytes(int na, int h, int K) {
+  return na * main_bytes(na, h) + (K % 128 ? up1024(kWarps / warps_along((K + 127) / 128, na) * h * 128) : 0);
 }
 
-template <bool PAIR>
-struct Unit {
-  uint4 a[PAIR ? 2 : 1][2][2];  // [matrix][row g, g + 8][64-byte half]
-  float s[PAIR ? 2 : 1][2];     // weight scale of the row's block
+// The groups [ga, gb) of problem p, the part of a CTA's range [.., q1) that begins at q.
+struct Segment {
+  int p, ga, gb;
+  __device__ Segment(long long q, long long q1, int per_problem) {
+    p = (int)(q / per_problem);
+    ga = (int)(q - (long long)p * per_problem);
+    gb = (int)min((long long)per_problem, ga + (q1 - q));
+  }
 };
 
 template <int NT, bool PAIR, bool GROUPED>
-__global__ void __launch_bounds__(kThreads, 1) stream8_kernel(const Stream8Params P) {
+__global__ void __launch_bounds__(kThreads, 1)
+    stream8_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ CUtensorMap tm1,
+                   const __grid_constant__ CUtensorMap ts0, const __grid_constant__ CUtensorMap ts1,
+                   const Stream8Params P) {
   constexpr int NA = PAIR ? 2 : 1;
-  constexpr int D = kDepth<PAIR>;
   constexpr int COLS = 8 * NT;
-  extern __shared__ __align__(16) uint8_t sm[];
-  const int KB = P.KB, pitch = row_pitch(P.K);
-  uint8_t* xq = sm;                                                              // [COLS][pitch]
-  float* xsc = reinterpret_cast<float*>(sm + (size_t)COLS * pitch);              // [KB][COLS]
-  float* red = xsc + (size_t)KB * COLS;                                          // [2 kWarps][NA * 4 * NT][32]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const uint64_t pol = policy_evict_first();
+  constexpr int VALUES = NA * NT * 4;  // totals a lane
+  constexpr int UW = blocks_each(NA);
+  constexpr int BATCH = 8 / UW;        // stages for which a warp's scales are loaded at once
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int KB = P.KB, WK = P.WK, WG = kWarps / WK, xpitch = pitch_of(P.K), h = P.height;
+  const int stage = stage_bytes(NA, h, P.K);
+  const int chunks = (KB + WK * UW - 1) / (WK * UW), per_problem = (P.R + h - 1) / h;
+  uint8_t* xq = ring + (size_t)P.stages * stage;                         // [xrows][xpitch]
+  float* xsc = reinterpret_cast<float*>(xq + (size_t)P.xrows * xpitch);  // [KB][COLS]
+  float* sums = xsc + (size_t)KB * COLS;                                 // [kSums][kWarps][VALUES][32]
+  uint64_t* full = reinterpret_cast<uint64_t*>(sums + kSums * kWarps * VALUES * 32);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* sfull = empty + kMaxStages;  // [kSums][WG]
+  uint64_t* sempty = sfull + kSums * kWarps;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sempty + kSums * kWarps);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < P.stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kWarps);
+    }
+    for (int i = 0; i < kSums * WG; ++i) {
+      mbar_init(&sfull[i], WK);
+      mbar_init(&sempty[i], 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const WaitCtl wc{abort_flag, P.err, P.wait_ns};
 
   long long problems = 1;
   if (GROUPED) {
     pdl_wait();
     problems = ld_act_s32(P.table);
   }
-  const long long total = problems * P.R, G = gridDim.x, c = blockIdx.x;
+  const long long total = problems * per_problem, G = gridDim.x, c = blockIdx.x;
   const long long q0 = c * total / G, q1 = (c + 1) * total / G;
-  bool waited = GROUPED;
+  const int* tokens = P.table + 1 + 3 * P.P_max;
 
-  for (long long q = q0; q < q1;) {
-    const int p = (int)(q / P.R), ra = (int)(q % P.R), rb = (int)min((long long)P.R, ra + (q1 - q));
-    q += rb - ra;
-    Stream8Bank B = P.bank;
-    int cnt = P.rows;
-    long long slot0 = 0;
-    if (GROUPED) {
-      const int e = ld_act_s32(P.table + 1 + 3 * p);
-      slot0 = ld_act_s32(P.table + 2 + 3 * p);
-      cnt = ld_act_s32(P.table + 3 + 3 * p);
-      if (e < 0) {
-        B = P.shared;
-      } else {
-        const size_t w = (size_t)e * P.R * P.K, s = (size_t)e * ((P.R + 127) / 128) * KB;
-        for (int a = 0; a < NA; ++a) B.W[a] += w, B.scales[a] += s;
-      }
-    }
-    const int groups = (rb - ra + 15) >> 4, U = groups * KB;
-    const int u0 = (int)((long long)warp * U / kWarps), u1 = (int)((long long)(warp + 1) * U / kWarps);
-
-    // The next unit to load: group lg, block lk.
-    int lg = u0 / KB, lk = u0 % KB;
-    Unit<PAIR> w[D];
-    auto load = [&](Unit<PAIR>& v) {
-      const int k = lk * 128 + t * 16;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = ra + lg * 16 + g + 8 * i;
-#pragma unroll
-        for (int a = 0; a < NA; ++a) {
-          const uint8_t* src = B.W[a] + (size_t)r * P.K + k;
-#pragma unroll
-          for (int half = 0; half < 2; ++half)
-            v.a[a][i][half] = r < rb && k + 64 * half < P.K ? ld_stream(src + 64 * half, pol) : make_uint4(0, 0, 0, 0);
-          v.s[a][i] = r < rb ? __ldg(B.scales[a] + (size_t)(r >> 7) * KB + lk) : 0.f;
+  if (warp == kWarps) {
+    // ------------------------------------------------------------ copies
+    if (lane != 0) return;
+    const uint64_t pol = policy_evict_first();
+    int s = 0;        // the next stage of the ring
+    uint32_t ph = 0;  // and how often the ring has gone round, mod 2
+    int issued = 0;   // stages, up to the ring's
+    bool ok = true;
+    for (long long q = q0; q < q1 && ok;) {
+      const Segment S(q, q1, per_problem);
+      q += S.gb - S.ga;
+      const int e = GROUPED ? ld_act_s32(P.table + 1 + 3 * S.p) : 0;
+      const CUtensorMap* m0 = e < 0 ? &ts0 : &tm0;
+      const CUtensorMap* m1 = e < 0 ? &ts1 : &tm1;
+      const int row = (e < 0 ? 0 : e) * P.R;  // at most 2^31 rows in a bank
+      for (int j = S.ga; j < S.gb && ok; j += WG)
+        for (int ch = 0; ch < chunks; ++ch) {
+          if (!mbar_wait(&empty[s], ph ^ 1u, wc)) {
+            ok = false;
+            break;
+          }
+          const int kb0 = ch * WK * UW;
+          const bool tail = !PAIR && kb0 + WK * UW > P.K / 128 && P.K % 128 != 0;  // the stage holds the short block
+          mbar_arrive_expect_tx(&full[s], (uint32_t)((NA * kWarps * UW + (tail ? WG : 0)) * h * 128));
+          uint8_t* dst = ring + (size_t)s * stage;
+          tma_load_3d(dst, m0, &full[s], 0, row + j * h, kb0, pol);
+          if (PAIR) tma_load_3d(dst + main_bytes(NA, h), m1, &full[s], 0, row + j * h, kb0, pol);
+          if (tail) tma_load_2d(dst + main_bytes(NA, h), &tm1, &full[s], (KB - 1) * 128, row + j * h, pol);
+          issued = min(issued + 1, P.stages);
+          if (++s == P.stages) s = 0, ph ^= 1u;
         }
-      }
-      if (++lk == KB) lk = 0, ++lg;
-    };
+    }
+    // No copy may still be in flight when the CTA exits: the ring's last stages, newest first.
+    for (; issued > 0; --issued) {
+      if (--s < 0) s = P.stages - 1, ph ^= 1u;
+      mbar_wait_drain(&full[s], ph, P.err, P.wait_ns);
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- products
+  const int g = lane >> 2, t = lane & 3;
+  const int rg = (g >> 1) + 4 * (g & 1);         // this lane's group rows: rg, rg + 8
+  const int sub = warp / WK, along = warp % WK;  // group of a stage, block of its width
+  // this lane's first 16 bytes of row rg in a stage (the second: 64 bytes on, swizzled), and in a stage's short blocks
+  const int line = along * UW * WG * h + sub * h + rg, short_line = sub * h + rg;
+  const int short_at = NA * main_bytes(NA, h) + short_line * 128 + ((t ^ (short_line & 7)) << 4);
+  const int short_kb = P.K % 128 != 0 ? KB - 1 : -1;
+  int at[UW];
 #pragma unroll
-    for (int d = 0; d < D; ++d)
-      if (u0 + d < u1) load(w[d]);
-
-    // This problem's activation rows: values zero up to a whole block.
-    if (!waited) pdl_wait();
-    waited = true;
-    __syncthreads();  // the previous segment is done with them
-    const int chunks = (pitch - 64) >> 4;
-    for (int i = threadIdx.x; i < cnt * chunks; i += kThreads) {
-      const int j = i / chunks, k = (i - j * chunks) * 16;
-      long long row = slot0 + j;
-      if (GROUPED && P.by_token) row = ld_act_s32(P.table + 1 + 3 * P.P_max + slot0 + j);
-      *reinterpret_cast<uint4*>(xq + (size_t)j * pitch + k) =
-          k < P.K ? ld_act16(P.x + row * P.ldx + k) : make_uint4(0, 0, 0, 0);
+  for (int u = 0; u < UW; ++u) at[u] = (line + u * WG * h) * 128 + ((t ^ ((line + u * WG * h) & 7)) << 4);
+  const uint32_t ring_at = smem_u32(ring), up_at = main_bytes(NA, h);
+  // its 16 bytes of an activation row and two columns' scales; columns behind the rows repeat the last one, and nothing
+  // reads their sums
+  uint32_t x_at[NT], xsc_at[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    x_at[nt] = smem_u32(xq) + (uint32_t)min(nt * 8 + g, P.xrows - 1) * xpitch + t * 16;
+    xsc_at[nt] = smem_u32(xsc) + (nt * 8 + 2 * t) * 4;
+  }
+  if (!GROUPED) pdl_wait();
+  int s = 0;           // the ring's next stage
+  uint32_t sph = 0;    // and how often the ring has gone round, mod 2
+  uint32_t turns = 0;  // groups whose sums this warp's group has left so far
+  bool ok = true;
+  for (long long q = q0; q < q1;) {
+    const Segment S(q, q1, per_problem);
+    q += S.gb - S.ga;
+    int slot0 = 0, cnt = P.rows;
+    if (GROUPED) {
+      slot0 = ld_act_s32(P.table + 2 + 3 * S.p);
+      cnt = ld_act_s32(P.table + 3 + 3 * S.p);
     }
-    for (int i = threadIdx.x; i < KB * COLS; i += kThreads) {
-      const int b = i / COLS, j = i % COLS;
-      float v = 0.f;
-      if (j < cnt) {
-        long long row = slot0 + j;
-        if (GROUPED && P.by_token) row = ld_act_s32(P.table + 1 + 3 * P.P_max + slot0 + j);
-        v = ld_act_f32(P.xs + row * P.ldxs + b);
+
+    // Weight scales of a warp's blocks in the BATCH stages from `ch` on of the group j: lane = matrix,
+    // block of rows (16 rows lie in two at most), block.
+    const int e = GROUPED ? ld_act_s32(P.table + 1 + 3 * S.p) : 0;
+    const float* sbase;
+    {
+      const Stream8Bank& B = e < 0 ? P.shared : P.bank;
+      sbase = B.scales[PAIR ? lane >> 4 : 0] + (e < 0 ? 0 : (size_t)e * ((P.R + 127) / 128) * KB);
+    }
+    auto load_scales = [&](int j, int ch) {
+      const int i = lane & 7, kb = ((ch + i / UW) * WK + along) * UW + i % UW;
+      const int block = ((j + sub) * h >> 7) + ((lane >> 3) & 1);
+      const bool in = (PAIR || lane < 16) && j + sub < S.gb && kb < KB && block <= (min((j + sub + 1) * h, P.R) - 1) >> 7;
+      return in ? __ldg(sbase + (size_t)block * KB + kb) : 0.f;
+    };
+    float sc = load_scales(S.ga, 0);
+
+    // This problem's activation rows, zeros up to a whole block.
+    if (!named_bar_and(1, kWarps * 32, ok)) return;  // the previous segment is done with them
+    {
+      const int parts = (xpitch - 64) >> 4;
+      for (int n = threadIdx.x; n < cnt * parts; n += kWarps * 32) {
+        const int j = n / parts, k = (n - j * parts) * 16;
+        const long long row = GROUPED && P.by_token ? ld_act_s32(tokens + slot0 + j) : slot0 + j;
+        *reinterpret_cast<uint4*>(xq + (size_t)j * xpitch + k) =
+            k < P.K ? ld_act16(P.x + row * P.ldx + k) : make_uint4(0, 0, 0, 0);
       }
-      xsc[i] = v;
+      for (int n = threadIdx.x; n < KB * COLS; n += kWarps * 32) {
+        const int b = n / COLS, j = n % COLS;
+        float v = 0.f;
+        if (j < cnt) {
+          const long long row = GROUPED && P.by_token ? ld_act_s32(tokens + slot0 + j) : slot0 + j;
+          v = ld_act_f32(P.xs + row * P.ldxs + b);
+        }
+        xsc[n] = v;
+      }
     }
-    __syncthreads();
+    named_bar_sync(1, kWarps * 32);
 
-    float tot[NA][NT][4];
-    auto clear = [&]() {
+    for (int j = S.ga; j < S.gb && ok; j += WG) {
+      const bool mine = j + sub < S.gb;
+      const int r0 = (j + sub) * h + rg;  // this lane's weight rows: r0, r0 + 8
+      // lanes that hold the scales of their blocks (the group's first or second block of rows)
+      const int from[2] = {((min(r0, P.R - 1) >> 7) - ((j + sub) * h >> 7)) << 3,
+                           min((min(r0 + 8, P.R - 1) >> 7) - ((j + sub) * h >> 7), 1) << 3};
+      float tot[NA][NT][4];
 #pragma unroll
       for (int a = 0; a < NA; ++a)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) tot[a][nt][i] = 0.f;
-    };
-    clear();
+          for (int e = 0; e < 4; ++e) tot[a][nt][e] = 0.f;
 
-    // Sixteen finished rows: this lane's rows g and g + 8, columns 2 t and 2 t + 1 of each eight.
-    auto emit = [&](int gi) {
+      for (int ch = 0; ch < chunks && ok; ch += BATCH) {
+        const float next = ch + BATCH < chunks ? load_scales(j, ch + BATCH) : load_scales(j + WG, 0);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int n = 0; n < BATCH; ++n) {
+          if (ch + n >= chunks) break;
+          if (!warp_wait(&full[s], sph, wc)) {
+            ok = false;
+            break;
+          }
+          const int kb0 = ((ch + n) * WK + along) * UW;
+          uint4 w[UW][NA][2][2];
+          const uint32_t base = ring_at + (uint32_t)(s * stage);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = ra + gi * 16 + g + 8 * (i >> 1), j = nt * 8 + 2 * t + (i & 1);
-          if (r >= rb || j >= cnt) continue;
-          if (PAIR) {
-            const float z = tot[0][nt][i];
-            static_cast<float*>(P.out)[(slot0 + j) * P.ldo + r] = z / (1.0f + expf(-z)) * tot[NA - 1][nt][i];
-          } else if (GROUPED) {
-            static_cast<float*>(P.out)[(slot0 + j) * P.ldo + r] = tot[0][nt][i];
-          } else {
-            float v = tot[0][nt][i];
-            if (P.res != nullptr) v += bf2f(ld_act_u16(P.res + j * P.ldr + r));
-            static_cast<uint16_t*>(P.out)[j * P.ldo + r] = f2bf(v);
+          for (int u = 0; u < UW; ++u) {
+            const uint32_t off = !PAIR && kb0 + u == short_kb ? short_at : at[u];
+#pragma unroll
+            for (int a = 0; a < NA; ++a)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                w[u][a][e][0] = lds16(base + off + a * up_at + e * 1024);
+                w[u][a][e][1] = lds16(base + (off ^ 64) + a * up_at + e * 1024);
+              }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty[s]);
+          if (++s == P.stages) s = 0, sph ^= 1u;
+          if (!mine) continue;
+#pragma unroll
+          for (int u = 0; u < UW; ++u) {
+            // blocks behind the last are zeros of the copies, with scales of zero
+            const int kb = min(kb0 + u, KB - 1);
+            float ws[NA][2];
+#pragma unroll
+            for (int a = 0; a < NA; ++a)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) ws[a][e] = __shfl_sync(0xffffffffu, sc, a * 16 + from[e] + n * UW + u);
+            auto column = [&](int nt) {
+              const uint4 b0 = lds16(x_at[nt] + kb * 128), b1 = lds16(x_at[nt] + kb * 128 + 64);
+              const float2 sx = lds8(xsc_at[nt] + kb * (COLS * 4));
+#pragma unroll
+              for (int a = 0; a < NA; ++a) {
+                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint4 l0 = w[u][a][0][0], l1 = w[u][a][0][1], h0 = w[u][a][1][0], h1 = w[u][a][1][1];
+                mma_e4m3(acc, l0.x, h0.x, l0.y, h0.y, b0.x, b0.y);
+                mma_e4m3(acc, l0.z, h0.z, l0.w, h0.w, b0.z, b0.w);
+                mma_e4m3(acc, l1.x, h1.x, l1.y, h1.y, b1.x, b1.y);
+                mma_e4m3(acc, l1.z, h1.z, l1.w, h1.w, b1.z, b1.w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  tot[a][nt][e] = fmaf(acc[e], ws[a][e >> 1] * ((e & 1) ? sx.y : sx.x), tot[a][nt][e]);
+              }
+            };
+            column(0);
+            if (NT == 2 && (!GROUPED || cnt > 8)) column(NT - 1);
           }
         }
-    };
+        sc = next;
+      }
+      if (!ok) break;
+      if (!mine) continue;
 
-    int gi = u0 / KB, kb = u0 % KB;
-    const int first = gi;
-    auto compute = [&](const Unit<PAIR>& v, int u) {
-      const uint8_t* xk = xq + (size_t)g * pitch + kb * 128 + t * 16;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const uint4 b0 = *reinterpret_cast<const uint4*>(xk + (size_t)nt * 8 * pitch);
-        const uint4 b1 = *reinterpret_cast<const uint4*>(xk + (size_t)nt * 8 * pitch + 64);
-        const float2 sx = *reinterpret_cast<const float2*>(xsc + (size_t)kb * COLS + nt * 8 + 2 * t);
-#pragma unroll
-        for (int a = 0; a < NA; ++a) {
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
-          const uint4 l0 = v.a[a][0][0], l1 = v.a[a][0][1], h0 = v.a[a][1][0], h1 = v.a[a][1][1];
-          mma_e4m3(acc, l0.x, h0.x, l0.y, h0.y, b0.x, b0.y);
-          mma_e4m3(acc, l0.z, h0.z, l0.w, h0.w, b0.z, b0.w);
-          mma_e4m3(acc, l1.x, h1.x, l1.y, h1.y, b1.x, b1.y);
-          mma_e4m3(acc, l1.z, h1.z, l1.w, h1.w, b1.z, b1.w);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            tot[a][nt][i] = fmaf(acc[i], v.s[a][i >> 1] * ((i & 1) ? sx.y : sx.x), tot[a][nt][i]);
+      if (WK > 1) {
+        // Every warp of the group leaves its sums; one of them, in turn, adds them up.
+        const int n = (int)(turns % kSums), b = n * WG + sub;
+        const uint32_t ph = (turns / kSums) & 1u;
+        const int reducer = (int)(turns % WK);
+        ++turns;
+        if (!warp_wait(&sempty[b], ph ^ 1u, wc)) {
+          ok = false;
+          break;
         }
-      }
-      if (++kb == KB || u + 1 == u1) {
-        if (gi * KB >= u0 && (gi + 1) * KB <= u1) {
-          emit(gi);
-        } else {
-          float* slot = red + (size_t)(2 * warp + (gi == first ? 0 : 1)) * (NA * 4 * NT) * 32 + lane;
-#pragma unroll
-          for (int a = 0; a < NA; ++a)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) slot[((a * NT + nt) * 4 + i) * 32] = tot[a][nt][i];
-        }
-        clear();
-        kb = 0;
-        ++gi;
-      }
-    };
-    for (int u = u0; u < u1; u += D) {
-#pragma unroll
-      for (int d = 0; d < D; ++d)
-        if (u + d < u1) {
-          compute(w[d], u + d);
-          if (u + d + D < u1) load(w[d]);
-        }
-    }
-    __syncthreads();
-    // Rows whose blocks several warps hold: a warp adds their pieces in block order.
-    for (int s = warp; s < groups; s += kWarps) {
-      const int wa = (int)((((long long)s * KB + 1) * kWarps - 1) / U);
-      const int wb = (int)((((long long)(s + 1) * KB) * kWarps - 1) / U);
-      if (wa == wb) continue;
-      clear();
-      for (int v = wa; v <= wb; ++v) {
-        const int a0 = (int)((long long)v * U / kWarps), a1 = (int)((long long)(v + 1) * U / kWarps);
-        if (a0 == a1) continue;
-        const float* slot = red + (size_t)(2 * v + (a0 / KB == s ? 0 : 1)) * (NA * 4 * NT) * 32 + lane;
+        float* slot = sums + (size_t)(n * kWarps + warp) * VALUES * 32 + lane;
 #pragma unroll
         for (int a = 0; a < NA; ++a)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) tot[a][nt][i] += slot[((a * NT + nt) * 4 + i) * 32];
+            for (int e = 0; e < 4; ++e) slot[((a * NT + nt) * 4 + e) * 32] = tot[a][nt][e];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sfull[b]);
+        if (along != reducer) continue;
+        if (!warp_wait(&sfull[b], ph, wc)) {
+          ok = false;
+          break;
+        }
+        const float* piece = sums + (size_t)(n * kWarps + sub * WK) * VALUES * 32 + lane;
+#pragma unroll
+        for (int a = 0; a < NA; ++a)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float* v = piece + ((a * NT + nt) * 4 + e) * 32;
+              float sum = v[0];
+#pragma unroll
+              for (int w = 1; w < kWarps; ++w)
+                if (w < WK) sum += v[w * VALUES * 32];
+              tot[a][nt][e] = sum;
+            }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sempty[b]);
       }
-      emit(s);
+      // Finished rows: this lane's two, columns 2 t and 2 t + 1 of each eight.
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = r0 + 8 * (e >> 1), col = nt * 8 + 2 * t + (e & 1);
+          if (rg + 8 * (e >> 1) >= h || r >= P.R || col >= cnt) continue;
+          const float v = tot[0][nt][e];
+          if (PAIR) {
+            static_cast<float*>(P.out)[(long long)(slot0 + col) * P.ldo + r] = v / (1.0f + expf(-v)) * tot[NA - 1][nt][e];
+          } else if (GROUPED) {
+            static_cast<float*>(P.out)[(long long)(slot0 + col) * P.ldo + r] = v;
+          } else {
+            const float a = P.res != nullptr ? bf2f(ld_act_u16(P.res + col * P.ldr + r)) : 0.f;
+            static_cast<uint16_t*>(P.out)[col * P.ldo + r] = f2bf(v + a);
+          }
+        }
     }
   }
 }
@@ -356,9 +502,80 @@ __global__ void __launch_bounds__(256) experts8_combine_kernel(const float* y, c
 }
 
 // ---------------------------------------------------------------- host side
+// Shared memory besides the ring.
+static size_t fixed_bytes(int xrows, int nt, int K, bool pair) {
+  const size_t KB = (K + 127) / 128;
+  return 1024 + (size_t)xrows * pitch_of(K) + KB * 8 * nt * 4 + (size_t)kSums * kWarps * (pair ? 2 : 1) * nt * 4 * 32 * 4 +
+         kBarBytes;
+}
+static size_t one_stage(int K, bool pair, int h) { return stage_bytes(pair ? 2 : 1, h, K); }
+// Ring stages that fit beside it.
+static int stages_for(int xrows, int nt, int K, bool pair, int h) {
+  const size_t fixed = fixed_bytes(xrows, nt, K, pair);
+  if (fixed >= (size_t)kMaxSmem) return 0;
+  return std::min<int>(kMaxStages, (int)((kMaxSmem - fixed) / one_stage(K, pair, h)));
+}
+
+// Rows of a group: the largest range of a CTA in rows, with two rows' time for each group.
+static int group_height(int R, double problems, int grid) {
+  int best = 16;
+  double least = 1e30;
+  for (int h = 16; h >= 8; --h) {
+    const double groups = std::ceil(problems * ((R + h - 1) / h) / grid);
+    const double cost = groups * (h + 2);
+    if (cost < least) least = cost, best = h;
+  }
+  return best;
+}
+
+// Weights [rows][K]: whole blocks of 128 as [K / 128][rows][128], boxes of `blocks` x `height` rows; or, for
+// the short block at a row's end, as they are (what is beyond K reads as zeros).
+static bool encode_blocks(const dec_handle* h, CUtensorMap* m, const uint8_t* W, int K, long long rows, int height,
+                          int blocks) {
+  const int whole = std::max(1, K / 128);
+  cuuint64_t dims[3] = {(cuuint64_t)std::min(128, K), (cuuint64_t)rows, (cuuint64_t)whole};
+  cuuint64_t strides[2] = {(cuuint64_t)K, 128};
+  cuuint32_t box[3] = {128, (cuuint32_t)height, (cuuint32_t)blocks};
+  cuuint32_t es[3] = {1, 1, 1};
+  return h->encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(W), dims, strides, box, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+static bool encode_short(const dec_handle* h, CUtensorMap* m, const uint8_t* W, int K, long long rows, int height) {
+  cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)K};
+  cuuint32_t box[2] = {128, (cuuint32_t)height};
+  cuuint32_t es[2] = {1, 1};
+  return h->encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(W), dims, strides, box, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// `problems`: how many there will be, about; E: experts in the bank (1 for one matrix).
 template <int NT, bool PAIR, bool GROUPED>
-static cudaError_t launch_one(dec_handle* h, const Stream8Params& P, int grid, cudaStream_t s) {
-  const size_t smem = smem_bytes<NT, PAIR>(P.K);
+static cudaError_t launch_one(dec_handle* h, Stream8Params P, int xrows, double problems, int E, cudaStream_t s) {
+  P.KB = (P.K + 127) / 128;
+  P.WK = warps_along(P.KB, PAIR ? 2 : 1);
+  P.xrows = xrows;
+  P.height = group_height(P.R, problems, h->sms);
+  P.stages = stages_for(xrows, NT, P.K, PAIR, P.height);
+  P.err = h->d_err;
+  P.wait_ns = h->wait_ns;
+  if (P.stages < 2) return cudaErrorInvalidConfiguration;
+  const int box = kWarps / P.WK * P.height;
+  const long long rows = (long long)E * P.R;
+  const Stream8Bank& S = P.shared.W[0] != nullptr ? P.shared : P.bank;
+  const long long srows = P.shared.W[0] != nullptr ? P.R : rows;
+  CUtensorMap m[4];
+  if (!encode_blocks(h, &m[0], P.bank.W[0], P.K, rows, box, P.WK * blocks_each(PAIR ? 2 : 1)) || !encode_blocks(h, &m[2], S.W[0], P.K, srows, box, P.WK * blocks_each(PAIR ? 2 : 1)))
+    return cudaErrorInvalidValue;
+  m[1] = m[0];
+  m[3] = m[2];
+  if (PAIR && (!encode_blocks(h, &m[1], P.bank.W[1], P.K, rows, box, P.WK * blocks_each(PAIR ? 2 : 1)) ||
+               !encode_blocks(h, &m[3], S.W[1], P.K, srows, box, P.WK * blocks_each(PAIR ? 2 : 1))))
+    return cudaErrorInvalidValue;
+  if (!PAIR && P.K % 128 != 0 && !encode_short(h, &m[1], P.bank.W[0], P.K, rows, box)) return cudaErrorInvalidValue;
+  const size_t smem = fixed_bytes(xrows, NT, P.K, PAIR) + (size_t)P.stages * one_stage(P.K, PAIR, P.height);
   static bool attr_set = false;  // per process; every device gets the same attribute
   if (!attr_set) {
     const cudaError_t e = cudaFuncSetAttribute(stream8_kernel<NT, PAIR, GROUPED>,
@@ -366,12 +583,13 @@ static cudaError_t launch_one(dec_handle* h, const Stream8Params& P, int grid, c
     if (e != cudaSuccess) return e;
     attr_set = true;
   }
-  return launch_k(h, stream8_kernel<NT, PAIR, GROUPED>, dim3(grid), dim3(kThreads), smem, s, P);
+  return launch_k(h, stream8_kernel<NT, PAIR, GROUPED>, dim3(h->sms), dim3(kThreads), smem, s, m[0], m[1], m[2], m[3], P);
 }
 
 int stream8_rows(int K, bool pair) {
-  if (pair) return smem_bytes<2, true>(K) <= kMaxSmem ? 16 : smem_bytes<1, true>(K) <= kMaxSmem ? 8 : 0;
-  return smem_bytes<2, false>(K) <= kMaxSmem ? 16 : smem_bytes<1, false>(K) <= kMaxSmem ? 8 : 0;
+  for (int rows = 16; rows > 0; --rows)
+    if (stages_for(rows, rows > 8 ? 2 : 1, K, pair, 16) >= 2) return rows;
+  return 0;
 }
 
 cudaError_t launch_stream8_linear(dec_handle* h, const Linear8& L, cudaStream_t s) {
@@ -384,14 +602,12 @@ cudaError_t launch_stream8_linear(dec_handle* h, const Linear8& L, cudaStream_t 
   P.bank.scales[0] = L.ws;
   P.R = L.N;
   P.K = L.K;
-  P.KB = (L.K + 127) / 128;
   P.rows = L.M;
   P.res = L.res;
   P.ldr = L.ldr;
   P.out = L.y;
   P.ldo = L.ldy;
-  const int grid = std::min(h->sms, L.N);
-  return L.M <= 8 ? launch_one<1, false, false>(h, P, grid, s) : launch_one<2, false, false>(h, P, grid, s);
+  return L.M <= 8 ? launch_one<1, false, false>(h, P, L.M, 1, 1, s) : launch_one<2, false, false>(h, P, L.M, 1, 1, s);
 }
 
 Experts8Plan experts8_plan(int M, int k, int E, int H, int I, bool shared) {
@@ -408,6 +624,9 @@ cudaError_t launch_experts8(dec_handle* h, const Experts8& X, const Experts8Plan
                             uint8_t* hq, float* hs, float* y, cudaStream_t s) {
   const int M = X.M, k = X.k, H = X.H, I = X.I;
   const bool shared = X.sgate.W[0] != nullptr;
+  const int xrows = std::min(plan.most, M * k);
+  // experts that at least one of M k even choices falls on
+  const double problems = X.E * (1.0 - std::pow(1.0 - 1.0 / X.E, M * k)) + (shared ? (M + plan.most - 1) / plan.most : 0);
   cudaError_t e;
   {
     LaunchScope scope(h, "experts8_table", s);
@@ -423,17 +642,16 @@ cudaError_t launch_experts8(dec_handle* h, const Experts8& X, const Experts8Plan
   P.bank = X.gate;
   P.shared = X.sgate;
   P.table = table;
-  P.slots = plan.slots;
   P.P_max = plan.P_max;
   P.by_token = true;
   P.R = I;
   P.K = H;
-  P.KB = H / 128;
   P.out = inner;
   P.ldo = I;
   {
     LaunchScope scope(h, "experts8_gate_up", s);
-    e = plan.most <= 8 ? launch_one<1, true, true>(h, P, h->sms, s) : launch_one<2, true, true>(h, P, h->sms, s);
+    e = plan.most <= 8 ? launch_one<1, true, true>(h, P, xrows, problems, X.E, s)
+                       : launch_one<2, true, true>(h, P, xrows, problems, X.E, s);
     if (e != cudaSuccess) return e;
   }
   {
@@ -458,12 +676,12 @@ cudaError_t launch_experts8(dec_handle* h, const Experts8& X, const Experts8Plan
   P.by_token = false;
   P.R = H;
   P.K = I;
-  P.KB = I / 128;
   P.out = y;
   P.ldo = H;
   {
     LaunchScope scope(h, "experts8_down", s);
-    e = plan.most <= 8 ? launch_one<1, false, true>(h, P, h->sms, s) : launch_one<2, false, true>(h, P, h->sms, s);
+    e = plan.most <= 8 ? launch_one<1, false, true>(h, P, xrows, problems, X.E, s)
+                       : launch_one<2, false, true>(h, P, xrows, problems, X.E, s);
     if (e != cudaSuccess) return e;
   }
   LaunchScope scope(h, "experts8_combine", s);
