@@ -46,6 +46,11 @@ constexpr int kMaxStages = 12;
 constexpr int kMaxSmem = 232448;
 constexpr int kBarBytes = 8 * (2 * kMaxStages + 2 * kWarps * kSums) + 16;
 
+// 4-byte asynchronous copy from global to shared memory.
+__device__ __forceinline__ void copy4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 // Shared memory by its 32-bit address: volatile, so that reads stay behind the waits.
 __device__ __forceinline__ uint4 lds16(uint32_t p) {
   uint4 v;
@@ -252,26 +257,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     float sc = load_scales(S.ga, 0);
 
-    // This problem's activation rows, zeros up to a whole block.
+    // This problem's activation rows, zeros up to a whole block: all copies in flight at once.
     if (!named_bar_and(1, kWarps * 32, ok)) return;  // the previous segment is done with them
-    {
-      const int parts = (xpitch - 64) >> 4;
-      for (int n = threadIdx.x; n < cnt * parts; n += kWarps * 32) {
-        const int j = n / parts, k = (n - j * parts) * 16;
-        const long long row = GROUPED && P.by_token ? ld_act_s32(tokens + slot0 + j) : slot0 + j;
-        *reinterpret_cast<uint4*>(xq + (size_t)j * xpitch + k) =
-            k < P.K ? ld_act16(P.x + row * P.ldx + k) : make_uint4(0, 0, 0, 0);
-      }
-      for (int n = threadIdx.x; n < KB * COLS; n += kWarps * 32) {
-        const int b = n / COLS, j = n % COLS;
-        float v = 0.f;
-        if (j < cnt) {
-          const long long row = GROUPED && P.by_token ? ld_act_s32(tokens + slot0 + j) : slot0 + j;
-          v = ld_act_f32(P.xs + row * P.ldxs + b);
+    for (int j = warp; j < COLS; j += kWarps) {
+      const bool in = j < cnt;
+      const long long row = in && GROUPED && P.by_token ? ld_act_s32(tokens + slot0 + j) : slot0 + j;
+      if (in) {
+        const uint8_t* src = P.x + row * P.ldx;
+        uint8_t* dst = xq + (size_t)j * xpitch;
+        for (int k = lane * 16; k < xpitch - 64; k += 512) {
+          if (k < P.K)
+            cp_async16(dst + k, src + k);
+          else
+            *reinterpret_cast<uint4*>(dst + k) = make_uint4(0, 0, 0, 0);
         }
-        xsc[n] = v;
+      }
+      for (int b = lane; b < KB; b += 32) {
+        if (in)
+          copy4(xsc + b * COLS + j, P.xs + row * P.ldxs + b);
+        else
+          xsc[b * COLS + j] = 0.f;
       }
     }
+    cp_async_wait_all();
     named_bar_sync(1, kWarps * 32);
 
     for (int j = S.ga; j < S.gb && ok; j += WG) {
