@@ -20,7 +20,7 @@ ARCH = os.environ.get("MOE_DECODE_ARCH", "103a")
 
 SOURCES = ["api.cu", "gemv.cu", "umma.cu", "router.cu", "misc.cu", "noalloc.cu", "gemv_moe.cu", "route_shared.cu",
            "batch.cu", "attention.cu", "attention_tc.cu", "api_attention.cu", "quant8.cu", "stream8.cu",
-           "api_fp8.cu"]
+           "gemm8.cu", "api_fp8.cu"]
 HEADERS = ["common.cuh", "internal.h", "attention.cuh", "fp8.cuh"]
 PUBLIC = os.path.join(ROOT, "include", "moe_decode.h")
 

@@ -34,6 +34,9 @@ bool linear_shape_ok(int M, int N, int K) {
   return M >= 1 && M <= kMaxRows && N >= 1 && N <= kMaxRows && K >= 16 && K <= kMaxWidth && K % 16 == 0;
 }
 
+// The streaming kernel up to 16 rows that fit in its shared memory, the tcgen05 kernel otherwise.
+bool linear_streams(int M, int K) { return M <= stream8_rows(K, false); }
+
 bool experts_shape_ok(const dec_moe_fp8_weights* W, int M, int k) {
   return W != nullptr && M >= 1 && M <= kMaxExpertRows && k >= 1 && k <= kMaxChoices && W->E >= 1 &&
          W->E <= kMaxExperts && W->H >= 128 && W->H % 128 == 0 && W->H <= kMaxWidth && W->I >= 128 && W->I % 128 == 0 &&
@@ -97,7 +100,7 @@ dec_status dec_quant_weight(dec_handle* h, const dec_bf16* W, int64_t N, int K, 
 
 dec_status dec_linear_fp8_workspace_size(const dec_handle* h, int M, int N, int K, size_t* bytes) {
   if (h == nullptr || bytes == nullptr || !linear_shape_ok(M, N, K)) return DEC_ERR_INVALID_ARG;
-  *bytes = 0;
+  *bytes = linear_streams(M, K) ? 0 : gemm8_ws_bytes(h, M, N, K);
   return DEC_OK;
 }
 
@@ -108,16 +111,14 @@ dec_status dec_linear_fp8(dec_handle* h, const dec_fp8_rows* x, const dec_fp8_we
   if (!rows_ok(x, K) || !weight_ok(*W) || !al(y, 2) || ldy < N || ldy > kMaxStride) return DEC_ERR_INVALID_ARG;
   if (residual != nullptr && (!al(residual, 2) || ldr < N || ldr > kMaxStride || (residual == y && ldr != ldy)))
     return DEC_ERR_INVALID_ARG;
-  const int most = stream8_rows(K, false);
+  const bool stream8 = linear_streams(M, K);
+  const size_t need = stream8 ? 0 : gemm8_ws_bytes(h, M, N, K);
+  if (need > 0 && (ws == nullptr || !al(ws, 16) || ws_bytes < need)) return DEC_ERR_INVALID_ARG;
   DeviceGuard dev(h->device);
   if (!dev.ok) return DEC_ERR_CUDA;
-  for (int m = 0; m < M; m += most) {
-    Linear8 L = {x->q + m * x->ldq, x->ldq, x->scales + m * x->lds, x->lds, W->q, W->scales,
-                 residual ? residual + m * ldr : nullptr, ldr, y + m * ldy, ldy, M - m < most ? M - m : most, N, K};
-    LaunchScope scope(h, "linear_fp8", stream);
-    if (launch_stream8_linear(h, L, stream) != cudaSuccess) return DEC_ERR_CUDA;
-  }
-  return DEC_OK;
+  const Linear8 L = {x->q, x->ldq, x->scales, x->lds, W->q, W->scales, residual, ldr, y, ldy, M, N, K};
+  LaunchScope scope(h, "linear_fp8", stream);
+  return status(stream8 ? launch_stream8_linear(h, L, stream) : launch_gemm8(h, L, ws, stream));
 }
 
 dec_status moe_experts_fp8_workspace_size(const dec_handle* h, const dec_moe_fp8_weights* Wt, int M, int k,

@@ -1,0 +1,448 @@
+// Products of 8-bit weights with many 8-bit rows, on tcgen05: decode batches above
+// what the streaming kernel takes, and prompts.
+//
+//   y[t][n] = [r[t][n] +] sum_b sx[t][b] sw[n / 128][b] sum_{k in b} xq[t][k] wq[n][k]
+//
+// A tile is 128 rows x BN weights. Its k-blocks of 128 values have scales of their own,
+// so the tensor cores' sum of a block is not kept: each block goes to a tensor-memory
+// buffer of its own, is fetched by eight warps, scaled and added to totals in registers,
+// while the next blocks are multiplied. Rows are the product's M side, so a thread owns
+// one row and BN / 2 columns of one block of weights: its scale is one number a k-block,
+// and a fetched value costs half a packed fused multiply-add.
+//
+// One CTA per SM. The sequence of all (tile, k-block) pairs is cut into one equal range
+// per CTA, so no wave is left half full and short sequences use every SM. A tile that
+// several CTAs share is finished by the one that publishes its piece last: it adds all
+// pieces in k order (no atomics on values; the results follow from the inputs and the
+// shape alone).
+//
+// Per CTA: warp 0 issues the TMA loads of a k-block's rows and weights (128-byte
+// swizzle) into a ring in shared memory, warp 1 the tcgen05.mma (128 x BN x 32, kind
+// f8f6f4), warps 2-9 fetch, scale and add.
+#include <algorithm>
+
+#include "common.cuh"
+#include "fp8.cuh"
+#include "internal.h"
+
+namespace dec {
+
+namespace {
+
+constexpr int kRows = 128;
+constexpr int kBlock = 128;  // k values of a block, one row of the swizzle
+constexpr int kThreads = 320;
+constexpr int kAdders = 256;
+constexpr int kTmem = 512;
+
+template <int BN>
+struct Plan {
+  static constexpr int kABytes = kRows * kBlock;
+  static constexpr int kStageBytes = kABytes + BN * kBlock;
+  static constexpr int kStages = 196608 / kStageBytes;  // 6 or 4
+  static constexpr int kBuffers = kTmem / BN;           // 4 or 2
+  static constexpr int kCols = BN / 2;                  // a thread's
+  static constexpr int kBarOff = kStages * kStageBytes;
+  static constexpr int kBytes = kBarOff + 8 * (2 * kStages + 2 * kBuffers + 1) + 64 + 1024;
+};
+
+struct Gemm8Params {
+  int M, N, K, KB, mtiles;
+  const float* xs;
+  long long ldxs;
+  const float* ws;
+  const uint16_t* res;
+  long long ldr;
+  uint16_t* y;
+  long long ldy;
+  float* pieces;
+  int piece_rows;  // rows of a published piece: the tile's, or the batch's up to a warp's
+  int* counters;   // one a CTA: pieces published of the tile whose first piece it holds
+  int* err;
+  unsigned long long wait_ns;
+};
+
+__device__ __forceinline__ long long range_start(long long c, long long W, long long G) { return c * W / G; }
+__device__ __forceinline__ int cta_of(long long j, long long W, long long G) { return (int)(((j + 1) * G - 1) / W); }
+
+// Instruction descriptor, kind::f8f6f4: D fp32, A and B e4m3, both K-major, 128 x N.
+constexpr uint32_t idesc_e4m3(int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24); }
+
+__device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 32 consecutive fp32 columns of this thread's tensor-memory lane, complete on return.
+__device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at)
+      : "memory");
+}
+
+// acc + v * f for two values, fp32.
+__device__ __forceinline__ uint64_t fma2(uint32_t lo, uint32_t hi, uint64_t f, uint64_t acc) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(f));
+  return acc;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  uint32_t lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(__float_as_uint(lo)), "r"(__float_as_uint(hi)));
+  return v;
+}
+
+}  // namespace
+
+template <int BN>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm8_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const Gemm8Params P) {
+  using L = Plan<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint64_t* empty = full + L::kStages;
+  uint64_t* tfull = empty + L::kStages;
+  uint64_t* tempty = tfull + L::kBuffers;
+  uint64_t* done = tempty + L::kBuffers;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* s_last = abort_flag + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int KB = P.KB, mtiles = P.mtiles;
+  const long long W = (long long)mtiles * ((P.N + BN - 1) / BN) * KB;
+  const long long G = gridDim.x, c = blockIdx.x;
+  const long long j0 = range_start(c, W, G), j1 = range_start(c + 1, W, G);
+
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < L::kBuffers; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], kAdders / 32);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tmap_prefetch(&tx);
+    tmap_prefetch(&tw);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtl wc{abort_flag, P.err, P.wait_ns};
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ copies
+    if (lane == 0) {
+      const uint64_t pol_w = mtiles == 1 ? policy_evict_first() : policy_evict_last();  // read once, or by every tile of rows
+      const uint64_t pol_x = policy_evict_last();
+      auto load_w = [&](int s, int kb, int nt) {
+        tma_load_2d(smem + s * L::kStageBytes + L::kABytes, &tw, &full[s], kb * kBlock, nt * BN, pol_w);
+      };
+      auto load_x = [&](int s, int kb, int mt) {
+        tma_load_2d(smem + s * L::kStageBytes, &tx, &full[s], kb * kBlock, mt * kRows, pol_x);
+      };
+      // Static weights of the first ring's worth before the dependency wait.
+      const int pre = (int)min(j1 - j0, (long long)L::kStages);
+      const int tile0 = (int)(j0 / KB), k0 = (int)(j0 - (long long)tile0 * KB);
+      int tile = tile0, kb = k0;
+      for (int s = 0; s < pre; ++s) {
+        mbar_arrive_expect_tx(&full[s], L::kStageBytes);
+        load_w(s, kb, tile / mtiles);
+        if (++kb == KB) kb = 0, ++tile;
+      }
+      pdl_wait();
+      tile = tile0, kb = k0;
+      int s = 0;
+      uint32_t ph = 0;
+      long long issued = 0;
+      for (long long i = 0; i < j1 - j0; ++i) {
+        if (i >= pre) {
+          if (!mbar_wait(&empty[s], ph ^ 1u, wc)) break;
+          mbar_arrive_expect_tx(&full[s], L::kStageBytes);
+          load_w(s, kb, tile / mtiles);
+        }
+        load_x(s, kb, tile % mtiles);
+        if (++kb == KB) kb = 0, ++tile;
+        if (++s == L::kStages) s = 0, ph ^= 1u;
+        ++issued;
+      }
+      // No copy may still be in flight when the CTA exits.
+      for (long long n = min(issued, (long long)L::kStages); n > 0; --n) {
+        if (--s < 0) s = L::kStages - 1, ph ^= 1u;
+        mbar_wait_drain(&full[s], ph, P.err, P.wait_ns);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      int s = 0, b = 0;
+      uint32_t ph = 0, tph = 0;
+      for (long long j = j0; j < j1; ++j) {
+        if (!mbar_wait(&tempty[b], tph ^ 1u, wc)) break;
+        if (!mbar_wait(&full[s], ph, wc)) break;
+        tc_fence_after();
+        const uint32_t a = smem_u32(smem + s * L::kStageBytes), w = a + L::kABytes, d = tmem + (uint32_t)(b * BN);
+#pragma unroll
+        for (int k = 0; k < kBlock / 32; ++k)
+          umma_e4m3(d, sw128_desc(a + k * 32), sw128_desc(w + k * 32), idesc_e4m3(BN), k > 0);
+        umma_commit(&empty[s]);
+        umma_commit(&tfull[b]);
+        if (++s == L::kStages) s = 0, ph ^= 1u;
+        if (++b == L::kBuffers) b = 0, tph ^= 1u;
+      }
+      // Every product issued above must complete before tensor memory is released.
+      umma_commit(done);
+      mbar_wait_drain(done, 0, P.err, P.wait_ns);
+    }
+  } else {
+    // ------------------------------------------------------------ sums
+    const int q = warp & 3, half = (warp - 2) >> 2;  // tensor-memory lanes 32 q .., columns of this half
+    const int row = q * 32 + lane, col0 = half * L::kCols;
+    const int et = threadIdx.x - 64;
+    const bool out_vec = (reinterpret_cast<uintptr_t>(P.y) & 15) == 0 && (P.ldy & 7) == 0;
+    const bool res_vec = (reinterpret_cast<uintptr_t>(P.res) & 15) == 0 && (P.ldr & 7) == 0;
+    pdl_wait();
+    int b = 0;
+    uint32_t tph = 0;
+    bool ok = true;
+    int seg = 0;
+    for (long long j = j0; j < j1; ++seg) {
+      const int tile = (int)(j / KB), kb0 = (int)(j - (long long)tile * KB);
+      const int kb1 = (int)min((long long)KB, kb0 + (j1 - j));
+      j += kb1 - kb0;
+      const int m0 = (tile % mtiles) * kRows, n0 = (tile / mtiles) * BN;
+      const bool rows_here = m0 + q * 32 < P.M;  // this warp's rows hold some of the batch's
+      const float* xs = P.xs + (long long)min(m0 + row, P.M - 1) * P.ldxs;
+      const float* ws = P.ws + (long long)min((n0 + col0) >> 7, (P.N - 1) >> 7) * KB;
+      uint64_t acc[L::kCols / 2];
+#pragma unroll
+      for (int i = 0; i < L::kCols / 2; ++i) acc[i] = 0;
+      // Scales of eight blocks at a time, the next eight's loads in flight: the row's, and
+      // the weights' spread over lanes 0-7.
+      float sx[8], nx[8], sw, nw;
+      auto load_scales = [&](int kb, float (&x)[8], float& w) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = kb + i < kb1 ? ld_act_f32(xs + kb + i) : 0.f;
+        w = kb + (lane & 7) < kb1 ? __ldg(ws + kb + (lane & 7)) : 0.f;
+      };
+      if (rows_here) load_scales(kb0, sx, sw);
+      for (int kb = kb0; kb < kb1 && ok; kb += 8) {
+        if (rows_here) load_scales(kb + 8, nx, nw);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (kb + i >= kb1) break;
+          if (!__all_sync(0xffffffffu, mbar_wait(&tfull[b], tph, wc))) {
+            ok = false;
+            break;
+          }
+          if (rows_here) {
+            tc_fence_after();
+            const float f = sx[i] * __shfl_sync(0xffffffffu, sw, i);
+            const uint64_t ff = pack2(f, f);
+            const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BN + col0);
+#pragma unroll
+            for (int ch = 0; ch < L::kCols / 32; ++ch) {
+              uint32_t v[32];
+              tmem_ld32(at + ch * 32, v);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) acc[ch * 16 + e] = fma2(v[2 * e], v[2 * e + 1], ff, acc[ch * 16 + e]);
+            }
+            tc_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[b]);
+          if (++b == L::kBuffers) b = 0, tph ^= 1u;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sx[i] = nx[i];
+        sw = nw;
+      }
+      if (!named_bar_and(1, kAdders, ok)) break;  // leave together if a warp gave up
+
+      if (kb1 - kb0 < KB) {
+        // A piece: published, four columns of a row at a time; whoever publishes the last adds them all in k order.
+        const int p_rows = P.piece_rows, c0 = cta_of((long long)tile * KB, W, G);
+        const int c1 = cta_of((long long)tile * KB + KB - 1, W, G);
+        auto piece = [&](int cc) {
+          const bool inside = range_start(cc, W, G) >= (long long)tile * KB;
+          return reinterpret_cast<float4*>(P.pieces) + (size_t)(cc * 2 + (inside ? 0 : 1)) * (BN / 4) * p_rows +
+                 (size_t)(col0 / 4) * p_rows + row;
+        };
+        if (rows_here) {
+          float4* dst = piece((int)c);
+#pragma unroll
+          for (int i = 0; i < L::kCols / 4; ++i) {
+            const float2 lo = unpack2(acc[2 * i]), hi = unpack2(acc[2 * i + 1]);
+            __stcg(dst + (size_t)i * p_rows, make_float4(lo.x, lo.y, hi.x, hi.y));
+          }
+        }
+        __threadfence();
+        named_bar_sync(1, kAdders);
+        if (et == 0) *s_last = atom_add_acq_rel_gpu(P.counters + c0, 1) == c1 - c0 ? 1 : 0;
+        named_bar_sync(1, kAdders);
+        const bool last = *s_last != 0;
+        named_bar_sync(1, kAdders);  // read by all before the next piece
+        if (!last) continue;
+        __threadfence();
+        if (et == 0) P.counters[c0] = 0;  // leave the workspace reusable
+        if (rows_here) {
+#pragma unroll
+          for (int i = 0; i < L::kCols / 2; ++i) acc[i] = 0;
+          for (int cc = c0; cc <= c1; ++cc) {
+            const float4* src = piece(cc);
+#pragma unroll
+            for (int i = 0; i < L::kCols / 4; ++i) {
+              const float4 v = __ldcg(src + (size_t)i * p_rows);
+              const float2 lo = unpack2(acc[2 * i]), hi = unpack2(acc[2 * i + 1]);
+              acc[2 * i] = pack2(lo.x + v.x, lo.y + v.y);
+              acc[2 * i + 1] = pack2(hi.x + v.z, hi.y + v.w);
+            }
+          }
+        }
+      }
+      // This thread's columns of its row.
+      if (m0 + row < P.M) {
+        const int n = n0 + col0;
+        uint16_t* out = P.y + (long long)(m0 + row) * P.ldy + n;
+        const uint16_t* res = P.res != nullptr ? P.res + (long long)(m0 + row) * P.ldr + n : nullptr;
+#pragma unroll
+        for (int i = 0; i < L::kCols / 8; ++i) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 d = unpack2(acc[4 * i + e]);
+            v[2 * e] = d.x, v[2 * e + 1] = d.y;
+          }
+          const int left = P.N - n - 8 * i;  // columns from here on
+          if (left <= 0) break;
+          if (res != nullptr) {
+            if (res_vec && left >= 8) {
+              const uint4 r = ld_act16(res + 8 * i);
+              const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[2 * e] += bf_lo(w[e]), v[2 * e + 1] += bf_hi(w[e]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (e < left) v[e] += bf2f(ld_act_u16(res + 8 * i + e));
+            }
+          }
+          if (out_vec && left >= 8) {
+            *reinterpret_cast<uint4*>(out + 8 * i) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (e < left) out[8 * i + e] = f2bf(v[e]);
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmem);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+// 256 weights a tile where the products bound the time (their rows then serve twice as
+// many weights from shared memory), 128 where the weights' bytes do, and short pieces count.
+static int tile_weights(int M) { return M > kRows ? 256 : 128; }
+
+static int gemm8_grid(const dec_handle* h, int M, int N, int K, int bn) {
+  const long long tiles = (long long)((M + kRows - 1) / kRows) * ((N + bn - 1) / bn), KB = (K + kBlock - 1) / kBlock;
+  // a range of at least four blocks, or a tile
+  return (int)std::min<long long>(h->sms, std::max(tiles, (tiles * KB + 3) / 4));
+}
+
+static int piece_rows(int M) { return std::min(kRows, (M + 31) / 32 * 32); }
+static size_t counter_bytes(const dec_handle* h) { return ((size_t)h->sms * 4 + 255) & ~size_t(255); }
+
+size_t gemm8_ws_bytes(const dec_handle* h, int M, int N, int K) {
+  const int bn = tile_weights(M);
+  return counter_bytes(h) + (size_t)2 * gemm8_grid(h, M, N, K, bn) * bn * piece_rows(M) * 4;
+}
+
+static bool encode_tile(const dec_handle* h, CUtensorMap* m, const uint8_t* p, int K, int rows, long long ld, int box_rows) {
+  cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)ld};
+  cuuint32_t box[2] = {kBlock, (cuuint32_t)box_rows};
+  cuuint32_t es[2] = {1, 1};
+  return h->encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p), dims, strides, box, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN>
+static cudaError_t launch_bn(dec_handle* h, const Linear8& A, void* ws, cudaStream_t s) {
+  using L = Plan<BN>;
+  static_assert(L::kBytes <= 232448, "shared memory above the opt-in maximum");
+  CUtensorMap tx, tw;
+  if (!encode_tile(h, &tx, A.x, A.K, A.M, A.ldx, kRows) || !encode_tile(h, &tw, A.W, A.K, A.N, A.K, BN))
+    return cudaErrorInvalidValue;
+  static bool attr_set = false;  // per process; every device gets the same attribute
+  if (!attr_set) {
+    const cudaError_t e = cudaFuncSetAttribute(gemm8_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+    if (e != cudaSuccess) return e;
+    attr_set = true;
+  }
+  Gemm8Params P = {};
+  P.M = A.M;
+  P.N = A.N;
+  P.K = A.K;
+  P.KB = (A.K + kBlock - 1) / kBlock;
+  P.mtiles = (A.M + kRows - 1) / kRows;
+  P.xs = A.xs;
+  P.ldxs = A.ldxs;
+  P.ws = A.ws;
+  P.res = A.res;
+  P.ldr = A.ldr;
+  P.y = A.y;
+  P.ldy = A.ldy;
+  P.counters = static_cast<int*>(ws);
+  P.pieces = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + counter_bytes(h));
+  P.piece_rows = piece_rows(A.M);
+  P.err = h->d_err;
+  P.wait_ns = h->wait_ns;
+  return launch_k(h, gemm8_kernel<BN>, dim3(gemm8_grid(h, A.M, A.N, A.K, BN)), dim3(kThreads), (size_t)L::kBytes, s, tx, tw,
+                  P);
+}
+
+cudaError_t launch_gemm8(dec_handle* h, const Linear8& A, void* ws, cudaStream_t s) {
+  return tile_weights(A.M) == 256 ? launch_bn<256>(h, A, ws, s) : launch_bn<128>(h, A, ws, s);
+}
+
+}  // namespace dec

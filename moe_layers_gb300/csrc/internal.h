@@ -253,6 +253,9 @@ struct Linear8 {
 };
 // Most rows that the streaming kernel takes at this reduction length, up to 16.
 int stream8_rows(int K, bool pair);
+// Any sizes, on tcgen05; the workspace's counters are zero between calls.
+size_t gemm8_ws_bytes(const dec_handle* h, int M, int N, int K);
+cudaError_t launch_gemm8(dec_handle* h, const Linear8& L, void* ws, cudaStream_t s);
 cudaError_t launch_stream8_linear(dec_handle* h, const Linear8& L, cudaStream_t s);
 
 // Weights of a SwiGLU pair (gate, up), or of one matrix (the first).
