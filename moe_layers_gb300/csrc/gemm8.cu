@@ -5,20 +5,22 @@
 //
 // A tile is 128 rows x BN weights. Its k-blocks of 128 values have scales of their own,
 // so the tensor cores' sum of a block is not kept: each block goes to a tensor-memory
-// buffer of its own, is fetched by eight warps, scaled and added to totals in registers,
+// buffer of its own, is fetched by sixteen warps, scaled and added to totals in registers,
 // while the next blocks are multiplied. Rows are the product's M side, so a thread owns
-// one row and BN / 2 columns of one block of weights: its scale is one number a k-block,
+// one row and BN / 4 columns of one block of weights: its scale is one number a k-block,
 // and a fetched value costs half a packed fused multiply-add.
 //
-// One CTA per SM. The sequence of all (tile, k-block) pairs is cut into one equal range
-// per CTA, so no wave is left half full and short sequences use every SM. A tile that
-// several CTAs share is finished by the one that publishes its piece last: it adds all
-// pieces in k order (no atomics on values; the results follow from the inputs and the
-// shape alone).
+// One CTA per SM. Whole tiles go round the CTAs as long as there is one for each, in panels
+// of 16 tiles of rows, so that the tiles in work at a time share rows and weights in L2. The
+// (tile, k-block) pairs of the tiles that are left (all, for a decode batch) form a sequence
+// that is cut into one equal range per CTA, so no round is left half full and few tiles
+// use every SM. A tile that several CTAs share is finished by the one that publishes its
+// piece last: it adds all pieces in k order (no atomics on values; the results follow from
+// the inputs and the shape alone).
 //
 // Per CTA: warp 0 issues the TMA loads of a k-block's rows and weights (128-byte
 // swizzle) into a ring in shared memory, warp 1 the tcgen05.mma (128 x BN x 32, kind
-// f8f6f4), warps 2-9 fetch, scale and add.
+// f8f6f4), warps 2-17 fetch, scale and add.
 #include <algorithm>
 
 #include "common.cuh"
@@ -31,8 +33,8 @@ namespace {
 
 constexpr int kRows = 128;
 constexpr int kBlock = 128;  // k values of a block, one row of the swizzle
-constexpr int kThreads = 320;
-constexpr int kAdders = 256;
+constexpr int kAdders = 512;
+constexpr int kThreads = 64 + kAdders;
 constexpr int kTmem = 512;
 
 template <int BN>
@@ -41,13 +43,13 @@ struct Plan {
   static constexpr int kStageBytes = kABytes + BN * kBlock;
   static constexpr int kStages = 196608 / kStageBytes;  // 6 or 4
   static constexpr int kBuffers = kTmem / BN;           // 4 or 2
-  static constexpr int kCols = BN / 2;                  // a thread's
+  static constexpr int kCols = BN / 4;                  // a thread's
   static constexpr int kBarOff = kStages * kStageBytes;
   static constexpr int kBytes = kBarOff + 8 * (2 * kStages + 2 * kBuffers + 1) + 64 + 1024;
 };
 
 struct Gemm8Params {
-  int M, N, K, KB, mtiles;
+  int M, N, K, KB, mtiles, ntiles;
   const float* xs;
   long long ldxs;
   const float* ws;
@@ -61,6 +63,8 @@ struct Gemm8Params {
   int* err;
   unsigned long long wait_ns;
 };
+
+constexpr int kPanel = 16;  // tiles of rows
 
 __device__ __forceinline__ long long range_start(long long c, long long W, long long G) { return c * W / G; }
 __device__ __forceinline__ int cta_of(long long j, long long W, long long G) { return (int)(((j + 1) * G - 1) / W); }
@@ -77,16 +81,13 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, ui
       : "memory");
 }
 
-// 32 consecutive fp32 columns of this thread's tensor-memory lane, complete on return.
-__device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32]) {
+// 16 consecutive fp32 columns of this thread's tensor-memory lane, complete on return.
+__device__ __forceinline__ void tmem_get16(uint32_t at, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(at)
       : "memory");
 }
@@ -111,6 +112,44 @@ __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
 
 }  // namespace
 
+// The work of a CTA: `rounds` whole tiles, then its range of what is left.
+struct Work {
+  int KB, mtiles, ntiles;
+  long long tiles, G, c, rounds, W, base;  // W: k-blocks left, from tile `base` on
+  long long r, j, j1;                      // the next round; the range
+  int tile, kb0, kb1;                      // the current part: k-blocks [kb0, kb1) of a tile
+  __device__ Work(const Gemm8Params& P)
+      : KB(P.KB), mtiles(P.mtiles), ntiles(P.ntiles), tiles((long long)P.mtiles * P.ntiles), G(gridDim.x), c(blockIdx.x) {
+    rounds = tiles / G;
+    base = rounds * G;
+    W = (tiles - base) * KB;
+    r = 0;
+    j = range_start(c, W, G);
+    j1 = range_start(c + 1, W, G);
+  }
+  __device__ bool next() {
+    if (r < rounds) {
+      tile = (int)(r++ * G + c);
+      kb0 = 0;
+      kb1 = KB;
+      return true;
+    }
+    if (j >= j1) return false;
+    const int t = (int)(j / KB);
+    tile = (int)(base + t);
+    kb0 = (int)(j - (long long)t * KB);
+    kb1 = (int)min((long long)KB, kb0 + (j1 - j));
+    j += kb1 - kb0;
+    return true;
+  }
+  __device__ void place(int& mt, int& nt) const {
+    const int whole = kPanel * ntiles, panel = tile / whole, in = tile - panel * whole;
+    const int height = min(kPanel, mtiles - panel * kPanel);
+    nt = in / height;
+    mt = panel * kPanel + in - nt * height;
+  }
+};
+
 template <int BN>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm8_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const Gemm8Params P) {
@@ -126,11 +165,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* s_last = abort_flag + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int KB = P.KB, mtiles = P.mtiles;
-  const long long W = (long long)mtiles * ((P.N + BN - 1) / BN) * KB;
-  const long long G = gridDim.x, c = blockIdx.x;
-  const long long j0 = range_start(c, W, G), j1 = range_start(c + 1, W, G);
-
   pdl_trigger();
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
@@ -162,41 +196,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ copies
     if (lane == 0) {
-      const uint64_t pol_w = mtiles == 1 ? policy_evict_first() : policy_evict_last();  // read once, or by every tile of rows
+      const uint64_t pol_w = P.mtiles == 1 ? policy_evict_first() : policy_evict_last();  // read once, or again
       const uint64_t pol_x = policy_evict_last();
-      auto load_w = [&](int s, int kb, int nt) {
-        tma_load_2d(smem + s * L::kStageBytes + L::kABytes, &tw, &full[s], kb * kBlock, nt * BN, pol_w);
-      };
-      auto load_x = [&](int s, int kb, int mt) {
-        tma_load_2d(smem + s * L::kStageBytes, &tx, &full[s], kb * kBlock, mt * kRows, pol_x);
-      };
       // Static weights of the first ring's worth before the dependency wait.
-      const int pre = (int)min(j1 - j0, (long long)L::kStages);
-      const int tile0 = (int)(j0 / KB), k0 = (int)(j0 - (long long)tile0 * KB);
-      int tile = tile0, kb = k0;
-      for (int s = 0; s < pre; ++s) {
-        mbar_arrive_expect_tx(&full[s], L::kStageBytes);
-        load_w(s, kb, tile / mtiles);
-        if (++kb == KB) kb = 0, ++tile;
+      int pre = 0, mt, nt;
+      for (Work work(P); pre < L::kStages && work.next();) {
+        work.place(mt, nt);
+        for (int kb = work.kb0; kb < work.kb1 && pre < L::kStages; ++kb, ++pre) {
+          mbar_arrive_expect_tx(&full[pre], L::kStageBytes);
+          tma_load_2d(smem + pre * L::kStageBytes + L::kABytes, &tw, &full[pre], kb * kBlock, nt * BN, pol_w);
+        }
       }
       pdl_wait();
-      tile = tile0, kb = k0;
-      int s = 0;
+      int s = 0, issued = 0;
       uint32_t ph = 0;
-      long long issued = 0;
-      for (long long i = 0; i < j1 - j0; ++i) {
-        if (i >= pre) {
-          if (!mbar_wait(&empty[s], ph ^ 1u, wc)) break;
-          mbar_arrive_expect_tx(&full[s], L::kStageBytes);
-          load_w(s, kb, tile / mtiles);
+      bool ok = true;
+      for (Work work(P); ok && work.next();) {
+        work.place(mt, nt);
+        for (int kb = work.kb0; kb < work.kb1; ++kb) {
+          uint8_t* st = smem + s * L::kStageBytes;
+          if (pre > 0) {
+            --pre;
+          } else {
+            if (!mbar_wait(&empty[s], ph ^ 1u, wc)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&full[s], L::kStageBytes);
+            tma_load_2d(st + L::kABytes, &tw, &full[s], kb * kBlock, nt * BN, pol_w);
+          }
+          tma_load_2d(st, &tx, &full[s], kb * kBlock, mt * kRows, pol_x);
+          if (++s == L::kStages) s = 0, ph ^= 1u;
+          issued = min(issued + 1, L::kStages);
         }
-        load_x(s, kb, tile % mtiles);
-        if (++kb == KB) kb = 0, ++tile;
-        if (++s == L::kStages) s = 0, ph ^= 1u;
-        ++issued;
       }
       // No copy may still be in flight when the CTA exits.
-      for (long long n = min(issued, (long long)L::kStages); n > 0; --n) {
+      for (; issued > 0; --issued) {
         if (--s < 0) s = L::kStages - 1, ph ^= 1u;
         mbar_wait_drain(&full[s], ph, P.err, P.wait_ns);
       }
@@ -206,9 +241,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       int s = 0, b = 0;
       uint32_t ph = 0, tph = 0;
-      for (long long j = j0; j < j1; ++j) {
-        if (!mbar_wait(&tempty[b], tph ^ 1u, wc)) break;
-        if (!mbar_wait(&full[s], ph, wc)) break;
+      bool ok = true;
+      for (Work work(P); ok && work.next();)
+      for (int kb = work.kb0; kb < work.kb1; ++kb) {
+        if (!mbar_wait(&tempty[b], tph ^ 1u, wc) || !mbar_wait(&full[s], ph, wc)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
         const uint32_t a = smem_u32(smem + s * L::kStageBytes), w = a + L::kABytes, d = tmem + (uint32_t)(b * BN);
 #pragma unroll
@@ -225,8 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ sums
-    const int q = warp & 3, half = (warp - 2) >> 2;  // tensor-memory lanes 32 q .., columns of this half
-    const int row = q * 32 + lane, col0 = half * L::kCols;
+    const int q = warp & 3, row = q * 32 + lane;  // tensor-memory lanes 32 q ..
+    const int col0 = ((warp - 2) >> 2) * L::kCols;
     const int et = threadIdx.x - 64;
     const bool out_vec = (reinterpret_cast<uintptr_t>(P.y) & 15) == 0 && (P.ldy & 7) == 0;
     const bool res_vec = (reinterpret_cast<uintptr_t>(P.res) & 15) == 0 && (P.ldr & 7) == 0;
@@ -234,33 +273,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     int b = 0;
     uint32_t tph = 0;
     bool ok = true;
-    int seg = 0;
-    for (long long j = j0; j < j1; ++seg) {
-      const int tile = (int)(j / KB), kb0 = (int)(j - (long long)tile * KB);
-      const int kb1 = (int)min((long long)KB, kb0 + (j1 - j));
-      j += kb1 - kb0;
-      const int m0 = (tile % mtiles) * kRows, n0 = (tile / mtiles) * BN;
+    const int KB = P.KB;
+    for (Work work(P); work.next();) {
+      const int kb0 = work.kb0, kb1 = work.kb1;
+      int mt, nt;
+      work.place(mt, nt);
+      const int m0 = mt * kRows, n0 = nt * BN;
       const bool rows_here = m0 + q * 32 < P.M;  // this warp's rows hold some of the batch's
       const float* xs = P.xs + (long long)min(m0 + row, P.M - 1) * P.ldxs;
       const float* ws = P.ws + (long long)min((n0 + col0) >> 7, (P.N - 1) >> 7) * KB;
       uint64_t acc[L::kCols / 2];
 #pragma unroll
       for (int i = 0; i < L::kCols / 2; ++i) acc[i] = 0;
-      // Scales of eight blocks at a time, the next eight's loads in flight: the row's, and
-      // the weights' spread over lanes 0-7.
-      float sx[8], nx[8], sw, nw;
-      auto load_scales = [&](int kb, float (&x)[8], float& w) {
+      // Scales of four blocks at a time, the next four's loads in flight: the row's, and
+      // the weights' spread over lanes 0-3.
+      float sx[4], nx[4], sw, nw;
+      auto load_scales = [&](int kb, float (&x)[4], float& w) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = kb + i < kb1 ? ld_act_f32(xs + kb + i) : 0.f;
-        w = kb + (lane & 7) < kb1 ? __ldg(ws + kb + (lane & 7)) : 0.f;
+        for (int i = 0; i < 4; ++i) x[i] = kb + i < kb1 ? ld_act_f32(xs + kb + i) : 0.f;
+        w = kb + (lane & 3) < kb1 ? __ldg(ws + kb + (lane & 3)) : 0.f;
       };
       if (rows_here) load_scales(kb0, sx, sw);
-      for (int kb = kb0; kb < kb1 && ok; kb += 8) {
-        if (rows_here) load_scales(kb + 8, nx, nw);
+      for (int kb = kb0; kb < kb1 && ok; kb += 4) {
+        if (rows_here) load_scales(kb + 4, nx, nw);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
           if (kb + i >= kb1) break;
-          if (!__all_sync(0xffffffffu, mbar_wait(&tfull[b], tph, wc))) {
+          if (!__all_sync(0xffffffffu, mbar_try_wait(&tfull[b], tph)) &&
+              !__all_sync(0xffffffffu, mbar_wait(&tfull[b], tph, wc))) {
             ok = false;
             break;
           }
@@ -270,35 +310,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t ff = pack2(f, f);
             const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BN + col0);
 #pragma unroll
-            for (int ch = 0; ch < L::kCols / 32; ++ch) {
-              uint32_t v[32];
-              tmem_ld32(at + ch * 32, v);
+            for (int ch = 0; ch < L::kCols / 16; ++ch) {
+              uint32_t v[16];
+              tmem_get16(at + ch * 16, v);
+              if (ch == L::kCols / 16 - 1) {
+                // all fetched: the buffer is free
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tempty[b]);
+              }
 #pragma unroll
-              for (int e = 0; e < 16; ++e) acc[ch * 16 + e] = fma2(v[2 * e], v[2 * e + 1], ff, acc[ch * 16 + e]);
+              for (int e = 0; e < 8; ++e) acc[ch * 8 + e] = fma2(v[2 * e], v[2 * e + 1], ff, acc[ch * 8 + e]);
             }
-            tc_fence_before();
+          } else if (lane == 0) {
+            mbar_arrive(&tempty[b]);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&tempty[b]);
           if (++b == L::kBuffers) b = 0, tph ^= 1u;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sx[i] = nx[i];
+        for (int i = 0; i < 4; ++i) sx[i] = nx[i];
         sw = nw;
       }
       if (!named_bar_and(1, kAdders, ok)) break;  // leave together if a warp gave up
 
       if (kb1 - kb0 < KB) {
         // A piece: published, four columns of a row at a time; whoever publishes the last adds them all in k order.
-        const int p_rows = P.piece_rows, c0 = cta_of((long long)tile * KB, W, G);
-        const int c1 = cta_of((long long)tile * KB + KB - 1, W, G);
+        const long long first = (work.tile - work.base) * KB;
+        const int p_rows = P.piece_rows, c0 = cta_of(first, work.W, work.G), c1 = cta_of(first + KB - 1, work.W, work.G);
         auto piece = [&](int cc) {
-          const bool inside = range_start(cc, W, G) >= (long long)tile * KB;
+          const bool inside = range_start(cc, work.W, work.G) >= first;
           return reinterpret_cast<float4*>(P.pieces) + (size_t)(cc * 2 + (inside ? 0 : 1)) * (BN / 4) * p_rows +
                  (size_t)(col0 / 4) * p_rows + row;
         };
         if (rows_here) {
-          float4* dst = piece((int)c);
+          float4* dst = piece((int)work.c);
 #pragma unroll
           for (int i = 0; i < L::kCols / 4; ++i) {
             const float2 lo = unpack2(acc[2 * i]), hi = unpack2(acc[2 * i + 1]);
@@ -425,6 +470,7 @@ static cudaError_t launch_bn(dec_handle* h, const Linear8& A, void* ws, cudaStre
   P.K = A.K;
   P.KB = (A.K + kBlock - 1) / kBlock;
   P.mtiles = (A.M + kRows - 1) / kRows;
+  P.ntiles = (A.N + BN - 1) / BN;
   P.xs = A.xs;
   P.ldxs = A.ldxs;
   P.ws = A.ws;
