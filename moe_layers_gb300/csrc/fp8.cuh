@@ -46,4 +46,12 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Bounded wait of a pipeline whose next step is near: mbar_wait reads the global timer
+// as soon as its first try fails, which costs more than the wait that is left.
+__device__ __forceinline__ bool mbar_wait_soon(uint64_t* bar, uint32_t parity, const WaitCtl& wc) {
+  for (int n = 0; n < 32; ++n)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, wc);
+}
+
 }  // namespace dec

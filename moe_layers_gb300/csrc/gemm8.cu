@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (pre > 0) {
             --pre;
           } else {
-            if (!mbar_wait(&empty[s], ph ^ 1u, wc)) {
+            if (!mbar_wait_soon(&empty[s], ph ^ 1u, wc)) {
               ok = false;
               break;
             }
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (Work work(P); ok && work.next();)
       for (int kb = work.kb0; kb < work.kb1; ++kb) {
-        if (!mbar_wait(&tempty[b], tph ^ 1u, wc) || !mbar_wait(&full[s], ph, wc)) {
+        if (!mbar_wait_soon(&tempty[b], tph ^ 1u, wc) || !mbar_wait_soon(&full[s], ph, wc)) {
           ok = false;
           break;
         }
@@ -299,8 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (kb + i >= kb1) break;
-          if (!__all_sync(0xffffffffu, mbar_try_wait(&tfull[b], tph)) &&
-              !__all_sync(0xffffffffu, mbar_wait(&tfull[b], tph, wc))) {
+          if (!__all_sync(0xffffffffu, mbar_wait_soon(&tfull[b], tph, wc))) {
             ok = false;
             break;
           }

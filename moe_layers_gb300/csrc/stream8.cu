@@ -63,7 +63,7 @@ __device__ __forceinline__ float2 lds8(uint32_t p) {
   return v;
 }
 
-// The fast way through a wait that is over already; the whole warp leaves together.
+// The whole warp leaves a wait together.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& wc) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc));
