@@ -45,7 +45,8 @@ struct Plan {
   static constexpr int kBuffers = kTmem / BN;           // 4 or 2
   static constexpr int kCols = BN / 4;                  // a thread's
   static constexpr int kBarOff = kStages * kStageBytes;
-  static constexpr int kBytes = kBarOff + 8 * (2 * kStages + 2 * kBuffers + 1) + 64 + 1024;
+  static constexpr int kScaleOff = kBarOff + 8 * (2 * kStages + 2 * kBuffers + 1) + 56;
+  static constexpr int kBytes = kScaleOff + 2 * 8 * kRows * 4 + 1024;
 };
 
 struct Gemm8Params {
@@ -164,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* s_last = abort_flag + 1;
+  float* s_scales = reinterpret_cast<float*>(smem + L::kScaleOff);  // [2][8][kRows]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
   if (threadIdx.x == 0) {
@@ -265,12 +267,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------------------ sums
     const int q = warp & 3, row = q * 32 + lane;  // tensor-memory lanes 32 q ..
-    const int col0 = ((warp - 2) >> 2) * L::kCols;
+    const int quarter = (warp - 2) >> 2, col0 = quarter * L::kCols;
     const int et = threadIdx.x - 64;
     const bool out_vec = (reinterpret_cast<uintptr_t>(P.y) & 15) == 0 && (P.ldy & 7) == 0;
     const bool res_vec = (reinterpret_cast<uintptr_t>(P.res) & 15) == 0 && (P.ldr & 7) == 0;
     pdl_wait();
-    int b = 0;
+    int b = 0, turn = 0;
     uint32_t tph = 0;
     bool ok = true;
     const int KB = P.KB;
@@ -285,27 +287,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t acc[L::kCols / 2];
 #pragma unroll
       for (int i = 0; i < L::kCols / 2; ++i) acc[i] = 0;
-      // Scales of four blocks at a time, the next four's loads in flight: the row's, and
-      // the weights' spread over lanes 0-3.
-      float sx[4], nx[4], sw, nw;
-      auto load_scales = [&](int kb, float (&x)[4], float& w) {
+      // Scales of eight blocks at a time, the next eight's loads in flight. The rows' lie far
+      // apart, so each of the four warps that share rows loads two blocks' and leaves them
+      // for the others; the weights' (of the warp's columns) are spread over lanes 0-7.
+      float nx[2], sw, nw;
+      auto load_scales = [&](int kb) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = kb + i < kb1 ? ld_act_f32(xs + kb + i) : 0.f;
-        w = kb + (lane & 3) < kb1 ? __ldg(ws + kb + (lane & 3)) : 0.f;
+        for (int i = 0; i < 2; ++i) nx[i] = kb + 2 * quarter + i < kb1 ? ld_act_f32(xs + kb + 2 * quarter + i) : 0.f;
+        nw = kb + (lane & 7) < kb1 ? __ldg(ws + kb + (lane & 7)) : 0.f;
       };
-      if (rows_here) load_scales(kb0, sx, sw);
-      for (int kb = kb0; kb < kb1 && ok; kb += 4) {
-        if (rows_here) load_scales(kb + 4, nx, nw);
+      if (rows_here) load_scales(kb0);
+      // a warp that gave up a wait goes on without waiting, through the same barriers as the others
+      for (int kb = kb0; kb < kb1; kb += 8) {
+        float* sx = s_scales + ((turn++ & 1) * 8) * kRows + row;
+        if (rows_here) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 2; ++i) sx[(2 * quarter + i) * kRows] = nx[i];
+          sw = nw;
+          load_scales(kb + 8);
+          named_bar_sync(2 + q, 128);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
           if (kb + i >= kb1) break;
-          if (!__all_sync(0xffffffffu, mbar_wait_soon(&tfull[b], tph, wc))) {
-            ok = false;
-            break;
-          }
+          ok = ok && __all_sync(0xffffffffu, mbar_wait_soon(&tfull[b], tph, wc));
+          if (!ok) break;
           if (rows_here) {
             tc_fence_after();
-            const float f = sx[i] * __shfl_sync(0xffffffffu, sw, i);
+            const float f = sx[i * kRows] * __shfl_sync(0xffffffffu, sw, i);
             const uint64_t ff = pack2(f, f);
             const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BN + col0);
 #pragma unroll
@@ -326,9 +335,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (++b == L::kBuffers) b = 0, tph ^= 1u;
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sx[i] = nx[i];
-        sw = nw;
       }
       if (!named_bar_and(1, kAdders, ok)) break;  // leave together if a warp gave up
 
