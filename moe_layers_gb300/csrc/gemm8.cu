@@ -41,16 +41,20 @@ template <int BN>
 struct Plan {
   static constexpr int kABytes = kRows * kBlock;
   static constexpr int kStageBytes = kABytes + BN * kBlock;
-  static constexpr int kStages = 196608 / kStageBytes;  // 6 or 4
-  static constexpr int kBuffers = kTmem / BN;           // 4 or 2
-  static constexpr int kCols = BN / 4;                  // a thread's
+  static constexpr int kStages = 221184 / kStageBytes;
+  static constexpr int kBuffers = kTmem / BN < 8 ? kTmem / BN : 8;
+  static constexpr int kCols = BN / 4;                            // a thread's
+  static constexpr int kFetch = kCols % 16 == 0 ? 16 : 8;         // columns fetched at once
+  static constexpr bool kStraddle = 128 % kCols != 0;             // they may lie in two blocks of weights
   static constexpr int kBarOff = kStages * kStageBytes;
-  static constexpr int kScaleOff = kBarOff + 8 * (2 * kStages + 2 * kBuffers + 1) + 56;
+  static constexpr int kScaleOff = kBarOff + (8 * (2 * kStages + 2 * kBuffers + 1) + 16 + 63) / 64 * 64;
   static constexpr int kBytes = kScaleOff + 2 * 8 * kRows * 4 + 1024;
+  static_assert(kBytes <= 232448, "shared memory above the opt-in maximum");
 };
 
 struct Gemm8Params {
   int M, N, K, KB, mtiles, ntiles;
+  int box_rows;  // rows of a copy: a tile's, or the whole batch's up to eight
   const float* xs;
   long long ldxs;
   const float* ws;
@@ -82,13 +86,21 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, ui
       : "memory");
 }
 
-// 16 consecutive fp32 columns of this thread's tensor-memory lane, complete on return.
-__device__ __forceinline__ void tmem_get16(uint32_t at, uint32_t (&r)[16]) {
+// Consecutive fp32 columns of this thread's tensor-memory lane, complete on return.
+__device__ __forceinline__ void tmem_get(uint32_t at, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_get(uint32_t at, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
       : "r"(at)
       : "memory");
 }
@@ -200,12 +212,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       const uint64_t pol_w = P.mtiles == 1 ? policy_evict_first() : policy_evict_last();  // read once, or again
       const uint64_t pol_x = policy_evict_last();
+      const uint32_t tx_bytes = (uint32_t)((P.box_rows + BN) * kBlock);
       // Static weights of the first ring's worth before the dependency wait.
       int pre = 0, mt, nt;
       for (Work work(P); pre < L::kStages && work.next();) {
         work.place(mt, nt);
         for (int kb = work.kb0; kb < work.kb1 && pre < L::kStages; ++kb, ++pre) {
-          mbar_arrive_expect_tx(&full[pre], L::kStageBytes);
+          mbar_arrive_expect_tx(&full[pre], tx_bytes);
           tma_load_2d(smem + pre * L::kStageBytes + L::kABytes, &tw, &full[pre], kb * kBlock, nt * BN, pol_w);
         }
       }
@@ -224,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ok = false;
               break;
             }
-            mbar_arrive_expect_tx(&full[s], L::kStageBytes);
+            mbar_arrive_expect_tx(&full[s], tx_bytes);
             tma_load_2d(st + L::kABytes, &tw, &full[s], kb * kBlock, nt * BN, pol_w);
           }
           tma_load_2d(st, &tx, &full[s], kb * kBlock, mt * kRows, pol_x);
@@ -283,13 +296,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int m0 = mt * kRows, n0 = nt * BN;
       const bool rows_here = m0 + q * 32 < P.M;  // this warp's rows hold some of the batch's
       const float* xs = P.xs + (long long)min(m0 + row, P.M - 1) * P.ldxs;
-      const float* ws = P.ws + (long long)min((n0 + col0) >> 7, (P.N - 1) >> 7) * KB;
+      const int block0 = (n0 + col0) >> 7;                      // the columns' first block of weights
+      const int edge = ((block0 + 1) << 7) - (n0 + col0);       // columns in it
+      const float* ws = P.ws + (long long)min(block0 + (L::kStraddle ? (lane >> 3) & 1 : 0), (P.N - 1) >> 7) * KB;
       uint64_t acc[L::kCols / 2];
 #pragma unroll
       for (int i = 0; i < L::kCols / 2; ++i) acc[i] = 0;
       // Scales of eight blocks at a time, the next eight's loads in flight. The rows' lie far
       // apart, so each of the four warps that share rows loads two blocks' and leaves them
-      // for the others; the weights' (of the warp's columns) are spread over lanes 0-7.
+      // for the others; the weights' (of the warp's columns) are spread over lanes 0-7, those of
+      // a second block over 8-15.
       float nx[2], sw, nw;
       auto load_scales = [&](int kb) {
 #pragma unroll
@@ -314,21 +330,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           if (rows_here) {
             tc_fence_after();
-            const float f = sx[i * kRows] * __shfl_sync(0xffffffffu, sw, i);
-            const uint64_t ff = pack2(f, f);
+            const float f0 = sx[i * kRows] * __shfl_sync(0xffffffffu, sw, i);
+            const float f1 = L::kStraddle ? sx[i * kRows] * __shfl_sync(0xffffffffu, sw, 8 + i) : f0;
+            const uint64_t ff0 = pack2(f0, f0), ff1 = pack2(f1, f1);
             const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BN + col0);
 #pragma unroll
-            for (int ch = 0; ch < L::kCols / 16; ++ch) {
-              uint32_t v[16];
-              tmem_get16(at + ch * 16, v);
-              if (ch == L::kCols / 16 - 1) {
+            for (int ch = 0; ch < L::kCols / L::kFetch; ++ch) {
+              uint32_t v[L::kFetch];
+              tmem_get(at + ch * L::kFetch, v);
+              if (ch == L::kCols / L::kFetch - 1) {
                 // all fetched: the buffer is free
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&tempty[b]);
               }
 #pragma unroll
-              for (int e = 0; e < 8; ++e) acc[ch * 8 + e] = fma2(v[2 * e], v[2 * e + 1], ff, acc[ch * 8 + e]);
+              for (int e = 0; e < L::kFetch / 2; ++e) {
+                const int i2 = ch * (L::kFetch / 2) + e;
+                acc[i2] = fma2(v[2 * e], v[2 * e + 1], L::kStraddle && i2 / 4 * 8 >= edge ? ff1 : ff0, acc[i2]);
+              }
             }
           } else if (lane == 0) {
             mbar_arrive(&tempty[b]);
@@ -428,22 +448,51 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- host side
-// 256 weights a tile where the products bound the time (their rows then serve twice as
-// many weights from shared memory), 128 where the weights' bytes do, and short pieces count.
-static int tile_weights(int M) { return M > kRows ? 256 : 128; }
-
-static int gemm8_grid(const dec_handle* h, int M, int N, int K, int bn) {
-  const long long tiles = (long long)((M + kRows - 1) / kRows) * ((N + bn - 1) / bn), KB = (K + kBlock - 1) / kBlock;
-  // a range of at least four blocks, or a tile
-  return (int)std::min<long long>(h->sms, std::max(tiles, (tiles * KB + 3) / 4));
+// Weights a tile and CTAs: by the time of the longest CTA, in clocks. A k-block of a tile
+// costs its rows and weights at the rate of copies (64 bytes a clock and SM; together at the
+// memory's for the weights, about 23), its products, and some 350 clocks of waits; a tile that
+// CTAs share costs an exchange of pieces.
+struct Choice {
+  int bn, grid;
+};
+static Choice choose(const dec_handle* h, int M, int N, int K) {
+  const long long mt = (M + kRows - 1) / kRows, KB = (K + kBlock - 1) / kBlock;
+  const double rows = std::min(M, kRows);
+  Choice best = {256, 1};
+  double least = 1e300;
+  for (int bn : {32, 64, 96, 128, 192, 256}) {
+    const long long tiles = mt * ((N + bn - 1) / bn);
+    const double block = std::max(350.0, std::max((rows + bn) * 128 / 40, bn * 4.0));
+    const double memory = (double)N * K / (h->sms * 23.0);
+    for (int split = 1; split <= 8; split *= 2) {
+      long long grid;
+      double blocks, exchange = 0;
+      if (tiles <= h->sms) {
+        grid = tiles * split;
+        if (grid > h->sms || KB / split < 4) continue;
+        blocks = (double)((KB + split - 1) / split);
+        if (split > 1) exchange = 4000 + 1500.0 * split;
+      } else {
+        if (split > 1) continue;
+        grid = h->sms;
+        const long long left = tiles % grid;
+        blocks = (double)(tiles / grid * KB) + (double)left * KB / grid;
+        if (left) exchange = 4000 + 1500.0 * std::min(8.0, (double)grid / left);
+        blocks += (double)(tiles / grid) * 2;
+      }
+      const double t = std::max(blocks * block, memory) + exchange;
+      if (t < least) least = t, best = {bn, (int)grid};
+    }
+  }
+  return best;
 }
 
 static int piece_rows(int M) { return std::min(kRows, (M + 31) / 32 * 32); }
 static size_t counter_bytes(const dec_handle* h) { return ((size_t)h->sms * 4 + 255) & ~size_t(255); }
 
 size_t gemm8_ws_bytes(const dec_handle* h, int M, int N, int K) {
-  const int bn = tile_weights(M);
-  return counter_bytes(h) + (size_t)2 * gemm8_grid(h, M, N, K, bn) * bn * piece_rows(M) * 4;
+  const Choice c = choose(h, M, N, K);
+  return counter_bytes(h) + (size_t)2 * c.grid * c.bn * piece_rows(M) * 4;
 }
 
 static bool encode_tile(const dec_handle* h, CUtensorMap* m, const uint8_t* p, int K, int rows, long long ld, int box_rows) {
@@ -457,11 +506,11 @@ static bool encode_tile(const dec_handle* h, CUtensorMap* m, const uint8_t* p, i
 }
 
 template <int BN>
-static cudaError_t launch_bn(dec_handle* h, const Linear8& A, void* ws, cudaStream_t s) {
+static cudaError_t launch_bn(dec_handle* h, const Linear8& A, int grid, void* ws, cudaStream_t s) {
   using L = Plan<BN>;
-  static_assert(L::kBytes <= 232448, "shared memory above the opt-in maximum");
+  const int box_rows = std::min(kRows, (A.M + 7) / 8 * 8);
   CUtensorMap tx, tw;
-  if (!encode_tile(h, &tx, A.x, A.K, A.M, A.ldx, kRows) || !encode_tile(h, &tw, A.W, A.K, A.N, A.K, BN))
+  if (!encode_tile(h, &tx, A.x, A.K, A.M, A.ldx, box_rows) || !encode_tile(h, &tw, A.W, A.K, A.N, A.K, BN))
     return cudaErrorInvalidValue;
   static bool attr_set = false;  // per process; every device gets the same attribute
   if (!attr_set) {
@@ -476,6 +525,7 @@ static cudaError_t launch_bn(dec_handle* h, const Linear8& A, void* ws, cudaStre
   P.KB = (A.K + kBlock - 1) / kBlock;
   P.mtiles = (A.M + kRows - 1) / kRows;
   P.ntiles = (A.N + BN - 1) / BN;
+  P.box_rows = box_rows;
   P.xs = A.xs;
   P.ldxs = A.ldxs;
   P.ws = A.ws;
@@ -488,12 +538,20 @@ static cudaError_t launch_bn(dec_handle* h, const Linear8& A, void* ws, cudaStre
   P.piece_rows = piece_rows(A.M);
   P.err = h->d_err;
   P.wait_ns = h->wait_ns;
-  return launch_k(h, gemm8_kernel<BN>, dim3(gemm8_grid(h, A.M, A.N, A.K, BN)), dim3(kThreads), (size_t)L::kBytes, s, tx, tw,
+  return launch_k(h, gemm8_kernel<BN>, dim3(grid), dim3(kThreads), (size_t)L::kBytes, s, tx, tw,
                   P);
 }
 
 cudaError_t launch_gemm8(dec_handle* h, const Linear8& A, void* ws, cudaStream_t s) {
-  return tile_weights(A.M) == 256 ? launch_bn<256>(h, A, ws, s) : launch_bn<128>(h, A, ws, s);
+  const Choice c = choose(h, A.M, A.N, A.K);
+  switch (c.bn) {
+    case 32: return launch_bn<32>(h, A, c.grid, ws, s);
+    case 64: return launch_bn<64>(h, A, c.grid, ws, s);
+    case 96: return launch_bn<96>(h, A, c.grid, ws, s);
+    case 128: return launch_bn<128>(h, A, c.grid, ws, s);
+    case 192: return launch_bn<192>(h, A, c.grid, ws, s);
+    default: return launch_bn<256>(h, A, c.grid, ws, s);
+  }
 }
 
 }  // namespace dec
