@@ -234,21 +234,6 @@ __device__ __forceinline__ void warm_l2(const AttentionParams& a) {
   for (int k = i; k * 32 < blocks; k += n) want(a.prefix_table + k * 32);
 }
 
-// One lane of a converged warp. Copies and products are issued behind it from
-// values that are the same in every lane: the instructions take their operands
-// from uniform registers, and a lane that diverges to issue them moves each
-// operand there first (100 cycles a copy or product instead of about 25).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r));
-  return r != 0;
-}
-__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
-
 __device__ __forceinline__ void named_bar_arrive(int id, int count) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }

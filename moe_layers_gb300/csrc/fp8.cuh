@@ -46,12 +46,24 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Bounded wait of a pipeline whose next step is near: mbar_wait reads the global timer
-// as soon as its first try fails, which costs more than the wait that is left.
+// Bounded wait of a pipeline whose next step is near. The first tries do without the global
+// timer, whose reading costs more than the wait that is left then; no call, so that a kernel
+// that moves registers between its warps can use it. Ends early when another role of the
+// CTA has given up (wc.abort null: only by the limit).
 __device__ __forceinline__ bool mbar_wait_soon(uint64_t* bar, uint32_t parity, const WaitCtl& wc) {
-  for (int n = 0; n < 32; ++n)
+  uint64_t t0 = 0;
+  for (uint32_t n = 1;; ++n) {
     if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait(bar, parity, wc);
+    if ((n & 31u) != 0) continue;
+    if (wc.abort != nullptr && *wc.abort) return false;
+    const uint64_t now = globaltimer();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > wc.limit_ns) {
+      if (wc.abort != nullptr) *wc.abort = 1;
+      atomicOr(wc.err, DEV_ERR_TIMEOUT);
+      return false;
+    }
+  }
 }
 
 }  // namespace dec

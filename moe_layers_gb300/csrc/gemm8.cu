@@ -20,7 +20,7 @@
 //
 // Per CTA: warp 0 issues the TMA loads of a k-block's rows and weights (128-byte
 // swizzle) into a ring in shared memory, warp 1 the tcgen05.mma (128 x BN x 32, kind
-// f8f6f4), warps 2-17 fetch, scale and add.
+// f8f6f4), warps 4-19 fetch, scale and add.
 #include <algorithm>
 
 #include "common.cuh"
@@ -34,7 +34,7 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kBlock = 128;  // k values of a block, one row of the swizzle
 constexpr int kAdders = 512;
-constexpr int kThreads = 64 + kAdders;
+constexpr int kThreads = 128 + kAdders;
 constexpr int kTmem = 512;
 
 template <int BN>
@@ -44,7 +44,9 @@ struct Plan {
   static constexpr int kStages = 221184 / kStageBytes;
   static constexpr int kBuffers = kTmem / BN < 8 ? kTmem / BN : 8;
   static constexpr int kCols = BN / 4;                            // a thread's
-  static constexpr int kFetch = kCols % 16 == 0 ? 16 : 8;         // columns fetched at once
+  static constexpr int kFetch = kCols % 16 == 0 ? 16 : 8;  // columns of one instruction
+  static constexpr int kTogether = BN <= 32 ? 4 : 1;               // k-blocks fetched at once
+  static constexpr int kAtOnce = kCols * kTogether <= 48 && BN < 128 ? kCols : kFetch;  // columns a thread fetches before it adds
   static constexpr bool kStraddle = 128 % kCols != 0;             // they may lie in two blocks of weights
   static constexpr int kBarOff = kStages * kStageBytes;
   static constexpr int kScaleOff = kBarOff + (8 * (2 * kStages + 2 * kBuffers + 1) + 16 + 63) / 64 * 64;
@@ -86,24 +88,42 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, ui
       : "memory");
 }
 
-// Consecutive fp32 columns of this thread's tensor-memory lane, complete on return.
-__device__ __forceinline__ void tmem_get(uint32_t at, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(at)
-      : "memory");
+// Consecutive fp32 columns of this thread's tensor-memory lane, there after tmem_wait
+// and, so that no use of them is moved before it, tmem_here.
+__device__ __forceinline__ void tmem_fetch(uint32_t at, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(at)
+               : "memory");
 }
-__device__ __forceinline__ void tmem_get(uint32_t at, uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-      : "r"(at)
-      : "memory");
+__device__ __forceinline__ void tmem_fetch(uint32_t at, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(at)
+               : "memory");
 }
+__device__ __forceinline__ void tmem_fetch(uint32_t at, uint32_t (&r)[32]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_here(uint32_t (&r)[8]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]));
+}
+__device__ __forceinline__ void tmem_here(uint32_t (&r)[16]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+__device__ __forceinline__ void tmem_here(uint32_t (&r)[32]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+
+// Moves registers between the warps that copy and multiply, which need few, and those that add.
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // acc + v * f for two values, fp32.
 __device__ __forceinline__ uint64_t fma2(uint32_t lo, uint32_t hi, uint64_t f, uint64_t acc) {
@@ -204,84 +224,95 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const WaitCtl wc{abort_flag, P.err, P.wait_ns};
+  const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot), smem_at = smem_u32(smem);
+  const WaitCtl wc{abort_flag, P.err, P.wait_ns}, drain{nullptr, P.err, P.wait_ns};
 
+  // 640 threads start with 96 registers each; 512 x 104 + 128 x 40 are fewer.
+  if (warp < 4) regs_down<40>();
   if (warp == 0) {
     // ------------------------------------------------------------ copies
-    if (lane == 0) {
-      const uint64_t pol_w = P.mtiles == 1 ? policy_evict_first() : policy_evict_last();  // read once, or again
-      const uint64_t pol_x = policy_evict_last();
-      const uint32_t tx_bytes = (uint32_t)((P.box_rows + BN) * kBlock);
-      // Static weights of the first ring's worth before the dependency wait.
-      int pre = 0, mt, nt;
-      for (Work work(P); pre < L::kStages && work.next();) {
-        work.place(mt, nt);
-        for (int kb = work.kb0; kb < work.kb1 && pre < L::kStages; ++kb, ++pre) {
-          mbar_arrive_expect_tx(&full[pre], tx_bytes);
-          tma_load_2d(smem + pre * L::kStageBytes + L::kABytes, &tw, &full[pre], kb * kBlock, nt * BN, pol_w);
+    const uint64_t pol_w = P.mtiles == 1 ? policy_evict_first() : policy_evict_last();  // read once, or again
+    const uint64_t pol_x = policy_evict_last();
+    const uint32_t tx_bytes = (uint32_t)((P.box_rows + BN) * kBlock);
+    // Static weights of the first ring's worth before the dependency wait.
+    int pre = 0, mt, nt;
+    for (Work work(P); pre < L::kStages && work.next();) {
+      work.place(mt, nt);
+      for (int kb = work.kb0; kb < work.kb1 && pre < L::kStages; ++kb, ++pre) {
+        const int su = uniform(pre), k = uniform(kb * kBlock), row = uniform(nt * BN);
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&full[su], tx_bytes);
+          tma_load_2d(smem + su * L::kStageBytes + L::kABytes, &tw, &full[su], k, row, pol_w);
         }
       }
-      pdl_wait();
-      int s = 0, issued = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      for (Work work(P); ok && work.next();) {
-        work.place(mt, nt);
-        for (int kb = work.kb0; kb < work.kb1; ++kb) {
-          uint8_t* st = smem + s * L::kStageBytes;
-          if (pre > 0) {
-            --pre;
-          } else {
-            if (!mbar_wait_soon(&empty[s], ph ^ 1u, wc)) {
-              ok = false;
-              break;
-            }
-            mbar_arrive_expect_tx(&full[s], tx_bytes);
-            tma_load_2d(st + L::kABytes, &tw, &full[s], kb * kBlock, nt * BN, pol_w);
+    }
+    pdl_wait();
+    int s = 0, issued = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (Work work(P); ok && work.next();) {
+      work.place(mt, nt);
+      const int row_w = uniform(nt * BN), row_x = uniform(mt * kRows);
+      for (int kb = work.kb0; kb < work.kb1; ++kb) {
+        const int su = uniform(s), k = uniform(kb * kBlock);
+        if (pre > 0) {
+          --pre;
+        } else {
+          if (!__all_sync(0xffffffffu, mbar_wait_soon(&empty[su], ph ^ 1u, wc))) {
+            ok = false;
+            break;
           }
-          tma_load_2d(st, &tx, &full[s], kb * kBlock, mt * kRows, pol_x);
-          if (++s == L::kStages) s = 0, ph ^= 1u;
-          issued = min(issued + 1, L::kStages);
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&full[su], tx_bytes);
+            tma_load_2d(smem + su * L::kStageBytes + L::kABytes, &tw, &full[su], k, row_w, pol_w);
+          }
         }
+        if (elect_one()) tma_load_2d(smem + su * L::kStageBytes, &tx, &full[su], k, row_x, pol_x);
+        __syncwarp();
+        if (++s == L::kStages) s = 0, ph ^= 1u;
+        issued = min(issued + 1, L::kStages);
       }
-      // No copy may still be in flight when the CTA exits.
-      for (; issued > 0; --issued) {
-        if (--s < 0) s = L::kStages - 1, ph ^= 1u;
-        mbar_wait_drain(&full[s], ph, P.err, P.wait_ns);
-      }
+    }
+    // No copy may still be in flight when the CTA exits.
+    for (; issued > 0; --issued) {
+      if (--s < 0) s = L::kStages - 1, ph ^= 1u;
+      mbar_wait_soon(&full[s], ph, drain);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
-      int s = 0, b = 0;
-      uint32_t ph = 0, tph = 0;
-      bool ok = true;
-      for (Work work(P); ok && work.next();)
+    int s = 0, b = 0;
+    uint32_t ph = 0, tph = 0;
+    bool ok = true;
+    for (Work work(P); ok && work.next();)
       for (int kb = work.kb0; kb < work.kb1; ++kb) {
-        if (!mbar_wait_soon(&tempty[b], tph ^ 1u, wc) || !mbar_wait_soon(&full[s], ph, wc)) {
+        const int su = uniform(s), bu = uniform(b);
+        if (!__all_sync(0xffffffffu, mbar_wait_soon(&tempty[bu], tph ^ 1u, wc) && mbar_wait_soon(&full[su], ph, wc))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t a = smem_u32(smem + s * L::kStageBytes), w = a + L::kABytes, d = tmem + (uint32_t)(b * BN);
+        const uint32_t d = tmem + (uint32_t)(bu * BN);
+        const uint64_t a = sw128_desc(smem_at + su * L::kStageBytes), w = sw128_desc(smem_at + su * L::kStageBytes + L::kABytes);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kBlock / 32; ++k)
-          umma_e4m3(d, sw128_desc(a + k * 32), sw128_desc(w + k * 32), idesc_e4m3(BN), k > 0);
-        umma_commit(&empty[s]);
-        umma_commit(&tfull[b]);
+          for (int k = 0; k < kBlock / 32; ++k) umma_e4m3(d, a + 2 * k, w + 2 * k, idesc_e4m3(BN), k > 0);
+          umma_commit(&empty[su]);
+          umma_commit(&tfull[bu]);
+        }
+        __syncwarp();
         if (++s == L::kStages) s = 0, ph ^= 1u;
         if (++b == L::kBuffers) b = 0, tph ^= 1u;
       }
-      // Every product issued above must complete before tensor memory is released.
-      umma_commit(done);
-      mbar_wait_drain(done, 0, P.err, P.wait_ns);
-    }
-  } else {
+    // Every product issued above must complete before tensor memory is released.
+    if (elect_one()) umma_commit(done);
+    __syncwarp();
+    mbar_wait_soon(done, 0, drain);
+  } else if (warp >= 4) {
     // ------------------------------------------------------------ sums
+    regs_up<104>();
     const int q = warp & 3, row = q * 32 + lane;  // tensor-memory lanes 32 q ..
-    const int quarter = (warp - 2) >> 2, col0 = quarter * L::kCols;
-    const int et = threadIdx.x - 64;
+    const int quarter = (warp - 4) >> 2, col0 = quarter * L::kCols;
+    const int et = threadIdx.x - 128;
     const bool out_vec = (reinterpret_cast<uintptr_t>(P.y) & 15) == 0 && (P.ldy & 7) == 0;
     const bool res_vec = (reinterpret_cast<uintptr_t>(P.res) & 15) == 0 && (P.ldr & 7) == 0;
     pdl_wait();
@@ -306,11 +337,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // apart, so each of the four warps that share rows loads two blocks' and leaves them
       // for the others; the weights' (of the warp's columns) are spread over lanes 0-7, those of
       // a second block over 8-15.
+      // (No load is conditional: the branch around it would wait for it.)
       float nx[2], sw, nw;
       auto load_scales = [&](int kb) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) nx[i] = kb + 2 * quarter + i < kb1 ? ld_act_f32(xs + kb + 2 * quarter + i) : 0.f;
-        nw = kb + (lane & 7) < kb1 ? __ldg(ws + kb + (lane & 7)) : 0.f;
+        for (int i = 0; i < 2; ++i) nx[i] = ld_act_f32(xs + min(kb + 2 * quarter + i, KB - 1));
+        nw = ld_act_f32(ws + min(kb + (lane & 7), KB - 1));
       };
       if (rows_here) load_scales(kb0);
       // a warp that gave up a wait goes on without waiting, through the same barriers as the others
@@ -324,36 +356,84 @@ __global__ void __launch_bounds__(kThreads, 1)
           named_bar_sync(2 + q, 128);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 8; i += L::kTogether) {
           if (kb + i >= kb1) break;
-          ok = ok && __all_sync(0xffffffffu, mbar_wait_soon(&tfull[b], tph, wc));
+          constexpr int T = L::kTogether;
+          uint64_t f0[T], f1[T];
+          if (rows_here) {
+#pragma unroll
+            for (int u = 0; u < T; ++u) {
+              const float x = sx[(i + u) * kRows];
+              const float a = x * __shfl_sync(0xffffffffu, sw, i + u);
+              const float c = L::kStraddle ? x * __shfl_sync(0xffffffffu, sw, 8 + i + u) : a;
+              f0[u] = pack2(a, a);
+              f1[u] = pack2(c, c);
+            }
+          }
+          const int n = min(T, kb1 - kb - i);  // k-blocks of this step
+          int bb = b;
+          uint32_t tp = tph;
+#pragma unroll
+          for (int u = 0; u < T; ++u)
+            if (u < n) {
+              ok = ok && __all_sync(0xffffffffu, mbar_wait_soon(&tfull[bb], tp, wc));
+              if (++bb == L::kBuffers) bb = 0, tp ^= 1u;
+            }
           if (!ok) break;
           if (rows_here) {
             tc_fence_after();
-            const float f0 = sx[i * kRows] * __shfl_sync(0xffffffffu, sw, i);
-            const float f1 = L::kStraddle ? sx[i * kRows] * __shfl_sync(0xffffffffu, sw, 8 + i) : f0;
-            const uint64_t ff0 = pack2(f0, f0), ff1 = pack2(f1, f1);
-            const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BN + col0);
+            const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)col0;
 #pragma unroll
-            for (int ch = 0; ch < L::kCols / L::kFetch; ++ch) {
-              uint32_t v[L::kFetch];
-              tmem_get(at + ch * L::kFetch, v);
-              if (ch == L::kCols / L::kFetch - 1) {
-                // all fetched: the buffer is free
+            for (int ch = 0; ch < L::kCols; ch += L::kAtOnce) {
+              uint32_t v[T][L::kAtOnce / L::kFetch][L::kFetch];
+              bb = b;
+#pragma unroll
+              for (int u = 0; u < T; ++u) {
+                // a step's missing blocks fetch the last one again and are not added
+#pragma unroll
+                for (int p = 0; p < L::kAtOnce / L::kFetch; ++p)
+                  tmem_fetch(lanes + (uint32_t)(bb * BN + ch + p * L::kFetch), v[u][p]);
+                if (u + 1 < n && ++bb == L::kBuffers) bb = 0;
+              }
+              tmem_wait();
+#pragma unroll
+              for (int u = 0; u < T; ++u)
+#pragma unroll
+                for (int p = 0; p < L::kAtOnce / L::kFetch; ++p) tmem_here(v[u][p]);
+              if (ch + L::kAtOnce == L::kCols) {
+                // all fetched: the buffers are free
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&tempty[b]);
+                bb = b;
+#pragma unroll
+                for (int u = 0; u < T; ++u)
+                  if (u < n) {
+                    if (lane == 0) mbar_arrive(&tempty[bb]);
+                    if (++bb == L::kBuffers) bb = 0;
+                  }
               }
 #pragma unroll
-              for (int e = 0; e < L::kFetch / 2; ++e) {
-                const int i2 = ch * (L::kFetch / 2) + e;
-                acc[i2] = fma2(v[2 * e], v[2 * e + 1], L::kStraddle && i2 / 4 * 8 >= edge ? ff1 : ff0, acc[i2]);
-              }
+              for (int u = 0; u < T; ++u)
+                if (u < n) {
+#pragma unroll
+                  for (int p = 0; p < L::kAtOnce / L::kFetch; ++p)
+#pragma unroll
+                    for (int e = 0; e < L::kFetch / 2; ++e) {
+                      const int at = (ch + p * L::kFetch) / 2 + e;
+                      acc[at] = fma2(v[u][p][2 * e], v[u][p][2 * e + 1], L::kStraddle && at / 4 * 8 >= edge ? f1[u] : f0[u],
+                                     acc[at]);
+                    }
+                }
             }
-          } else if (lane == 0) {
-            mbar_arrive(&tempty[b]);
+          } else {
+            bb = b;
+            for (int u = 0; u < n; ++u) {
+              if (lane == 0) mbar_arrive(&tempty[bb]);
+              if (++bb == L::kBuffers) bb = 0;
+            }
           }
-          if (++b == L::kBuffers) b = 0, tph ^= 1u;
+          b = bb;
+          tph = tp;
         }
       }
       if (!named_bar_and(1, kAdders, ok)) break;  // leave together if a warp gave up

@@ -169,7 +169,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ copies
-    if (lane != 0) return;
     const uint64_t pol = policy_evict_first();
     int s = 0;        // the next stage of the ring
     uint32_t ph = 0;  // and how often the ring has gone round, mod 2
@@ -184,17 +183,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row = (e < 0 ? 0 : e) * P.R;  // at most 2^31 rows in a bank
       for (int j = S.ga; j < S.gb && ok; j += WG)
         for (int ch = 0; ch < chunks; ++ch) {
-          if (!mbar_wait(&empty[s], ph ^ 1u, wc)) {
+          if (!warp_wait(&empty[s], ph ^ 1u, wc)) {
             ok = false;
             break;
           }
-          const int kb0 = ch * WK * UW;
+          const int su = uniform(s), kb0 = uniform(ch * WK * UW), from = uniform(row + j * h);
           const bool tail = !PAIR && kb0 + WK * UW > P.K / 128 && P.K % 128 != 0;  // the stage holds the short block
-          mbar_arrive_expect_tx(&full[s], (uint32_t)((NA * kWarps * UW + (tail ? WG : 0)) * h * 128));
-          uint8_t* dst = ring + (size_t)s * stage;
-          tma_load_3d(dst, m0, &full[s], 0, row + j * h, kb0, pol);
-          if (PAIR) tma_load_3d(dst + main_bytes(NA, h), m1, &full[s], 0, row + j * h, kb0, pol);
-          if (tail) tma_load_2d(dst + main_bytes(NA, h), &tm1, &full[s], (KB - 1) * 128, row + j * h, pol);
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&full[su], (uint32_t)((NA * kWarps * UW + (tail ? WG : 0)) * h * 128));
+            uint8_t* dst = ring + (size_t)su * stage;
+            tma_load_3d(dst, m0, &full[su], 0, from, kb0, pol);
+            if (PAIR) tma_load_3d(dst + main_bytes(NA, h), m1, &full[su], 0, from, kb0, pol);
+            if (tail) tma_load_2d(dst + main_bytes(NA, h), &tm1, &full[su], (KB - 1) * 128, from, pol);
+          }
+          __syncwarp();
           issued = min(issued + 1, P.stages);
           if (++s == P.stages) s = 0, ph ^= 1u;
         }
@@ -250,10 +252,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       sbase = B.scales[PAIR ? lane >> 4 : 0] + (e < 0 ? 0 : (size_t)e * ((P.R + 127) / 128) * KB);
     }
     auto load_scales = [&](int j, int ch) {
-      const int i = lane & 7, kb = ((ch + i / UW) * WK + along) * UW + i % UW;
-      const int block = ((j + sub) * h >> 7) + ((lane >> 3) & 1);
-      const bool in = (PAIR || lane < 16) && j + sub < S.gb && kb < KB && block <= (min((j + sub + 1) * h, P.R) - 1) >> 7;
-      return in ? __ldg(sbase + (size_t)block * KB + kb) : 0.f;
+      const int i = lane & 7, kb = min(((ch + i / UW) * WK + along) * UW + i % UW, KB - 1);
+      const int block = min(((j + sub) * h >> 7) + ((lane >> 3) & 1), (P.R - 1) >> 7);
+      return ld_act_f32(sbase + (size_t)block * KB + kb);  // not conditional: a branch around it would wait for it
     };
     float sc = load_scales(S.ga, 0);
 
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!mine) continue;
 #pragma unroll
           for (int u = 0; u < UW; ++u) {
-            // blocks behind the last are zeros of the copies, with scales of zero
+            // blocks behind the last are zeros of the copies
             const int kb = min(kb0 + u, KB - 1);
             float ws[NA][2];
 #pragma unroll
