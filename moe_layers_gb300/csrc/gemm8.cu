@@ -5,22 +5,20 @@
 //
 // A tile is 128 rows x BN weights. Its k-blocks of 128 values have scales of their own,
 // so the tensor cores' sum of a block is not kept: each block goes to a tensor-memory
-// buffer of its own, is fetched by sixteen warps, scaled and added to totals in registers,
+// buffer of its own, is fetched by eight warps, scaled and added to totals in registers,
 // while the next blocks are multiplied. Rows are the product's M side, so a thread owns
-// one row and BN / 4 columns of one block of weights: its scale is one number a k-block,
+// one row and BN / 2 columns of one block of weights: its scale is one number a k-block,
 // and a fetched value costs half a packed fused multiply-add.
 //
 // One CTA per SM. Whole tiles go round the CTAs as long as there is one for each, in panels
-// of 16 tiles of rows, so that the tiles in work at a time share rows and weights in L2. The
-// (tile, k-block) pairs of the tiles that are left (all, for a decode batch) form a sequence
-// that is cut into one equal range per CTA, so no round is left half full and few tiles
-// use every SM. A tile that several CTAs share is finished by the one that publishes its
-// piece last: it adds all pieces in k order (no atomics on values; the results follow from
-// the inputs and the shape alone).
+// of 16 tiles of rows, so that the tiles in work at a time share rows and weights in L2. A
+// tile that is left over (any, for a decode batch) may be shared by up to four CTAs, a run of
+// k-blocks each; the one that publishes its piece last adds all pieces in k order (no atomics
+// on values; the results follow from the inputs and the shape alone).
 //
 // Per CTA: warp 0 issues the TMA loads of a k-block's rows and weights (128-byte
 // swizzle) into a ring in shared memory, warp 1 the tcgen05.mma (128 x BN x 32, kind
-// f8f6f4), warps 4-19 fetch, scale and add.
+// f8f6f4), warps 4-11 fetch, scale and add.
 #include <algorithm>
 
 #include "common.cuh"
@@ -33,7 +31,7 @@ namespace {
 
 constexpr int kRows = 128;
 constexpr int kBlock = 128;  // k values of a block, one row of the swizzle
-constexpr int kAdders = 512;
+constexpr int kAdders = 256;
 constexpr int kThreads = 128 + kAdders;
 constexpr int kTmem = 512;
 
@@ -43,10 +41,11 @@ struct Plan {
   static constexpr int kStageBytes = kABytes + BN * kBlock;
   static constexpr int kStages = 221184 / kStageBytes;
   static constexpr int kBuffers = kTmem / BN < 8 ? kTmem / BN : 8;
-  static constexpr int kCols = BN / 4;                            // a thread's
-  static constexpr int kFetch = kCols % 16 == 0 ? 16 : 8;  // columns of one instruction
-  static constexpr int kTogether = BN <= 32 ? 4 : 1;               // k-blocks fetched at once
-  static constexpr int kAtOnce = kCols * kTogether <= 48 && BN < 128 ? kCols : kFetch;  // columns a thread fetches before it adds
+  static constexpr int kCols = BN / 2;                            // a thread's
+  static constexpr int kFetch = kCols % 32 == 0 && kCols != 96 ? 32 : 16;        // columns of one instruction
+  static constexpr int kTogether = BN <= 32 ? 4 : BN <= 96 ? 2 : 1;              // k-blocks fetched at once
+  static constexpr int kAtOnce = kCols <= 64 ? kCols : kCols == 96 ? 48 : 64;    // columns a thread fetches before it adds
+  static_assert(kCols % kAtOnce == 0 && kAtOnce % kFetch == 0, "whole instructions");
   static constexpr bool kStraddle = 128 % kCols != 0;             // they may lie in two blocks of weights
   static constexpr int kBarOff = kStages * kStageBytes;
   static constexpr int kScaleOff = kBarOff + (8 * (2 * kStages + 2 * kBuffers + 1) + 16 + 63) / 64 * 64;
@@ -56,6 +55,7 @@ struct Plan {
 
 struct Gemm8Params {
   int M, N, K, KB, mtiles, ntiles;
+  int split;     // CTAs that share a tile of those left after whole rounds
   int box_rows;  // rows of a copy: a tile's, or the whole batch's up to eight
   const float* xs;
   long long ldxs;
@@ -66,15 +66,12 @@ struct Gemm8Params {
   long long ldy;
   float* pieces;
   int piece_rows;  // rows of a published piece: the tile's, or the batch's up to a warp's
-  int* counters;   // one a CTA: pieces published of the tile whose first piece it holds
+  int* counters;   // one for each shared tile: pieces published
   int* err;
   unsigned long long wait_ns;
 };
 
 constexpr int kPanel = 16;  // tiles of rows
-
-__device__ __forceinline__ long long range_start(long long c, long long W, long long G) { return c * W / G; }
-__device__ __forceinline__ int cta_of(long long j, long long W, long long G) { return (int)(((j + 1) * G - 1) / W); }
 
 // Instruction descriptor, kind::f8f6f4: D fp32, A and B e4m3, both K-major, 128 x N.
 constexpr uint32_t idesc_e4m3(int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24); }
@@ -145,34 +142,29 @@ __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
 
 }  // namespace
 
-// The work of a CTA: `rounds` whole tiles, then its range of what is left.
+// The work of a CTA: `rounds` whole tiles, then, of what is left, a part of a tile.
 struct Work {
-  int KB, mtiles, ntiles;
-  long long tiles, G, c, rounds, W, base;  // W: k-blocks left, from tile `base` on
-  long long r, j, j1;                      // the next round; the range
-  int tile, kb0, kb1;                      // the current part: k-blocks [kb0, kb1) of a tile
-  __device__ Work(const Gemm8Params& P)
-      : KB(P.KB), mtiles(P.mtiles), ntiles(P.ntiles), tiles((long long)P.mtiles * P.ntiles), G(gridDim.x), c(blockIdx.x) {
-    rounds = tiles / G;
-    base = rounds * G;
-    W = (tiles - base) * KB;
-    r = 0;
-    j = range_start(c, W, G);
-    j1 = range_start(c + 1, W, G);
+  int KB, mtiles, ntiles, split, rounds, left;
+  int r = 0;
+  int tile, kb0, kb1;  // the current part: k-blocks [kb0, kb1) of a tile
+  __device__ Work(const Gemm8Params& P) : KB(P.KB), mtiles(P.mtiles), ntiles(P.ntiles), split(P.split) {
+    const int tiles = P.mtiles * P.ntiles;
+    rounds = tiles / (int)gridDim.x;
+    left = tiles - rounds * (int)gridDim.x;
   }
   __device__ bool next() {
+    const int c = blockIdx.x;
     if (r < rounds) {
-      tile = (int)(r++ * G + c);
+      tile = r++ * (int)gridDim.x + c;
       kb0 = 0;
       kb1 = KB;
       return true;
     }
-    if (j >= j1) return false;
-    const int t = (int)(j / KB);
-    tile = (int)(base + t);
-    kb0 = (int)(j - (long long)t * KB);
-    kb1 = (int)min((long long)KB, kb0 + (j1 - j));
-    j += kb1 - kb0;
+    if (r++ > rounds || c >= left * split) return false;
+    const int t = c / split, part = c - t * split;
+    tile = rounds * (int)gridDim.x + t;
+    kb0 = part * KB / split;
+    kb1 = (part + 1) * KB / split;
     return true;
   }
   __device__ void place(int& mt, int& nt) const {
@@ -227,8 +219,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot), smem_at = smem_u32(smem);
   const WaitCtl wc{abort_flag, P.err, P.wait_ns}, drain{nullptr, P.err, P.wait_ns};
 
-  // 640 threads start with 96 registers each; 512 x 104 + 128 x 40 are fewer.
-  if (warp < 4) regs_down<40>();
+  // 384 threads start with 168 registers each; 256 x 208 + 128 x 80 are fewer.
+  if (warp < 4) regs_down<80>();
   if (warp == 0) {
     // ------------------------------------------------------------ copies
     const uint64_t pol_w = P.mtiles == 1 ? policy_evict_first() : policy_evict_last();  // read once, or again
@@ -309,9 +301,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait_soon(done, 0, drain);
   } else if (warp >= 4) {
     // ------------------------------------------------------------ sums
-    regs_up<104>();
+    regs_up<208>();
     const int q = warp & 3, row = q * 32 + lane;  // tensor-memory lanes 32 q ..
-    const int quarter = (warp - 4) >> 2, col0 = quarter * L::kCols;
+    const int half = (warp - 4) >> 2, col0 = half * L::kCols;
     const int et = threadIdx.x - 128;
     const bool out_vec = (reinterpret_cast<uintptr_t>(P.y) & 15) == 0 && (P.ldy & 7) == 0;
     const bool res_vec = (reinterpret_cast<uintptr_t>(P.res) & 15) == 0 && (P.ldr & 7) == 0;
@@ -334,14 +326,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < L::kCols / 2; ++i) acc[i] = 0;
       // Scales of eight blocks at a time, the next eight's loads in flight. The rows' lie far
-      // apart, so each of the four warps that share rows loads two blocks' and leaves them
-      // for the others; the weights' (of the warp's columns) are spread over lanes 0-7, those of
+      // apart, so each of the two warps that share rows loads four blocks' and leaves them
+      // for both; the weights' (of the warp's columns) are spread over lanes 0-7, those of
       // a second block over 8-15.
       // (No load is conditional: the branch around it would wait for it.)
-      float nx[2], sw, nw;
+      float nx[4], sw, nw;
       auto load_scales = [&](int kb) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) nx[i] = ld_act_f32(xs + min(kb + 2 * quarter + i, KB - 1));
+        for (int i = 0; i < 4; ++i) nx[i] = ld_act_f32(xs + min(kb + 4 * half + i, KB - 1));
         nw = ld_act_f32(ws + min(kb + (lane & 7), KB - 1));
       };
       if (rows_here) load_scales(kb0);
@@ -350,10 +342,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* sx = s_scales + ((turn++ & 1) * 8) * kRows + row;
         if (rows_here) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) sx[(2 * quarter + i) * kRows] = nx[i];
+          for (int i = 0; i < 4; ++i) sx[(4 * half + i) * kRows] = nx[i];
           sw = nw;
           load_scales(kb + 8);
-          named_bar_sync(2 + q, 128);
+          named_bar_sync(2 + q, 64);
         }
 #pragma unroll
         for (int i = 0; i < 8; i += L::kTogether) {
@@ -440,15 +432,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       if (kb1 - kb0 < KB) {
         // A piece: published, four columns of a row at a time; whoever publishes the last adds them all in k order.
-        const long long first = (work.tile - work.base) * KB;
-        const int p_rows = P.piece_rows, c0 = cta_of(first, work.W, work.G), c1 = cta_of(first + KB - 1, work.W, work.G);
+        const int p_rows = P.piece_rows, shared = (int)blockIdx.x / P.split;
         auto piece = [&](int cc) {
-          const bool inside = range_start(cc, work.W, work.G) >= first;
-          return reinterpret_cast<float4*>(P.pieces) + (size_t)(cc * 2 + (inside ? 0 : 1)) * (BN / 4) * p_rows +
-                 (size_t)(col0 / 4) * p_rows + row;
+          return reinterpret_cast<float4*>(P.pieces) + (size_t)cc * (BN / 4) * p_rows + (size_t)(col0 / 4) * p_rows + row;
         };
         if (rows_here) {
-          float4* dst = piece((int)work.c);
+          float4* dst = piece((int)blockIdx.x);
 #pragma unroll
           for (int i = 0; i < L::kCols / 4; ++i) {
             const float2 lo = unpack2(acc[2 * i]), hi = unpack2(acc[2 * i + 1]);
@@ -457,17 +446,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __threadfence();
         named_bar_sync(1, kAdders);
-        if (et == 0) *s_last = atom_add_acq_rel_gpu(P.counters + c0, 1) == c1 - c0 ? 1 : 0;
+        if (et == 0) *s_last = atom_add_acq_rel_gpu(P.counters + shared, 1) == P.split - 1 ? 1 : 0;
         named_bar_sync(1, kAdders);
         const bool last = *s_last != 0;
         named_bar_sync(1, kAdders);  // read by all before the next piece
         if (!last) continue;
         __threadfence();
-        if (et == 0) P.counters[c0] = 0;  // leave the workspace reusable
+        if (et == 0) P.counters[shared] = 0;  // leave the workspace reusable
         if (rows_here) {
 #pragma unroll
           for (int i = 0; i < L::kCols / 2; ++i) acc[i] = 0;
-          for (int cc = c0; cc <= c1; ++cc) {
+          for (int cc = shared * P.split; cc < (shared + 1) * P.split; ++cc) {
             const float4* src = piece(cc);
 #pragma unroll
             for (int i = 0; i < L::kCols / 4; ++i) {
@@ -533,35 +522,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 // memory's for the weights, about 23), its products, and some 350 clocks of waits; a tile that
 // CTAs share costs an exchange of pieces.
 struct Choice {
-  int bn, grid;
+  int bn, grid, split;
 };
 static Choice choose(const dec_handle* h, int M, int N, int K) {
   const long long mt = (M + kRows - 1) / kRows, KB = (K + kBlock - 1) / kBlock;
   const double rows = std::min(M, kRows);
-  Choice best = {256, 1};
+  Choice best = {256, 1, 1};
   double least = 1e300;
   for (int bn : {32, 64, 96, 128, 192, 256}) {
     const long long tiles = mt * ((N + bn - 1) / bn);
-    const double block = std::max(350.0, std::max((rows + bn) * 128 / 40, bn * 4.0));
+    const double block = std::max(300.0, std::max((rows + bn) * 128 / 40, bn * 3.0));
     const double memory = (double)N * K / (h->sms * 23.0);
-    for (int split = 1; split <= 8; split *= 2) {
-      long long grid;
-      double blocks, exchange = 0;
-      if (tiles <= h->sms) {
-        grid = tiles * split;
-        if (grid > h->sms || KB / split < 4) continue;
-        blocks = (double)((KB + split - 1) / split);
-        if (split > 1) exchange = 4000 + 1500.0 * split;
-      } else {
-        if (split > 1) continue;
-        grid = h->sms;
-        const long long left = tiles % grid;
-        blocks = (double)(tiles / grid * KB) + (double)left * KB / grid;
-        if (left) exchange = 4000 + 1500.0 * std::min(8.0, (double)grid / left);
-        blocks += (double)(tiles / grid) * 2;
-      }
-      const double t = std::max(blocks * block, memory) + exchange;
-      if (t < least) least = t, best = {bn, (int)grid};
+    for (int split = 1; split <= 4; ++split) {
+      const long long rounds = tiles / h->sms, left = tiles - rounds * h->sms;
+      if (split > 1 && (left * split > h->sms || KB / split < 4)) continue;
+      const double blocks = (double)(rounds * KB) + (left ? (double)((KB + split - 1) / split) : 0.0);
+      const double exchange = left && split > 1 ? 10000 + 3000.0 * split : 0;
+      const double t = std::max(blocks * block + (rounds + (left > 0)) * 1500.0, memory) + exchange;
+      if (t < least) least = t, best = {bn, (int)(rounds ? h->sms : left * split), split};
     }
   }
   return best;
@@ -572,7 +550,7 @@ static size_t counter_bytes(const dec_handle* h) { return ((size_t)h->sms * 4 + 
 
 size_t gemm8_ws_bytes(const dec_handle* h, int M, int N, int K) {
   const Choice c = choose(h, M, N, K);
-  return counter_bytes(h) + (size_t)2 * c.grid * c.bn * piece_rows(M) * 4;
+  return counter_bytes(h) + (c.split > 1 ? (size_t)c.grid * c.bn * piece_rows(M) * 4 : 0);
 }
 
 static bool encode_tile(const dec_handle* h, CUtensorMap* m, const uint8_t* p, int K, int rows, long long ld, int box_rows) {
@@ -586,7 +564,7 @@ static bool encode_tile(const dec_handle* h, CUtensorMap* m, const uint8_t* p, i
 }
 
 template <int BN>
-static cudaError_t launch_bn(dec_handle* h, const Linear8& A, int grid, void* ws, cudaStream_t s) {
+static cudaError_t launch_bn(dec_handle* h, const Linear8& A, const Choice& c, void* ws, cudaStream_t s) {
   using L = Plan<BN>;
   const int box_rows = std::min(kRows, (A.M + 7) / 8 * 8);
   CUtensorMap tx, tw;
@@ -606,6 +584,7 @@ static cudaError_t launch_bn(dec_handle* h, const Linear8& A, int grid, void* ws
   P.mtiles = (A.M + kRows - 1) / kRows;
   P.ntiles = (A.N + BN - 1) / BN;
   P.box_rows = box_rows;
+  P.split = c.split;
   P.xs = A.xs;
   P.ldxs = A.ldxs;
   P.ws = A.ws;
@@ -618,19 +597,19 @@ static cudaError_t launch_bn(dec_handle* h, const Linear8& A, int grid, void* ws
   P.piece_rows = piece_rows(A.M);
   P.err = h->d_err;
   P.wait_ns = h->wait_ns;
-  return launch_k(h, gemm8_kernel<BN>, dim3(grid), dim3(kThreads), (size_t)L::kBytes, s, tx, tw,
+  return launch_k(h, gemm8_kernel<BN>, dim3(c.grid), dim3(kThreads), (size_t)L::kBytes, s, tx, tw,
                   P);
 }
 
 cudaError_t launch_gemm8(dec_handle* h, const Linear8& A, void* ws, cudaStream_t s) {
   const Choice c = choose(h, A.M, A.N, A.K);
   switch (c.bn) {
-    case 32: return launch_bn<32>(h, A, c.grid, ws, s);
-    case 64: return launch_bn<64>(h, A, c.grid, ws, s);
-    case 96: return launch_bn<96>(h, A, c.grid, ws, s);
-    case 128: return launch_bn<128>(h, A, c.grid, ws, s);
-    case 192: return launch_bn<192>(h, A, c.grid, ws, s);
-    default: return launch_bn<256>(h, A, c.grid, ws, s);
+    case 32: return launch_bn<32>(h, A, c, ws, s);
+    case 64: return launch_bn<64>(h, A, c, ws, s);
+    case 96: return launch_bn<96>(h, A, c, ws, s);
+    case 128: return launch_bn<128>(h, A, c, ws, s);
+    case 192: return launch_bn<192>(h, A, c, ws, s);
+    default: return launch_bn<256>(h, A, c, ws, s);
   }
 }
 
