@@ -42,9 +42,10 @@ struct Plan {
   static constexpr int kStages = 221184 / kStageBytes;
   static constexpr int kBuffers = kTmem / BN < 8 ? kTmem / BN : 8;
   static constexpr int kCols = BN / 2;                            // a thread's
-  static constexpr int kFetch = kCols % 32 == 0 && kCols != 96 ? 32 : 16;        // columns of one instruction
-  static constexpr int kTogether = BN <= 32 ? 4 : BN <= 96 ? 2 : 1;              // k-blocks fetched at once
-  static constexpr int kAtOnce = kCols <= 64 ? kCols : kCols == 96 ? 48 : 64;    // columns a thread fetches before it adds
+  static constexpr int kFetch = kCols % 32 == 0 ? 32 : 16;        // columns of one instruction
+  // Columns fetched before any is added. (More at once would take registers that are not there:
+  // 64 of 128 columns spill, and 4096 rows take 506 us instead of 379.)
+  static constexpr int kAtOnce = kCols <= 48 ? kCols : 32;
   static_assert(kCols % kAtOnce == 0 && kAtOnce % kFetch == 0, "whole instructions");
   static constexpr bool kStraddle = 128 % kCols != 0;             // they may lie in two blocks of weights
   static constexpr int kBarOff = kStages * kStageBytes;
@@ -87,12 +88,6 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, ui
 
 // Consecutive fp32 columns of this thread's tensor-memory lane, there after tmem_wait
 // and, so that no use of them is moved before it, tmem_here.
-__device__ __forceinline__ void tmem_fetch(uint32_t at, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(at)
-               : "memory");
-}
 __device__ __forceinline__ void tmem_fetch(uint32_t at, uint32_t (&r)[16]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
@@ -106,9 +101,6 @@ __device__ __forceinline__ void tmem_fetch(uint32_t at, uint32_t (&r)[32]) {
                : "memory");
 }
 __device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_here(uint32_t (&r)[8]) {
-  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]));
-}
 __device__ __forceinline__ void tmem_here(uint32_t (&r)[16]) {
   asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 }
@@ -288,8 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kBlock / 32; ++k) umma_e4m3(d, a + 2 * k, w + 2 * k, idesc_e4m3(BN), k > 0);
-          umma_commit(&empty[su]);
           umma_commit(&tfull[bu]);
+          umma_commit(&empty[su]);
         }
         __syncwarp();
         if (++s == L::kStages) s = 0, ph ^= 1u;
@@ -348,84 +340,52 @@ __global__ void __launch_bounds__(kThreads, 1)
           named_bar_sync(2 + q, 64);
         }
 #pragma unroll
-        for (int i = 0; i < 8; i += L::kTogether) {
+        for (int i = 0; i < 8; ++i) {
           if (kb + i >= kb1) break;
-          constexpr int T = L::kTogether;
-          uint64_t f0[T], f1[T];
+          uint64_t f0, f1;
           if (rows_here) {
-#pragma unroll
-            for (int u = 0; u < T; ++u) {
-              const float x = sx[(i + u) * kRows];
-              const float a = x * __shfl_sync(0xffffffffu, sw, i + u);
-              const float c = L::kStraddle ? x * __shfl_sync(0xffffffffu, sw, 8 + i + u) : a;
-              f0[u] = pack2(a, a);
-              f1[u] = pack2(c, c);
-            }
+            const float x = sx[i * kRows];
+            const float a = x * __shfl_sync(0xffffffffu, sw, i);
+            const float c = L::kStraddle ? x * __shfl_sync(0xffffffffu, sw, 8 + i) : a;
+            f0 = pack2(a, a);
+            f1 = pack2(c, c);
           }
-          const int n = min(T, kb1 - kb - i);  // k-blocks of this step
-          int bb = b;
-          uint32_t tp = tph;
-#pragma unroll
-          for (int u = 0; u < T; ++u)
-            if (u < n) {
-              ok = ok && __all_sync(0xffffffffu, mbar_wait_soon(&tfull[bb], tp, wc));
-              if (++bb == L::kBuffers) bb = 0, tp ^= 1u;
-            }
+          ok = ok && __all_sync(0xffffffffu, mbar_wait_soon(&tfull[b], tph, wc));
           if (!ok) break;
+          const int here = min(1, kb1 - kb - i);  // 1
           if (rows_here) {
             tc_fence_after();
-            const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)col0;
+            const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BN + col0);
 #pragma unroll
             for (int ch = 0; ch < L::kCols; ch += L::kAtOnce) {
-              uint32_t v[T][L::kAtOnce / L::kFetch][L::kFetch];
-              bb = b;
+              uint32_t v[L::kAtOnce / L::kFetch][L::kFetch];
 #pragma unroll
-              for (int u = 0; u < T; ++u) {
-                // a step's missing blocks fetch the last one again and are not added
-#pragma unroll
-                for (int p = 0; p < L::kAtOnce / L::kFetch; ++p)
-                  tmem_fetch(lanes + (uint32_t)(bb * BN + ch + p * L::kFetch), v[u][p]);
-                if (u + 1 < n && ++bb == L::kBuffers) bb = 0;
-              }
+              for (int p = 0; p < L::kAtOnce / L::kFetch; ++p) tmem_fetch(at + ch + p * L::kFetch, v[p]);
               tmem_wait();
 #pragma unroll
-              for (int u = 0; u < T; ++u)
-#pragma unroll
-                for (int p = 0; p < L::kAtOnce / L::kFetch; ++p) tmem_here(v[u][p]);
+              for (int p = 0; p < L::kAtOnce / L::kFetch; ++p) tmem_here(v[p]);
               if (ch + L::kAtOnce == L::kCols) {
-                // all fetched: the buffers are free
+                // all fetched: the buffer is free
                 tc_fence_before();
                 __syncwarp();
-                bb = b;
+                if (lane == 0) mbar_arrive(&tempty[b]);
+              }
+              // Always so: behind a branch the additions stay together, before the next fetch. Mixed with
+              // it they spill registers, and 4096 rows take 475 us instead of 380.
+              if (here > 0) {
 #pragma unroll
-                for (int u = 0; u < T; ++u)
-                  if (u < n) {
-                    if (lane == 0) mbar_arrive(&tempty[bb]);
-                    if (++bb == L::kBuffers) bb = 0;
+                for (int p = 0; p < L::kAtOnce / L::kFetch; ++p)
+#pragma unroll
+                  for (int e = 0; e < L::kFetch / 2; ++e) {
+                    const int pair = (ch + p * L::kFetch) / 2 + e;
+                    acc[pair] = fma2(v[p][2 * e], v[p][2 * e + 1], L::kStraddle && pair / 4 * 8 >= edge ? f1 : f0, acc[pair]);
                   }
               }
-#pragma unroll
-              for (int u = 0; u < T; ++u)
-                if (u < n) {
-#pragma unroll
-                  for (int p = 0; p < L::kAtOnce / L::kFetch; ++p)
-#pragma unroll
-                    for (int e = 0; e < L::kFetch / 2; ++e) {
-                      const int at = (ch + p * L::kFetch) / 2 + e;
-                      acc[at] = fma2(v[u][p][2 * e], v[u][p][2 * e + 1], L::kStraddle && at / 4 * 8 >= edge ? f1[u] : f0[u],
-                                     acc[at]);
-                    }
-                }
             }
-          } else {
-            bb = b;
-            for (int u = 0; u < n; ++u) {
-              if (lane == 0) mbar_arrive(&tempty[bb]);
-              if (++bb == L::kBuffers) bb = 0;
-            }
+          } else if (lane == 0) {
+            mbar_arrive(&tempty[b]);
           }
-          b = bb;
-          tph = tp;
+          if (++b == L::kBuffers) b = 0, tph ^= 1u;
         }
       }
       if (!named_bar_and(1, kAdders, ok)) break;  // leave together if a warp gave up
@@ -517,21 +477,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- host side
-// Weights a tile and CTAs: by the time of the longest CTA, in clocks. A k-block of a tile
-// costs its rows and weights at the rate of copies (64 bytes a clock and SM; together at the
-// memory's for the weights, about 23), its products, and some 350 clocks of waits; a tile that
-// CTAs share costs an exchange of pieces.
+// Weights a tile, and CTAs to a left-over tile: by the time of the longest CTA, in clocks. A
+// k-block of a tile takes 520 + 2.5 BN (measured at 4096 x 12288 x 7168, BN 32 to 256: 609, 636,
+// 757, 750, 1030, 1170), a tile's output some 1500 and the exchange of a shared tile's pieces
+// 10000 to 20000; the weights' bytes pass at 23 a clock and SM at most.
 struct Choice {
   int bn, grid, split;
 };
 static Choice choose(const dec_handle* h, int M, int N, int K) {
   const long long mt = (M + kRows - 1) / kRows, KB = (K + kBlock - 1) / kBlock;
-  const double rows = std::min(M, kRows);
   Choice best = {256, 1, 1};
   double least = 1e300;
   for (int bn : {32, 64, 96, 128, 192, 256}) {
     const long long tiles = mt * ((N + bn - 1) / bn);
-    const double block = std::max(300.0, std::max((rows + bn) * 128 / 40, bn * 3.0));
+    const double block = 520 + 2.5 * bn;
     const double memory = (double)N * K / (h->sms * 23.0);
     for (int split = 1; split <= 4; ++split) {
       const long long rounds = tiles / h->sms, left = tiles - rounds * h->sms;

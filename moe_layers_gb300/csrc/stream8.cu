@@ -44,6 +44,7 @@ constexpr int kThreads = (kWarps + 1) * 32;  // and one that copies
 constexpr int kSums = 2;                    // groups whose sums may wait for their turn
 constexpr int kMaxStages = 12;
 constexpr int kMaxSmem = 232448;
+constexpr int kHalfSmem = 115712;           // with two CTAs to an SM
 constexpr int kBarBytes = 8 * (2 * kMaxStages + 2 * kWarps * kSums) + 16;
 
 // 4-byte asynchronous copy from global to shared memory.
@@ -119,7 +120,7 @@ struct Segment {
 };
 
 template <int NT, bool PAIR, bool GROUPED>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     stream8_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ CUtensorMap tm1,
                    const __grid_constant__ CUtensorMap ts0, const __grid_constant__ CUtensorMap ts1,
                    const Stream8Params P) {
@@ -519,10 +520,10 @@ static size_t fixed_bytes(int xrows, int nt, int K, bool pair) {
 }
 static size_t one_stage(int K, bool pair, int h) { return stage_bytes(pair ? 2 : 1, h, K); }
 // Ring stages that fit beside it.
-static int stages_for(int xrows, int nt, int K, bool pair, int h) {
+static int stages_for(int xrows, int nt, int K, bool pair, int h, int smem = kMaxSmem) {
   const size_t fixed = fixed_bytes(xrows, nt, K, pair);
-  if (fixed >= (size_t)kMaxSmem) return 0;
-  return std::min<int>(kMaxStages, (int)((kMaxSmem - fixed) / one_stage(K, pair, h)));
+  if (fixed >= (size_t)smem) return 0;
+  return std::min<int>(kMaxStages, (int)((smem - fixed) / one_stage(K, pair, h)));
 }
 
 // Rows of a group: the largest range of a CTA in rows, with two rows' time for each group.
@@ -566,8 +567,16 @@ static cudaError_t launch_one(dec_handle* h, Stream8Params P, int xrows, double 
   P.KB = (P.K + 127) / 128;
   P.WK = warps_along(P.KB, PAIR ? 2 : 1);
   P.xrows = xrows;
-  P.height = group_height(P.R, problems, h->sms);
-  P.stages = stages_for(xrows, NT, P.K, PAIR, P.height);
+  // Two CTAs to an SM where each has a ring of three stages: the next launch's CTAs then start, and
+  // fill their rings, beside the last of this one's.
+  int ctas = 2;
+  P.height = group_height(P.R, problems, h->sms * ctas);
+  P.stages = stages_for(xrows, NT, P.K, PAIR, P.height, kHalfSmem);
+  if (NT > 1 || P.stages < 3) {
+    ctas = 1;
+    P.height = group_height(P.R, problems, h->sms);
+    P.stages = stages_for(xrows, NT, P.K, PAIR, P.height);
+  }
   P.err = h->d_err;
   P.wait_ns = h->wait_ns;
   if (P.stages < 2) return cudaErrorInvalidConfiguration;
@@ -592,7 +601,7 @@ static cudaError_t launch_one(dec_handle* h, Stream8Params P, int xrows, double 
     if (e != cudaSuccess) return e;
     attr_set = true;
   }
-  return launch_k(h, stream8_kernel<NT, PAIR, GROUPED>, dim3(h->sms), dim3(kThreads), smem, s, m[0], m[1], m[2], m[3], P);
+  return launch_k(h, stream8_kernel<NT, PAIR, GROUPED>, dim3(h->sms * ctas), dim3(kThreads), smem, s, m[0], m[1], m[2], m[3], P);
 }
 
 int stream8_rows(int K, bool pair) {
