@@ -47,18 +47,14 @@ bool experts_width_ok(const dec_moe_fp8_weights* W) { return W->H <= kMaxExpertW
 
 bool has_shared(const dec_moe_fp8_weights* W) { return W->gate_s.q != nullptr; }
 
-// Workspace of the experts: the table, the experts' inner rows in fp32 and in 8
-// bits with their scales, and their outputs.
+// Workspace of the experts: the table, the experts' inner rows and their outputs.
 struct ExpertsWs {
-  size_t inner, hq, hs, y, bytes;
+  size_t inner, y, bytes;
   ExpertsWs(const Experts8Plan& p, int H, int I) {
     auto up = [](size_t b) { return (b + 255) & ~size_t(255); };
-    const size_t n = p.slots;
     inner = up((size_t)p.words * 4);
-    hq = inner + up(n * I * 4);
-    hs = hq + up(n * I);
-    y = hs + up(n * (I / 128) * 4);
-    bytes = y + up(n * H * 4);
+    y = inner + up((size_t)p.slots * I * 4);
+    bytes = y + up((size_t)p.slots * H * 4);
   }
 };
 
@@ -84,7 +80,7 @@ dec_status dec_rmsnorm_quant(dec_handle* h, const dec_bf16* x, int64_t ldx, cons
   if (!dev.ok) return DEC_ERR_CUDA;
   QuantRows P = {x, ldx, residual, ldr, gamma, eps, sum, lds, y, ldy, out->q, out->ldq, out->scales, out->lds, H};
   LaunchScope scope(h, "rmsnorm_quant", stream);
-  return status(launch_norm_quant(h, P, M, false, stream));
+  return status(launch_norm_quant(h, P, M, stream));
 }
 
 dec_status dec_quant_weight(dec_handle* h, const dec_bf16* W, int64_t N, int K, dec_e4m3* q, float* scales,
@@ -149,8 +145,8 @@ dec_status moe_experts_fp8(dec_handle* h, const dec_fp8_rows* x, const int32_t* 
   Experts8 X = {x->q, x->ldq, x->scales, x->lds, idx, w, M, k, Wt->E, Wt->H, Wt->I, bank(Wt->gate, Wt->up),
                 bank(Wt->down, Wt->down), bank(Wt->gate_s, Wt->up_s), bank(Wt->down_s, Wt->down_s), residual, out};
   uint8_t* b = static_cast<uint8_t*>(ws);
-  return status(launch_experts8(h, X, p, reinterpret_cast<int*>(b), reinterpret_cast<float*>(b + at.inner), b + at.hq,
-                                reinterpret_cast<float*>(b + at.hs), reinterpret_cast<float*>(b + at.y), stream));
+  return status(launch_experts8(h, X, p, reinterpret_cast<int*>(b), reinterpret_cast<float*>(b + at.inner),
+                                reinterpret_cast<float*>(b + at.y), stream));
 }
 
 }  // extern "C"

@@ -217,7 +217,7 @@ bool attention_shape_ok(int M, int q_heads, const dec_kv_cache* c, const dec_bat
 
 // ---------------------------------------------------------------- 8-bit numbers
 struct QuantRows {
-  const void* x;  // bf16 rows (fp32 for the wide form: no residual, no gains, no bf16 outputs)
+  const uint16_t* x;
   long long ldx;
   const uint16_t* res;  // or null
   long long ldr;
@@ -233,7 +233,7 @@ struct QuantRows {
   long long ldsc;
   int H;
 };
-cudaError_t launch_norm_quant(dec_handle* h, const QuantRows& P, int M, bool wide, cudaStream_t s);
+cudaError_t launch_norm_quant(dec_handle* h, const QuantRows& P, int M, cudaStream_t s);
 cudaError_t launch_weight_quant(dec_handle* h, const uint16_t* W, long long N, int K, uint8_t* q, float* scales,
                                 cudaStream_t s);
 
@@ -282,8 +282,8 @@ struct Experts8Plan {
   int words = 0;  // of the table
 };
 Experts8Plan experts8_plan(int M, int k, int E, int H, int I, bool shared);
-cudaError_t launch_experts8(dec_handle* h, const Experts8& X, const Experts8Plan& plan, int* table, float* inner,
-                            uint8_t* hq, float* hs, float* y, cudaStream_t s);
+cudaError_t launch_experts8(dec_handle* h, const Experts8& X, const Experts8Plan& plan, int* table, float* inner, float* y,
+                            cudaStream_t s);
 
 // Makes the handle's device current for the lifetime of the object.
 struct DeviceGuard {

@@ -25,7 +25,7 @@ namespace dec {
 //
 // Bound by memory: 2 bytes in (4 with the residual), 1 + 4/128 out (3 with the
 // sum kept, 5 with y as well).
-template <int VPT, typename T>
+template <int VPT>
 __global__ void __launch_bounds__(256) norm_quant_kernel(const QuantRows P) {
   const int tid = threadIdx.x;
   const long long row = blockIdx.x;
@@ -33,57 +33,36 @@ __global__ void __launch_bounds__(256) norm_quant_kernel(const QuantRows P) {
   pdl_trigger();
   pdl_wait();
   const int H8 = P.H >> 3;
-  constexpr bool kWide = sizeof(T) == 4;  // fp32 input: no residual, no norm
-  float4 wide[kWide ? VPT : 1][2];
-  uint4 xv[kWide ? 1 : VPT];
-  const T* xr = static_cast<const T*>(P.x) + row * P.ldx;
-  if (kWide) {
+  uint4 xv[VPT];
+  const uint16_t* xr = P.x + row * P.ldx;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = tid + 256 * j;
+    xv[j] = v < H8 ? ld_act16(xr + (size_t)v * 8) : make_uint4(0, 0, 0, 0);
+  }
+  if (P.res != nullptr) {
+    uint4 rv[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = tid + 256 * j;
-      wide[j][0] = wide[j][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (v < H8) {
-        wide[j][0] = ld_act_f4(xr + (size_t)v * 8);
-        wide[j][1] = ld_act_f4(xr + (size_t)v * 8 + 4);
-      }
+      rv[j] = v < H8 ? ld_act16(P.res + row * P.ldr + (size_t)v * 8) : make_uint4(0, 0, 0, 0);
     }
-  } else {
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = tid + 256 * j;
-      xv[j] = v < H8 ? ld_act16(xr + (size_t)v * 8) : make_uint4(0, 0, 0, 0);
-    }
-    if (P.res != nullptr) {
-      uint4 rv[VPT];
-#pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        const int v = tid + 256 * j;
-        rv[j] = v < H8 ? ld_act16(P.res + row * P.ldr + (size_t)v * 8) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        const int v = tid + 256 * j;
-        xv[j] = make_uint4(add_bf16x2(xv[j].x, rv[j].x), add_bf16x2(xv[j].y, rv[j].y), add_bf16x2(xv[j].z, rv[j].z),
-                           add_bf16x2(xv[j].w, rv[j].w));
-        if (P.sum != nullptr && v < H8)
-          *reinterpret_cast<uint4*>(P.sum + row * P.lds + (size_t)v * 8) = xv[j];
-      }
+      xv[j] = make_uint4(add_bf16x2(xv[j].x, rv[j].x), add_bf16x2(xv[j].y, rv[j].y), add_bf16x2(xv[j].z, rv[j].z),
+                         add_bf16x2(xv[j].w, rv[j].w));
+      if (P.sum != nullptr && v < H8) *reinterpret_cast<uint4*>(P.sum + row * P.lds + (size_t)v * 8) = xv[j];
     }
   }
   float rho = 1.f;
-  if (!kWide && P.gamma != nullptr) {
-    const float ss = thread_sumsq<kWide ? 1 : VPT, 256>(xv, H8);
-    rho = block_rms_scale<8>(ss, P.H, P.eps, red);
-  }
+  if (P.gamma != nullptr) rho = block_rms_scale<8>(thread_sumsq<VPT, 256>(xv, H8), P.H, P.eps, red);
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int v = tid + 256 * j;
     if (256 * j >= H8) break;  // the whole CTA leaves together: the shuffles below take full warps
     float y[8];
-    if (kWide) {
-      const float4 a = wide[j][0], b = wide[j][1];
-      y[0] = a.x, y[1] = a.y, y[2] = a.z, y[3] = a.w, y[4] = b.x, y[5] = b.y, y[6] = b.z, y[7] = b.w;
-    } else {
+    {
       const uint32_t w[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) y[2 * i] = bf_lo(w[i]), y[2 * i + 1] = bf_hi(w[i]);
@@ -153,21 +132,15 @@ __global__ void __launch_bounds__(256) weight_quant_kernel(const uint16_t* W, lo
   if (t == 0) scales[(long long)blockIdx.x * gridDim.y + blockIdx.y] = s.scale;
 }
 
-template <typename T>
-static cudaError_t launch_rows(dec_handle* h, const QuantRows& P, int M, cudaStream_t s) {
+cudaError_t launch_norm_quant(dec_handle* h, const QuantRows& P, int M, cudaStream_t s) {
   const int n = (P.H / 8 + 255) / 256;
   const dim3 g(M), b(256);
-  if (n <= 1) return launch_k(h, norm_quant_kernel<1, T>, g, b, 0, s, P);
-  if (n <= 2) return launch_k(h, norm_quant_kernel<2, T>, g, b, 0, s, P);
-  if (n <= 4) return launch_k(h, norm_quant_kernel<4, T>, g, b, 0, s, P);
-  if (n <= 8) return launch_k(h, norm_quant_kernel<8, T>, g, b, 0, s, P);
-  if (n <= 16) return launch_k(h, norm_quant_kernel<16, T>, g, b, 0, s, P);
-  if constexpr (sizeof(T) == 2) return launch_k(h, norm_quant_kernel<32, T>, g, b, 0, s, P);
-  return cudaErrorInvalidValue;  // the experts' inner rows are shorter
-}
-
-cudaError_t launch_norm_quant(dec_handle* h, const QuantRows& P, int M, bool wide, cudaStream_t s) {
-  return wide ? launch_rows<float>(h, P, M, s) : launch_rows<uint16_t>(h, P, M, s);
+  if (n <= 1) return launch_k(h, norm_quant_kernel<1>, g, b, 0, s, P);
+  if (n <= 2) return launch_k(h, norm_quant_kernel<2>, g, b, 0, s, P);
+  if (n <= 4) return launch_k(h, norm_quant_kernel<4>, g, b, 0, s, P);
+  if (n <= 8) return launch_k(h, norm_quant_kernel<8>, g, b, 0, s, P);
+  if (n <= 16) return launch_k(h, norm_quant_kernel<16>, g, b, 0, s, P);
+  return launch_k(h, norm_quant_kernel<32>, g, b, 0, s, P);
 }
 
 cudaError_t launch_weight_quant(dec_handle* h, const uint16_t* W, long long N, int K, uint8_t* q, float* scales,

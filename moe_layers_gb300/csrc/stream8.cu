@@ -78,8 +78,11 @@ struct Stream8Params {
   const float* xs;   // their scales
   long long ldxs;
   Stream8Bank bank, shared;  // the routed (or only) weights, and the shared expert's
+  const float* inner;        // or fp32 rows [slots][K], quantised as they are read (x and xs unused)
   const int* table;          // problems (grouped), see experts8_table_kernel
   int P_max;
+  const int32_t* idx;        // or, for one token: its k choices are the problems, and the shared expert
+  int k, E;
   bool by_token;  // activation rows by the slot's token, else by the slot
   int R, K, KB, rows;
   int height;      // rows of a group
@@ -162,8 +165,28 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
   long long problems = 1;
   if (GROUPED) {
     pdl_wait();
-    problems = ld_act_s32(P.table);
+    problems = P.idx != nullptr ? P.k + (P.shared.W[0] != nullptr ? 1 : 0) : ld_act_s32(P.table);
   }
+  // Problem p: expert (-1: the shared one), first slot and rows (none for an id outside [0, E)).
+  struct Problem {
+    int e = 0, slot0 = 0, cnt = 0;
+  };
+  auto problem = [&](int p) {
+    Problem r;
+    if (!GROUPED) {
+      r.cnt = P.rows;
+    } else if (P.idx != nullptr) {
+      const int id = p < P.k ? ld_act_s32(P.idx + p) : -1;
+      r.slot0 = p;
+      r.cnt = p == P.k || (id >= 0 && id < P.E) ? 1 : 0;
+      r.e = p == P.k ? -1 : r.cnt ? id : 0;
+    } else {
+      r.e = ld_act_s32(P.table + 1 + 3 * p);
+      r.slot0 = ld_act_s32(P.table + 2 + 3 * p);
+      r.cnt = ld_act_s32(P.table + 3 + 3 * p);
+    }
+    return r;
+  };
   const long long total = problems * per_problem, G = gridDim.x, c = blockIdx.x;
   const long long q0 = c * total / G, q1 = (c + 1) * total / G;
   const int* tokens = P.table + 1 + 3 * P.P_max;
@@ -178,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     for (long long q = q0; q < q1 && ok;) {
       const Segment S(q, q1, per_problem);
       q += S.gb - S.ga;
-      const int e = GROUPED ? ld_act_s32(P.table + 1 + 3 * S.p) : 0;
+      const int e = problem(S.p).e;
       const CUtensorMap* m0 = e < 0 ? &ts0 : &tm0;
       const CUtensorMap* m1 = e < 0 ? &ts1 : &tm1;
       const int row = (e < 0 ? 0 : e) * P.R;  // at most 2^31 rows in a bank
@@ -238,15 +261,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
   for (long long q = q0; q < q1;) {
     const Segment S(q, q1, per_problem);
     q += S.gb - S.ga;
-    int slot0 = 0, cnt = P.rows;
-    if (GROUPED) {
-      slot0 = ld_act_s32(P.table + 2 + 3 * S.p);
-      cnt = ld_act_s32(P.table + 3 + 3 * S.p);
-    }
+    const Problem pr = problem(S.p);
+    const int slot0 = pr.slot0, cnt = pr.cnt, e = pr.e;
 
     // Weight scales of a warp's blocks in the BATCH stages from `ch` on of the group j: lane = matrix,
     // block of rows (16 rows lie in two at most), block.
-    const int e = GROUPED ? ld_act_s32(P.table + 1 + 3 * S.p) : 0;
     const float* sbase;
     {
       const Stream8Bank& B = e < 0 ? P.shared : P.bank;
@@ -261,11 +280,26 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
 
     // This problem's activation rows, zeros up to a whole block: all copies in flight at once.
     if (!named_bar_and(1, kWarps * 32, ok)) return;  // the previous segment is done with them
+    if (GROUPED && P.inner != nullptr) {
+      // a warp's lanes take four values each of a group of 128: its largest, its scale, 8 bits
+      for (int n = warp; n < cnt * KB; n += kWarps) {
+        const int j = n / KB, b = n - j * KB;
+        const float4 v = ld_act_f4(P.inner + (size_t)(slot0 + j) * P.K + b * 128 + lane * 4);
+        uint32_t most = 0;
+        for (float f : {v.x, v.y, v.z, v.w}) most = max(most, __float_as_uint(f) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+        const Scale8 sc = scale_e4m3(__uint_as_float(most));
+        *reinterpret_cast<uint32_t*>(xq + (size_t)j * xpitch + b * 128 + lane * 4) =
+            pack_e4m3x4(v.x * sc.up, v.y * sc.up, v.z * sc.up, v.w * sc.up);
+        if (lane == 0) xsc[b * COLS + j] = sc.scale;
+      }
+    } else
     for (int j = warp; j < COLS; j += kWarps) {
       const bool in = j < cnt;
-      const long long row = in && GROUPED && P.by_token ? ld_act_s32(tokens + slot0 + j) : slot0 + j;
+      const long long row = in && GROUPED && P.by_token && P.idx == nullptr ? ld_act_s32(tokens + slot0 + j) : slot0 + j;
       if (in) {
-        const uint8_t* src = P.x + row * P.ldx;
+        const uint8_t* src = P.x + (GROUPED && P.idx != nullptr ? 0 : row) * P.ldx;
         uint8_t* dst = xq + (size_t)j * xpitch;
         for (int k = lane * 16; k < xpitch - 64; k += 512) {
           if (k < P.K)
@@ -276,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
       }
       for (int b = lane; b < KB; b += 32) {
         if (in)
-          copy4(xsc + b * COLS + j, P.xs + row * P.ldxs + b);
+          copy4(xsc + b * COLS + j, P.xs + (GROUPED && P.idx != nullptr ? 0 : row) * P.ldxs + b);
         else
           xsc[b * COLS + j] = 0.f;
       }
@@ -485,16 +519,22 @@ __global__ void __launch_bounds__(1024) experts8_table_kernel(const int32_t* idx
 }
 
 // out[t] = bf16(sum_j w[t][j] y[slot(t, j)] (+ y[shared slot of t]) (+ res[t])), fp32 sums in that order.
-__global__ void __launch_bounds__(256) experts8_combine_kernel(const float* y, const int* entry, const float* w, int M,
-                                                               int k, bool shared, const uint16_t* res, uint16_t* out,
-                                                               int H) {
+__global__ void __launch_bounds__(256) experts8_combine_kernel(const float* y, const int* entry, const int32_t* idx,
+                                                               int E, const float* w, int M, int k, bool shared,
+                                                               const uint16_t* res, uint16_t* out, int H) {
   const int t = blockIdx.y, c = (blockIdx.x * 256 + threadIdx.x) * 4;
   pdl_trigger();
   pdl_wait();
   if (c >= H) return;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int j = 0; j < k; ++j) {
-    const int slot = ld_act_s32(entry + t * k + j);
+    int slot = j;  // one token: choice j's, if it has one
+    if (entry != nullptr) {
+      slot = ld_act_s32(entry + t * k + j);
+    } else {
+      const int id = ld_act_s32(idx + j);
+      if (id < 0 || id >= E) slot = -1;
+    }
     if (slot < 0) continue;
     const float wj = ld_act_f32(w + t * k + j);
     const float4 v = ld_act_f4(y + (size_t)slot * H + c);
@@ -630,7 +670,10 @@ cudaError_t launch_stream8_linear(dec_handle* h, const Linear8& L, cudaStream_t 
 
 Experts8Plan experts8_plan(int M, int k, int E, int H, int I, bool shared) {
   Experts8Plan p;
-  p.most = std::min(std::min(stream8_rows(H, true), stream8_rows(I, false)), M * k <= 8 ? 8 : 16);
+  // Problems of up to 16 rows where the experts have four tokens and more in the mean, else of 8,
+  // whose rows leave twice the room for weights in flight (64 tokens, 384 experts of 7168 x 256: S8_TODO).
+  const int want = M * k >= 4 * E ? 16 : 8;
+  p.most = std::min(std::min(stream8_rows(H, true), stream8_rows(I, false)), want);
   p.slots = M * k + M;
   const int most = std::max(p.most, 1);
   p.P_max = std::min(M * k, E + M * k / most) + (shared ? (M + most - 1) / most : 0);
@@ -638,29 +681,33 @@ Experts8Plan experts8_plan(int M, int k, int E, int H, int I, bool shared) {
   return p;
 }
 
-cudaError_t launch_experts8(dec_handle* h, const Experts8& X, const Experts8Plan& plan, int* table, float* inner,
-                            uint8_t* hq, float* hs, float* y, cudaStream_t s) {
+cudaError_t launch_experts8(dec_handle* h, const Experts8& X, const Experts8Plan& plan, int* table, float* inner, float* y,
+                            cudaStream_t s) {
   const int M = X.M, k = X.k, H = X.H, I = X.I;
   const bool shared = X.sgate.W[0] != nullptr;
-  const int xrows = std::min(plan.most, M * k);
   // experts that at least one of M k even choices falls on
   const double problems = X.E * (1.0 - std::pow(1.0 - 1.0 / X.E, M * k)) + (shared ? (M + plan.most - 1) / plan.most : 0);
+  const int xrows = std::min(plan.most, M * k);
   cudaError_t e;
-  {
+  Stream8Params P = {};
+  if (M == 1) {
+    P.idx = X.idx;
+    P.k = k;
+    P.E = X.E;
+  } else {
+    P.table = table;
+    P.P_max = plan.P_max;
     LaunchScope scope(h, "experts8_table", s);
     e = launch_k(h, experts8_table_kernel, dim3(1), dim3(1024), 0, s, X.idx, M, k, X.E, shared, plan.most, plan.P_max,
                  table);
     if (e != cudaSuccess) return e;
   }
-  Stream8Params P = {};
   P.x = X.x;
   P.ldx = X.ldx;
   P.xs = X.xs;
   P.ldxs = X.ldxs;
   P.bank = X.gate;
   P.shared = X.sgate;
-  P.table = table;
-  P.P_max = plan.P_max;
   P.by_token = true;
   P.R = I;
   P.K = H;
@@ -672,23 +719,7 @@ cudaError_t launch_experts8(dec_handle* h, const Experts8& X, const Experts8Plan
                        : launch_one<2, true, true>(h, P, xrows, problems, X.E, s);
     if (e != cudaSuccess) return e;
   }
-  {
-    QuantRows Q = {};
-    Q.x = inner;
-    Q.ldx = I;
-    Q.q = hq;
-    Q.ldq = I;
-    Q.scales = hs;
-    Q.ldsc = I / 128;
-    Q.H = I;
-    LaunchScope scope(h, "experts8_quant", s);
-    e = launch_norm_quant(h, Q, shared ? plan.slots : M * k, true, s);
-    if (e != cudaSuccess) return e;
-  }
-  P.x = hq;
-  P.ldx = I;
-  P.xs = hs;
-  P.ldxs = I / 128;
+  P.inner = inner;
   P.bank = X.down;
   P.shared = X.sdown;
   P.by_token = false;
@@ -704,7 +735,8 @@ cudaError_t launch_experts8(dec_handle* h, const Experts8& X, const Experts8Plan
   }
   LaunchScope scope(h, "experts8_combine", s);
   return launch_k(h, experts8_combine_kernel, dim3((H / 4 + 255) / 256, M), dim3(256), 0, s, (const float*)y,
-                  (const int*)(table + 1 + 3 * plan.P_max + plan.slots), X.w, M, k, shared, X.res, X.out, H);
+                  M == 1 ? (const int*)nullptr : (const int*)(table + 1 + 3 * plan.P_max + plan.slots), X.idx, X.E, X.w, M, k,
+                  shared, X.res, X.out, H);
 }
 
 }  // namespace dec
