@@ -12,9 +12,11 @@
 //
 // One CTA per SM. Whole tiles go round the CTAs as long as there is one for each, in panels
 // of 16 tiles of rows, so that the tiles in work at a time share rows and weights in L2. A
-// tile that is left over (any, for a decode batch) may be shared by up to four CTAs, a run of
-// k-blocks each; the one that publishes its piece last adds all pieces in k order (no atomics
-// on values; the results follow from the inputs and the shape alone).
+// tile that is left over (any, for a decode batch) may be shared by two to four CTAs, a run of
+// k-blocks each. Without whole rounds they are a cluster, and each finishes its part of the
+// columns from the pieces that the others put into its shared memory; else the one that
+// publishes its piece last adds all of them. Either way in k order, without atomics on values:
+// the results follow from the inputs and the shape alone.
 //
 // Per CTA: warp 0 issues the TMA loads of a k-block's rows and weights (128-byte
 // swizzle) into a ring in shared memory, warp 1 the tcgen05.mma (128 x BN x 32, kind
@@ -57,6 +59,7 @@ struct Plan {
 struct Gemm8Params {
   int M, N, K, KB, mtiles, ntiles;
   int split;     // CTAs that share a tile of those left after whole rounds
+  int cluster;   // they are a cluster (no whole rounds then): pieces go through its shared memory
   int box_rows;  // rows of a copy: a tile's, or the whole batch's up to eight
   const float* xs;
   long long ldxs;
@@ -106,6 +109,20 @@ __device__ __forceinline__ void tmem_here(uint32_t (&r)[16]) {
 }
 __device__ __forceinline__ void tmem_here(uint32_t (&r)[32]) {
   asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+
+// Another CTA's shared memory of the cluster, and the barrier of all its threads.
+__device__ __forceinline__ uint32_t peer_at(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void peer_store(uint32_t at, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // Moves registers between the warps that copy and multiply, which need few, and those that add.
@@ -294,6 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 4) {
     // ------------------------------------------------------------ sums
     regs_up<208>();
+    int syncs = P.cluster ? 2 : 0;  // barriers of the cluster that are still to come
     const int q = warp & 3, row = q * 32 + lane;  // tensor-memory lanes 32 q ..
     const int half = (warp - 4) >> 2, col0 = half * L::kCols;
     const int et = threadIdx.x - 128;
@@ -390,7 +408,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!named_bar_and(1, kAdders, ok)) break;  // leave together if a warp gave up
 
-      if (kb1 - kb0 < KB) {
+      int from = 0, to = L::kCols;  // this thread's columns that this CTA finishes
+      if (P.cluster) {
+        // Each CTA finishes an equal part of the columns: a thread's half of them, or (of four) a half of that. Its
+        // ring, empty once all have multiplied their last block, receives a piece of it from every CTA.
+        const int rank = (int)blockIdx.x % P.split, width = P.split == 2 ? L::kCols : L::kCols / 2;
+        cluster_sync();
+        --syncs;
+        if (rows_here) {
+#pragma unroll
+          for (int i = 0; i < L::kCols / 4; ++i) {
+            const int part = P.split == 4 && 4 * i >= L::kCols / 2 ? 1 : 0;
+            const int owner = P.split == 2 ? half : 2 * half + part, in = 4 * i - part * width;
+            const float2 lo = unpack2(acc[2 * i]), hi = unpack2(acc[2 * i + 1]);
+            peer_store(peer_at(smem_at + (uint32_t)(((rank * width + in) / 4 * kRows + row) * 16), owner),
+                       make_float4(lo.x, lo.y, hi.x, hi.y));
+          }
+        }
+        cluster_sync();
+        --syncs;
+        if (rank * 2 / P.split != half) continue;  // the other half of the columns
+        from = P.split == 2 ? 0 : (rank & 1) * width;
+        to = from + width;
+#pragma unroll
+        for (int i = 0; i < L::kCols / 2; ++i) acc[i] = 0;
+        if (rows_here)
+          for (int r = 0; r < P.split; ++r) {  // in k order
+            const float4* src = reinterpret_cast<const float4*>(smem) + (r * width - from) / 4 * kRows + row;
+#pragma unroll
+            for (int i = 0; i < L::kCols / 4; ++i)
+              if (4 * i >= from && 4 * i < to) {
+                const float4 v = src[i * kRows];
+                const float2 lo = unpack2(acc[2 * i]), hi = unpack2(acc[2 * i + 1]);
+                acc[2 * i] = pack2(lo.x + v.x, lo.y + v.y);
+                acc[2 * i + 1] = pack2(hi.x + v.z, hi.y + v.w);
+              }
+          }
+      } else if (kb1 - kb0 < KB) {
         // A piece: published, four columns of a row at a time; whoever publishes the last adds them all in k order.
         const int p_rows = P.piece_rows, shared = (int)blockIdx.x / P.split;
         auto piece = [&](int cc) {
@@ -443,6 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const int left = P.N - n - 8 * i;  // columns from here on
           if (left <= 0) break;
+          if (8 * i < from || 8 * i >= to) continue;
           if (res != nullptr) {
             if (res_vec && left >= 8) {
               const uint4 r = ld_act16(res + 8 * i);
@@ -466,6 +521,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    for (; syncs > 0; --syncs) cluster_sync();
+  }
+  if (P.cluster && warp < 4) {
+    cluster_sync();
+    cluster_sync();
   }
 
   tc_fence_before();
@@ -480,13 +540,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Weights a tile, and CTAs to a left-over tile: by the time of the longest CTA, in clocks. A
 // k-block of a tile takes 520 + 2.5 BN (measured at 4096 x 12288 x 7168, BN 32 to 256: 609, 636,
 // 757, 750, 1030, 1170), a tile's output some 1500 and the exchange of a shared tile's pieces
-// 10000 to 20000; the weights' bytes pass at 23 a clock and SM at most.
+// 10000 to 20000 through L2, half of that in a cluster; the weights' bytes pass at 23 a clock and SM at most.
 struct Choice {
   int bn, grid, split;
+  bool cluster;
 };
 static Choice choose(const dec_handle* h, int M, int N, int K) {
   const long long mt = (M + kRows - 1) / kRows, KB = (K + kBlock - 1) / kBlock;
-  Choice best = {256, 1, 1};
+  Choice best = {256, 1, 1, false};
   double least = 1e300;
   for (int bn : {32, 64, 96, 128, 192, 256}) {
     const long long tiles = mt * ((N + bn - 1) / bn);
@@ -495,10 +556,12 @@ static Choice choose(const dec_handle* h, int M, int N, int K) {
     for (int split = 1; split <= 4; ++split) {
       const long long rounds = tiles / h->sms, left = tiles - rounds * h->sms;
       if (split > 1 && (left * split > h->sms || KB / split < 4)) continue;
+      // clusters: as many as the parts of the chip hold for sure
+      if (rounds == 0 && split > 1 && (split == 3 || left * split > (split == 2 ? 144 : 128))) continue;
       const double blocks = (double)(rounds * KB) + (left ? (double)((KB + split - 1) / split) : 0.0);
-      const double exchange = left && split > 1 ? 10000 + 3000.0 * split : 0;
+      const double exchange = left == 0 || split == 1 ? 0 : rounds == 0 ? 4000 + 800.0 * split : 10000 + 3000.0 * split;
       const double t = std::max(blocks * block + (rounds + (left > 0)) * 1500.0, memory) + exchange;
-      if (t < least) least = t, best = {bn, (int)(rounds ? h->sms : left * split), split};
+      if (t < least) least = t, best = {bn, (int)(rounds ? h->sms : left * split), split, rounds == 0 && split > 1};
     }
   }
   return best;
@@ -509,7 +572,7 @@ static size_t counter_bytes(const dec_handle* h) { return ((size_t)h->sms * 4 + 
 
 size_t gemm8_ws_bytes(const dec_handle* h, int M, int N, int K) {
   const Choice c = choose(h, M, N, K);
-  return counter_bytes(h) + (c.split > 1 ? (size_t)c.grid * c.bn * piece_rows(M) * 4 : 0);
+  return counter_bytes(h) + (c.split > 1 && !c.cluster ? (size_t)c.grid * c.bn * piece_rows(M) * 4 : 0);
 }
 
 static bool encode_tile(const dec_handle* h, CUtensorMap* m, const uint8_t* p, int K, int rows, long long ld, int box_rows) {
@@ -544,6 +607,7 @@ static cudaError_t launch_bn(dec_handle* h, const Linear8& A, const Choice& c, v
   P.ntiles = (A.N + BN - 1) / BN;
   P.box_rows = box_rows;
   P.split = c.split;
+  P.cluster = c.cluster ? 1 : 0;
   P.xs = A.xs;
   P.ldxs = A.ldxs;
   P.ws = A.ws;
@@ -556,8 +620,20 @@ static cudaError_t launch_bn(dec_handle* h, const Linear8& A, const Choice& c, v
   P.piece_rows = piece_rows(A.M);
   P.err = h->d_err;
   P.wait_ns = h->wait_ns;
-  return launch_k(h, gemm8_kernel<BN>, dim3(c.grid), dim3(kThreads), (size_t)L::kBytes, s, tx, tw,
-                  P);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(c.grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = L::kBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = h->pdl ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = c.cluster ? c.split : 1;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, gemm8_kernel<BN>, tx, tw, P);
 }
 
 cudaError_t launch_gemm8(dec_handle* h, const Linear8& A, void* ws, cudaStream_t s) {
