@@ -295,6 +295,7 @@ class Handle:
 
     def set_force_variant(self, v: int) -> None:
         _check(_load().dec_set_force_variant(self._h, int(v)), "dec_set_force_variant")
+        self._fp8_ws.clear()  # dec_linear_fp8's workspace goes by the kernel family
 
     def set_shared_sms(self, n: int) -> None:
         """0: automatic SM share by expected bytes; -1: every SM, overlapped; n > 0: a fixed n-SM partition."""

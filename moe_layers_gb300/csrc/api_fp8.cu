@@ -34,8 +34,13 @@ bool linear_shape_ok(int M, int N, int K) {
   return M >= 1 && M <= kMaxRows && N >= 1 && N <= kMaxRows && K >= 16 && K <= kMaxWidth && K % 16 == 0;
 }
 
-// The streaming kernel up to 16 rows that fit in its shared memory, the tcgen05 kernel otherwise.
-bool linear_streams(int M, int K) { return M <= stream8_rows(K, false); }
+// The streaming kernel up to 8 rows, and up to 16 with weights of at most 64 MB, where the tcgen05 kernel's
+// ramp counts (16 rows, streaming / tcgen05: 4096 x 4096 8.5 / 9.1 us, 7168 x 8192 18.4 / 18.4, 12288 x 7168
+// 25.2 / 21.2; 8 rows: 7.0 / 9.0, 13.3 / 18.4, 18.8 / 21.2); as forced where its shared memory holds the rows.
+bool linear_streams(const dec_handle* h, int M, int N, int K) {
+  if (h->force_variant == DEC_VARIANT_SPLIT_K || M > stream8_rows(K, false)) return false;
+  return h->force_variant == DEC_VARIANT_SMALL_M || M <= 8 || (int64_t)N * K <= (int64_t)64 << 20;
+}
 
 bool experts_shape_ok(const dec_moe_fp8_weights* W, int M, int k) {
   return W != nullptr && M >= 1 && M <= kMaxExpertRows && k >= 1 && k <= kMaxChoices && W->E >= 1 &&
@@ -96,7 +101,7 @@ dec_status dec_quant_weight(dec_handle* h, const dec_bf16* W, int64_t N, int K, 
 
 dec_status dec_linear_fp8_workspace_size(const dec_handle* h, int M, int N, int K, size_t* bytes) {
   if (h == nullptr || bytes == nullptr || !linear_shape_ok(M, N, K)) return DEC_ERR_INVALID_ARG;
-  *bytes = linear_streams(M, K) ? 0 : gemm8_ws_bytes(h, M, N, K);
+  *bytes = linear_streams(h, M, N, K) ? 0 : gemm8_ws_bytes(h, M, N, K);
   return DEC_OK;
 }
 
@@ -107,12 +112,13 @@ dec_status dec_linear_fp8(dec_handle* h, const dec_fp8_rows* x, const dec_fp8_we
   if (!rows_ok(x, K) || !weight_ok(*W) || !al(y, 2) || ldy < N || ldy > kMaxStride) return DEC_ERR_INVALID_ARG;
   if (residual != nullptr && (!al(residual, 2) || ldr < N || ldr > kMaxStride || (residual == y && ldr != ldy)))
     return DEC_ERR_INVALID_ARG;
-  const bool stream8 = linear_streams(M, K);
+  const bool stream8 = linear_streams(h, M, N, K);
   const size_t need = stream8 ? 0 : gemm8_ws_bytes(h, M, N, K);
   if (need > 0 && (ws == nullptr || !al(ws, 16) || ws_bytes < need)) return DEC_ERR_INVALID_ARG;
   DeviceGuard dev(h->device);
   if (!dev.ok) return DEC_ERR_CUDA;
   const Linear8 L = {x->q, x->ldq, x->scales, x->lds, W->q, W->scales, residual, ldr, y, ldy, M, N, K};
+  h->last_variant = stream8 ? DEC_VARIANT_SMALL_M : DEC_VARIANT_SPLIT_K;
   LaunchScope scope(h, "linear_fp8", stream);
   return status(stream8 ? launch_stream8_linear(h, L, stream) : launch_gemm8(h, L, ws, stream));
 }

@@ -145,6 +145,22 @@ def test_linear(ml, h, m, n, k, residual):
     assert torch.equal(bits(y), bits(again))
 
 
+@pytest.mark.parametrize("family", [1, 2])
+@pytest.mark.parametrize("m,n,k", [(1, 300, 1040), (5, 4096, 4096), (8, 640, 16384), (9, 1000, 2064), (16, 7168, 1024),
+                                   (16, 12288, 7168), (13, 130, 144)])
+def test_linear_kernel_families(ml, h, family, m, n, k):
+    g = gen(m)
+    x, w = rand_rows(g, m, k), rand_weight(g, n, k)
+    r = torch.randn(m, n, generator=g, device="cuda").bfloat16()
+    h.set_force_variant(family)
+    try:
+        y = ml.dec_linear_fp8(h, ml.Fp8Rows(*x), ml.Fp8Weight(*w), residual=r)
+        assert h.last_variant == (2 if k * m > 200_000 else family)
+    finally:
+        h.set_force_variant(0)
+    assert_within(y, *linear64(*x, *w, r))
+
+
 @pytest.mark.parametrize("m", [5, 40, 150])
 def test_linear_in_place_and_strided(ml, h, m):
     g = gen(m)
