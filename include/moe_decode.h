@@ -120,11 +120,12 @@ dec_status dec_set_shared_sms(dec_handle* h, int sms);
 dec_status dec_set_l2_ahead(dec_handle* h, int bytes);
 
 /* Force a projection kernel family (DEC_VARIANT_AUTO restores the choice by
- * batch) so that tests can run both families at the same batch. */
+ * batch) so that tests can run both families at the same batch. It holds for
+ * dec_linear, dec_linear_residual and dec_linear_fp8. */
 dec_status dec_set_force_variant(dec_handle* h, int variant);
 
-/* Variant used by the most recent dec_linear / dec_linear_residual call on
- * this handle (a dec_variant value; 0 before any call). */
+/* Variant used by the most recent dec_linear / dec_linear_residual /
+ * dec_linear_fp8 call on this handle (a dec_variant value; 0 before any call). */
 int dec_last_variant(const dec_handle* h);
 
 /* Kernel family of the most recent expert launches (moe_experts,
@@ -581,6 +582,12 @@ dec_status dec_linear_fp8_workspace_size(const dec_handle* h, int M, int N, int 
  * scaled and added to the total in fp32, and y is rounded once. y and residual
  * have row strides ldy, ldr >= N in elements (any, 2-byte aligned); y may be
  * residual itself with the same stride and overlaps nothing else.
+ * Kernel families as for dec_linear: SMALL_M streams the weights past the rows
+ * (M <= 16), SPLIT_K is the tcgen05 kernel; AUTO takes the first up to M = 8, and
+ * up to 16 for weights of at most 64 MB. Weights may be read before the launch's
+ * dependency wait, as static data; dec_quant_weight just before is safe.
+ * The workspace (none for SMALL_M) is zeroed before its first use and then serves
+ * calls of any shape, one at a time; its size depends on the forced family.
  * 1 <= M <= 2^20 (prompts too), 1 <= N <= 2^20, K a multiple of 16 in
  * [16, 65536]. */
 dec_status dec_linear_fp8(dec_handle* h, const dec_fp8_rows* x, const dec_fp8_weight* W, const dec_bf16* residual,
@@ -608,8 +615,9 @@ dec_status moe_experts_fp8_workspace_size(const dec_handle* h, const dec_moe_fp8
  * dec_rmsnorm_quant does. Everything else is fp32 until out is rounded to bf16.
  * x [M][H]; idx int32 [M][k] and w fp32 [M][k] as from moe_route_topk; an entry
  * whose id is outside [0, E) is left out. residual bf16 [M][H] or NULL; out bf16
- * [M][H], which may be residual itself and overlaps nothing else. The workspace
- * needs no particular contents. 1 <= M <= 64, 1 <= k <= 16, H and I up to 16384
+ * [M][H], which may be residual itself and overlaps nothing else. Each problem
+ * (an expert with up to 8 or 16 of its tokens) streams the expert's weights once.
+ * The workspace needs no particular contents. 1 <= M <= 64, 1 <= k <= 16, H and I up to 16384
  * (else DEC_ERR_UNSUPPORTED). */
 dec_status moe_experts_fp8(dec_handle* h, const dec_fp8_rows* x, const int32_t* idx, const float* w, int M, int k,
                            const dec_moe_fp8_weights* Wt, const dec_bf16* residual, dec_bf16* out, void* ws,

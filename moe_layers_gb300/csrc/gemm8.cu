@@ -541,6 +541,35 @@ __global__ void __launch_bounds__(kThreads, 1)
 // k-block of a tile takes 520 + 2.5 BN (measured at 4096 x 12288 x 7168, BN 32 to 256: 609, 636,
 // 757, 750, 1030, 1170), a tile's output some 1500 and the exchange of a shared tile's pieces
 // 10000 to 20000 through L2, half of that in a cluster; the weights' bytes pass at 23 a clock and SM at most.
+// How many clusters of 2 or 4 CTAs, one CTA to an SM, this device holds at a time: the parts of the chip have
+// different numbers of SMs, and not the same ones on every chip. (None if the runtime does not say.)
+static int clusters_held(const dec_handle* h, int size) {
+  static int held[16][5];  // by device; 0: not asked yet, -1: none
+  if (h->device < 0 || h->device >= 16) return 0;
+  int& n = held[h->device][size];
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(size);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Plan<256>::kBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    DeviceGuard dev(h->device);
+    int got = 0;
+    const bool ok = dev.ok &&
+                    cudaFuncSetAttribute(gemm8_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Plan<256>::kBytes) == cudaSuccess &&
+                    cudaOccupancyMaxActiveClusters(&got, gemm8_kernel<256>, &cfg) == cudaSuccess;
+    if (!ok) cudaGetLastError();  // the answer is no; nothing else failed
+    n = ok && got > 0 ? got : -1;
+  }
+  return std::max(n, 0);
+}
+
 struct Choice {
   int bn, grid, split;
   bool cluster;
@@ -556,8 +585,7 @@ static Choice choose(const dec_handle* h, int M, int N, int K) {
     for (int split = 1; split <= 4; ++split) {
       const long long rounds = tiles / h->sms, left = tiles - rounds * h->sms;
       if (split > 1 && (left * split > h->sms || KB / split < 4)) continue;
-      // clusters: as many as the parts of the chip hold for sure
-      if (rounds == 0 && split > 1 && (split == 3 || left * split > (split == 2 ? 144 : 128))) continue;
+      if (rounds == 0 && split > 1 && (split == 3 || left > clusters_held(h, split))) continue;
       const double blocks = (double)(rounds * KB) + (left ? (double)((KB + split - 1) / split) : 0.0);
       const double exchange = left == 0 || split == 1 ? 0 : rounds == 0 ? 4000 + 800.0 * split : 10000 + 3000.0 * split;
       const double t = std::max(blocks * block + (rounds + (left > 0)) * 1500.0, memory) + exchange;

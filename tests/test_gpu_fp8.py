@@ -129,7 +129,8 @@ def test_weights(ml, h, shape):
 # ---------------------------------------------------------------------------- linear
 LINEARS = [(1, 128, 128), (1, 1, 16), (2, 17, 144), (3, 1000, 2064), (8, 304, 7168), (9, 129, 512), (16, 12288, 256),
            (15, 500, 4096), (17, 640, 384), (33, 77, 1040), (64, 1536, 7168), (65, 256, 128), (128, 130, 640),
-           (200, 1000, 2064), (333, 129, 272), (1, 12288, 7168), (4, 4096, 4096), (1, 40, 65536), (5, 33, 30000)]
+           (200, 1000, 2064), (333, 129, 272), (1, 12288, 7168), (4, 4096, 4096), (1, 40, 65536), (5, 33, 30000), (40, 100, 16384), (17, 64, 65536),
+           (130, 128, 8192), (64, 2048, 8208), (100, 4096, 1024)]
 
 
 @pytest.mark.parametrize("m,n,k", LINEARS)
