@@ -18,6 +18,11 @@
 // publishes its piece last adds all of them. Either way in k order, without atomics on values:
 // the results follow from the inputs and the shape alone.
 //
+// Measured, in a replayed graph: 12288 x 7168 at 4096 rows 390 us (1.85 PFLOP/s), 64 rows 22.0
+// us (0.61 of the copy rate), 64 x 4096 x 4096 9.6 us. Bound, at many rows, by the adding warps: a
+// k-block of 128 x 256 is multiplied in some 540 clocks (the same without them) and takes 1170; at
+// few rows by the 600 clocks a k-block that pass between product, fetch and next product.
+//
 // Per CTA: warp 0 issues the TMA loads of a k-block's rows and weights (128-byte
 // swizzle) into a ring in shared memory, warp 1 the tcgen05.mma (128 x BN x 32, kind
 // f8f6f4), warps 4-11 fetch, scale and add.

@@ -5,17 +5,17 @@
 //
 // over blocks b of 128 values. Every weight byte is used for a few rows only, so
 // the kernel is a stream of weights. The products are mma.sync's (16 weight rows x
-// 8 activation rows x 32 values; measured 1.3 clocks a warp instruction and SM,
-// which is 30 times what the stream needs at 8 rows): a block's fp32 sum lies in
+// 8 activation rows x 32 values; measured 1.2 clocks an instruction and SM, a
+// seventeenth of the stream's time at 8 rows): a block's fp32 sum lies in
 // registers, where it is scaled and added to the total, while tcgen05's would have
 // to be fetched from tensor memory for every block of 128.
 //
 // One thread copies weights by TMA into a ring in shared memory, a stage with one copy
-// (of each matrix): groups of h <= 16 rows x blocks of 128 bytes, eight in all, of which
-// each of eight warps multiplies one. (A copy costs its thread about 150 clocks whatever
-// its size, and a stage has 700 at the memory's rate: eight copies of 2 KB streamed at 0.25
-// of the copy rate. Loads from global memory straight into the products' registers, which
-// touch 64 bytes of 8 rows an instruction, streamed at 0.6.) A lane reads 16 bytes of a
+// (of each matrix): groups of h <= 16 rows x blocks of 128 bytes, of
+// which each of eight warps multiplies one (two of a single matrix). Large copies: with eight
+// of 2 KB to a stage the weights streamed at 0.25 of the copy rate, and loads from global memory
+// straight into the products' registers, which touch 64 bytes of 8 rows an instruction, at 0.6.
+// A lane reads 16 bytes of a
 // row for two products, both operands in the same permuted order, which a sum does not
 // mind. The boxes have the 128-byte swizzle; product row g is group row g / 2 + 4 (g % 2),
 // so that the two rows that are read at once lie in different halves of the banks.
@@ -24,10 +24,16 @@
 // alone.
 //
 // Work: a problem is R weight rows for up to 8 NT activation rows, cut into groups of h
-// rows; all problems' groups form one sequence, cut into one equal range per CTA (one
-// CTA per SM). h is chosen so that the largest range holds few rows beyond the mean. The
-// groups of a CTA's range that belong to one problem are a segment. The ring runs on from
-// one segment into the next, while the activation rows change.
+// rows; all problems' groups form one sequence, cut into one equal range per CTA. h is
+// chosen so that the largest range holds few rows beyond the mean. Two CTAs to an SM where
+// their rings fit (one or two rows of 7168): the next launch's then fill their rings beside
+// the last of this one's. The groups of a CTA's range that belong to one problem are a
+// segment. The ring runs on from one segment into the next, while the activation rows change.
+//
+// Measured, in a replayed graph, of the copy rate of 6.7 TB/s: 12288 x 7168 at one row 15.8 us
+// (0.83), at eight 18.7 (0.71: one CTA to an SM); 64 tokens of 384 experts of 7168 x 256 263 us
+// (0.89), 8 tokens of 32 experts of 7168 x 2048 248 (0.80). Bound by memory, and by 3 us a launch
+// of ramp and last sums.
 #include <algorithm>
 #include <cmath>
 
@@ -671,7 +677,8 @@ cudaError_t launch_stream8_linear(dec_handle* h, const Linear8& L, cudaStream_t 
 Experts8Plan experts8_plan(int M, int k, int E, int H, int I, bool shared) {
   Experts8Plan p;
   // Problems of up to 16 rows where the experts have four tokens and more in the mean, else of 8,
-  // whose rows leave twice the room for weights in flight (64 tokens, 384 experts of 7168 x 256: S8_TODO).
+  // whose rows leave twice the room for weights in flight (64 tokens, 384 experts of 7168 x 256: 263 us, with 16 rows 350; 64 tokens that
+  // all choose the same 8 experts of 7168 x 2048 read each expert four times with 16: 443 us).
   const int want = M * k >= 4 * E ? 16 : 8;
   p.most = std::min(std::min(stream8_rows(H, true), stream8_rows(I, false)), want);
   p.slots = M * k + M;
