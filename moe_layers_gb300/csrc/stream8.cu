@@ -89,6 +89,7 @@ struct Stream8Params {
   int P_max;
   const int32_t* idx;        // or, for one token: its k choices are the problems, and the shared expert
   int k, E;
+  bool first;     // of the experts' two products (gate and up)
   bool by_token;  // activation rows by the slot's token, else by the slot
   int R, K, KB, rows;
   int height;      // rows of a group
@@ -152,7 +153,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
   uint64_t* sempty = sfull + kSums * kWarps;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sempty + kSums * kWarps);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_trigger();
+  // The experts' first product lets its dependent start only after its own dependency wait: when the
+  // second one starts, the routing is complete, and it reads that and streams weights before it waits.
+  if (!P.first) pdl_trigger();
   if (threadIdx.x == 0) {
     for (int i = 0; i < P.stages; ++i) {
       mbar_init(&full[i], 1);
@@ -170,7 +173,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
 
   long long problems = 1;
   if (GROUPED) {
-    pdl_wait();
+    if (P.first) {
+      pdl_wait();
+      pdl_trigger();
+    }
     problems = P.idx != nullptr ? P.k + (P.shared.W[0] != nullptr ? 1 : 0) : ld_act_s32(P.table);
   }
   // Problem p: expert (-1: the shared one), first slot and rows (none for an id outside [0, E)).
@@ -259,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     x_at[nt] = smem_u32(xq) + (uint32_t)min(nt * 8 + g, P.xrows - 1) * xpitch + t * 16;
     xsc_at[nt] = smem_u32(xsc) + (nt * 8 + 2 * t) * 4;
   }
-  if (!GROUPED) pdl_wait();
+  if (!GROUPED || !P.first) pdl_wait();
   int s = 0;           // the ring's next stage
   uint32_t sph = 0;    // and how often the ring has gone round, mod 2
   uint32_t turns = 0;  // groups whose sums this warp's group has left so far
@@ -716,6 +722,7 @@ cudaError_t launch_experts8(dec_handle* h, const Experts8& X, const Experts8Plan
   P.bank = X.gate;
   P.shared = X.sgate;
   P.by_token = true;
+  P.first = true;
   P.R = I;
   P.K = H;
   P.out = inner;
@@ -730,6 +737,7 @@ cudaError_t launch_experts8(dec_handle* h, const Experts8& X, const Experts8Plan
   P.bank = X.down;
   P.shared = X.sdown;
   P.by_token = false;
+  P.first = false;
   P.R = H;
   P.K = I;
   P.out = y;
