@@ -531,26 +531,38 @@ __global__ void __launch_bounds__(1024) experts8_table_kernel(const int32_t* idx
 }
 
 // out[t] = bf16(sum_j w[t][j] y[slot(t, j)] (+ y[shared slot of t]) (+ res[t])), fp32 sums in that order.
-__global__ void __launch_bounds__(256) experts8_combine_kernel(const float* y, const int* entry, const int32_t* idx,
+__global__ void __launch_bounds__(128) experts8_combine_kernel(const float* y, const int* entry, const int32_t* idx,
                                                                int E, const float* w, int M, int k, bool shared,
                                                                const uint16_t* res, uint16_t* out, int H) {
-  const int t = blockIdx.y, c = (blockIdx.x * 256 + threadIdx.x) * 4;
+  const int t = blockIdx.y, c = (blockIdx.x * 128 + threadIdx.x) * 4;
   pdl_trigger();
   pdl_wait();
   if (c >= H) return;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j = 0; j < k; ++j) {
-    int slot = j;  // one token: choice j's, if it has one
-    if (entry != nullptr) {
-      slot = ld_act_s32(entry + t * k + j);
-    } else {
-      const int id = ld_act_s32(idx + j);
-      if (id < 0 || id >= E) slot = -1;
+  // Eight choices at a time: their slots and weights, then their values, all loads in flight before any is used.
+  for (int j0 = 0; j0 < k; j0 += 8) {
+    int slot[8];
+    float wj[8];
+    float4 v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int j = min(j0 + u, k - 1);
+      slot[u] = ld_act_s32(entry != nullptr ? entry + t * k + j : idx + j);
+      wj[u] = ld_act_f32(w + t * k + j);
     }
-    if (slot < 0) continue;
-    const float wj = ld_act_f32(w + t * k + j);
-    const float4 v = ld_act_f4(y + (size_t)slot * H + c);
-    a.x = fmaf(wj, v.x, a.x), a.y = fmaf(wj, v.y, a.y), a.z = fmaf(wj, v.z, a.z), a.w = fmaf(wj, v.w, a.w);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int j = min(j0 + u, k - 1);
+      // one token: choice j's slot is j, if its id is one
+      if (entry == nullptr) slot[u] = slot[u] >= 0 && slot[u] < E ? j : -1;
+      v[u] = ld_act_f4(y + (size_t)max(slot[u], 0) * H + c);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (j0 + u < k && slot[u] >= 0) {
+        a.x = fmaf(wj[u], v[u].x, a.x), a.y = fmaf(wj[u], v[u].y, a.y);
+        a.z = fmaf(wj[u], v[u].z, a.z), a.w = fmaf(wj[u], v[u].w, a.w);
+      }
   }
   if (shared) {
     const float4 v = ld_act_f4(y + (size_t)(M * k + t) * H + c);
@@ -749,7 +761,7 @@ cudaError_t launch_experts8(dec_handle* h, const Experts8& X, const Experts8Plan
     if (e != cudaSuccess) return e;
   }
   LaunchScope scope(h, "experts8_combine", s);
-  return launch_k(h, experts8_combine_kernel, dim3((H / 4 + 255) / 256, M), dim3(256), 0, s, (const float*)y,
+  return launch_k(h, experts8_combine_kernel, dim3((H / 4 + 127) / 128, M), dim3(128), 0, s, (const float*)y,
                   M == 1 ? (const int*)nullptr : (const int*)(table + 1 + 3 * plan.P_max + plan.slots), X.idx, X.E, X.w, M, k,
                   shared, X.res, X.out, H);
 }
