@@ -51,7 +51,7 @@ struct Plan {
   static constexpr int kCols = BN / 2;                            // a thread's
   static constexpr int kFetch = kCols % 32 == 0 ? 32 : 16;        // columns of one instruction
   // Columns fetched before any is added. (More at once would take registers that are not there:
-  // 64 of 128 columns spill, and 4096 rows take 506 us instead of 379.)
+  // 64 of 128 columns spill, and 4096 rows take 506 us instead of 398.)
   static constexpr int kAtOnce = kCols <= 48 ? kCols : 32;
   static_assert(kCols % kAtOnce == 0 && kAtOnce % kFetch == 0, "whole instructions");
   static constexpr bool kStraddle = 128 % kCols != 0;             // they may lie in two blocks of weights
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&tempty[b]);
               }
               // Always so: behind a branch the additions stay together, before the next fetch. Mixed with
-              // it they spill registers, and 4096 rows take 475 us instead of 380.
+              // it they spill registers, and 4096 rows take 475 us instead of 398.
               if (here > 0) {
 #pragma unroll
                 for (int p = 0; p < L::kAtOnce / L::kFetch; ++p)
