@@ -146,6 +146,15 @@ def test_linear(ml, h, m, n, k, residual):
     assert torch.equal(bits(y), bits(again))
 
 
+@pytest.mark.parametrize("m,n,k", [(20, 1, 16), (300, 5, 16), (1 << 20, 8, 16), (1, 1 << 20, 16), (70, 1 << 20, 16),
+                                   (16, 300, 65536), (2, 3, 65536), (129, 257, 65536)])
+def test_linear_at_its_limits(ml, h, m, n, k):
+    g = gen(m + n)
+    x, w = rand_rows(g, m, k), rand_weight(g, n, k)
+    y = ml.dec_linear_fp8(h, ml.Fp8Rows(*x), ml.Fp8Weight(*w))
+    assert_within(y, *linear64(*x, *w))
+
+
 @pytest.mark.parametrize("family", [1, 2])
 @pytest.mark.parametrize("m,n,k", [(1, 300, 1040), (5, 4096, 4096), (8, 640, 16384), (9, 1000, 2064), (16, 7168, 1024),
                                    (16, 12288, 7168), (13, 130, 144)])
@@ -233,6 +242,17 @@ def test_experts(ml, h, m, e, k, hidden, inner, shared):
     assert torch.equal(bits(out), bits(again))
     bare = ml.moe_experts_fp8(h, ml.Fp8Rows(*x), idx, w, W)
     assert_within(bare, *experts64(*x, idx, w, *banks, one))
+
+
+@pytest.mark.parametrize("m,e,k,hidden,inner", [(1, 2, 2, 16384, 128), (5, 2, 1, 128, 16384), (64, 1024, 16, 256, 128),
+                                                (3, 4, 2, 16384, 256), (1, 1, 1, 128, 128)])
+def test_experts_at_their_limits(ml, h, m, e, k, hidden, inner):
+    g = gen(m + e)
+    banks, one, W = expert_weights(ml, g, e, hidden, inner, True)
+    x = rand_rows(g, m, hidden)
+    idx, w = choices(g, m, e, k)
+    out = ml.moe_experts_fp8(h, ml.Fp8Rows(*x), idx, w, W)
+    assert_within(out, *experts64(*x, idx, w, *banks, one))
 
 
 @pytest.mark.parametrize("m,k", [(1, 4), (6, 4), (64, 3)])
