@@ -31,8 +31,8 @@
 // segment. The ring runs on from one segment into the next, while the activation rows change.
 //
 // Measured, in a replayed graph, of the copy rate of 6.7 TB/s: 12288 x 7168 at one row 15.8 us
-// (0.83), at eight 18.7 (0.71: one CTA to an SM); 64 tokens of 384 experts of 7168 x 256 260 us
-// (0.9), 8 tokens of 32 experts of 7168 x 2048 246 (0.8). Bound by memory, and by 3 us a launch
+// (0.83), at eight 18.7 (0.71: one CTA to an SM); 64 tokens of 384 experts of 7168 x 256 254 us
+// (0.91), 8 tokens of 32 experts of 7168 x 2048 221 (0.88). Bound by memory, and by 3 us a launch
 // of ramp and last sums.
 #include <algorithm>
 #include <cmath>
@@ -630,6 +630,10 @@ template <int NT, bool PAIR, bool GROUPED>
 static cudaError_t launch_one(dec_handle* h, Stream8Params P, int xrows, double problems, int E, cudaStream_t s) {
   P.KB = (P.K + 127) / 128;
   P.WK = warps_along(P.KB, PAIR ? 2 : 1);
+  // The experts' second product has rows enough for several groups a stage: fewer warps along a group, so
+  // that its sums are joined every four stages at most (8 tokens of 32 experts of 7168 x 2048: 244 -> 221 us).
+  if (GROUPED && !PAIR)
+    while (P.WK > 1 && P.KB < 4 * P.WK * blocks_each(1)) P.WK /= 2;
   P.xrows = xrows;
   // Two CTAs to an SM where each has a ring of three stages: the next launch's CTAs then start, and
   // fill their rings, beside the last of this one's.
@@ -696,7 +700,7 @@ Experts8Plan experts8_plan(int M, int k, int E, int H, int I, bool shared) {
   Experts8Plan p;
   // Problems of up to 16 rows where the experts have four tokens and more in the mean, else of 8,
   // whose rows leave twice the room for weights in flight (64 tokens, 384 experts of 7168 x 256: 260 us, with 16 rows 350; 64 tokens that
-  // all choose the same 8 experts of 7168 x 2048 read each expert four times with 16: 443 us).
+  // all choose the same 8 experts of 7168 x 2048 read each expert four times with 16: 395 us).
   const int want = M * k >= 4 * E ? 16 : 8;
   p.most = std::min(std::min(stream8_rows(H, true), stream8_rows(I, false)), want);
   p.slots = M * k + M;
