@@ -411,7 +411,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (++b == L::kBuffers) b = 0, tph ^= 1u;
         }
       }
-      if (!named_bar_and(1, kAdders, ok)) break;  // leave together if a warp gave up
+      if (!named_bar_and(1, kAdders, ok)) {  // leave together if a warp gave up
+        // This call's result is lost, and the error word says so. The CTA takes its turn at its shared tile's counter
+        // all the same (a piece is its last work): the counters are zero after every call.
+        if (!P.cluster && P.split > 1 && et == 0 && (int)blockIdx.x < work.left * P.split) {
+          int* counter = P.counters + (int)blockIdx.x / P.split;
+          if (atom_add_acq_rel_gpu(counter, 1) == P.split - 1) *counter = 0;
+        }
+        break;
+      }
 
       int from = 0, to = L::kCols;  // this thread's columns that this CTA finishes
       if (P.cluster) {
