@@ -246,7 +246,9 @@ __device__ __forceinline__ float sigmoid_f(float z) { return 1.0f / (1.0f + expf
 // ---------------------------------------------------------------- PDL
 // Programmatic dependent launch: a kernel may start while its predecessor on
 // the stream drains. Everything before pdl_wait() may touch only memory that
-// no earlier kernel writes (static weights, shared memory, tensor memory).
+// no earlier kernel writes (static weights, shared memory, tensor memory), or
+// that a kernel two launches back wrote, read past L1 (.cg), where the kernel
+// between waits for that one before it triggers this one.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

@@ -154,7 +154,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sempty + kSums * kWarps);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // The experts' first product lets its dependent start only after its own dependency wait: when the
-  // second one starts, the routing is complete, and it reads that and streams weights before it waits.
+  // second one starts, the routing is complete, and it reads that and streams weights before it waits
+  // (past L1, which may hold what lay at the same addresses for an earlier call).
   if (!P.first) pdl_trigger();
   if (threadIdx.x == 0) {
     for (int i = 0; i < P.stages; ++i) {
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
       pdl_wait();
       pdl_trigger();
     }
-    problems = P.idx != nullptr ? P.k + (P.shared.W[0] != nullptr ? 1 : 0) : ld_act_s32(P.table);
+    problems = P.idx != nullptr ? P.k + (P.shared.W[0] != nullptr ? 1 : 0) : ld_cg_s32(P.table);
   }
   // Problem p: expert (-1: the shared one), first slot and rows (none for an id outside [0, E)).
   struct Problem {
@@ -188,14 +189,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     if (!GROUPED) {
       r.cnt = P.rows;
     } else if (P.idx != nullptr) {
-      const int id = p < P.k ? ld_act_s32(P.idx + p) : -1;
+      const int id = p < P.k ? ld_cg_s32(P.idx + p) : -1;
       r.slot0 = p;
       r.cnt = p == P.k || (id >= 0 && id < P.E) ? 1 : 0;
       r.e = p == P.k ? -1 : r.cnt ? id : 0;
     } else {
-      r.e = ld_act_s32(P.table + 1 + 3 * p);
-      r.slot0 = ld_act_s32(P.table + 2 + 3 * p);
-      r.cnt = ld_act_s32(P.table + 3 + 3 * p);
+      r.e = ld_cg_s32(P.table + 1 + 3 * p);
+      r.slot0 = ld_cg_s32(P.table + 2 + 3 * p);
+      r.cnt = ld_cg_s32(P.table + 3 + 3 * p);
     }
     return r;
   };

@@ -1,0 +1,87 @@
+"""The 8-bit experts where calls follow one another, choices are left out, and rows and weights hold what is not finite."""
+import pytest
+import torch
+
+from _fp8 import assert_within, experts64, rand_rows
+from test_gpu_fp8 import bits, choices, expert_weights, gen
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ml():
+    import moe_layers_gb300 as M
+    M.build()
+    return M
+
+
+@pytest.fixture()
+def h(ml):
+    with ml.Handle(0) as handle:
+        yield handle
+
+
+# ---------------------------------------------------------------------------- calls back to back
+def routings(g, m, e, k):
+    """Few problems after many and the other way round: even choices, all tokens on the same experts, most or all left out."""
+    out = []
+    for i in range(12):
+        idx, w = choices(g, m, e, k)
+        if i % 4 == 1:
+            idx[:] = idx[0].clone()
+        elif i % 4 == 2:
+            idx[:, 1:] = -1
+        elif i % 4 == 3 and i > 4:
+            idx[:] = e
+        out.append((idx, w))
+    return out
+
+
+@pytest.mark.parametrize("m,shared", [(1, True), (1, False), (4, True), (24, False), (64, True)])
+def test_routing_that_changes_from_call_to_call(ml, h, m, shared):
+    """The second product reads the routing before the first one has ended, at one address for all calls."""
+    g = gen(40 + m)
+    E, k, H, I = 40, 4, 512, 256
+    banks, one, W = expert_weights(ml, g, E, H, I, shared)
+    x = rand_rows(g, m, H)
+    X = ml.Fp8Rows(*x)
+    ways = routings(g, m, E, k)
+    n = -(-m * k // 4) * 4  # the copying kernel takes whole 16 bytes
+    held = torch.zeros(len(ways), 2, n, dtype=torch.int32, device="cuda")  # each call's ids and weights
+    for i, (idx, w) in enumerate(ways):
+        held[i, 0, :m * k], held[i, 1, :m * k] = idx.flatten(), w.flatten().view(torch.int32)
+    now = torch.zeros(2, n, dtype=torch.int32, device="cuda")
+    idx0, w0 = now[0, :m * k].view(m, k), now[1, :m * k].view(torch.float32).view(m, k)
+    alone = []
+    for idx, w in ways:
+        alone.append(ml.moe_experts_fp8(h, X, idx, w, W))
+        torch.cuda.synchronize()
+        want, room = experts64(*x, idx, w, *banks, one)
+        assert_within(alone[-1], want, room + 1e-300)
+    ws = torch.empty(ml.moe_experts_fp8_workspace_size(h, W, m, k), dtype=torch.uint8, device="cuda")
+    outs = torch.empty(len(ways), m, H, dtype=torch.bfloat16, device="cuda")
+    stream = torch.cuda.Stream()
+
+    def run():
+        for i, _ in enumerate(ways):
+            ml.test_delayed_copy(h, now, held[i], 0, stream=stream)
+            ml.moe_experts_fp8(h, X, idx0, w0, W, out=outs[i], ws=ws, stream=stream)
+
+    def check():
+        torch.cuda.synchronize()
+        for i, want in enumerate(alone):
+            assert torch.equal(bits(outs[i]), bits(want)), i
+        outs.zero_()
+        torch.cuda.synchronize()
+
+    torch.cuda.synchronize()
+    for _ in range(5):
+        run()
+    check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        run()
+    for _ in range(5):
+        graph.replay()
+    check()
+    assert h.check_device_error() == 0
