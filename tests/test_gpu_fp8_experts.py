@@ -85,3 +85,70 @@ def test_routing_that_changes_from_call_to_call(ml, h, m, shared):
         graph.replay()
     check()
     assert h.check_device_error() == 0
+
+
+# ---------------------------------------------------------------------------- choices left out
+def replay_us(run):
+    """A call in a replayed graph of ten, the quickest of seven replays."""
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        for _ in range(10):
+            run()
+    took = []
+    for _ in range(7):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        with torch.cuda.stream(stream):
+            a.record()
+            graph.replay()
+            b.record()
+        torch.cuda.synchronize()
+        took.append(a.elapsed_time(b) * 100)
+    return min(took)
+
+
+@pytest.mark.parametrize("m", [1, 2])
+def test_choices_left_out_stream_no_weights(ml, h, m):
+    """One choice of sixteen is here, as on a rank that holds a part of the experts. An expert's weights (400 MB) pass in
+    some 60 us, all sixteen's in a millisecond: twice the time of a call with that choice alone leaves room for noise."""
+    E, k, H, I = 2, 16, 16384, 8192
+    g = gen(m)
+
+    def bank(*shape):
+        q = torch.empty(*shape, dtype=torch.uint8, device="cuda").random_(0x20, 0x58, generator=g)
+        return ml.Fp8Weight(q.view(torch.float8_e4m3fn), torch.full((*shape[:-2], shape[-2] // 128, shape[-1] // 128), 1e-4,
+                                                                    device="cuda"))
+
+    W = ml.MoeFp8Weights(bank(E, I, H), bank(E, I, H), bank(E, H, I))
+    X = ml.Fp8Rows(*rand_rows(g, m, H))
+    idx = torch.full((m, k), -1, dtype=torch.int32, device="cuda")
+    idx[:, 5] = 1
+    w = torch.rand(m, k, generator=g, device="cuda")
+    one, w1 = idx[:, 5:6].contiguous(), w[:, 5:6].contiguous()
+    out, out1 = (torch.empty(m, H, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    few = replay_us(lambda: ml.moe_experts_fp8(h, X, one, w1, W, out=out1))
+    left_out = replay_us(lambda: ml.moe_experts_fp8(h, X, idx, w, W, out=out))
+    assert torch.equal(bits(out), bits(out1))
+    assert left_out < 2 * few, f"{left_out:.1f} us with fifteen choices left out, {few:.1f} us without them"
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_one_token_s_choices_in_and_out(ml, h, shared):
+    """Every pattern of four choices here or not."""
+    g = gen(17)
+    E, k, H, I = 6, 4, 256, 128
+    banks, one, W = expert_weights(ml, g, E, H, I, shared)
+    x = rand_rows(g, 1, H)
+    r = torch.randn(1, H, generator=g, device="cuda").bfloat16()
+    for pattern in range(16):
+        idx, w = choices(g, 1, E, k)
+        for j in range(k):
+            if not pattern >> j & 1:
+                idx[0, j] = (-1, E, -2 ** 31, 2 ** 31 - 1)[j]
+                w[0, j] = float("nan")  # a weight that nothing takes
+        out = ml.moe_experts_fp8(h, ml.Fp8Rows(*x), idx, w, W, residual=r)
+        assert_within(out, *experts64(*x, idx, w.nan_to_num(), *banks, one, r))
