@@ -557,9 +557,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // How many clusters of 2 or 4 CTAs, one CTA to an SM, this device holds at a time: the parts of the chip have
 // different numbers of SMs, and not the same ones on every chip. (None if the runtime does not say.)
 static int clusters_held(const dec_handle* h, int size) {
-  static int held[16][5];  // by device; 0: not asked yet, -1: none
+  static std::atomic<int> held[16][5];  // by device; 0: not asked yet, -1: none
   if (h->device < 0 || h->device >= 16) return 0;
-  int& n = held[h->device][size];
+  int n = held[h->device][size].load();
   if (n == 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(size);
@@ -579,6 +579,7 @@ static int clusters_held(const dec_handle* h, int size) {
                     cudaOccupancyMaxActiveClusters(&got, gemm8_kernel<256>, &cfg) == cudaSuccess;
     if (!ok) cudaGetLastError();  // the answer is no; nothing else failed
     n = ok && got > 0 ? got : -1;
+    held[h->device][size].store(n);
   }
   return std::max(n, 0);
 }
@@ -633,12 +634,9 @@ static cudaError_t launch_bn(dec_handle* h, const Linear8& A, const Choice& c, v
   CUtensorMap tx, tw;
   if (!encode_tile(h, &tx, A.x, A.K, A.M, A.ldx, box_rows) || !encode_tile(h, &tw, A.W, A.K, A.N, A.K, BN))
     return cudaErrorInvalidValue;
-  static bool attr_set = false;  // per process; every device gets the same attribute
-  if (!attr_set) {
-    const cudaError_t e = cudaFuncSetAttribute(gemm8_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(h, ready, (const void*)gemm8_kernel<BN>, L::kBytes);
+  if (e != cudaSuccess) return e;
   Gemm8Params P = {};
   P.M = A.M;
   P.N = A.N;

@@ -1,6 +1,7 @@
 // Internal interfaces between the C-ABI layer (api.cu) and the kernels.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -312,6 +313,16 @@ inline cudaEvent_t pool_event(dec_handle* h) {
   }
   cudaEvent_t e = nullptr;
   cudaEventCreate(&e);
+  return e;
+}
+
+// A kernel's dynamic shared memory above 48 KB has to be allowed once on each device: the runtime
+// sets the attribute for the current one alone. `ready` is the kernel's own: the devices where it is set.
+inline cudaError_t allow_smem(const dec_handle* h, std::atomic<uint64_t>& ready, const void* kernel, int bytes) {
+  const uint64_t bit = 1ull << (h->device & 63);
+  if (h->device < 64 && (ready.load() & bit)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && h->device < 64) ready.fetch_or(bit);
   return e;
 }
 

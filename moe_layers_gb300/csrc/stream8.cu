@@ -674,13 +674,9 @@ static cudaError_t launch_one(dec_handle* h, Stream8Params P, int xrows, double 
     return cudaErrorInvalidValue;
   if (!PAIR && P.K % 128 != 0 && !encode_short(h, &m[1], P.bank.W[0], P.K, rows, box)) return cudaErrorInvalidValue;
   const size_t smem = fixed_bytes(xrows, NT, P.K, PAIR) + (size_t)P.stages * one_stage(P.K, PAIR, P.height);
-  static bool attr_set = false;  // per process; every device gets the same attribute
-  if (!attr_set) {
-    const cudaError_t e = cudaFuncSetAttribute(stream8_kernel<NT, PAIR, GROUPED>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(h, ready, (const void*)stream8_kernel<NT, PAIR, GROUPED>, kMaxSmem);
+  if (e != cudaSuccess) return e;
   return launch_k(h, stream8_kernel<NT, PAIR, GROUPED>, dim3(h->sms * ctas), dim3(kThreads), smem, s, m[0], m[1], m[2], m[3], P);
 }
 

@@ -712,13 +712,9 @@ static cudaError_t launch_epi(dec_handle* h, const CUtensorMap& ta, const CUtens
                               const EngineParams& P, int grid, cudaStream_t s) {
   constexpr int NA = (EPI == EPI_SWIGLU) ? 2 : 1;
   using S = EngineSmem<NA, BROWS>;
-  static bool attr_set = false;  // per process; every device gets the same attribute
-  if (!attr_set) {
-    cudaError_t e =
-        cudaFuncSetAttribute(engine_kernel<EPI, BROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kTotal);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(h, ready, (const void*)engine_kernel<EPI, BROWS>, S::kTotal);
+  if (e != cudaSuccess) return e;
   return launch_k(h, engine_kernel<EPI, BROWS>, dim3(grid), dim3(kEngineThreads), (size_t)S::kTotal, s, ta, ta2, tb,
                   P);
 }
