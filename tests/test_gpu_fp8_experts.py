@@ -152,3 +152,46 @@ def test_one_token_s_choices_in_and_out(ml, h, shared):
                 w[0, j] = float("nan")  # a weight that nothing takes
         out = ml.moe_experts_fp8(h, ml.Fp8Rows(*x), idx, w, W, residual=r)
         assert_within(out, *experts64(*x, idx, w.nan_to_num(), *banks, one, r))
+
+
+# ---------------------------------------------------------------------------- rows
+@pytest.mark.parametrize("m", [1, 2, 11, 64])
+def test_strided_rows(ml, h, m):
+    """Columns of wider rows, from a group's start on: values and scales with strides of their own."""
+    g = gen(60 + m)
+    E, k, H, I = 9, 3, 640, 256
+    banks, one, W = expert_weights(ml, g, E, H, I, True)
+    q, s = rand_rows(g, m, 2048)
+    x = (q[:, 384:384 + H], s[:, 3:8])
+    idx, w = choices(g, m, E, k)
+    out = ml.moe_experts_fp8(h, ml.Fp8Rows(*x), idx, w, W)
+    assert_within(out, *experts64(*x, idx, w, *banks, one))
+    dense = ml.moe_experts_fp8(h, ml.Fp8Rows(x[0].contiguous(), x[1].contiguous()), idx, w, W)
+    assert torch.equal(bits(out), bits(dense))
+
+
+@pytest.mark.parametrize("m", [1, 3, 40])
+@pytest.mark.parametrize("what", ["value", "nan scale", "inf scale", "nan weight", "inf weight", "overflow"])
+def test_what_is_not_finite_stays_with_its_token(ml, h, m, what):
+    """The last token's row or routing weight; the others are as without it. An inner row past fp32's range counts as
+    infinite, and a group that holds an infinity is not finite."""
+    g = gen(70 + m)
+    E, k, H, I = 5, 3, 384, 256
+    banks, one, W = expert_weights(ml, g, E, H, I, True)
+    q, s = rand_rows(g, m, H)
+    idx, w = choices(g, m, E, k)
+    before = ml.moe_experts_fp8(h, ml.Fp8Rows(q, s), idx, w, W)
+    assert_within(before, *experts64(q, s, idx, w, *banks, one))
+    q, s, w = q.clone(), s.clone(), w.clone()
+    if what == "value":
+        bits(q)[m - 1, 200] = 0x7F
+    elif what == "nan weight":
+        w[m - 1, 1] = float("nan")
+    elif what == "inf weight":
+        w[m - 1, 1] = float("inf")
+    else:
+        s[m - 1, 1] = {"nan scale": float("nan"), "inf scale": float("inf"), "overflow": 1e25}[what]
+    out = ml.moe_experts_fp8(h, ml.Fp8Rows(q, s), idx, w, W)
+    assert torch.equal(bits(out[:m - 1]), bits(before[:m - 1]))
+    assert not torch.isfinite(out[m - 1]).any()
+    assert h.check_device_error() == 0
