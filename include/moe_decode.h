@@ -584,10 +584,13 @@ dec_status dec_linear_fp8_workspace_size(const dec_handle* h, int M, int N, int 
  * residual itself with the same stride and overlaps nothing else.
  * Kernel families as for dec_linear: SMALL_M streams the weights past the rows
  * (M <= 16), SPLIT_K is the tcgen05 kernel; AUTO takes the first up to M = 8, and
- * up to 16 for weights of at most 64 MB. Weights may be read before the launch's
+ * up to 16 for weights of at most 64 MB. Rows that the first's shared memory does
+ * not hold (16 of 8192 values fit, 8 of 16384, 2 of 65536) take the second, forced
+ * or not. Weights may be read before the launch's
  * dependency wait, as static data; dec_quant_weight just before is safe.
  * The workspace (none for SMALL_M) is zeroed before its first use and then serves
- * calls of any shape, one at a time; its size depends on the forced family.
+ * calls of any shape, one at a time, also after DEC_ERR_TIMEOUT; its size depends
+ * on the forced family.
  * 1 <= M <= 2^20 (prompts too), 1 <= N <= 2^20, K a multiple of 16 in
  * [16, 65536]. */
 dec_status dec_linear_fp8(dec_handle* h, const dec_fp8_rows* x, const dec_fp8_weight* W, const dec_bf16* residual,

@@ -36,7 +36,7 @@ bool linear_shape_ok(int M, int N, int K) {
 
 // The streaming kernel up to 8 rows, and up to 16 with weights of at most 64 MB, where the tcgen05 kernel's
 // ramp counts (16 rows, streaming / tcgen05: 4096 x 4096 8.5 / 9.1 us, 7168 x 8192 18.4 / 18.4, 12288 x 7168
-// 25.2 / 21.2; 8 rows: 7.0 / 9.0, 13.3 / 18.4, 18.8 / 21.2); as forced where its shared memory holds the rows.
+// 25.2 / 21.2; 8 rows: 7.0 / 9.0, 13.3 / 18.4, 18.2 / 21.2); as forced where its shared memory holds the rows.
 bool linear_streams(const dec_handle* h, int M, int N, int K) {
   if (h->force_variant == DEC_VARIANT_SPLIT_K || M > stream8_rows(K, false)) return false;
   return h->force_variant == DEC_VARIANT_SMALL_M || M <= 8 || (int64_t)N * K <= (int64_t)64 << 20;

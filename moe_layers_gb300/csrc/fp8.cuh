@@ -24,8 +24,9 @@ __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
 }
 
 // The scale of a group whose largest absolute value is `most`, and the factor
-// that takes its values to e4m3's range. Below 2^-116 the factor would pass
-// fp32's range: such a group counts as zeros. An infinity has factor 0 (the
+// that takes its values to e4m3's range. Both are normal fp32 numbers down to
+// 2^-117.2 (the scale; the factor would pass fp32's range at 2^-119.2): below
+// 2^-116 a group counts as zeros. An infinity has factor 0 (the
 // group's infinities become NaN, the rest 0) and scale infinity.
 struct Scale8 {
   float scale, up;

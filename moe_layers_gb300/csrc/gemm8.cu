@@ -18,8 +18,8 @@
 // publishes its piece last adds all of them. Either way in k order, without atomics on values:
 // the results follow from the inputs and the shape alone.
 //
-// Measured, in a replayed graph: 12288 x 7168 at 4096 rows 390 us (1.85 PFLOP/s), 64 rows 22.0
-// us (0.61 of the copy rate), 64 x 4096 x 4096 9.6 us. Bound, at many rows, by the adding warps: a
+// Measured, in a replayed graph: 12288 x 7168 at 4096 rows 392 us (1.84 PFLOP/s), 64 rows 22.2
+// us (0.61 of the copy rate), 64 x 4096 x 4096 9.7 us. Bound, at many rows, by the adding warps: a
 // k-block of 128 x 256 is multiplied in some 540 clocks (the same without them) and takes 1170; at
 // few rows by the 600 clocks a k-block that pass between product, fetch and next product.
 //
@@ -550,10 +550,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- host side
-// Weights a tile, and CTAs to a left-over tile: by the time of the longest CTA, in clocks. A
-// k-block of a tile takes 520 + 2.5 BN (measured at 4096 x 12288 x 7168, BN 32 to 256: 609, 636,
-// 757, 750, 1030, 1170), a tile's output some 1500 and the exchange of a shared tile's pieces
-// 10000 to 20000 through L2, half of that in a cluster; the weights' bytes pass at 23 a clock and SM at most.
 // How many clusters of 2 or 4 CTAs, one CTA to an SM, this device holds at a time: the parts of the chip have
 // different numbers of SMs, and not the same ones on every chip. (None if the runtime does not say.)
 static int clusters_held(const dec_handle* h, int size) {
@@ -588,6 +584,12 @@ struct Choice {
   int bn, grid, split;
   bool cluster;
 };
+// Weights a tile, and CTAs to a left-over tile: by the time of the longest CTA, in clocks. A
+// k-block of a tile takes 520 + 2.5 BN (measured at 4096 x 12288 x 7168, BN 32 to 256: 609, 636,
+// 757, 750, 1030, 1170), a tile's output some 1500; the weights' bytes pass at 23 a clock and SM at
+// most. The exchange of a shared tile's pieces counts 16000 to 22000 through L2 and 5600 or 7200 in a
+// cluster: not measured by itself, but set from whole launches (64 x 4096 x 4096: 13.1 us through L2,
+// 9.6 in clusters).
 static Choice choose(const dec_handle* h, int M, int N, int K) {
   const long long mt = (M + kRows - 1) / kRows, KB = (K + kBlock - 1) / kBlock;
   Choice best = {256, 1, 1, false};

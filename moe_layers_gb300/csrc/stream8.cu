@@ -31,8 +31,8 @@
 // segment. The ring runs on from one segment into the next, while the activation rows change.
 //
 // Measured, in a replayed graph, of the copy rate of 6.7 TB/s: 12288 x 7168 at one row 15.8 us
-// (0.83), at eight 18.7 (0.71: one CTA to an SM); 64 tokens of 384 experts of 7168 x 256 254 us
-// (0.91), 8 tokens of 32 experts of 7168 x 2048 221 (0.88). Bound by memory, and by 3 us a launch
+// (0.83), at eight 18.2 (0.72: one CTA to an SM); 64 tokens of 384 experts of 7168 x 256 259 us
+// (0.91), 8 tokens of 32 experts of 7168 x 2048 222 (0.88). Bound by memory, and by 3 us a launch
 // of ramp and last sums.
 #include <algorithm>
 #include <cmath>
@@ -318,25 +318,27 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
             pack_e4m3x4(v.x * sc.up, v.y * sc.up, v.z * sc.up, v.w * sc.up);
         if (lane == 0) xsc[b * COLS + j] = sc.scale;
       }
-    } else
-    for (int j = warp; j < COLS; j += kWarps) {
-      const bool in = j < cnt;
-      const long long row = in && GROUPED && P.by_token && P.idx == nullptr ? ld_act_s32(tokens + slot0 + j) : slot0 + j;
-      if (in) {
-        const uint8_t* src = P.x + (GROUPED && P.idx != nullptr ? 0 : row) * P.ldx;
-        uint8_t* dst = xq + (size_t)j * xpitch;
-        for (int k = lane * 16; k < xpitch - 64; k += 512) {
-          if (k < P.K)
-            cp_async16(dst + k, src + k);
-          else
-            *reinterpret_cast<uint4*>(dst + k) = make_uint4(0, 0, 0, 0);
+    } else {
+      for (int j = warp; j < COLS; j += kWarps) {
+        const bool in = j < cnt;
+        const long long row =
+            in && GROUPED && P.by_token && P.idx == nullptr ? ld_act_s32(tokens + slot0 + j) : slot0 + j;
+        if (in) {
+          const uint8_t* src = P.x + (GROUPED && P.idx != nullptr ? 0 : row) * P.ldx;
+          uint8_t* dst = xq + (size_t)j * xpitch;
+          for (int k = lane * 16; k < xpitch - 64; k += 512) {
+            if (k < P.K)
+              cp_async16(dst + k, src + k);
+            else
+              *reinterpret_cast<uint4*>(dst + k) = make_uint4(0, 0, 0, 0);
+          }
         }
-      }
-      for (int b = lane; b < KB; b += 32) {
-        if (in)
-          copy4(xsc + b * COLS + j, P.xs + (GROUPED && P.idx != nullptr ? 0 : row) * P.ldxs + b);
-        else
-          xsc[b * COLS + j] = 0.f;
+        for (int b = lane; b < KB; b += 32) {
+          if (in)
+            copy4(xsc + b * COLS + j, P.xs + (GROUPED && P.idx != nullptr ? 0 : row) * P.ldxs + b);
+          else
+            xsc[b * COLS + j] = 0.f;
+        }
       }
     }
     cp_async_wait_all();
@@ -660,24 +662,26 @@ static cudaError_t launch_one(dec_handle* h, Stream8Params P, int xrows, double 
   P.err = h->d_err;
   P.wait_ns = h->wait_ns;
   if (P.stages < 2) return cudaErrorInvalidConfiguration;
-  const int box = kWarps / P.WK * P.height;
+  const int box = kWarps / P.WK * P.height, across = P.WK * blocks_each(PAIR ? 2 : 1);
   const long long rows = (long long)E * P.R;
   const Stream8Bank& S = P.shared.W[0] != nullptr ? P.shared : P.bank;
   const long long srows = P.shared.W[0] != nullptr ? P.R : rows;
   CUtensorMap m[4];
-  if (!encode_blocks(h, &m[0], P.bank.W[0], P.K, rows, box, P.WK * blocks_each(PAIR ? 2 : 1)) || !encode_blocks(h, &m[2], S.W[0], P.K, srows, box, P.WK * blocks_each(PAIR ? 2 : 1)))
+  if (!encode_blocks(h, &m[0], P.bank.W[0], P.K, rows, box, across) ||
+      !encode_blocks(h, &m[2], S.W[0], P.K, srows, box, across))
     return cudaErrorInvalidValue;
   m[1] = m[0];
   m[3] = m[2];
-  if (PAIR && (!encode_blocks(h, &m[1], P.bank.W[1], P.K, rows, box, P.WK * blocks_each(PAIR ? 2 : 1)) ||
-               !encode_blocks(h, &m[3], S.W[1], P.K, srows, box, P.WK * blocks_each(PAIR ? 2 : 1))))
+  if (PAIR && (!encode_blocks(h, &m[1], P.bank.W[1], P.K, rows, box, across) ||
+               !encode_blocks(h, &m[3], S.W[1], P.K, srows, box, across)))
     return cudaErrorInvalidValue;
   if (!PAIR && P.K % 128 != 0 && !encode_short(h, &m[1], P.bank.W[0], P.K, rows, box)) return cudaErrorInvalidValue;
   const size_t smem = fixed_bytes(xrows, NT, P.K, PAIR) + (size_t)P.stages * one_stage(P.K, PAIR, P.height);
   static std::atomic<uint64_t> ready{0};
   const cudaError_t e = allow_smem(h, ready, (const void*)stream8_kernel<NT, PAIR, GROUPED>, kMaxSmem);
   if (e != cudaSuccess) return e;
-  return launch_k(h, stream8_kernel<NT, PAIR, GROUPED>, dim3(h->sms * ctas), dim3(kThreads), smem, s, m[0], m[1], m[2], m[3], P);
+  return launch_k(h, stream8_kernel<NT, PAIR, GROUPED>, dim3(h->sms * ctas), dim3(kThreads), smem, s, m[0], m[1], m[2],
+                  m[3], P);
 }
 
 int stream8_rows(int K, bool pair) {
@@ -707,8 +711,9 @@ cudaError_t launch_stream8_linear(dec_handle* h, const Linear8& L, cudaStream_t 
 Experts8Plan experts8_plan(int M, int k, int E, int H, int I, bool shared) {
   Experts8Plan p;
   // Problems of up to 16 rows where the experts have four tokens and more in the mean, else of 8,
-  // whose rows leave twice the room for weights in flight (64 tokens, 384 experts of 7168 x 256: 260 us, with 16 rows 350; 64 tokens that
-  // all choose the same 8 experts of 7168 x 2048 read each expert four times with 16: 395 us).
+  // whose rows leave twice the room for weights in flight (64 tokens, 384 experts of 7168 x 256: 260 us,
+  // with 16 rows 350; 64 tokens that all choose the same 8 experts of 7168 x 2048 read each expert four
+  // times with 16: 395 us).
   const int want = M * k >= 4 * E ? 16 : 8;
   p.most = std::min(std::min(stream8_rows(H, true), stream8_rows(I, false)), want);
   p.slots = M * k + M;
