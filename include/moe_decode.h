@@ -687,6 +687,13 @@ dec_status dec_test_set_moe_front(dec_handle* h, int enable);
  * DEC_ERR_INVALID_ARG. */
 dec_status dec_test_set_engine_finish(dec_handle* h, int mode);
 
+/* every > 0: in the tcgen05 kernel of dec_linear_fp8 the CTAs whose index is a
+ * multiple of `every` act as if their first wait had run past the limit: they
+ * set the device error word, drain what they have in flight and leave. 0
+ * (default): none. Used to test that a call whose waits ran out in part of its
+ * CTAs leaves its workspace ready. */
+dec_status dec_test_set_linear_fp8_give_up(dec_handle* h, int every);
+
 /* Hold `ctas` SMs (1 <= ctas <= the device's SM count) for hold_ns
  * nanoseconds (at most 2 s) with a kernel on `stream`: one CTA per SM that
  * takes the whole per-block shared memory, so nothing else fits beside it,

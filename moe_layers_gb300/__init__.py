@@ -117,6 +117,7 @@ def _load():
         "dec_set_l2_ahead": [P, I],
         "dec_test_set_moe_front": [P, I],
         "dec_test_set_engine_finish": [P, I],
+        "dec_test_set_linear_fp8_give_up": [P, I],
         "dec_check_device_error": [P],
         "dec_linear_workspace_size": [P, I, I, I, ctypes.POINTER(Z)],
         "dec_linear": [P, P, I, P, P, I, I, I, P, Z, P],
@@ -308,6 +309,10 @@ class Handle:
     def test_set_engine_finish(self, mode: int) -> None:
         """Test hook: how the split-K kernel finishes split tiles (0 default; 1, 2 the fallback paths)."""
         _check(_load().dec_test_set_engine_finish(self._h, int(mode)), "dec_test_set_engine_finish")
+
+    def test_set_linear_fp8_give_up(self, every: int) -> None:
+        """Test hook: every n-th CTA of dec_linear_fp8's tcgen05 kernel gives up its first wait (0: none)."""
+        _check(_load().dec_test_set_linear_fp8_give_up(self._h, int(every)), "dec_test_set_linear_fp8_give_up")
 
     def set_l2_ahead(self, nbytes: int) -> None:
         _check(_load().dec_set_l2_ahead(self._h, int(nbytes)), "dec_set_l2_ahead")

@@ -747,6 +747,12 @@ dec_status dec_test_set_engine_finish(dec_handle* h, int mode) {
   return DEC_OK;
 }
 
+dec_status dec_test_set_linear_fp8_give_up(dec_handle* h, int every) {
+  if (h == nullptr || every < 0) return DEC_ERR_INVALID_ARG;
+  h->gemm8_give_up = every;
+  return DEC_OK;
+}
+
 dec_status dec_set_l2_ahead(dec_handle* h, int bytes) {
   if (h == nullptr || bytes < 0 || bytes > (16 << 20)) return DEC_ERR_INVALID_ARG;
   h->l2_ahead = bytes;

@@ -78,6 +78,7 @@ struct Gemm8Params {
   int* counters;   // one for each shared tile: pieces published
   int* err;
   unsigned long long wait_ns;
+  int give_up;  // a test's: CTAs of a multiple of this index give up at once
 };
 
 constexpr int kPanel = 16;  // tiles of rows
@@ -325,7 +326,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     int b = 0, turn = 0;
     uint32_t tph = 0;
-    bool ok = true;
+    bool ok = P.give_up == 0 || (int)blockIdx.x % P.give_up != 0;
+    if (!ok && et == 0) {
+      *abort_flag = 1;
+      atomicOr(P.err, DEV_ERR_TIMEOUT);
+    }
     const int KB = P.KB;
     for (Work work(P); work.next();) {
       const int kb0 = work.kb0, kb1 = work.kb1;
@@ -661,6 +666,7 @@ static cudaError_t launch_bn(dec_handle* h, const Linear8& A, const Choice& c, v
   P.piece_rows = piece_rows(A.M);
   P.err = h->d_err;
   P.wait_ns = h->wait_ns;
+  P.give_up = h->gemm8_give_up;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(c.grid);
   cfg.blockDim = dim3(kThreads);

@@ -27,6 +27,7 @@ struct dec_handle {
   int shared_ctas = 0;              // CTAs for the shared expert's kernels (0 = default)
   int moe_front = 1;                // one to a few tokens: the MoE front launches (0: test hook, the fallback path)
   int engine_finish = 0;            // split-K split-tile finish (test hook: 1, 2 force the fallback paths)
+  int gemm8_give_up = 0;            // 8-bit tcgen05 product (test hook: every n-th CTA gives up its first wait)
   int l2_ahead = 49152;             // small-matrix kernels: weight bytes per CTA requested into L2 ahead
   PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   // measurement

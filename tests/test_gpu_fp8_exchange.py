@@ -1,7 +1,5 @@
 """The 8-bit product where CTAs exchange pieces of a tile through the workspace: whole rounds of tiles, then left-over
 ones that two to four CTAs share."""
-import time
-
 import pytest
 import torch
 
@@ -48,34 +46,38 @@ def counters(ws):
     return ws[:counter_bytes()].view(torch.int32)
 
 
-def test_a_wait_that_runs_out_leaves_the_workspace_ready(ml, h):
-    """Part of the CTAs give up: those that start while the kernel ahead is still running wait for its rows past the
-    handle's limit, the others start when an SM is free again. A shared tile of CTAs of both kinds is lost, and the
-    error word says so; the next call on the workspace is not."""
-    m, n, k = ragged(30, 3, 7168)  # 31 tiles of four CTAs each where a device has 152 SMs
+@pytest.mark.parametrize("every", [1, 2, 3, 5])
+@pytest.mark.parametrize("at,kw", [((30, 3, 7168), {}), ((40, 3, 7184), {}), ((52, 3, 16384), {})], ids=str)
+def test_a_wait_that_runs_out_leaves_the_workspace_ready(ml, h, at, kw, every):
+    """Part of the CTAs give up: of a tile that four, three or two share some, all or none. The call is lost, and the error
+    word says so; the next one on the workspace is not."""
+    m, n, k = ragged(*at, **kw)
     g = gen(5)
     x, w = rand_rows(g, m, k), rand_weight(g, n, k)
     X, W = ml.Fp8Rows(*x), ml.Fp8Weight(*w)
     ws = workspace(ml, h, m, n, k)
-    early = 3 * sms() // 16 * 4 + 2  # CTAs that start at once, less one where the kernel ahead has its SM
-    src, dst = (torch.zeros(4, device="cuda") for _ in range(2))
-    main, side = torch.cuda.Stream(), torch.cuda.Stream()
-    ml.dec_linear_fp8(h, X, W, ws=ws)  # the code is loaded
-    ml.test_delayed_copy(h, dst, src, 1000)
-    ml.test_occupy_sms(h, 1, 1000)
-    torch.cuda.synchronize()
-    h.set_wait_limit_ns(20_000_000)
-    try:
-        ml.test_occupy_sms(h, sms() - early, 900_000_000, stream=side)
-        time.sleep(0.002)  # it is resident before the others are launched
-        ml.test_delayed_copy(h, dst, src, 500_000_000, stream=main)
-        ml.dec_linear_fp8(h, X, W, ws=ws, stream=main)
-        torch.cuda.synchronize()
-    finally:
-        h.set_wait_limit_ns(500_000_000)
-    assert h.check_device_error() == ml.DEC_ERR_TIMEOUT
-    assert not counters(ws).any()
+    h.test_set_linear_fp8_give_up(every)
+    for _ in range(2):
+        ml.dec_linear_fp8(h, X, W, ws=ws)
+        assert h.check_device_error() == ml.DEC_ERR_TIMEOUT
+        assert not counters(ws).any()
+    h.test_set_linear_fp8_give_up(0)
     y = ml.dec_linear_fp8(h, X, W, ws=ws)
+    assert h.check_device_error() == ml.DEC_OK
+    assert_within(y, *linear64(*x, *w))
+
+
+@pytest.mark.parametrize("every", [1, 2, 3])
+@pytest.mark.parametrize("m,n,k", [(64, 4096, 4096), (64, 12288, 7168), (20, 300, 1040), (700, 7168, 1024)])
+def test_a_wait_that_runs_out_in_clusters_and_whole_tiles(ml, h, m, n, k, every):
+    g = gen(6)
+    x, w = rand_rows(g, m, k), rand_weight(g, n, k)
+    X, W = ml.Fp8Rows(*x), ml.Fp8Weight(*w)
+    h.test_set_linear_fp8_give_up(every)
+    ml.dec_linear_fp8(h, X, W)
+    assert h.check_device_error() == ml.DEC_ERR_TIMEOUT
+    h.test_set_linear_fp8_give_up(0)
+    y = ml.dec_linear_fp8(h, X, W)
     assert h.check_device_error() == ml.DEC_OK
     assert_within(y, *linear64(*x, *w))
 
