@@ -287,6 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
+    pdl_wait();  // the time of the kernel ahead is not a wait's
     int s = 0, b = 0;
     uint32_t ph = 0, tph = 0;
     bool ok = true;

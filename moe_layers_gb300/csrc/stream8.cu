@@ -246,7 +246,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
           }
           __syncwarp();
           issued = min(issued + 1, P.stages);
-          if (++s == P.stages) s = 0, ph ^= 1u;
+          if (++s == P.stages) {
+            // From here on stages have to come back: not before the kernel ahead has ended, whose time is not a wait's.
+            if (ph == 0) pdl_wait();
+            s = 0, ph ^= 1u;
+          }
         }
     }
     // No copy may still be in flight when the CTA exits: the ring's last stages, newest first.

@@ -291,3 +291,23 @@ def test_experts_past_32_bits(ml, h):
         wt = torch.rand(m, 4, generator=g, device="cuda")
         out = ml.moe_experts_fp8(h, ml.Fp8Rows(*x), idx, wt, W)
         assert_within(out, *experts64(*x, idx, wt, *made))
+
+
+# ---------------------------------------------------------------------------- waits
+@pytest.mark.parametrize("m,n,k", [(1, 12288, 7168), (16, 4096, 4096), (64, 4096, 4096), (40, 300, 1040), (300, 20000, 7168)])
+def test_a_slow_kernel_ahead_is_no_wait_that_runs_out(ml, h, m, n, k):
+    """The launch starts early and has filled its rings long before its rows are there: the limit of a wait counts from then."""
+    g = gen(m)
+    (q, s), w = rand_rows(g, m, k), rand_weight(g, n, k)
+    (qf, _), (qf0, q0) = padded(q), padded(torch.zeros_like(q))
+    x, W = ml.Fp8Rows(q0, s), ml.Fp8Weight(*w)
+    ml.dec_linear_fp8(h, x, W)
+    ml.test_delayed_copy(h, qf0, qf, 1000)
+    qf0.view(torch.uint8).zero_()
+    torch.cuda.synchronize()
+    h.set_wait_limit_ns(20_000_000)
+    for _ in range(2):
+        ml.test_delayed_copy(h, qf0, qf, 100_000_000)
+        y = ml.dec_linear_fp8(h, x, W)
+        assert h.check_device_error() == 0
+        assert_within(y, *linear64(q, s, *w))
